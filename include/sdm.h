@@ -45,7 +45,9 @@ typedef enum sdm_status {
     SDM_ERR_WORKSPACE = 7     /* workspace missing or too small                  */
 } sdm_status;
 
-typedef enum sdm_dtype { SDM_F32 = 0, SDM_BF16 = 1 } sdm_dtype;
+/* SDM_E4M3 (8-bit floats of 4 exponent and 3 mantissa bits, largest value 448)
+ * is an output type of sdm_residual_norm only. */
+typedef enum sdm_dtype { SDM_F32 = 0, SDM_BF16 = 1, SDM_E4M3 = 2 } sdm_dtype;
 
 /* The two write rules the notes keep side by side ([SDM] §2.4-§2.5):
  *   SDM_DELTA_EQ4:  M[i] <- a M[i] + b w_i (v - a M[i])         (Eq. (4), per slot)
@@ -355,6 +357,157 @@ int sdm_gates(const void* x, int x_dtype, const void* W_a, const void* W_b, int 
  */
 int sdm_output_gate(const float* y, const float* gamma, const void* g, int g_dtype, float eps,
                     int64_t B, int64_t H, int64_t T, int64_t dv, float* o, void* stream);
+
+/*
+ * The dense gated recurrence: the layers that a stack puts beside its sparse
+ * ones, with the scan's gates, v and y ([SDM] §2.1 Eq. (1) with the gates of
+ * §2.4: a state of dk rows, all of them decayed and written by every token).
+ */
+
+/*
+ * sdm_dense_scan_workspace_bytes -- device workspace sdm_dense_scan_forward
+ * needs (0: none, e.g. when there is no work or T <= 8; -1: invalid sizes).
+ */
+int64_t sdm_dense_scan_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
+
+/*
+ * sdm_dense_scan_forward -- for t = 0 .. T-1, for each (b, h):
+ *     S_t = alpha_t S_{t-1} + beta_t k_t (x) v_t
+ *     y_t = q_t S_t                                  (after this token's write)
+ *   q, k         [B, H, T, dk]  in_dtype (SDM_F32 or SDM_BF16); a scale of the
+ *                queries is the caller's
+ *   v            [B, H, T, dv]  in_dtype
+ *   alpha, beta  [B, H, T]      fp32 gates (as sdm_gates writes them; alpha = 0
+ *                starts a new sequence, alpha = 1 with beta = 0 skips a token)
+ *   S0           [B, H, dk, dv] fp32: the state before token 0, or NULL (zeros)
+ *   S            [B, H, dk, dv] fp32 (out): the state after token T-1, or NULL
+ *                (not wanted); may be S0 itself (decoding)
+ *   y            [B, H, T, dv]  fp32 (out), the layout sdm_output_gate reads
+ *   workspace    >= sdm_dense_scan_workspace_bytes bytes, 16-byte aligned (may be
+ *                NULL where that is 0)
+ * Products and sums are fp32 for both input types, states fp32. A sequence may
+ * be split over several calls. Inputs must be finite: tokens are worked in
+ * tiles, and a NaN or infinity may reach earlier tokens of its tile. T = 0
+ * passes the state on (S = S0).
+ * Supported: dk, dv multiples of 8 up to 256; B*H*ceil(T/64)*4 < 2^31.
+ */
+int sdm_dense_scan_forward(const void* q, const void* k, const void* v, int in_dtype,
+                           const float* alpha, const float* beta, const float* S0, float* S, float* y,
+                           int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * sdm_dense_scan_backward_workspace_bytes -- device workspace
+ * sdm_dense_scan_backward needs: the states S and G at the bounds of segments
+ * of at most 512 tokens, and two numbers a token (0: no work, -1: invalid sizes).
+ */
+int64_t sdm_dense_scan_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
+
+/*
+ * sdm_dense_scan_backward -- the gradients of sdm_dense_scan_forward, with
+ *   G_t = alpha_{t+1} G_{t+1} + q_t (x) dy_t, and dL/dS_T in place of alpha G past the end:
+ *   dq_t = S_t dy_t    dk_t = beta_t G_t v_t    dv_t = beta_t G_t^T k_t    dbeta_t = k_t^T G_t v_t
+ *   dlog_alpha_t = alpha_t dL/dalpha_t = <G_t, alpha_t S_{t-1}>
+ * The decay's gradient is the one to ln alpha: it is finite for alpha = 0, and
+ * with alpha = exp(-A softplus(z)) the gate's inputs follow as
+ * dz = -A sigmoid(z) dlog_alpha, dA = -softplus(z) dlog_alpha.
+ *   q, k, v, in_dtype, alpha, beta, S0: as given to the forward call
+ *   dy [B, H, T, dv] fp32: dL/dy;  dS [B, H, dk, dv] fp32: dL/dS, or NULL (zeros)
+ *   dq, dk_out [B, H, T, dk], dv_out [B, H, T, dv], dlog_alpha, dbeta [B, H, T]: fp32 (out)
+ *   dS0 [B, H, dk, dv] fp32 (out): dL/dS0, or NULL (not wanted); may be dS itself
+ *   workspace >= sdm_dense_scan_backward_workspace_bytes bytes, 16-byte aligned
+ * The states are formed again from the inputs; nothing is kept from the forward
+ * call. Split sequences are differentiated last call first, dS0 passed on as dS.
+ * Same support and preconditions as the forward; T = 0 gives dS0 = dS.
+ */
+int sdm_dense_scan_backward(const void* q, const void* k, const void* v, int in_dtype,
+                            const float* alpha, const float* beta, const float* dy,
+                            const float* S0, const float* dS,
+                            float* dq, float* dk_out, float* dv_out, float* dlog_alpha, float* dbeta, float* dS0,
+                            int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * sdm_residual_norm -- the residual stream's addition and RMS-Norm in front of a
+ * layer, per row (token):
+ *   h = x + res,   y = h / sqrt(mean_j h_j^2 + eps) * gamma
+ *   x [rows, d] x_dtype;  res [rows, d], h [rows, d] (out) h_dtype, both or neither
+ *   NULL (then h = x and nothing is stored; h_dtype still names a dtype);
+ *   gamma [d] fp32; eps >= 0
+ *   y [rows, d] (out) y_dtype: SDM_F32, SDM_BF16, or SDM_E4M3 with
+ *   scale (out, fp32; else unused, may be NULL): with group = 0 one per row, [rows, 1]; else
+ *   one per `group` columns, [rows, d / group]. scale = max |y| / 448 over its columns (0
+ *   where all are 0, else at least 2^-126), and y holds y / scale, rounded to nearest even
+ * The norm is that of the fp32 sum; h is stored rounded to its dtype. h may
+ * be res, or x in x's dtype (in place); y may not alias x, res or h.
+ * Supported: 1 <= d <= 16384; group 0, or a power of two from 32 to 512 that
+ * divides d; rows < 2^31. rows = 0 is empty work.
+ */
+int sdm_residual_norm(const void* x, int x_dtype, const void* res, void* h, int h_dtype, const float* gamma,
+                      float eps, int64_t rows, int64_t d, void* y, int y_dtype, float* scale, int64_t group,
+                      void* stream);
+
+/*
+ * sdm_residual_norm_backward_workspace_bytes -- device workspace
+ * sdm_residual_norm_backward needs (0: no work, -1: invalid sizes).
+ */
+int64_t sdm_residual_norm_backward_workspace_bytes(int64_t rows, int64_t d);
+
+/*
+ * sdm_residual_norm_backward -- its gradients, from the stored h (x where there was no
+ * residual), with r = 1 / sqrt(mean h^2 + eps) and n = h r:
+ *   dx = dh + r (gamma dy - n mean_j(gamma dy n)),   dgamma = sum over rows of dy n
+ *   dy [rows, d]: dL/dy; dh [rows, d]: what arrives at h from the layers behind, or
+ *   NULL (nothing); dx [rows, d] (out): the gradient of x and of res alike; all three
+ *   g_dtype; h [rows, d] h_dtype; gamma [d], dgamma [d] (out) fp32
+ *   workspace >= sdm_residual_norm_backward_workspace_bytes bytes, 16-byte aligned
+ * dx may be dy or dh, or h in h's dtype. The sums' order follows from the sizes alone.
+ * Support as sdm_residual_norm; rows = 0 is empty work (dgamma is not written).
+ */
+int sdm_residual_norm_backward(const void* dy, const void* dh, int g_dtype, const void* h, int h_dtype,
+                               const float* gamma, float eps, int64_t rows, int64_t d, void* dx, float* dgamma,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * sdm_balance_workspace_bytes -- device workspace sdm_balance_forward needs (-1:
+ * invalid sizes).
+ */
+int64_t sdm_balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t K, int64_t N);
+
+/*
+ * sdm_balance_forward -- how evenly an addressing result uses the slots, per
+ * head over the n tokens that the mask keeps:
+ *   counts[h,i] = selections of slot i;   mass[h,i] = the sum of their weights
+ *   loss[h] = N sum_i f_i P_i,  f_i = counts / (n K),  P_i = mass / n
+ * (1 when the slots are chosen evenly with weights that sum to 1, N / K when
+ * all tokens choose the same K; 0 when no token is kept).
+ *   idx, wt  [B, H, T, K]  int32 slots, fp32 weights, as sdm_address writes them
+ *            (W or R as K); |wt| <= 2
+ *   mask     [B, T] bytes, non-zero: kept; or NULL (all are). Any alignment
+ *   counts, mass [H, N]  int32 / fp32 (out);  tokens [1] int32 (out): n;  loss [H] fp32 (out)
+ *   workspace >= sdm_balance_workspace_bytes bytes, 16-byte aligned
+ * Selections outside [0, N) are left out; a kept weight that is NaN or beyond 2
+ * in magnitude makes its head's mass and loss NaN. Masked tokens are not
+ * looked at. Weights are added in fixed point (to 2^-40, or with more than 2^21
+ * selections B*H*T*K to 2^-(61 - ceil(log2 B*H*T*K))), so results do not
+ * depend on the order of the additions. Without tokens (B or T = 0) the outputs are zeros.
+ * Supported: N <= 2^18, K <= 256, H <= 4096, B*T*K < 2^31.
+ */
+int sdm_balance_forward(const int32_t* idx, const float* wt, const uint8_t* mask,
+                        int64_t B, int64_t H, int64_t T, int64_t K, int64_t N,
+                        int32_t* counts, float* mass, int32_t* tokens, float* loss,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * sdm_balance_backward -- the loss's gradient to the weights (the counts are
+ * constants): dwt[b,h,t,p] = dloss[h] N / n * f[idx] at kept tokens and slots in
+ * range, 0 elsewhere. It adds to what sdm_scan_backward gives for the same weights.
+ *   idx, mask as given, counts and tokens as written by the forward call;
+ *   dloss [H] fp32: dL/dloss;  dwt [B, H, T, K] fp32 (out)
+ */
+int sdm_balance_backward(const int32_t* idx, const uint8_t* mask, const int32_t* counts, const int32_t* tokens,
+                         const float* dloss, int64_t B, int64_t H, int64_t T, int64_t K, int64_t N, float* dwt,
+                         void* stream);
 
 #ifdef __cplusplus
 }

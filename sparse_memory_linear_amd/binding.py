@@ -16,7 +16,7 @@ import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsdm.so")
 
-SDM_F32, SDM_BF16 = 0, 1
+SDM_F32, SDM_BF16, SDM_E4M3 = 0, 1, 2
 SDM_DELTA_EQ4, SDM_DELTA_FIG2 = 0, 1
 FORMS = {"eq4": SDM_DELTA_EQ4, "fig2": SDM_DELTA_FIG2}
 
@@ -51,6 +51,19 @@ _SIGS = {
     "sdm_state_init_backward": (_I, [_P, _P, _I64, _I64, _I64, _I64, _P]),
     "sdm_gates": (_I, [_P, _I, _P, _P, _I, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P]),
     "sdm_output_gate": (_I, [_P, _P, _P, _I, ctypes.c_float, _I64, _I64, _I64, _I64, _P, _P]),
+    "sdm_dense_scan_workspace_bytes": (_I64, [_I64, _I64, _I64, _I64, _I64]),
+    "sdm_dense_scan_forward": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64,
+                                    _P, _I64, _P]),
+    "sdm_dense_scan_backward_workspace_bytes": (_I64, [_I64, _I64, _I64, _I64, _I64]),
+    "sdm_dense_scan_backward": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                     _I64, _I64, _I64, _I64, _I64, _P, _I64, _P]),
+    "sdm_residual_norm": (_I, [_P, _I, _P, _P, _I, _P, ctypes.c_float, _I64, _I64, _P, _I, _P, _I64, _P]),
+    "sdm_residual_norm_backward_workspace_bytes": (_I64, [_I64, _I64]),
+    "sdm_residual_norm_backward": (_I, [_P, _P, _I, _P, _I, _P, ctypes.c_float, _I64, _I64, _P, _P,
+                                        _P, _I64, _P]),
+    "sdm_balance_workspace_bytes": (_I64, [_I64, _I64, _I64, _I64, _I64]),
+    "sdm_balance_forward": (_I, [_P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P]),
+    "sdm_balance_backward": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P]),
 }
 
 _lib = None
@@ -431,3 +444,223 @@ def sdm_state_init_backward(dM: torch.Tensor, out: Optional[torch.Tensor] = None
     _check("sdm_state_init_backward", lib().sdm_state_init_backward(
         _ptr(dM), _ptr(dM0), B, H, N, dv, _stream(d)))
     return dM0
+
+
+def sdm_dense_scan_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int) -> int:
+    n = lib().sdm_dense_scan_workspace_bytes(B, H, T, dk, dv)
+    if n < 0:
+        raise ValueError("invalid sizes for the dense scan workspace")
+    return n
+
+
+def _dense_inputs(fn, q, k, v, alpha, beta, states):
+    d = _dev(q, k, v, alpha, beta)
+    B, H, T, dk = q.shape
+    dv = v.shape[3]
+    for name, t, shp in (("k", k, (B, H, T, dk)), ("v", v, (B, H, T, dv)), ("alpha", alpha, (B, H, T)),
+                         ("beta", beta, (B, H, T))):
+        if tuple(t.shape) != shp:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shp}")
+    if k.dtype != q.dtype or v.dtype != q.dtype or alpha.dtype != torch.float32 or beta.dtype != torch.float32:
+        raise ValueError(f"dtype mismatch in {fn}")
+    for name, t in states:
+        if t is not None:
+            _f32_out(t, (B, H, dk, dv), d, name)
+    return d, (B, H, T, dk, dv)
+
+
+def sdm_dense_scan_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor,
+                           beta: torch.Tensor, S0: Optional[torch.Tensor] = None,
+                           S: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Dense gated recurrence S_t = alpha_t S_{t-1} + beta_t k_t (x) v_t, y_t = q_t S_t.
+
+    q, k [B,H,T,dk], v [B,H,T,dv] (one dtype, fp32 or bf16), alpha, beta [B,H,T] fp32,
+    S0 [B,H,dk,dv] fp32 or None (zeros). Returns (y [B,H,T,dv] fp32, S the last state);
+    ``S`` and ``y`` may pass them preallocated, and S may be S0 (updated in place).
+    """
+    d, (B, H, T, dk, dv) = _dense_inputs("sdm_dense_scan_forward", q, k, v, alpha, beta, (("S0", S0), ("S", S)))
+    S = _f32_out(S, (B, H, dk, dv), d, "S")
+    y = _f32_out(y, (B, H, T, dv), d, "y")
+    n = sdm_dense_scan_workspace_bytes(B, H, T, dk, dv)
+    ws = _workspace(workspace, n, d) if n or workspace is not None else None
+    _check("sdm_dense_scan_forward", lib().sdm_dense_scan_forward(
+        _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(alpha), _ptr(beta), _ptr(S0), _ptr(S), _ptr(y),
+        B, H, T, dk, dv, _ptr(ws), ws.numel() if ws is not None else 0, _stream(d)))
+    return y, S
+
+
+def sdm_dense_scan_backward_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int) -> int:
+    n = lib().sdm_dense_scan_backward_workspace_bytes(B, H, T, dk, dv)
+    if n < 0:
+        raise ValueError("invalid sizes for the dense backward workspace")
+    return n
+
+
+def sdm_dense_scan_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor,
+                            beta: torch.Tensor, dy: torch.Tensor, S0: Optional[torch.Tensor] = None,
+                            dS: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                            workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of one sdm_dense_scan_forward call (nothing is kept from it).
+
+    dy [B,H,T,dv] fp32; dS [B,H,dk,dv] fp32 or None: the gradient of the last state. Returns
+    a dict with dq, dk [B,H,T,dk], dv [B,H,T,dv], dlog_alpha (to ln alpha), dbeta [B,H,T] and
+    dS0 [B,H,dk,dv], all fp32; ``out`` may pass those tensors preallocated.
+    """
+    d, (B, H, T, dk, dv) = _dense_inputs("sdm_dense_scan_backward", q, k, v, alpha, beta, (("S0", S0), ("dS", dS)))
+    _f32_out(dy, (B, H, T, dv), d, "dy")
+    out = dict(out or {})
+    shapes = {"dq": (B, H, T, dk), "dk": (B, H, T, dk), "dv": (B, H, T, dv), "dlog_alpha": (B, H, T),
+              "dbeta": (B, H, T), "dS0": (B, H, dk, dv)}
+    for name, shp in shapes.items():
+        out[name] = _f32_out(out.get(name), shp, d, name)
+    workspace = _workspace(workspace, sdm_dense_scan_backward_workspace_bytes(B, H, T, dk, dv), d)
+    _check("sdm_dense_scan_backward", lib().sdm_dense_scan_backward(
+        _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(alpha), _ptr(beta), _ptr(dy), _ptr(S0), _ptr(dS),
+        _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dlog_alpha"]), _ptr(out["dbeta"]),
+        _ptr(out["dS0"]), B, H, T, dk, dv, _ptr(workspace), workspace.numel(), _stream(d)))
+    return out
+
+
+NORM_OUT = {"f32": (SDM_F32, torch.float32), "bf16": (SDM_BF16, torch.bfloat16),
+            "e4m3": (SDM_E4M3, torch.float8_e4m3fn)}
+
+
+def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.Tensor] = None,
+                      eps: float = 1e-6, dtype: str = "bf16", group: int = 0,
+                      out: Optional[dict] = None) -> dict:
+    """h = x + res and its RMS-Norm y = h / sqrt(mean h^2 + eps) * gamma, per row.
+
+    x [..., d], res the same shape or None, gamma [d] fp32. ``dtype`` is y's: "f32",
+    "bf16" or "e4m3", the last with fp32 scales per row (group 0: [..., 1]) or per ``group``
+    columns ([..., d / group]). Returns a dict with y, h (with res; in res's dtype) and
+    scale (for e4m3); ``out`` may pass those tensors preallocated, h may be res or x.
+    """
+    d_ = _dev(x, gamma, *(() if res is None else (res,)))
+    if dtype not in NORM_OUT:
+        raise ValueError(f"unknown output dtype {dtype!r}")
+    if x.dim() < 1 or gamma.shape != x.shape[-1:] or gamma.dtype != torch.float32 \
+            or (res is not None and res.shape != x.shape):
+        raise ValueError("shape or dtype mismatch in sdm_residual_norm")
+    d = x.shape[-1]
+    rows = x.numel() // d if d else 0
+    code, yt = NORM_OUT[dtype]
+    out = dict(out or {})
+    want = {"y": (x.shape, yt)}
+    if res is not None:
+        want["h"] = (x.shape, res.dtype)
+    if dtype == "e4m3":
+        if group < 0 or (group and d % group):
+            raise ValueError("group must be 0 or divide d")
+        want["scale"] = (x.shape[:-1] + (d // group if group else 1,), torch.float32)
+    if set(out) - set(want):
+        raise ValueError(f"no such output: {sorted(set(out) - set(want))}")
+    for name, (shp, dt) in want.items():
+        t = out.get(name)
+        if t is None:
+            out[name] = torch.empty(shp, dtype=dt, device=d_)
+        elif t.shape != shp or t.dtype != dt:
+            raise ValueError(f"{name} has the wrong shape or dtype")
+        _dev(x, out[name])
+    h, scale = out.get("h"), out.get("scale")
+    _check("sdm_residual_norm", lib().sdm_residual_norm(
+        _ptr(x), _dtype_code(x), _ptr(res), _ptr(h), _dtype_code(x if res is None else res), _ptr(gamma),
+        float(eps), rows, d, _ptr(out["y"]), code, _ptr(scale), group, _stream(d_)))
+    return out
+
+
+def sdm_residual_norm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor,
+                               dh: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                               out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of sdm_residual_norm from the stored h (x where there was no residual).
+
+    dy, dh [..., d] of one dtype (dh: what arrives at h from behind, or None), h [..., d],
+    gamma [d] fp32. Returns a dict with dx (the gradient of x and of res, in dy's dtype) and
+    dgamma [d] fp32; ``out`` may pass them preallocated.
+    """
+    d_ = _dev(dy, h, gamma, *(() if dh is None else (dh,)))
+    if dy.dim() < 1 or gamma.shape != dy.shape[-1:] or gamma.dtype != torch.float32 or h.shape != dy.shape \
+            or (dh is not None and (dh.shape != dy.shape or dh.dtype != dy.dtype)):
+        raise ValueError("shape or dtype mismatch in sdm_residual_norm_backward")
+    d = dy.shape[-1]
+    rows = dy.numel() // d if d else 0
+    out = dict(out or {})
+    dx = out.get("dx")
+    if dx is None:
+        dx = torch.empty_like(dy)
+    elif dx.shape != dy.shape or dx.dtype != dy.dtype:
+        raise ValueError("dx has the wrong shape or dtype")
+    _dev(dy, dx)
+    dgamma = _f32_out(out.get("dgamma"), (d,), d_, "dgamma")
+    if rows == 0:
+        dgamma.zero_()
+    n = lib().sdm_residual_norm_backward_workspace_bytes(rows, d)
+    ws = _workspace(workspace, max(n, 0), d_)
+    _check("sdm_residual_norm_backward", lib().sdm_residual_norm_backward(
+        _ptr(dy), _ptr(dh), _dtype_code(dy), _ptr(h), _dtype_code(h), _ptr(gamma), float(eps), rows, d,
+        _ptr(dx), _ptr(dgamma), _ptr(ws), ws.numel(), _stream(d_)))
+    return {"dx": dx, "dgamma": dgamma}
+
+
+def sdm_balance_workspace_bytes(B: int, H: int, T: int, K: int, N: int) -> int:
+    n = lib().sdm_balance_workspace_bytes(B, H, T, K, N)
+    if n < 0:
+        raise ValueError("invalid sizes for the balance workspace")
+    return n
+
+
+def _mask(mask, B, T, d):
+    if mask is None:
+        return
+    if tuple(mask.shape) != (B, T) or mask.dtype not in (torch.uint8, torch.bool):
+        raise ValueError("mask must be [B, T], uint8 or bool")
+    _dev(mask)
+    if mask.device != d:
+        raise ValueError("all tensors must be on the same GPU")
+
+
+def sdm_balance_forward(idx: torch.Tensor, wt: torch.Tensor, N: int, mask: Optional[torch.Tensor] = None,
+                        out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Slot counts and balance loss of an addressing result, per head over the kept tokens.
+
+    idx [B,H,T,K] int32, wt [B,H,T,K] fp32 (as sdm_address gives them), mask [B,T] uint8 or
+    bool (non-zero: kept) or None. Returns a dict with counts [H,N] int32, mass [H,N] fp32,
+    tokens [1] int32 and loss [H] fp32 (1 when even); ``out`` may pass them preallocated.
+    """
+    d = _dev(idx, wt)
+    B, H, T, K = idx.shape
+    if wt.shape != idx.shape or idx.dtype != torch.int32 or wt.dtype != torch.float32:
+        raise ValueError("shape or dtype mismatch in sdm_balance_forward")
+    _mask(mask, B, T, d)
+    out = dict(out or {})
+    for name, shp, dt in (("counts", (H, N), torch.int32), ("mass", (H, N), torch.float32),
+                          ("tokens", (1,), torch.int32), ("loss", (H,), torch.float32)):
+        t = out.get(name)
+        if t is None:
+            out[name] = torch.empty(shp, dtype=dt, device=d)
+        elif tuple(t.shape) != shp or t.dtype != dt:
+            raise ValueError(f"{name} has the wrong shape or dtype")
+        _dev(idx, out[name])
+    workspace = _workspace(workspace, sdm_balance_workspace_bytes(B, H, T, K, N), d)
+    _check("sdm_balance_forward", lib().sdm_balance_forward(
+        _ptr(idx), _ptr(wt), _ptr(mask), B, H, T, K, N, _ptr(out["counts"]), _ptr(out["mass"]),
+        _ptr(out["tokens"]), _ptr(out["loss"]), _ptr(workspace), workspace.numel(), _stream(d)))
+    return out
+
+
+def sdm_balance_backward(idx: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, dloss: torch.Tensor,
+                         mask: Optional[torch.Tensor] = None, dwt: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The balance loss's gradient to the weights: dwt [B,H,T,K] fp32 from dloss [H] fp32 and the
+    counts [H,N] and tokens [1] of sdm_balance_forward on the same idx and mask."""
+    d = _dev(idx, counts, tokens, dloss)
+    B, H, T, K = idx.shape
+    if idx.dtype != torch.int32 or counts.dtype != torch.int32 or tokens.dtype != torch.int32 \
+            or dloss.dtype != torch.float32 or counts.dim() != 2 or counts.shape[0] != H \
+            or tuple(tokens.shape) != (1,) or tuple(dloss.shape) != (H,):
+        raise ValueError("shape or dtype mismatch in sdm_balance_backward")
+    _mask(mask, B, T, d)
+    dwt = _f32_out(dwt, (B, H, T, K), d, "dwt")
+    _check("sdm_balance_backward", lib().sdm_balance_backward(
+        _ptr(idx), _ptr(mask), _ptr(counts), _ptr(tokens), _ptr(dloss), B, H, T, K, counts.shape[1],
+        _ptr(dwt), _stream(d)))
+    return dwt

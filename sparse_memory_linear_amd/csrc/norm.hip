@@ -1,0 +1,367 @@
+// norm.hip -- RMS-Norm of a token's row with the residual's addition, and its
+// gradients, on gfx950:
+//   h = x + res,   y = h / sqrt(mean(h^2) + eps) * gamma,
+// y in fp32, bf16 or e4m3 with fp32 scales (per row, or per group of columns).
+// Backward, with r = 1 / sqrt(mean(h^2) + eps) and n = h r:
+//   dx = dh + r (gamma dy - n mean(gamma dy n)),   dgamma = sum over rows of dy n.
+//
+// Both read each input once and write each output once: a row stays in the
+// registers of the TPR threads that own it (NV pieces of VEC elements each),
+// between its sums and its outputs. HBM-bound.
+//
+// The norm is taken of the fp32 sum x + res; h is stored rounded to its type,
+// and the backward works from the stored h, so that it reads no statistics.
+#include "sdm_buffer.h"
+#include "sdm_internal.h"
+
+namespace sdm {
+namespace {
+
+template <int VEC>
+__device__ __forceinline__ void load_vec(const void* p, bool bf16, int64_t e, float (&v)[VEC]) {
+    if (bf16) {
+        const uint16_t* b = static_cast<const uint16_t*>(p) + e;
+        uint32_t u[(VEC + 1) / 2];
+        if constexpr (VEC == 8) {
+            const uint4 x = *reinterpret_cast<const uint4*>(b);
+            u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+        } else if constexpr (VEC == 4) {
+            const uint2 x = *reinterpret_cast<const uint2*>(b);
+            u[0] = x.x; u[1] = x.y;
+        } else {
+            u[0] = *b;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+    } else {
+        const float* f = static_cast<const float*>(p) + e;
+        if constexpr (VEC == 1) {
+            v[0] = *f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(f + i);
+                v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+            }
+        }
+    }
+}
+
+// nearest even; a NaN stays one
+__device__ __forceinline__ uint32_t to_bf16(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if (f != f) return (u >> 16) | 0x40u;
+    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_vec(void* p, bool bf16, int64_t e, const float (&v)[VEC]) {
+    if (bf16) {
+        uint16_t* b = static_cast<uint16_t*>(p) + e;
+        uint32_t u[(VEC + 1) / 2];
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) u[i / 2] = to_bf16(v[i]) | (VEC > 1 ? to_bf16(v[i + (VEC > 1)]) << 16 : 0u);
+        if constexpr (VEC == 8) *reinterpret_cast<uint4*>(b) = make_uint4(u[0], u[1], u[2], u[3]);
+        else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(b) = make_uint2(u[0], u[1]);
+        else *b = (uint16_t)u[0];
+    } else {
+        float* f = static_cast<float*>(p) + e;
+        if constexpr (VEC == 1) {
+            *f = v[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; i += 4)
+                *reinterpret_cast<float4*>(f + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+    }
+}
+
+// v / scale in e4m3 (nearest even), by the scale's reciprocal; |v| <= 448 scale
+template <int VEC>
+__device__ __forceinline__ void store_e4m3(void* p, int64_t e, const float (&v)[VEC], float inv) {
+    uint8_t* b = static_cast<uint8_t*>(p) + e;
+    if constexpr (VEC == 1) {
+        *b = (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, 0.f, 0, false) & 0xFF);
+    } else {
+        uint32_t u[VEC / 4];
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inv, v[4 * i + 1] * inv, 0, false);
+            u[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, q, true);
+        }
+        if constexpr (VEC == 8) *reinterpret_cast<uint2*>(b) = make_uint2(u[0], u[1]);
+        else *reinterpret_cast<uint32_t*>(b) = u[0];
+    }
+}
+
+// The scale that maps the largest magnitude onto e4m3's largest value, 448. It
+// stays a normal number, so that its reciprocal is finite; 0 for a row of zeros.
+__device__ __forceinline__ float e4m3_scale(float amax) {
+    return amax > 0.f ? fmaxf(amax * (1.f / 448.f), 1.17549435e-38f) : 0.f;
+}
+
+// Sum and maximum over the TPR threads that own a row (the same on all of them)
+template <int TPR>
+__device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*buf)[2]) {
+    for (int m = 1; m < 64; m <<= 1) {
+        sum += __shfl_xor(sum, m);
+        mx = fmaxf(mx, __shfl_xor(mx, m));
+    }
+    if constexpr (TPR > 64) {
+        const int w = threadIdx.x >> 6;
+        __syncthreads();  // the last row's values have been read
+        if ((threadIdx.x & 63) == 0) { buf[w][0] = sum; buf[w][1] = mx; }
+        __syncthreads();
+        sum = 0.f; mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) { sum += buf[i][0]; mx = fmaxf(mx, buf[i][1]); }
+    }
+}
+
+template <int VEC, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    __shared__ float buf[TPR / 64][2];
+    const int lane = threadIdx.x % TPR;
+    float ga[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + lane) * VEC;
+        if (c < a.d) load_vec<VEC>(a.gamma, false, c, ga[j]);
+    }
+    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+        float v[NV][VEC];
+        const int64_t at = row * a.d;
+        float ss = 0.f, mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+            load_vec<VEC>(a.x, a.x_bf16, at + c, v[j]);
+            if (a.res) {
+                float r[VEC];
+                load_vec<VEC>(a.res, a.h_bf16, at + c, r);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[j][i] += r[i];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+            if (a.res) store_vec<VEC>(a.h, a.h_bf16, at + c, v[j]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                ss = fmaf(v[j][i], v[j][i], ss);
+                v[j][i] *= ga[j][i];
+                mx = fmaxf(mx, fabsf(v[j][i]));
+            }
+        }
+        row_reduce<TPR>(ss, mx, buf);
+        const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+        float scale = 0.f, inv = 0.f;
+        if (a.y_type == NORM_E4M3 && a.group == 0) {
+            scale = e4m3_scale(mx * r);
+            inv = scale > 0.f ? 1.f / scale : 0.f;
+            if (lane == 0) a.scale[row] = scale;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if constexpr (VEC == 8) {
+                if (a.y_type == NORM_E4M3 && a.group) {  // group / 8 neighbouring lanes share a scale
+                    float m = 0.f;
+                    if (c < a.d)
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(v[j][i] * r));
+                    for (int k = 1; k < a.group / 8; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
+                    scale = e4m3_scale(m);
+                    inv = scale > 0.f ? 1.f / scale : 0.f;
+                    if (c < a.d && c % a.group == 0) a.scale[row * (a.d / a.group) + c / a.group] = scale;
+                }
+            }
+            if (c >= a.d) continue;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[j][i] *= r;
+            if (a.y_type == NORM_E4M3) store_e4m3<VEC>(a.y, at + c, v[j], inv);
+            else store_vec<VEC>(a.y, a.y_type == NORM_BF16, at + c, v[j]);
+        }
+    }
+}
+
+// A block's rows' share of dgamma stays in registers, its wavefronts' shares are
+// added in order in LDS, and the blocks' rows of `part` by norm_dgamma_kernel:
+// the order of all sums follows from the sizes alone.
+template <int VEC, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwdArgs a) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    extern __shared__ float dg[];  // [d] (TPR < 256)
+    __shared__ float buf[TPR / 64][2];
+    const int lane = threadIdx.x % TPR;
+    float ga[NV][VEC], acc[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + lane) * VEC;
+        if (c < a.d) load_vec<VEC>(a.gamma, false, c, ga[j]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
+    }
+    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+        float h[NV][VEC], dy[NV][VEC];
+        const int64_t at = row * a.d;
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+            load_vec<VEC>(a.h, a.h_bf16, at + c, h[j]);
+            load_vec<VEC>(a.dy, a.g_bf16, at + c, dy[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                ss = fmaf(h[j][i], h[j][i], ss);
+                dot = fmaf(dy[j][i] * ga[j][i], h[j][i], dot);
+            }
+        }
+        for (int m = 1; m < 64; m <<= 1) {
+            ss += __shfl_xor(ss, m);
+            dot += __shfl_xor(dot, m);
+        }
+        if constexpr (TPR > 64) {
+            const int w = threadIdx.x >> 6;
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) { buf[w][0] = ss; buf[w][1] = dot; }
+            __syncthreads();
+            ss = 0.f; dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < TPR / 64; ++i) { ss += buf[i][0]; dot += buf[i][1]; }
+        }
+        const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+        const float k = dot * r * r / (float)a.d;  // n mean(g dy n) = h (dot r^2 / d)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+            float o[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                acc[j][i] = fmaf(dy[j][i], h[j][i] * r, acc[j][i]);
+                o[i] = r * (dy[j][i] * ga[j][i] - h[j][i] * k);
+            }
+            if (a.dh) {
+                float t[VEC];
+                load_vec<VEC>(a.dh, a.g_bf16, at + c, t);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o[i] += t[i];
+            }
+            store_vec<VEC>(a.dx, a.g_bf16, at + c, o);
+        }
+    }
+    float* part = a.part + (int64_t)blockIdx.x * a.d;
+    if constexpr (TPR < 256) {
+        for (int w = 0; w < RPB; ++w) {
+            if (threadIdx.x / TPR == w)
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = (j * TPR + lane) * VEC;
+                    if (c >= a.d) break;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) dg[c + i] = w ? dg[c + i] + acc[j][i] : acc[j][i];
+                }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < a.d; c += 256) part[c] = dg[c];
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+            store_vec<VEC>(part, false, c, acc[j]);
+        }
+    }
+}
+
+// dgamma = the sum of the blocks' rows: 64 columns a workgroup, 16 wavefronts
+// each adding every 16th row, then the 16 sums in order.
+__global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* part, float* dgamma, int blocks, int d) {
+    __shared__ float s[16][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+    float x = 0.f;
+    if (c < d)
+        for (int b = w; b < blocks; b += 16) x += part[(int64_t)b * d + c];
+    s[w][lane] = x;
+    __syncthreads();
+    if (w || c >= d) return;
+    for (int i = 1; i < 16; ++i) x += s[i][lane];
+    dgamma[c] = x;
+}
+
+template <int VEC, int TPR, int NV>
+void norm_launch(const NormArgs& a, hipStream_t st) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1, THR = TPR < 256 ? 256 : TPR;
+    const int64_t need = (a.rows + RPB - 1) / RPB, most = 256 * (2048 / THR);
+    hipLaunchKernelGGL((norm_kernel<VEC, TPR, NV>), dim3((unsigned)(need < most ? need : most)), dim3(THR), 0, st, a);
+}
+template <int VEC, int TPR, int NV>
+void norm_launch(const NormBwdArgs& a, hipStream_t st) {
+    constexpr int THR = TPR < 256 ? 256 : TPR;
+    hipLaunchKernelGGL((norm_bwd_kernel<VEC, TPR, NV>), dim3((unsigned)a.blocks), dim3(THR), TPR < 256 ? a.d * 4 : 0, st, a);
+}
+
+// Threads a row: a wavefront while its pieces fit 4 a lane (no LDS exchange),
+// else 256 or 1024 threads.
+template <int VEC, typename A>
+hipError_t norm_dispatch(const A& a, hipStream_t st) {
+    const int n = (a.d + VEC - 1) / VEC;
+    if (n <= 64) norm_launch<VEC, 64, 1>(a, st);
+    else if (n <= 128) norm_launch<VEC, 64, 2>(a, st);
+    else if (n <= 256) norm_launch<VEC, 64, 4>(a, st);
+    else if (n <= 512) norm_launch<VEC, 256, 2>(a, st);
+    else if (n <= 1024) norm_launch<VEC, 256, 4>(a, st);
+    else if (n <= 2048) norm_launch<VEC, 256, 8>(a, st);
+    else if constexpr (VEC < 8) {
+        if (n <= 4096) norm_launch<VEC, 1024, 4>(a, st);
+        else if constexpr (VEC < 4) {
+            if (n <= 8192) norm_launch<VEC, 1024, 8>(a, st);
+            else norm_launch<VEC, 1024, 16>(a, st);
+        }
+    }
+    return hipGetLastError();
+}
+template <typename A>
+hipError_t norm_any(const A& a, hipStream_t st) {
+    if (a.d % 8 == 0) return norm_dispatch<8>(a, st);
+    if (a.d % 4 == 0) return norm_dispatch<4>(a, st);
+    return norm_dispatch<1>(a, st);
+}
+
+int row_threads(int d) {
+    const int n = d % 8 == 0 ? d / 8 : d % 4 == 0 ? d / 4 : d;
+    return n <= 256 ? 64 : n <= 2048 ? 256 : 1024;
+}
+
+}  // namespace
+
+int64_t norm_bwd_blocks(int64_t rows, int d) {
+    const int tpr = row_threads(d), rpb = tpr < 256 ? 256 / tpr : 1;
+    const int64_t need = (rows + rpb - 1) / rpb, most = 256 * (tpr == 1024 ? 1 : 4);
+    return need < most ? need : most;
+}
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t st) { return norm_any(a, st); }
+
+hipError_t launch_norm_backward(NormBwdArgs a, hipStream_t st) {
+    a.blocks = (int)norm_bwd_blocks(a.rows, a.d);
+    hipError_t e = norm_any(a, st);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((a.d + 63) / 64)), dim3(1024), 0, st, a.part, a.dgamma,
+                       a.blocks, a.d);
+    return hipGetLastError();
+}
+
+}  // namespace sdm

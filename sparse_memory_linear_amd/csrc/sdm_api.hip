@@ -516,3 +516,236 @@ int sdm_state_init_backward(const float* dM, float* dM0, int64_t B, int64_t H, i
 }
 
 }  // extern "C"
+
+namespace {
+
+// Sizes, dtype and the row tensors of the dense recurrence (0, NO_WORK for no
+// streams, or the status).
+int check_dense(const char* fn, int in_dtype, int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
+    if (in_dtype != SDM_F32 && in_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown dtype %d", fn, in_dtype);
+    if (B < 0 || H < 0 || T < 0 || dk < 1 || dv < 1) return fail(SDM_ERR_SHAPE, "%s: invalid sizes", fn);
+    if (dk % 8 != 0 || dv % 8 != 0 || dk > 256 || dv > 256)
+        return fail(SDM_ERR_UNSUPPORTED, "%s: dk=%lld, dv=%lld: multiples of 8 up to 256", fn, (long long)dk,
+                    (long long)dv);
+    // B, H and T below 2^31 each, so that the products below stay in 64 bits
+    if (B > 0x7FFFFFFFll || H > 0x7FFFFFFFll || T > 0x7FFFFFFFll || B * H > 0x7FFFFFFFll ||
+        B * H * 4 * ((T + 63) / 64) > 0x7FFFFFFFll || B * H * (dk * dv / 4) / 256 >= 0x7FFFFFFFll)
+        return fail(SDM_ERR_UNSUPPORTED, "%s: too many streams or tokens for one launch", fn);
+    return B == 0 || H == 0 ? NO_WORK : 0;
+}
+
+bool dense_sizes_ok(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
+    return B >= 0 && H >= 0 && T >= 0 && B <= 0x7FFFFFFFll && H <= 0x7FFFFFFFll && T <= 0x7FFFFFFFll &&
+           B * H <= 0x7FFFFFFFll && dk >= 8 && dv >= 8 && dk <= 256 && dv <= 256 && dk % 8 == 0 && dv % 8 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sdm_dense_scan_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
+    if (!dense_sizes_ok(B, H, T, dk, dv)) return -1;
+    if (B == 0 || H == 0 || T == 0) return 0;
+    return sdm::dense_workspace_bytes(B * H, T, (int)dk, (int)dv);
+}
+
+int sdm_dense_scan_forward(const void* q, const void* k, const void* v, int in_dtype, const float* alpha,
+                           const float* beta, const float* S0, float* S, float* y, int64_t B, int64_t H, int64_t T,
+                           int64_t dk, int64_t dv, void* workspace, int64_t workspace_bytes, void* stream) {
+    const char* fn = "sdm_dense_scan_forward";
+    int rc = check_dense(fn, in_dtype, B, H, T, dk, dv);
+    if (rc == NO_WORK) return ok();
+    if (rc) return rc;
+    if (T > 0 && (rc = check_buffers(fn, {q, k, v, alpha, beta, y}))) return rc;
+    if (S0 && !aligned16(S0)) return fail(SDM_ERR_ALIGN, "%s: S0 not 16-byte aligned", fn);
+    if (S && !aligned16(S)) return fail(SDM_ERR_ALIGN, "%s: S not 16-byte aligned", fn);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (T == 0) {
+        if (!S || S == S0) return ok();
+        e = sdm::launch_dense_pass_on(S0, S, B * H, dk * dv, st);
+        return e == hipSuccess ? ok() : hip_fail(e, fn);
+    }
+    const int64_t need = sdm::dense_workspace_bytes(B * H, T, (int)dk, (int)dv);
+    if (need > 0 && (rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+    sdm::DenseFwdArgs a{};
+    a.q = q; a.k = k; a.v = v; a.bf16 = in_dtype == SDM_BF16;
+    a.alpha = alpha; a.beta = beta; a.S0 = S0; a.S = S; a.y = y;
+    a.NS = B * H; a.T = T; a.dk = (int)dk; a.dv = (int)dv;
+    a.workspace = workspace;
+    e = sdm::launch_dense_forward(a, st);
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+int64_t sdm_dense_scan_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
+    if (!dense_sizes_ok(B, H, T, dk, dv)) return -1;
+    if (B == 0 || H == 0 || T == 0) return 0;
+    return sdm::dense_backward_workspace_bytes(B * H, T, (int)dk, (int)dv);
+}
+
+int sdm_dense_scan_backward(const void* q, const void* k, const void* v, int in_dtype, const float* alpha,
+                            const float* beta, const float* dy, const float* S0, const float* dS, float* dq,
+                            float* dk_out, float* dv_out, float* dlog_alpha, float* dbeta, float* dS0, int64_t B,
+                            int64_t H, int64_t T, int64_t dk, int64_t dv, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
+    const char* fn = "sdm_dense_scan_backward";
+    int rc = check_dense(fn, in_dtype, B, H, T, dk, dv);
+    if (rc == NO_WORK) return ok();
+    if (rc) return rc;
+    if (T > 0 && (rc = check_buffers(fn, {q, k, v, alpha, beta, dy, dq, dk_out, dv_out, dlog_alpha, dbeta}))) return rc;
+    const void* opt[] = {S0, dS, dS0};
+    for (const void* p : opt)
+        if (p && !aligned16(p)) return fail(SDM_ERR_ALIGN, "%s: pointer %p not 16-byte aligned", fn, p);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (T == 0) {
+        if (!dS0 || dS0 == dS) return ok();
+        e = sdm::launch_dense_pass_on(dS, dS0, B * H, dk * dv, st);
+        return e == hipSuccess ? ok() : hip_fail(e, fn);
+    }
+    if ((rc = check_workspace(workspace, workspace_bytes,
+                              sdm::dense_backward_workspace_bytes(B * H, T, (int)dk, (int)dv))))
+        return rc;
+    sdm::DenseBwdArgs a{};
+    a.q = q; a.k = k; a.v = v; a.bf16 = in_dtype == SDM_BF16;
+    a.alpha = alpha; a.beta = beta; a.dy = dy; a.S0 = S0; a.dS = dS;
+    a.dq = dq; a.dk_out = dk_out; a.dv_out = dv_out; a.dlog_alpha = dlog_alpha; a.dbeta = dbeta; a.dS0 = dS0;
+    a.NS = B * H; a.T = T; a.dk = (int)dk; a.dv = (int)dv;
+    a.workspace = workspace;
+    e = sdm::launch_dense_backward(a, st);
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_norm_sizes(const char* fn, int64_t rows, int64_t d, float eps) {
+    if (rows < 0 || d < 1 || !(eps >= 0.f)) return fail(SDM_ERR_SHAPE, "%s: invalid sizes or eps", fn);
+    if (d > 16384) return fail(SDM_ERR_UNSUPPORTED, "%s: d=%lld: at most 16384", fn, (long long)d);
+    if (rows > 0x7FFFFFFFll) return fail(SDM_ERR_UNSUPPORTED, "%s: at most 2^31 - 1 rows per call", fn);
+    return 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sdm_residual_norm(const void* x, int x_dtype, const void* res, void* h, int h_dtype, const float* gamma,
+                      float eps, int64_t rows, int64_t d, void* y, int y_dtype, float* scale, int64_t group,
+                      void* stream) {
+    const char* fn = "sdm_residual_norm";
+    if (x_dtype != SDM_F32 && x_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown x dtype %d", fn, x_dtype);
+    if (h_dtype != SDM_F32 && h_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown h dtype %d", fn, h_dtype);
+    if (y_dtype != SDM_F32 && y_dtype != SDM_BF16 && y_dtype != SDM_E4M3)
+        return fail(SDM_ERR_DTYPE, "%s: unknown y dtype %d", fn, y_dtype);
+    int rc = check_norm_sizes(fn, rows, d, eps);
+    if (rc) return rc;
+    if (group != 0) {
+        if (y_dtype != SDM_E4M3) return fail(SDM_ERR_SHAPE, "%s: groups belong to an e4m3 output", fn);
+        if (group < 32 || group > 512 || (group & (group - 1)) != 0 || d % group != 0)
+            return fail(SDM_ERR_UNSUPPORTED, "%s: group=%lld: 0, or a power of two from 32 to 512 that divides d=%lld",
+                        fn, (long long)group, (long long)d);
+    }
+    if (rows == 0) return ok();
+    if ((rc = check_buffers(fn, {x, gamma, y}))) return rc;
+    if ((res == nullptr) != (h == nullptr)) return fail(SDM_ERR_NULL, "%s: res and h go together", fn);
+    if (res && (rc = check_buffers(fn, {res, h}))) return rc;
+    if (y_dtype == SDM_E4M3 && (rc = check_buffers(fn, {scale}))) return rc;
+    if (y == x || y == h || (res && y == res)) return fail(SDM_ERR_SHAPE, "%s: y may not alias x, res or h", fn);
+    if (h && h == x && x_dtype != h_dtype) return fail(SDM_ERR_SHAPE, "%s: h may alias x only in the same dtype", fn);
+    sdm::NormArgs a{};
+    a.x = x; a.res = res; a.h = h; a.gamma = gamma; a.y = y; a.scale = scale;
+    a.rows = rows; a.d = (int)d; a.group = (int)group; a.eps = eps;
+    a.y_type = y_dtype == SDM_E4M3 ? sdm::NORM_E4M3 : y_dtype == SDM_BF16 ? sdm::NORM_BF16 : sdm::NORM_F32;
+    a.x_bf16 = x_dtype == SDM_BF16; a.h_bf16 = h_dtype == SDM_BF16;
+    hipError_t e = sdm::launch_norm(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+int64_t sdm_residual_norm_backward_workspace_bytes(int64_t rows, int64_t d) {
+    if (rows < 0 || d < 1 || d > 16384 || rows > 0x7FFFFFFFll) return -1;
+    return rows == 0 ? 0 : sdm::norm_bwd_blocks(rows, (int)d) * d * 4;
+}
+
+int sdm_residual_norm_backward(const void* dy, const void* dh, int g_dtype, const void* h, int h_dtype,
+                               const float* gamma, float eps, int64_t rows, int64_t d, void* dx, float* dgamma,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+    const char* fn = "sdm_residual_norm_backward";
+    if (g_dtype != SDM_F32 && g_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown gradient dtype %d", fn, g_dtype);
+    if (h_dtype != SDM_F32 && h_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown h dtype %d", fn, h_dtype);
+    int rc = check_norm_sizes(fn, rows, d, eps);
+    if (rc) return rc;
+    if (rows == 0) return ok();
+    if ((rc = check_buffers(fn, {dy, h, gamma, dx, dgamma}))) return rc;
+    if (dh && !aligned16(dh)) return fail(SDM_ERR_ALIGN, "%s: dh not 16-byte aligned", fn);
+    if (dx == h && g_dtype != h_dtype) return fail(SDM_ERR_SHAPE, "%s: dx may alias h only in the same dtype", fn);
+    if ((rc = check_workspace(workspace, workspace_bytes, sdm::norm_bwd_blocks(rows, (int)d) * d * 4))) return rc;
+    sdm::NormBwdArgs a{};
+    a.dy = dy; a.dh = dh; a.h = h; a.gamma = gamma; a.dx = dx; a.dgamma = dgamma;
+    a.part = static_cast<float*>(workspace);
+    a.rows = rows; a.d = (int)d; a.eps = eps;
+    a.g_bf16 = g_dtype == SDM_BF16; a.h_bf16 = h_dtype == SDM_BF16;
+    hipError_t e = sdm::launch_norm_backward(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_balance(const char* fn, int64_t B, int64_t H, int64_t T, int64_t K, int64_t N) {
+    if (B < 0 || H < 0 || T < 0 || K < 1 || N < 1) return fail(SDM_ERR_SHAPE, "%s: invalid sizes", fn);
+    if (N > (1 << 18)) return fail(SDM_ERR_UNSUPPORTED, "%s: N=%lld: at most 2^18 slots", fn, (long long)N);
+    if (K > 256) return fail(SDM_ERR_UNSUPPORTED, "%s: K=%lld: at most 256 slots a token", fn, (long long)K);
+    // counts are 32-bit; each factor is bounded first, so that the products stay in 64 bits
+    if (B > 0x7FFFFFFFll || H > 4096 || T > 0x7FFFFFFFll || B * T > 0x7FFFFFFFll || B * T * K > 0x7FFFFFFFll)
+        return fail(SDM_ERR_UNSUPPORTED, "%s: at most 4096 heads, and 2^31 - 1 selections a head", fn);
+    return 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sdm_balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t K, int64_t N) {
+    if (check_balance("sdm_balance_workspace_bytes", B, H, T, K, N)) return -1;
+    return H == 0 ? 0 : sdm::balance_workspace_bytes(H, N);
+}
+
+int sdm_balance_forward(const int32_t* idx, const float* wt, const uint8_t* mask, int64_t B, int64_t H, int64_t T,
+                        int64_t K, int64_t N, int32_t* counts, float* mass, int32_t* tokens, float* loss,
+                        void* workspace, int64_t workspace_bytes, void* stream) {
+    const char* fn = "sdm_balance_forward";
+    int rc = check_balance(fn, B, H, T, K, N);
+    if (rc) return rc;
+    if (H == 0) return ok();
+    const bool some = B > 0 && T > 0;
+    if (some && (rc = check_buffers(fn, {idx, wt}))) return rc;
+    if ((rc = check_buffers(fn, {counts, mass, tokens, loss}))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, sdm::balance_workspace_bytes(H, N)))) return rc;
+    sdm::BalanceArgs a{};
+    a.idx = idx; a.wt = wt; a.mask = some ? mask : nullptr;
+    a.counts = counts; a.mass = mass; a.tokens = tokens; a.loss = loss;
+    a.B = B; a.H = H; a.T = T; a.K = K; a.N = N;
+    a.workspace = workspace;
+    hipError_t e = sdm::launch_balance(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+int sdm_balance_backward(const int32_t* idx, const uint8_t* mask, const int32_t* counts, const int32_t* tokens,
+                         const float* dloss, int64_t B, int64_t H, int64_t T, int64_t K, int64_t N, float* dwt,
+                         void* stream) {
+    const char* fn = "sdm_balance_backward";
+    int rc = check_balance(fn, B, H, T, K, N);
+    if (rc) return rc;
+    if (B == 0 || H == 0 || T == 0) return ok();
+    if ((rc = check_buffers(fn, {idx, counts, tokens, dloss, dwt}))) return rc;
+    sdm::BalanceBwdArgs a{};
+    a.idx = idx; a.mask = mask; a.counts = counts; a.tokens = tokens; a.dloss = dloss; a.dwt = dwt;
+    a.B = B; a.H = H; a.T = T; a.K = K; a.N = N;
+    hipError_t e = sdm::launch_balance_backward(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+}  // extern "C"

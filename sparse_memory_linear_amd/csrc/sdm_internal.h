@@ -135,4 +135,112 @@ struct YGateArgs {
 };
 hipError_t launch_ypart_gate(const YGateArgs& a, hipStream_t st);
 
+// The dense gated recurrence. One pass (see dense.hip): rows xi, kap [NS][T][DK]
+// and omg [NS][T][DV], the state X [DK][DV] per stream.
+struct DenseArgs {
+    const void* xi; const void* kap; const void* omg;
+    bool xi_bf16, kap_bf16, omg_bf16;
+    const float* a;          // [NS][T] gates
+    const float* b;          // [NS][T] factor of the added product (nullptr: 1)
+    const float* o;          // [NS][T] factor of the output (nullptr: 1)
+    float* out;              // [NS][T][DV]
+    const float* X0;         // starting state(s); nullptr: zeros
+    bool X0_seg;             // one per segment ([nseg][NS][..]) rather than one per stream
+    int x_row, x_col;        // X0's strides (a state may be taken transposed)
+    float* Xend;             // optional: the state after the stream (or, in the first pass, each segment's own)
+    float* segdec;           // first pass: [nseg][NS] product of the segment's gates
+    const void* with; bool with_bf16;  // [NS][T][DV]: rows multiplied with the (unscaled) output
+    float* dot;              // optional [nslab][NS][T]: those products, per column slab
+    int64_t NS, T, L;        // L: tokens per segment
+    int nseg, nslab, DK, DV;
+    bool rev;                // from the last token to the first
+};
+struct CarryArgs {
+    float* ws;               // [nseg][NS][per]: own sums in, starting states out
+    const float* segdec;     // [nseg][NS]
+    const float* X0;         // [NS][per] or nullptr (zeros)
+    float* Xend;             // [NS][per] or nullptr
+    const float* gate;       // backwards: [NS][T], the first of which decays Xend
+    int64_t NS, T, per;
+    int nseg;
+    bool rev;
+};
+struct DenseGatesArgs {
+    const float* G; const float* S;   // [nseg][NS][per]: states from behind, states at the starts
+    const float* ST;                  // [NS][per]: after the last token
+    const float* qdq; const float* kdk;  // [nslab][NS][T]
+    const float* alpha; const float* beta;
+    float* dlog_alpha; float* dbeta;
+    int64_t NS, T, L, per;
+    int nseg, nslab_q, nslab_k;
+    bool has_dS;
+};
+struct DenseFwdArgs {
+    const void* q; const void* k; const void* v; bool bf16;
+    const float* alpha; const float* beta;
+    const float* S0; float* S; float* y;
+    int64_t NS, T;
+    int dk, dv;
+    void* workspace;
+};
+struct DenseBwdArgs {
+    const void* q; const void* k; const void* v; bool bf16;
+    const float* alpha; const float* beta; const float* dy;
+    const float* S0; const float* dS;
+    float* dq; float* dk_out; float* dv_out; float* dlog_alpha; float* dbeta; float* dS0;
+    int64_t NS, T;
+    int dk, dv;
+    void* workspace;
+};
+int64_t dense_workspace_bytes(int64_t NS, int64_t T, int dk, int dv);
+int64_t dense_backward_workspace_bytes(int64_t NS, int64_t T, int dk, int dv);
+hipError_t launch_dense_forward(const DenseFwdArgs& a, hipStream_t st);
+hipError_t launch_dense_backward(const DenseBwdArgs& a, hipStream_t st);
+// X = X0 (zeros for nullptr): a call of no tokens
+hipError_t launch_dense_pass_on(const float* X0, float* X, int64_t NS, int64_t per, hipStream_t st);
+
+enum NormType { NORM_F32 = 0, NORM_BF16 = 1, NORM_E4M3 = 2 };
+struct NormArgs {
+    const void* x; const void* res; void* h;  // res and h: both or neither
+    const float* gamma;
+    void* y; float* scale;
+    int64_t rows;
+    int d, group, y_type;
+    float eps;
+    bool x_bf16, h_bf16;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t st);
+struct NormBwdArgs {
+    const void* dy; const void* h; const void* dh; const float* gamma;
+    void* dx; float* dgamma;
+    float* part;             // [blocks][d]
+    int64_t rows;
+    int d, blocks;
+    float eps;
+    bool g_bf16, h_bf16;     // dy, dh, dx; h
+};
+int64_t norm_bwd_blocks(int64_t rows, int d);
+hipError_t launch_norm_backward(NormBwdArgs a, hipStream_t st);
+
+struct BalanceArgs {
+    const int32_t* idx; const float* wt;  // [B,H,T,K]
+    const uint8_t* mask;                  // [B,T] or nullptr
+    int32_t* counts; float* mass;         // [H,N]
+    int32_t* tokens;                      // [1]
+    float* loss;                          // [H]
+    int64_t B, H, T, K, N;
+    void* workspace;
+    // set by the launcher
+    int64_t* fixed; int32_t* bad; double* part;
+    int nblk, per, shift;
+};
+int64_t balance_workspace_bytes(int64_t H, int64_t N);
+hipError_t launch_balance(BalanceArgs a, hipStream_t st);
+struct BalanceBwdArgs {
+    const int32_t* idx; const uint8_t* mask; const int32_t* counts; const int32_t* tokens; const float* dloss;
+    float* dwt;
+    int64_t B, H, T, K, N;
+};
+hipError_t launch_balance_backward(const BalanceBwdArgs& a, hipStream_t st);
+
 }  // namespace sdm

@@ -1,0 +1,287 @@
+"""The dense gated recurrence and its gradients against a token-by-token walk in
+64 bits.
+
+Tolerances: every output is a sum of products, and each product passes through
+at most n roundings of fp32 (half a step each, 2^-24 relative): its own
+contractions over dk and dv, a chunk's sums and decays, and a few per chunk
+crossed. So an output is off by at most n 2^-24 times the same sum taken over
+the magnitudes, which a second walk with all inputs' magnitudes gives. d/d ln
+alpha is a running sum over at most 512 tokens of q.dq - k.dk from the segment's
+end, so its magnitude is that of the whole sum.
+"""
+import pytest
+import torch
+
+import sparse_memory_linear_amd as sdm
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF, F32 = torch.bfloat16, torch.float32
+EPS = torch.finfo(F32).eps / 2
+SEGMENT = 512
+
+
+def make(B, H, T, dk, dv, dtype, seed, gates="mid", states=True):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    x = {"q": r(B, H, T, dk).mul_(dk ** -0.5).to(dtype), "k": r(B, H, T, dk).mul_(dk ** -0.5).to(dtype),
+         "v": r(B, H, T, dv).to(dtype), "alpha": torch.sigmoid(r(B, H, T) * 0.5 + 2.0),
+         "beta": torch.sigmoid(r(B, H, T)), "dy": r(B, H, T, dv)}
+    if gates == "extreme":  # zeros (a new sequence), ones, tiny ones, writes of nothing
+        u = torch.rand((B, H, T), generator=g)
+        x["alpha"] = torch.where(u < 0.05, 0.0, torch.where(u < 0.3, 1.0, torch.where(u < 0.4, 1e-30, x["alpha"])))
+        x["beta"] = torch.where(torch.rand((B, H, T), generator=g) < 0.2, 0.0, x["beta"])
+    x["S0"] = r(B, H, dk, dv) if states else None
+    x["dS"] = r(B, H, dk, dv) if states else None
+    return x
+
+
+def walk(x, magnitudes=False):
+    """y, S and all gradients in 64 bits, on the CPU, one token at a time."""
+    f = lambda t: None if t is None else (t.double().abs() if magnitudes else t.double())  # noqa: E731
+    q, k, v, al, be, dy, S0, dS = (f(x[n]) for n in ("q", "k", "v", "alpha", "beta", "dy", "S0", "dS"))
+    B, H, T, dk = q.shape
+    dv = v.shape[-1]
+    S = torch.zeros(B, H, dk, dv, dtype=torch.float64) if S0 is None else S0
+    y, states = torch.zeros(B, H, T, dv, dtype=torch.float64), [S]
+    for t in range(T):
+        S = al[:, :, t, None, None] * S + be[:, :, t, None, None] * k[:, :, t, :, None] * v[:, :, t, None, :]
+        states.append(S)
+        y[:, :, t] = (q[:, :, t, :, None] * S).sum(-2)
+    o = {"y": y, "S": S, "dq": torch.zeros_like(q), "dk": torch.zeros_like(k), "dv": torch.zeros_like(v),
+         "dlog_alpha": torch.zeros_like(al), "dbeta": torch.zeros_like(be)}
+    G = torch.zeros_like(S) if dS is None else dS
+    for t in reversed(range(T)):
+        G = G + q[:, :, t, :, None] * dy[:, :, t, None, :]
+        o["dq"][:, :, t] = (states[t + 1] * dy[:, :, t, None, :]).sum(-1)
+        Gv = (G * v[:, :, t, None, :]).sum(-1)
+        o["dk"][:, :, t] = be[:, :, t, None] * Gv
+        o["dv"][:, :, t] = be[:, :, t, None] * (G * k[:, :, t, :, None]).sum(-2)
+        o["dbeta"][:, :, t] = (k[:, :, t] * Gv).sum(-1)
+        aS = al[:, :, t, None, None] * states[t]
+        o["dlog_alpha"][:, :, t] = (G * aS).sum((-1, -2))
+        G = al[:, :, t, None, None] * G
+    o["dS0"] = G
+    if magnitudes:  # the running sum's terms, over the tokens of up to a segment ahead, and its start
+        c = (q * o["dq"]).sum(-1) + (k * o["dk"]).sum(-1)
+        run = torch.nn.functional.pad(c.flip(-1).cumsum(-1).flip(-1), (0, 1))  # run[t]: tokens t and behind
+        ahead = torch.arange(T).add(SEGMENT).clamp_max(T)
+        E = torch.nn.functional.pad(o["dlog_alpha"], (0, 1))
+        E[..., T] = 0.0 if dS is None else (dS * S).sum((-1, -2))
+        # the segment's end lies at most SEGMENT tokens ahead, with a value E there
+        far = torch.stack([E[..., t + 1:t + SEGMENT + 1].amax(-1) for t in range(T)], -1)
+        o["dlog_alpha"] = run[..., :T] - run[..., ahead] + far
+    return o
+
+
+def roundings(T, dk, dv):
+    chunks = (T + 31) // 32
+    return 2 * (dk + dv) + 2 * 64 + 64 + 4 * chunks + 64
+
+
+def check(got, want, mag, n, names):
+    for name in names:
+        w, m = want[name], mag[name]
+        e = (got[name].cpu().double() - w).abs()
+        tol = n * EPS * m + 1e-37
+        assert torch.isfinite(got[name]).all(), name
+        worst = (e / tol).max().item() if e.numel() else 0.0
+        assert worst <= 1.0, (name, worst, e.max().item())
+
+
+def dev(x):
+    return {n: None if t is None else t.to(DEV) for n, t in x.items()}
+
+
+def forward(x, **kw):
+    y, S = sdm.sdm_dense_scan_forward(x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["S0"], **kw)
+    return {"y": y, "S": S}
+
+
+def backward(x, **kw):
+    return sdm.sdm_dense_scan_backward(x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["dy"], x["S0"], x["dS"], **kw)
+
+
+GRADS = ("dq", "dk", "dv", "dlog_alpha", "dbeta", "dS0")
+
+SIZES = [  # B, H, T, dk, dv: one token to several segments, tiles filled and not
+    (1, 1, 1, 8, 8), (3, 2, 1, 128, 128), (2, 2, 3, 256, 72), (1, 3, 8, 64, 40), (1, 1, 9, 16, 8),
+    (2, 1, 31, 40, 24), (1, 2, 64, 64, 64), (2, 2, 65, 72, 136), (1, 2, 300, 128, 128),
+    (1, 1, 517, 256, 256), (2, 1, 1100, 96, 80), (1, 2, 577, 200, 64), (1, 1, 1537, 32, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,H,T,dk,dv", SIZES)
+def test_forward_and_backward(B, H, T, dk, dv, dtype):
+    x = make(B, H, T, dk, dv, dtype, 7 * T + dk + dv)
+    want, mag, n = walk(x), walk(x, True), roundings(T, dk, dv)
+    g = dev(x)
+    check(forward(g), want, mag, n, ("y", "S"))
+    check(backward(g), want, mag, n, GRADS)
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv,dtype", [(2, 2, 5, 64, 64, BF), (1, 2, 700, 128, 64, BF), (1, 2, 700, 64, 128, F32)])
+@pytest.mark.parametrize("states", [True, False], ids=["states", "zeros"])
+def test_extreme_gates_and_missing_states(B, H, T, dk, dv, dtype, states):
+    x = make(B, H, T, dk, dv, dtype, 5, gates="extreme", states=states)
+    want, mag, n = walk(x), walk(x, True), roundings(T, dk, dv)
+    g = dev(x)
+    check(forward(g), want, mag, n, ("y", "S"))
+    check(backward(g), want, mag, n, GRADS)
+
+
+def test_state_in_place_and_preallocated_outputs():
+    for T in (1, 4, 40, 1500):
+        g = dev(make(2, 2, T, 64, 96, BF, T))
+        want = forward(g)
+        big = torch.full((2 * 2 * T * 96 + 64,), 7.0, device=DEV)
+        y = big[32:-32].view(2, 2, T, 96)
+        S = g["S0"].clone()
+        y2, S2 = sdm.sdm_dense_scan_forward(g["q"], g["k"], g["v"], g["alpha"], g["beta"], S, S, y)
+        assert y2.data_ptr() == y.data_ptr() and S2.data_ptr() == S.data_ptr()
+        assert torch.equal(y, want["y"]) and torch.equal(S, want["S"])
+        assert (big[:32] == 7).all() and (big[-32:] == 7).all()  # nothing before or behind is touched
+        dS = g["dS"].clone()
+        ref = backward(g)
+        g["dS"] = dS
+        got = backward(g, out={"dS0": dS})
+        assert got["dS0"].data_ptr() == dS.data_ptr()
+        for name in GRADS:
+            assert torch.equal(got[name], ref[name]), name
+
+
+def test_no_tokens_pass_the_states_on():
+    x = dev(make(2, 3, 4, 16, 8, F32, 1))
+    z = {n: x[n][:, :, :0].contiguous() for n in ("q", "k", "v", "alpha", "beta", "dy")}
+    z["S0"], z["dS"] = x["S0"], x["dS"]
+    got = forward(z)
+    assert got["y"].shape == (2, 3, 0, 8) and torch.equal(got["S"], x["S0"])
+    assert torch.equal(backward(z)["dS0"], x["dS"])
+    z["S0"] = None
+    assert (forward(z)["S"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_split_calls_continue_the_sequence(dtype):
+    x = make(1, 2, 900, 64, 64, dtype, 3)
+    want, mag, n = walk(x), walk(x, True), roundings(900, 64, 64) + 128
+    g = dev(x)
+    at = [0, 1, 2, 70, 611, 900]
+    S, ys, starts = g["S0"], [], []
+    cut = lambda a, b: {m: g[m][:, :, a:b].contiguous() for m in ("q", "k", "v", "alpha", "beta", "dy")}  # noqa: E731
+    for a, b in zip(at, at[1:]):
+        c = cut(a, b)
+        starts.append(S)
+        y, S = sdm.sdm_dense_scan_forward(c["q"], c["k"], c["v"], c["alpha"], c["beta"], S)
+        ys.append(y)
+    check({"y": torch.cat(ys, 2), "S": S}, want, mag, n, ("y", "S"))
+    parts, dS = [], g["dS"]
+    for (a, b), S in reversed(list(zip(zip(at, at[1:]), starts))):
+        c = cut(a, b)
+        parts.insert(0, sdm.sdm_dense_scan_backward(c["q"], c["k"], c["v"], c["alpha"], c["beta"], c["dy"], S, dS))
+        dS = parts[0]["dS0"]
+    got = {m: torch.cat([p[m] for p in parts], 2) for m in GRADS[:-1]}
+    got["dS0"] = dS
+    check(got, want, mag, n, GRADS)
+
+
+def test_gradients_against_differences():
+    """The directional derivative of the loss, by differences of the walk in 64
+    bits. A step of 2^-20 leaves an error of the third derivative's size, 2^-40, and
+    2^-53 / 2^-20 of rounding: both far below the kernels' own."""
+    x = make(1, 2, 90, 24, 16, F32, 11)
+    g = backward(dev(x))
+    gen = torch.Generator().manual_seed(2)
+    loss = lambda z: sum((walk(z)[a] * z0).sum() for a, z0 in (("y", x["dy"].double()), ("S", x["dS"].double())))  # noqa: E731
+    names = {"q": "dq", "k": "dk", "v": "dv", "beta": "dbeta", "S0": "dS0", "alpha": "dlog_alpha"}
+    for a, b in names.items():
+        d = torch.randn(x[a].shape, generator=gen, dtype=torch.float64)
+        sides = []
+        for s in (2.0 ** -20, -2.0 ** -20):
+            z = {m: t.double() for m, t in x.items()}
+            z[a] = z[a] * torch.exp(s * d) if a == "alpha" else z[a] + s * d
+            sides.append(loss(z))
+        want = (sides[0] - sides[1]) / 2.0 ** -19
+        got = (g[b].cpu().double() * d).sum()
+        size = (g[b].cpu().double() * d).abs().sum()
+        assert abs(want - got) <= 1e-5 * size, (a, float(want), float(got))
+
+
+def test_captured_and_replayed_between_other_work():
+    for T in (2, 130, 1300):
+        g = dev(make(2, 2, T, 64, 64, BF, T))
+        want_f, want_b = forward(g), backward(g)
+        outs = {}
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s):
+            forward(g), backward(g)
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph, stream=s):
+                outs.update(forward(g))
+                outs.update(backward(g))
+        for _ in range(4):
+            for t in outs.values():
+                t.fill_(float("nan"))
+            other = dev(make(1, 2, 70, 64, 64, BF, 1))
+            forward(other)
+            graph.replay()
+            backward(other)
+            torch.cuda.synchronize()
+            for name, t in outs.items():
+                assert torch.equal(t, want_f[name] if name in want_f else want_b[name]), name
+
+
+def test_two_streams_at_once():
+    a, b = dev(make(2, 2, 1200, 128, 64, BF, 1)), dev(make(1, 3, 800, 64, 128, F32, 2))
+    want = [forward(a), backward(a), forward(b), backward(b)]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            r1 = [forward(a), backward(a)]
+        with torch.cuda.stream(s2):
+            r2 = [forward(b), backward(b)]
+        torch.cuda.synchronize()
+        for got, ref in zip(r1 + r2, want):
+            for name in ref:
+                assert torch.equal(got[name], ref[name]), name
+
+
+def test_offsets_beyond_32_bits():
+    """One stream of 8.6 M tokens, 256 wide: rows lie beyond 2^32 bytes. A gate of 0
+    near the end starts the sequence anew, so the tokens behind it equal a call of their own."""
+    T, n, d = 8_600_001, 200, 256
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    x = {m: torch.empty((1, 1, T, d), dtype=BF, device=DEV).normal_(generator=gen) for m in ("q", "k", "v")}
+    al = torch.full((1, 1, T), 0.9, device=DEV)
+    al[..., T - n] = 0.0
+    be = torch.rand((1, 1, T), generator=gen, device=DEV)
+    y, S = sdm.sdm_dense_scan_forward(x["q"], x["k"], x["v"], al, be)
+    end = {m: t[:, :, T - n:].clone() for m, t in x.items()}
+    y2, S2 = sdm.sdm_dense_scan_forward(end["q"], end["k"], end["v"], al[..., T - n:].clone(), be[..., T - n:].clone())
+    # the same sums in other chunks: n roundings of the magnitudes, here of 256 + 10 (decay 0.9) products
+    assert (y[:, :, T - n:] - y2).abs().max() <= 1e-5 * y2.abs().max()
+    assert (S - S2).abs().max() <= 1e-5 * S2.abs().max()
+
+
+def test_refusals():
+    g = dev(make(1, 2, 9, 16, 8, BF, 1))
+    args = [g[m] for m in ("q", "k", "v", "alpha", "beta")]
+    bad = lambda i, t: [t if j == i else a for j, a in enumerate(args)]  # noqa: E731
+    for a in (bad(1, g["k"].float()), bad(2, g["v"][:, :1]), bad(3, g["alpha"].double()),
+              bad(0, g["q"].transpose(2, 3).contiguous().transpose(2, 3)), bad(4, g["beta"].cpu())):
+        with pytest.raises(ValueError):
+            sdm.sdm_dense_scan_forward(*a)
+    with pytest.raises(ValueError):
+        sdm.sdm_dense_scan_forward(*args, g["S0"].to(BF))
+    with pytest.raises(ValueError):
+        sdm.sdm_dense_scan_backward(*args, g["dy"].to(BF))
+    q = torch.zeros((1, 2, 9, 264), dtype=BF, device=DEV)
+    with pytest.raises((ValueError, sdm.SdmError)):
+        sdm.sdm_dense_scan_forward(q, q, g["v"], g["alpha"], g["beta"])
+    long = dev(make(1, 2, 2000, 16, 8, BF, 1))
+    with pytest.raises(sdm.SdmError):
+        forward(long, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
