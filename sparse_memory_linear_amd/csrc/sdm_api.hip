@@ -701,6 +701,8 @@ int check_balance(const char* fn, int64_t B, int64_t H, int64_t T, int64_t K, in
     // counts are 32-bit; each factor is bounded first, so that the products stay in 64 bits
     if (B > 0x7FFFFFFFll || H > 4096 || T > 0x7FFFFFFFll || B * T > 0x7FFFFFFFll || B * T * K > 0x7FFFFFFFll)
         return fail(SDM_ERR_UNSUPPORTED, "%s: at most 4096 heads, and 2^31 - 1 selections a head", fn);
+    if (B * H > 0x7FFFFFFFll / 2 || B * H * (1 + T * K / sdm::BALANCE_PIECE) > 0x7FFFFFFFll)
+        return fail(SDM_ERR_UNSUPPORTED, "%s: too many heads and sequences for one launch", fn);
     return 0;
 }
 
@@ -710,7 +712,7 @@ extern "C" {
 
 int64_t sdm_balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t K, int64_t N) {
     if (check_balance("sdm_balance_workspace_bytes", B, H, T, K, N)) return -1;
-    return H == 0 ? 0 : sdm::balance_workspace_bytes(H, N);
+    return H == 0 ? 0 : sdm::balance_workspace_bytes(B, H, T, N);
 }
 
 int sdm_balance_forward(const int32_t* idx, const float* wt, const uint8_t* mask, int64_t B, int64_t H, int64_t T,
@@ -723,7 +725,7 @@ int sdm_balance_forward(const int32_t* idx, const float* wt, const uint8_t* mask
     const bool some = B > 0 && T > 0;
     if (some && (rc = check_buffers(fn, {idx, wt}))) return rc;
     if ((rc = check_buffers(fn, {counts, mass, tokens, loss}))) return rc;
-    if ((rc = check_workspace(workspace, workspace_bytes, sdm::balance_workspace_bytes(H, N)))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, sdm::balance_workspace_bytes(B, H, T, N)))) return rc;
     sdm::BalanceArgs a{};
     a.idx = idx; a.wt = wt; a.mask = some ? mask : nullptr;
     a.counts = counts; a.mass = mass; a.tokens = tokens; a.loss = loss;
