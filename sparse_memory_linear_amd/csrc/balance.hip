@@ -25,7 +25,7 @@ namespace {
 
 constexpr int RANGE = 13312;   // slots a workgroup: 12 bytes each, 156 KiB of LDS
 constexpr int ADD_THREADS = 1024;
-constexpr int MERGE_SLOTS = 2048;
+constexpr int MERGE_SLOTS = 512;
 
 // fp64 whose unit in the last place is 2^-shift
 __device__ __forceinline__ double fix_base(int shift) { return ldexp(1.5, 52 - shift); }
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(ADD_THREADS) void balance_add_kernel(BalanceArgs a)
     int r;
     block_unit((int)blockIdx.x, a.H * a.nshare, a.nrange, s, r);
     if (s >= a.H * a.nshare) return;
-    const int64_t h = s % a.H, share = s / a.H;
+    const int64_t h = s % a.H, share = s / a.H;  // s = share * H + h
     const uint32_t lo = (uint32_t)r * a.range, len = min((uint32_t)a.range, (uint32_t)a.N - lo);
     for (uint32_t i = tid; i < len; i += ADD_THREADS) { mass[i] = 0; count[i] = 0; }
     if (tid == 0) { bad = 0; kept = 0; }
@@ -52,15 +52,11 @@ __global__ __launch_bounds__(ADD_THREADS) void balance_add_kernel(BalanceArgs a)
         const uint32_t i = (uint32_t)slot - lo;
         if (i < len) {
             atomicAdd(&count[i], 1u);
-            if (fabsf(w) <= 2.f) {
-                atomicAdd(reinterpret_cast<unsigned long long*>(&mass[i]),
-                          (unsigned long long)__double_as_longlong((double)w + base));
-            } else {  // NaN or out of range: the constant alone
-                atomicAdd(reinterpret_cast<unsigned long long*>(&mass[i]), (unsigned long long)__double_as_longlong(base));
-                bad = 1;
-            }
+            atomicAdd(reinterpret_cast<unsigned long long*>(&mass[i]),
+                      (unsigned long long)__double_as_longlong((double)w + base));
         }
     };
+    // (a weight that is NaN or out of range spoils its head's sums; the first range looks)
     const int64_t ntok = a.B * a.T;
     const int64_t u0 = share * a.share, u1 = u0 + a.share < ntok ? u0 + a.share : ntok;
     for (int64_t u = u0; u < u1;) {  // one sequence's tokens at a time: contiguous selections
@@ -68,22 +64,43 @@ __global__ __launch_bounds__(ADD_THREADS) void balance_add_kernel(BalanceArgs a)
         const int64_t m = a.T - t < u1 - u ? a.T - t : u1 - u;
         const int64_t at = ((b * a.H + h) * a.T + t) * a.K;
         const uint8_t* keep = a.mask ? a.mask + b * a.T + t : nullptr;
-        const uint32_t n = (uint32_t)(m * a.K);
+        const uint32_t n = (uint32_t)(m * a.K);  // < 2^31 (host)
         auto on = [&](uint32_t e) { return !keep || keep[((uint64_t)e * kdiv) >> 40] != 0; };
-        if constexpr (VEC) {  // K a multiple of 4: a token's selections in pieces of 16 bytes
-            const int4* ip = reinterpret_cast<const int4*>(a.idx + at);
-            const float4* wp = reinterpret_cast<const float4*>(a.wt + at);
-#pragma unroll 4
-            for (uint32_t e = tid; e < n / 4; e += ADD_THREADS) {
-                if (!on(e * 4)) continue;
-                const int4 i = ip[e];
-                const float4 w = wp[e];
-                take(i.x, w.x); take(i.y, w.y); take(i.z, w.z); take(i.w, w.w);
+        // a batch's loads are all issued before its first selection is taken
+        constexpr int NB = 4, W = VEC ? 4 : 1;  // VEC: K a multiple of 4, pieces of 16 bytes
+        for (uint32_t e0 = tid; e0 < n / W; e0 += NB * ADD_THREADS) {
+            int32_t i[NB][W];
+            float w[NB][W];
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const uint32_t e = e0 + k * ADD_THREADS;
+                const bool in = e < n / W && on(e * W);
+                if constexpr (VEC) {
+                    int4 x = make_int4(-1, -1, -1, -1);
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (in) {
+                        x = reinterpret_cast<const int4*>(a.idx + at)[e];
+                        y = reinterpret_cast<const float4*>(a.wt + at)[e];
+                    }
+                    i[k][0] = x.x; i[k][1] = x.y; i[k][2] = x.z; i[k][3] = x.w;
+                    w[k][0] = y.x; w[k][1] = y.y; w[k][2] = y.z; w[k][3] = y.w;
+                } else {
+                    i[k][0] = in ? a.idx[at + e] : -1;
+                    w[k][0] = in ? a.wt[at + e] : 0.f;
+                }
             }
-        } else {
-#pragma unroll 4
-            for (uint32_t e = tid; e < n; e += ADD_THREADS)
-                if (on(e)) take(a.idx[at + e], a.wt[at + e]);
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+                for (int j = 0; j < W; ++j) take(i[k][j], w[k][j]);
+            if (r == 0) {
+                bool b = false;
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) b |= !(fabsf(w[k][j]) <= 2.f) && (uint32_t)i[k][j] < (uint32_t)a.N;
+                if (b) bad = 1;
+            }
         }
         if (h == 0 && r == 0 && keep) {
             int c = 0;
@@ -100,7 +117,7 @@ __global__ __launch_bounds__(ADD_THREADS) void balance_add_kernel(BalanceArgs a)
         a.part_counts[o + i] = (int32_t)count[i];
     }
     if (tid == 0) {
-        a.bad[s * a.nrange + r] = bad;
+        if (r == 0) a.bad[s] = bad;
         if (h == 0 && r == 0) a.kept[share] = a.mask ? kept : (int32_t)(u1 - u0);
     }
 }
@@ -113,8 +130,8 @@ __global__ __launch_bounds__(256) void balance_mass_kernel(BalanceArgs a) {
     const int blk = (int)(blockIdx.x % a.nblk);
     if (threadIdx.x == 0) any = 0;
     __syncthreads();
-    for (int64_t i = threadIdx.x; i < a.nshare * (int64_t)a.nrange; i += 256)
-        if (a.bad[(i / a.nrange * a.H + h) * a.nrange + i % a.nrange]) any = 1;
+    for (int64_t i = threadIdx.x; i < a.nshare; i += 256)
+        if (a.bad[i * a.H + h]) any = 1;
     __syncthreads();
     const double unit = ldexp(1.0, -a.shift);
     const bool bad = any != 0;
@@ -123,6 +140,7 @@ __global__ __launch_bounds__(256) void balance_mass_kernel(BalanceArgs a) {
     for (int64_t i = (int64_t)blk * MERGE_SLOTS + threadIdx.x; i < end; i += 256) {
         int64_t f = 0;
         int32_t c = 0;
+#pragma unroll 8
         for (int64_t s = 0; s < a.nshare; ++s) {
             f += a.fixed[(s * a.H + h) * a.N + i];
             c += a.part_counts[(s * a.H + h) * a.N + i];
@@ -155,47 +173,84 @@ __global__ __launch_bounds__(64) void balance_loss_kernel(BalanceArgs a) {
     if (h == 0) *a.tokens = tok;
 }
 
-// A workgroup per piece of one (b, h)'s selections; the head's counts are
-// gathered from the L2.
-template <bool VEC>
-__global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceBwdArgs a) {
-    const int64_t bh = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces;
-    const int64_t b = bh / a.H, h = bh - b * a.H, run = a.T * a.K;
+// A workgroup per piece of one head's selections. TABLE: the head's counts sit in
+// LDS, 16 bits each (65535: that many or more, taken from memory), so that the
+// gather does not go to the L2, a line a selection; else they are gathered there.
+template <bool VEC, bool TABLE>
+__global__ __launch_bounds__(TABLE ? 1024 : 256) void balance_bwd_kernel(BalanceBwdArgs a) {
+    constexpr int THR = TABLE ? 1024 : 256;
+    extern __shared__ __align__(16) uint16_t table[];
+    const int64_t h = blockIdx.x % a.H, piece = blockIdx.x / a.H;
     const double n = (double)*a.tokens;
     const float c = n > 0.0 ? (float)((double)a.dloss[h] * ((double)a.N / (n * n * (double)a.K))) : 0.f;
     const int32_t* counts = a.counts + h * a.N;
     const uint32_t N = (uint32_t)a.N;
-    const uint8_t* keep = a.mask ? a.mask + b * a.T : nullptr;
+    if constexpr (TABLE) {
+        for (uint32_t i = threadIdx.x; i < N; i += THR) table[i] = (uint16_t)min(counts[i], 65535);
+        __syncthreads();
+    }
     const uint64_t kdiv = ((1ull << 40) / (uint64_t)a.K) + 1;  // e / K = e kdiv >> 40 for e < 2^32, K <= 256
-    auto on = [&](uint32_t e) { return !keep || keep[((uint64_t)e * kdiv) >> 40] != 0; };
-    auto grad = [&](int32_t slot) { return (uint32_t)slot < N ? c * (float)counts[slot] : 0.f; };
-    const int64_t e0 = piece * BALANCE_PIECE, e1 = e0 + BALANCE_PIECE < run ? e0 + BALANCE_PIECE : run;
-    if constexpr (VEC) {
-        const int4* ip = reinterpret_cast<const int4*>(a.idx + bh * run);
-        float4* op = reinterpret_cast<float4*>(a.dwt + bh * run);
-#pragma unroll 4
-        for (int64_t e = e0 / 4 + threadIdx.x; e < e1 / 4; e += 256) {
-            const int4 i = ip[e];
-            op[e] = on((uint32_t)e * 4) ? make_float4(grad(i.x), grad(i.y), grad(i.z), grad(i.w)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    auto grad = [&](int32_t slot) {
+        if ((uint32_t)slot >= N) return 0.f;
+        int k;
+        if constexpr (TABLE) {
+            k = table[slot];
+            if (k == 65535) k = counts[slot];
+        } else {
+            k = counts[slot];
         }
-    } else {
-        for (int64_t e = e0 + threadIdx.x; e < e1; e += 256)
-            a.dwt[bh * run + e] = on((uint32_t)e) ? grad(a.idx[bh * run + e]) : 0.f;
+        return c * (float)k;
+    };
+    const int64_t ntok = a.B * a.T;
+    const int64_t u0 = piece * a.piece, u1 = u0 + a.piece < ntok ? u0 + a.piece : ntok;
+    for (int64_t u = u0; u < u1;) {  // one sequence's tokens at a time: contiguous selections
+        const int64_t b = u / a.T, t = u - b * a.T;
+        const int64_t m = a.T - t < u1 - u ? a.T - t : u1 - u;
+        const int64_t at = ((b * a.H + h) * a.T + t) * a.K;
+        const uint8_t* keep = a.mask ? a.mask + b * a.T + t : nullptr;
+        const uint32_t e1 = (uint32_t)(m * a.K);
+        auto on = [&](uint32_t e) { return !keep || keep[((uint64_t)e * kdiv) >> 40] != 0; };
+        if constexpr (VEC) {
+            const int4* ip = reinterpret_cast<const int4*>(a.idx + at);
+            float4* op = reinterpret_cast<float4*>(a.dwt + at);
+#pragma unroll 4
+            for (uint32_t e = threadIdx.x; e < e1 / 4; e += THR) {
+                const int4 i = ip[e];
+                op[e] = on(e * 4) ? make_float4(grad(i.x), grad(i.y), grad(i.z), grad(i.w)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        } else {
+            for (uint32_t e = threadIdx.x; e < e1; e += THR) a.dwt[at + e] = on(e) ? grad(a.idx[at + e]) : 0.f;
+        }
+        u += m;
     }
 }
 
+template <bool VEC>
+void balance_bwd_launch(BalanceBwdArgs a, hipStream_t st) {
+    // The table pays where a workgroup per CU has at least half as many selections as
+    // slots to load, and holds up to 80 K slots.
+    const int64_t sel = a.B * a.T * a.K, wgs = a.H < 256 ? 256 / a.H : 1;
+    const bool table = a.N <= 80 * 1024 && sel / wgs >= a.N / 2;
+    a.piece = table ? (a.B * a.T + wgs - 1) / wgs : (BALANCE_PIECE + a.K - 1) / a.K;
+    const dim3 grid((unsigned)(a.H * ((a.B * a.T + a.piece - 1) / a.piece)));
+    if (table) hipLaunchKernelGGL((balance_bwd_kernel<VEC, true>), grid, dim3(1024), (a.N * 2 + 15) / 16 * 16, st, a);
+    else hipLaunchKernelGGL((balance_bwd_kernel<VEC, false>), grid, dim3(256), 0, st, a);
+}
+
 // Shares of the tokens: a workgroup per CU (an LDS range fills one), but no
-// share below 256 tokens, whose tables would cost more than its selections.
+// share with fewer selections than a quarter of the slots: a share's table is
+// written and read once more.
 struct BalanceLayout {
     int64_t nrange, range, nshare, share, nblk, fixed, counts, bad, kept, bytes;
 };
-BalanceLayout balance_layout(int64_t B, int64_t H, int64_t T, int64_t N) {
+BalanceLayout balance_layout(int64_t B, int64_t H, int64_t T, int64_t K, int64_t N) {
     BalanceLayout y{};
     y.nrange = (N + RANGE - 1) / RANGE;
     y.range = (N + y.nrange - 1) / y.nrange;
     const int64_t tok = B * T;
     int64_t n = 256 / (H * y.nrange);
-    if (n > (tok + 255) / 256) n = (tok + 255) / 256;
+    const int64_t most = tok * K / (N / 4 + 1);
+    if (n > most) n = most;
     if (n < 1) n = 1;
     y.share = (tok + n - 1) / n;
     y.nshare = y.share > 0 ? (tok + y.share - 1) / y.share : 1;
@@ -203,7 +258,7 @@ BalanceLayout balance_layout(int64_t B, int64_t H, int64_t T, int64_t N) {
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     y.fixed = up(y.nshare * H * N * 8);
     y.counts = up(y.nshare * H * N * 4);
-    y.bad = up(y.nshare * H * y.nrange * 4);
+    y.bad = up(y.nshare * H * 4);
     y.kept = up(y.nshare * 4);
     y.bytes = y.fixed + y.counts + y.bad + y.kept + H * y.nblk * 8;
     return y;
@@ -211,10 +266,12 @@ BalanceLayout balance_layout(int64_t B, int64_t H, int64_t T, int64_t N) {
 
 }  // namespace
 
-int64_t balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t N) { return balance_layout(B, H, T, N).bytes; }
+int64_t balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t K, int64_t N) {
+    return balance_layout(B, H, T, K, N).bytes;
+}
 
 hipError_t launch_balance(BalanceArgs a, hipStream_t st) {
-    const BalanceLayout y = balance_layout(a.B, a.H, a.T, a.N);
+    const BalanceLayout y = balance_layout(a.B, a.H, a.T, a.K, a.N);
     char* p = static_cast<char*>(a.workspace);
     a.fixed = reinterpret_cast<int64_t*>(p);
     a.part_counts = reinterpret_cast<int32_t*>(p += y.fixed);
@@ -235,10 +292,8 @@ hipError_t launch_balance(BalanceArgs a, hipStream_t st) {
 }
 
 hipError_t launch_balance_backward(BalanceBwdArgs a, hipStream_t st) {
-    a.pieces = (a.T * a.K + BALANCE_PIECE - 1) / BALANCE_PIECE;
-    const dim3 grid((unsigned)(a.B * a.H * a.pieces));
-    if (a.K % 4 == 0) hipLaunchKernelGGL(balance_bwd_kernel<true>, grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL(balance_bwd_kernel<false>, grid, dim3(256), 0, st, a);
+    if (a.K % 4 == 0) balance_bwd_launch<true>(a, st);
+    else balance_bwd_launch<false>(a, st);
     return hipGetLastError();
 }
 

@@ -712,7 +712,7 @@ extern "C" {
 
 int64_t sdm_balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t K, int64_t N) {
     if (check_balance("sdm_balance_workspace_bytes", B, H, T, K, N)) return -1;
-    return H == 0 ? 0 : sdm::balance_workspace_bytes(B, H, T, N);
+    return H == 0 ? 0 : sdm::balance_workspace_bytes(B, H, T, K, N);
 }
 
 int sdm_balance_forward(const int32_t* idx, const float* wt, const uint8_t* mask, int64_t B, int64_t H, int64_t T,
@@ -725,7 +725,7 @@ int sdm_balance_forward(const int32_t* idx, const float* wt, const uint8_t* mask
     const bool some = B > 0 && T > 0;
     if (some && (rc = check_buffers(fn, {idx, wt}))) return rc;
     if ((rc = check_buffers(fn, {counts, mass, tokens, loss}))) return rc;
-    if ((rc = check_workspace(workspace, workspace_bytes, sdm::balance_workspace_bytes(B, H, T, N)))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, sdm::balance_workspace_bytes(B, H, T, K, N)))) return rc;
     sdm::BalanceArgs a{};
     a.idx = idx; a.wt = wt; a.mask = some ? mask : nullptr;
     a.counts = counts; a.mass = mass; a.tokens = tokens; a.loss = loss;

@@ -232,21 +232,21 @@ struct BalanceArgs {
     void* workspace;
     // set by the launcher
     int64_t* fixed; int32_t* part_counts;  // [nshare][H][N]
-    int32_t* bad;                          // [nshare * H][nrange]
+    int32_t* bad;                          // [nshare][H]
     int32_t* kept;                         // [nshare]
     double* part;                          // [H][nblk]
     int64_t nshare, share;                 // shares of the tokens, and tokens a share
     int nrange, range, nblk, shift;        // slot ranges, and slots a range
 };
-int64_t balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t N);
+int64_t balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t K, int64_t N);
 hipError_t launch_balance(BalanceArgs a, hipStream_t st);
 struct BalanceBwdArgs {
     const int32_t* idx; const uint8_t* mask; const int32_t* counts; const int32_t* tokens; const float* dloss;
     float* dwt;
     int64_t B, H, T, K, N;
-    int64_t pieces;          // set by the launcher
+    int64_t piece;           // tokens a workgroup; set by the launcher
 };
-constexpr int64_t BALANCE_PIECE = 8192;  // selections a workgroup of the backward
+constexpr int64_t BALANCE_PIECE = 4096;  // selections a workgroup of the backward's gathering form
 hipError_t launch_balance_backward(BalanceBwdArgs a, hipStream_t st);
 
 }  // namespace sdm
