@@ -1,0 +1,521 @@
+// dense_pass.h -- one pass of the dense gated recurrence (dense.hip says which
+// recurrence and how its passes make the forward and the gradients).
+//
+//   X_u = a_u X_{u-1} + b_u kap_u (x) omg_u,    out_u = o_u xi_u X_u
+//
+// A workgroup carries SV = 16 NCT NW columns of X in registers over a segment's
+// tokens, C at a time; a wavefront owns 16 NCT of them. Within a chunk, with
+// D_ts = a_{s+1} .. a_t,
+//   out = o (pre X_start + (tril(xi kap^T) . D . b) omg),   pre_t = a_c0 .. a_t
+//   X_end = total X_start + sum_s kap_s (x) (D_end,s b_s omg_s).
+// The decays are products of the gates, never quotients or differences of
+// logarithms: a gate of 0 gives exact zeros and no 0/0. Off the diagonal blocks
+// of 16 x 16, D_ts is the product from t's block start, the whole blocks
+// between, and to s's block end; the diagonal block's wavefront forms its own.
+//
+// All four products run on bf16 matrix instructions (16x16x32, fp32 sums) with
+// fp32 operands kept to fp32's precision: a value is cut into three bf16 planes
+// of 8 bits each (high, middle, low; their sum is the value), and a product of an
+// fp32 operand with a bf16 one takes 3 matrix products, of two fp32 operands 6
+// (the terms left out are 2^-24 of the product or less). That is 1/3 and 1/6 of the bf16
+// rate, against 1/16 for the fp32 matrix instructions.
+//
+// Layouts. xi and kap lie in LDS as rows (token-major, a plane an array), padded by
+// 16 bytes so that 16 rows' pieces fall into different banks. A lane of the 16x16x32
+// instruction takes 8 consecutive k; X's tiles are numbered so that the 8 rows that
+// a lane's accumulators hold in tiles 2p and 2p+1 are 32p + 8 (lane / 16) + 0..7,
+// so X goes from accumulator to operand without leaving its registers. kap^T and omg as
+// operands over the tokens come from the same rows by transposing LDS reads; their
+// token order (4 (lane / 16) + i of two tiles of 16) is the accumulators', so P^T =
+// kap xi^T is written by the wavefront that computes it in the order in which the
+// others read it.
+#pragma once
+#include "sdm_buffer.h"
+#include "sdm_internal.h"
+
+namespace sdm {
+namespace {
+
+typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8_t;
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+__device__ __forceinline__ float load1(const void* p, bool bf16, int64_t e) {
+    return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[e] << 16) : static_cast<const float*>(p)[e];
+}
+
+// two values' planes, packed: a's in the low half
+__device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) {
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    h = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+    const float ra = a - __uint_as_float(ua & 0xFFFF0000u), rb = b - __uint_as_float(ub & 0xFFFF0000u);
+    const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
+    m = __builtin_amdgcn_perm(vb, va, 0x07060302u);
+    const float sa = ra - __uint_as_float(va & 0xFFFF0000u), sb = rb - __uint_as_float(vb & 0xFFFF0000u);
+    l = __builtin_amdgcn_perm(__float_as_uint(sb), __float_as_uint(sa), 0x07060302u);
+}
+// 8 values -> three operand planes
+__device__ __forceinline__ void split8(const float (&v)[8], uint4 (&p)[3]) {
+    split2(v[0], v[1], p[0].x, p[1].x, p[2].x);
+    split2(v[2], v[3], p[0].y, p[1].y, p[2].y);
+    split2(v[4], v[5], p[0].z, p[1].z, p[2].z);
+    split2(v[6], v[7], p[0].w, p[1].w, p[2].w);
+}
+
+// acc += A B over the operands' planes
+template <int NA, int NB>
+__device__ __forceinline__ void mma(const uint4 (&a)[NA], const uint4 (&b)[NB], f32x4_t& acc) {
+    auto one = [&](int i, int j) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a[i]), __builtin_bit_cast(bf16x8_t, b[j]),
+                                                      acc, 0, 0, 0);
+    };
+#pragma unroll
+    for (int s = 2; s >= 0; --s)  // the smallest terms first
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                if (i + j == s) one(i, j);
+}
+
+// 8 elements from global memory: bf16 (one register quad) or fp32 (two)
+template <int NP>
+struct Piece;
+template <>
+struct Piece<1> {
+    uint4 x;
+    __device__ __forceinline__ void zero() { x = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void load(const void* p, int64_t e) {
+        x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e);
+    }
+    __device__ __forceinline__ void store(char* lds, int) const { *reinterpret_cast<uint4*>(lds) = x; }
+};
+template <>
+struct Piece<3> {
+    float4 x, y;
+    __device__ __forceinline__ void zero() { x = y = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const void* p, int64_t e) {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
+        x = f[0];
+        y = f[1];
+    }
+    __device__ __forceinline__ void store(char* lds, int plane) const {
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        uint4 p[3];
+        split8(v, p);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(lds + i * plane) = p[i];
+    }
+};
+
+// transposing read of 4 rows x 16 columns by 16 lanes: this lane's piece is 8
+// bytes at p; it gets its own column of the 4 rows
+__device__ __forceinline__ uint2 read_tr(const char* p) {
+    typedef __attribute__((address_space(3))) s16x4_t lds_t;
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)p));
+}
+
+// NX, NK, NO: planes of xi, kap and omg (1: bf16 in memory, 3: fp32)
+template <int DKT_, int NCT_, int NW_, int C_, int NX_, int NK_, int NO_, bool OUT_>
+struct DensePass {
+    static constexpr int DKT = DKT_, NCT = NCT_, NW = NW_, C = C_, NX = NX_, NK = NK_, NO = NO_;
+    static constexpr bool OUT = OUT_;
+    static constexpr int DKP = DKT * 16, SV = 16 * NCT * NW, NT = C / 16, THR = NW * 64;
+    static constexpr int RK = DKP * 2 + 16, RV = SV * 2 + 16;        // bytes of an LDS row
+    static constexpr int PK = C * RK, PV = C * RV;                   // bytes of a plane
+    static constexpr int TILES = NT * (NT + 1) / 2;
+    static constexpr int O_KA = 0, O_OM = O_KA + NK * PK, O_XI = O_OM + NO * PV, O_P = O_XI + (OUT ? NX * PK : 0),
+                         O_F = O_P + (OUT ? TILES * 3 * 512 : 0), LDS = O_F + (3 * C + 2 * NT + NW * C + NW) * 4;
+    static_assert(NW >= NT, "a diagonal block's decays are formed by its own wavefront");
+    static_assert(LDS <= 160 * 1024, "a workgroup's LDS");
+};
+
+template <class P>
+__global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
+    constexpr int DKT = P::DKT, NCT = P::NCT, C = P::C, NT = P::NT, THR = P::THR, DKP = P::DKP, SV = P::SV, NW = P::NW;
+    extern __shared__ __align__(16) char lds[];
+    char* const Ka = lds + P::O_KA;
+    char* const Om = lds + P::O_OM;
+    char* const Xi = lds + P::O_XI;
+    char* const Pf = lds + P::O_P;
+    float* const fpre = reinterpret_cast<float*>(lds + P::O_F);  // gates from the block's start through t
+    float* const fsuf = fpre + C;                                // gates after s through the block's end
+    float* const fin = fsuf + C;                                 // b_s
+    float* const ftot = fin + C;                                 // a block's gates
+    float* const fdot = ftot + 2 * NT;                           // [NW][C]
+    float* const fsum = fdot + NW * C;                           // [NW]
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), m16 = lane & 15, g4 = lane >> 4;
+    int64_t us;
+    int slab;
+    block_unit((int)blockIdx.x, a.NS * a.nseg, a.nslab, us, slab);
+    if (us >= a.NS * a.nseg) return;
+    const int64_t s = us / a.nseg;  // stream
+    const int seg = (int)(us % a.nseg);
+    const int64_t lo = (int64_t)seg * a.L, hi = lo + a.L < a.T ? lo + a.L : a.T;
+    const int c0 = slab * SV;
+    const int64_t row0 = s * a.T, per = (int64_t)a.DK * a.DV;
+    const int64_t st_seg = (seg * a.NS + s) * per, st_one = s * per;
+    int col[NCT];
+#pragma unroll
+    for (int n = 0; n < NCT; ++n) col[n] = c0 + (w * NCT + n) * 16 + m16;
+
+    // rows 32p + 8 g4 + 4h + i in X[2p + h][..][i]
+    f32x4_t X[DKT][NCT];
+#pragma unroll
+    for (int k = 0; k < DKT; ++k)
+#pragma unroll
+        for (int n = 0; n < NCT; ++n) {
+            X[k][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            const int r = 32 * (k >> 1) + 8 * g4 + 4 * (k & 1);
+            if (P::OUT && a.X0 && r < a.DK && col[n] < a.DV) {  // DK a multiple of 8: 4 rows at once
+                const float* x = a.X0 + (a.X0_seg ? st_seg : st_one) + r * (int64_t)a.x_row + col[n] * (int64_t)a.x_col;
+                if (a.x_row == 1) {
+                    const float4 v = *reinterpret_cast<const float4*>(x);
+                    X[k][n] = f32x4_t{v.x, v.y, v.z, v.w};
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) X[k][n][i] = x[i * (int64_t)a.x_row];
+                }
+            }
+        }
+
+    constexpr int KP = C * (DKP / 8) / THR, VP = (C * (SV / 8) + THR - 1) / THR;  // pieces a thread
+    static_assert(C * (DKP / 8) % THR == 0, "whole pieces");
+    Piece<P::NK> pk[KP];
+    Piece<P::NX> px[P::OUT ? KP : 1];
+    Piece<P::NO> po[VP];
+    float pg = 1.f, pb = 0.f;
+    const int nch = (int)((hi - lo + C - 1) / C);
+    auto span = [&](int ch, int64_t& t0, int& n) {  // the chunk's first token and length, in processing order
+        const int64_t at = lo + (int64_t)(a.rev ? nch - 1 - ch : ch) * C;
+        t0 = at;
+        n = (int)(hi - at < C ? hi - at : C);
+    };
+    auto fetch = [&](int ch) {
+        int64_t t0;
+        int n;
+        span(ch, t0, n);
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+            const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
+            pk[i].zero();
+            if (P::OUT) px[P::OUT ? i : 0].zero();
+            if (j < n && q < a.DK) {
+                const int64_t at = (row0 + (a.rev ? t0 + n - 1 - j : t0 + j)) * a.DK + q;
+                pk[i].load(a.kap, at);
+                if (P::OUT) px[P::OUT ? i : 0].load(a.xi, at);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int e = tid + i * THR, j = e / (SV / 8), q = e % (SV / 8) * 8;
+            po[i].zero();
+            if (j < n && c0 + q < a.DV) po[i].load(a.omg, (row0 + (a.rev ? t0 + n - 1 - j : t0 + j)) * a.DV + c0 + q);
+        }
+        pg = 1.f;
+        pb = 0.f;
+        const int j = w * 16 + m16;
+        if (w < NT && j < n) {
+            const int64_t t = a.rev ? t0 + n - 1 - j : t0 + j;
+            if (!a.rev) pg = a.a[row0 + t];
+            else if (t + 1 < a.T) pg = a.a[row0 + t + 1];
+            pb = a.b ? a.b[row0 + t] : 1.f;
+        }
+    };
+    fetch(0);
+    float segdec = 1.f;
+    for (int ch = 0; ch < nch; ++ch) {
+        int64_t t0;
+        int n;
+        span(ch, t0, n);
+        auto token = [&](int j) { return a.rev ? t0 + n - 1 - j : t0 + j; };
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+            const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
+            pk[i].store(Ka + j * P::RK + q * 2, P::PK);
+            if constexpr (P::OUT) px[i].store(Xi + j * P::RK + q * 2, P::PK);
+        }
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int e = tid + i * THR, j = e / (SV / 8), q = e % (SV / 8) * 8;
+            if (C * (SV / 8) % THR == 0 || j < C) po[i].store(Om + j * P::RV + q * 2, P::PV);
+        }
+        float dg[4] = {0.f, 0.f, 0.f, 0.f};  // D_ts of block w: t = m16, s = 4 g4 + i
+        if (w < NT) {
+            float p = 1.f, q = 1.f;
+#pragma unroll
+            for (int r = 15; r >= 0; --r) {
+                const float gr = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(pg), r));
+                if (P::OUT && g4 == r >> 2) dg[r & 3] = r <= m16 ? p : 0.f;
+                p *= r <= m16 ? gr : 1.f;
+                q *= r > m16 ? gr : 1.f;
+            }
+            if (lane < 16) {
+                fpre[w * 16 + lane] = p;
+                fsuf[w * 16 + lane] = q;
+                fin[w * 16 + lane] = pb;
+                if (lane == 15) ftot[w] = p;
+            }
+        }
+        __syncthreads();
+        if (ch + 1 < nch) fetch(ch + 1);
+        float tot[NT], total = 1.f;
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+            tot[b] = ftot[b];
+            total *= tot[b];
+        }
+        f32x4_t acc[P::OUT ? NT : 1][NCT];
+        if constexpr (P::OUT) {
+            // P^T = kap xi^T, scaled: a tile (s block st, t block tt) by one wavefront, its planes
+            // stored as the operand of the product with omg
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                for (int st = 0; st <= tt; ++st) {
+                    const int owner = st == tt ? tt : (NT + tt * (tt - 1) / 2 + st) % NW;
+                    if (w != owner) continue;
+                    f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < DKP; k += 32) {
+                        uint4 ka[P::NK], xb[P::NX];
+#pragma unroll
+                        for (int i = 0; i < P::NK; ++i)
+                            ka[i] = *reinterpret_cast<const uint4*>(Ka + i * P::PK + (st * 16 + m16) * P::RK + k * 2 + g4 * 16);
+#pragma unroll
+                        for (int i = 0; i < P::NX; ++i)
+                            xb[i] = *reinterpret_cast<const uint4*>(Xi + i * P::PK + (tt * 16 + m16) * P::RK + k * 2 + g4 * 16);
+                        mma<P::NK, P::NX>(ka, xb, p);
+                    }
+                    const float4 in = *reinterpret_cast<const float4*>(fin + st * 16 + 4 * g4);
+                    float f[4] = {in.x, in.y, in.z, in.w};
+                    if (st == tt) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[i] *= dg[i];
+                    } else {
+                        const float4 sf = *reinterpret_cast<const float4*>(fsuf + st * 16 + 4 * g4);
+                        float pr = fpre[tt * 16 + m16];
+#pragma unroll
+                        for (int b = st + 1; b < tt; ++b) pr *= tot[b];
+                        f[0] *= sf.x * pr; f[1] *= sf.y * pr; f[2] *= sf.z * pr; f[3] *= sf.w * pr;
+                    }
+                    uint2 o[3];
+                    split2(p[0] * f[0], p[1] * f[1], o[0].x, o[1].x, o[2].x);
+                    split2(p[2] * f[2], p[3] * f[3], o[0].y, o[1].y, o[2].y);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        *reinterpret_cast<uint2*>(Pf + ((tt * (tt + 1) / 2 + st) * 3 + i) * 512 + lane * 8) = o[i];
+                }
+            // xi X_start
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int c = 0; c < NCT; ++c) acc[t][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = 0; p < DKT / 2; ++p) {
+                uint4 xb[NCT][3];
+#pragma unroll
+                for (int c = 0; c < NCT; ++c) {
+                    const float v[8] = {X[2 * p][c][0], X[2 * p][c][1], X[2 * p][c][2], X[2 * p][c][3],
+                                        X[2 * p + 1][c][0], X[2 * p + 1][c][1], X[2 * p + 1][c][2], X[2 * p + 1][c][3]};
+                    split8(v, xb[c]);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    uint4 xa[P::NX];
+#pragma unroll
+                    for (int i = 0; i < P::NX; ++i)
+                        xa[i] = *reinterpret_cast<const uint4*>(Xi + i * P::PK + (t * 16 + m16) * P::RK + p * 64 + g4 * 16);
+#pragma unroll
+                    for (int c = 0; c < NCT; ++c) mma<P::NX, 3>(xa, xb[c], acc[t][c]);
+                }
+            }
+            float inter = 0.f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float4 pr = *reinterpret_cast<const float4*>(fpre + t * 16 + 4 * g4);
+                float q = 1.f;
+#pragma unroll
+                for (int b = 0; b < t; ++b) q *= tot[b];
+                const float f[4] = {pr.x * q, pr.y * q, pr.z * q, pr.w * q};
+#pragma unroll
+                for (int c = 0; c < NCT; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[t][c][i] *= f[i];
+                if (a.dot) {  // what the chunk's start gives to xi_t X_t . with_t, summed over the chunk
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = t * 16 + 4 * g4 + i;
+                        if (j >= n) continue;
+                        const int64_t at = row0 + token(j);
+                        float d = 0.f;
+#pragma unroll
+                        for (int c = 0; c < NCT; ++c)
+                            if (col[c] < a.DV) d = fmaf(acc[t][c][i], load1(a.with, a.with_bf16, at * a.DV + col[c]), d);
+                        inter = fmaf(d, a.o ? a.o[at] : 1.f, inter);
+                    }
+                }
+            }
+            if (a.dot) {
+                inter = wave_sum(inter);
+                if (lane == 0) fsum[w] = inter;
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < DKT; ++k)
+#pragma unroll
+            for (int c = 0; c < NCT; ++c) X[k][c] *= total;
+        // over the tokens, two blocks of 16 at a time
+#pragma unroll
+        for (int b = 0; b < NT; b += 2) {
+            uint4 om[NCT][P::NO], ow[NCT][3];
+            float f[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 sf = *reinterpret_cast<const float4*>(fsuf + (b + h) * 16 + 4 * g4);
+                const float4 in = *reinterpret_cast<const float4*>(fin + (b + h) * 16 + 4 * g4);
+                float q = 1.f;
+#pragma unroll
+                for (int e = b + h + 1; e < NT; ++e) q *= tot[e];
+                f[4 * h] = sf.x * in.x * q; f[4 * h + 1] = sf.y * in.y * q;
+                f[4 * h + 2] = sf.z * in.z * q; f[4 * h + 3] = sf.w * in.w * q;
+            }
+#pragma unroll
+            for (int c = 0; c < NCT; ++c) {
+#pragma unroll
+                for (int i = 0; i < P::NO; ++i) {
+                    const char* o = Om + i * P::PV + (b * 16 + 4 * g4 + (m16 >> 2)) * P::RV + ((w * NCT + c) * 16 + (m16 & 3) * 4) * 2;
+                    const uint2 x = read_tr(o), y = read_tr(o + 16 * P::RV);
+                    om[c][i] = make_uint4(x.x, x.y, y.x, y.y);
+                }
+                const uint32_t u[4] = {om[c][0].x, om[c][0].y, om[c][0].z, om[c][0].w};
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[2 * i] = bf_lo(u[i]);
+                    v[2 * i + 1] = bf_hi(u[i]);
+                }
+                if constexpr (P::NO == 3) {  // the planes' sum is the value
+                    const uint32_t m[4] = {om[c][1].x, om[c][1].y, om[c][1].z, om[c][1].w};
+                    const uint32_t l[4] = {om[c][2].x, om[c][2].y, om[c][2].z, om[c][2].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[2 * i] += bf_lo(m[i]) + bf_lo(l[i]);
+                        v[2 * i + 1] += bf_hi(m[i]) + bf_hi(l[i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= f[i];
+                split8(v, ow[c]);
+            }
+            if constexpr (P::OUT) {
+#pragma unroll
+                for (int t = b; t < NT; ++t) {
+                    uint4 pa[3];
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const char* p = Pf + ((t * (t + 1) / 2 + b) * 3 + i) * 512 + lane * 8;
+                        const uint2 x = *reinterpret_cast<const uint2*>(p);
+                        const uint2 y = b < t ? *reinterpret_cast<const uint2*>(p + 3 * 512) : make_uint2(0u, 0u);
+                        pa[i] = make_uint4(x.x, x.y, y.x, y.y);
+                    }
+#pragma unroll
+                    for (int c = 0; c < NCT; ++c) mma<3, P::NO>(pa, om[c], acc[t][c]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < DKT; ++k) {
+                uint4 ka[P::NK];
+#pragma unroll
+                for (int i = 0; i < P::NK; ++i) {
+                    const char* o = Ka + i * P::PK + (b * 16 + 4 * g4 + (m16 >> 2)) * P::RK + (32 * (k >> 1) + 8 * (m16 & 3) + 4 * (k & 1)) * 2;
+                    const uint2 x = read_tr(o), y = read_tr(o + 16 * P::RK);
+                    ka[i] = make_uint4(x.x, x.y, y.x, y.y);
+                }
+#pragma unroll
+                for (int c = 0; c < NCT; ++c) mma<P::NK, 3>(ka, ow[c], X[k][c]);
+            }
+        }
+        if constexpr (P::OUT) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = t * 16 + 4 * g4 + i;
+                    const int64_t at = row0 + token(j < n ? j : 0);
+                    float d = 0.f;
+#pragma unroll
+                    for (int c = 0; c < NCT; ++c)
+                        if (j < n && col[c] < a.DV) {
+                            if (a.dot) d = fmaf(acc[t][c][i], load1(a.with, a.with_bf16, at * a.DV + col[c]), d);
+                            a.out[at * a.DV + col[c]] = a.o ? acc[t][c][i] * a.o[at] : acc[t][c][i];
+                        }
+                    if (a.dot) {
+                        d = ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(d))));
+                        if (m16 == 0) fdot[w * C + j] = d;
+                    }
+                }
+            if (a.dot) {
+                __syncthreads();
+                if (tid < n) {
+                    float d = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NW; ++i) d += fdot[i * C + tid];
+                    a.dot[((int64_t)slab * a.NS + s) * a.T + token(tid)] = d;
+                }
+                if (tid == 0) {
+                    float d = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NW; ++i) d += fsum[i];
+                    a.inter[((int64_t)slab * a.NS + s) * a.nchunk + t0 / C] = d;
+                }
+            }
+        } else {
+            segdec *= total;
+        }
+    }
+    if (a.Xend) {
+#pragma unroll
+        for (int k = 0; k < DKT; ++k)
+#pragma unroll
+            for (int c = 0; c < NCT; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 32 * (k >> 1) + 8 * g4 + 4 * (k & 1) + i;
+                    if (r < a.DK && col[c] < a.DV) a.Xend[(P::OUT ? st_one : st_seg) + r * (int64_t)a.DV + col[c]] = X[k][c][i];
+                }
+    }
+    if (!P::OUT && slab == 0 && tid == 0) a.segdec[seg * a.NS + s] = segdec;
+}
+
+template <class P>
+hipError_t launch_dense_pass(DenseArgs a, hipStream_t st) {
+    a.nslab = (a.DV + P::SV - 1) / P::SV;
+    a.nchunk = (a.T + P::C - 1) / P::C;
+    hipLaunchKernelGGL(dense_pass_kernel<P>, dim3((unsigned)unit_grid(a.NS * a.nseg, a.nslab)), dim3(P::THR), P::LDS, st, a);
+    return hipGetLastError();
+}
+
+// Columns a workgroup: 64, or 128 where there are that many (the products over
+// the contracted width are then done once for all of them).
+constexpr int dense_slab(int dv) { return dv <= 64 ? 64 : 128; }
+
+template <int C, int NX, int NK, int NO, bool OUT>
+hipError_t launch_dense_sized(const DenseArgs& a, hipStream_t st) {
+    const bool wide = dense_slab(a.DV) == 128;
+    if (a.DK <= 64)
+        return wide ? launch_dense_pass<DensePass<4, 2, 4, C, NX, NK, NO, OUT>>(a, st)
+                    : launch_dense_pass<DensePass<4, 1, 4, C, NX, NK, NO, OUT>>(a, st);
+    if (a.DK <= 128)
+        return wide ? launch_dense_pass<DensePass<8, 2, 4, C, NX, NK, NO, OUT>>(a, st)
+                    : launch_dense_pass<DensePass<8, 1, 4, C, NX, NK, NO, OUT>>(a, st);
+    return wide ? launch_dense_pass<DensePass<16, 1, 8, C, NX, NK, NO, OUT>>(a, st)
+                : launch_dense_pass<DensePass<16, 1, 4, C, NX, NK, NO, OUT>>(a, st);
+}
+
+}  // namespace
+}  // namespace sdm

@@ -150,8 +150,10 @@ struct DenseArgs {
     float* Xend;             // optional: the state after the stream (or, in the first pass, each segment's own)
     float* segdec;           // first pass: [nseg][NS] product of the segment's gates
     const void* with; bool with_bf16;  // [NS][T][DV]: rows multiplied with the (unscaled) output
-    float* dot;              // optional [nslab][NS][T]: those products, per column slab
+    float* dot;              // optional [nslab][NS][T]: those products, per column slab, and
+    float* inter;            // [nslab][NS][nchunk]: the part (scaled by o) of the chunk's starting state, summed
     int64_t NS, T, L;        // L: tokens per segment
+    int64_t nchunk;          // chunks of a stream; set by the launcher
     int nseg, nslab, DK, DV;
     bool rev;                // from the last token to the first
 };
@@ -169,12 +171,24 @@ struct DenseGatesArgs {
     const float* G; const float* S;   // [nseg][NS][per]: states from behind, states at the starts
     const float* ST;                  // [NS][per]: after the last token
     const float* qdq; const float* kdk;  // [nslab][NS][T]
+    const float* inter_q; const float* inter_k;  // [nslab][NS][nchunk]
     const float* alpha; const float* beta;
     float* dlog_alpha; float* dbeta;
-    int64_t NS, T, L, per;
-    int nseg, nslab_q, nslab_k;
+    int64_t NS, T, L, per, nchunk;
+    int nseg, nslab, C;
     bool has_dS;
 };
+// Tokens per chunk: 64, or 32 where some rows are fp32 (three planes of each in LDS).
+constexpr int DENSE_CHUNK = 64, DENSE_CHUNK_F32 = 32;
+// The passes by their rows' types (those named are fp32, the others bf16; all of f32's)
+hipError_t launch_dense_bf16(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_bf16_state(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_xi32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_kap32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_omg32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_omg32_state(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_f32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_f32_state(const DenseArgs& a, hipStream_t st);
 struct DenseFwdArgs {
     const void* q; const void* k; const void* v; bool bf16;
     const float* alpha; const float* beta;
