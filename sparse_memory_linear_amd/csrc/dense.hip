@@ -123,6 +123,10 @@ __global__ __launch_bounds__(256) void dense_gates_kernel(DenseGatesArgs a) {
     }
 }
 
+__device__ __forceinline__ float load1(const void* p, bool bf16, int64_t e) {
+    return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[e] << 16) : static_cast<const float*>(p)[e];
+}
+
 // A few tokens a call (decoding): the state is read and written once, as rows
 // of 64 columns; thread (r, c) holds rows r + 16 i, columns 4c .. 4c + 3.
 template <int NR>

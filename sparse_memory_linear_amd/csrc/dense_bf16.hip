@@ -3,7 +3,7 @@
 
 namespace sdm {
 
-hipError_t launch_dense_bf16(const DenseArgs& a, hipStream_t st) { return launch_dense_sized<DENSE_CHUNK, 1, 1, 1, true>(a, st); }
-hipError_t launch_dense_bf16_state(const DenseArgs& a, hipStream_t st) { return launch_dense_sized<DENSE_CHUNK, 1, 1, 1, false>(a, st); }
+hipError_t launch_dense_bf16(const DenseArgs& a, hipStream_t st) { return launch_dense_sized<DENSE_CHUNK, 1, 1, 1, true, false>(a, st); }
+hipError_t launch_dense_bf16_state(const DenseArgs& a, hipStream_t st) { return launch_dense_sized<DENSE_CHUNK, 1, 1, 1, false, false>(a, st); }
 
 }  // namespace sdm

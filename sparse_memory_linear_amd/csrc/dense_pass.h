@@ -42,9 +42,6 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-__device__ __forceinline__ float load1(const void* p, bool bf16, int64_t e) {
-    return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[e] << 16) : static_cast<const float*>(p)[e];
-}
 
 // two values' planes, packed: a's in the low half
 __device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) {
@@ -86,20 +83,20 @@ struct Piece;
 template <>
 struct Piece<1> {
     uint4 x;
-    __device__ __forceinline__ void zero() { x = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void load(const void* p, int64_t e) {
-        x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e);
+    static constexpr uint32_t ESZ = 2;
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
+        const int4 v = ld_i4(r, off, 0);
+        x = make_uint4((uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w);
     }
     __device__ __forceinline__ void store(char* lds, int) const { *reinterpret_cast<uint4*>(lds) = x; }
 };
 template <>
 struct Piece<3> {
     float4 x, y;
-    __device__ __forceinline__ void zero() { x = y = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void load(const void* p, int64_t e) {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
-        x = f[0];
-        y = f[1];
+    static constexpr uint32_t ESZ = 4;
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
+        x = ld_f4(r, off, 0);
+        y = ld_f4(r, off + 16u, 0);
     }
     __device__ __forceinline__ void store(char* lds, int plane) const {
         const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -118,16 +115,17 @@ __device__ __forceinline__ uint2 read_tr(const char* p) {
 }
 
 // NX, NK, NO: planes of xi, kap and omg (1: bf16 in memory, 3: fp32)
-template <int DKT_, int NCT_, int NW_, int C_, int NX_, int NK_, int NO_, bool OUT_>
+// OUT: outputs (else only the segment's own state, from zero); DOT: also their products with `with`
+template <int DKT_, int NCT_, int NW_, int C_, int NX_, int NK_, int NO_, bool OUT_, bool DOT_>
 struct DensePass {
     static constexpr int DKT = DKT_, NCT = NCT_, NW = NW_, C = C_, NX = NX_, NK = NK_, NO = NO_;
-    static constexpr bool OUT = OUT_;
+    static constexpr bool OUT = OUT_, DOT = DOT_;
     static constexpr int DKP = DKT * 16, SV = 16 * NCT * NW, NT = C / 16, THR = NW * 64;
     static constexpr int RK = DKP * 2 + 16, RV = SV * 2 + 16;        // bytes of an LDS row
     static constexpr int PK = C * RK, PV = C * RV;                   // bytes of a plane
     static constexpr int TILES = NT * (NT + 1) / 2;
     static constexpr int O_KA = 0, O_OM = O_KA + NK * PK, O_XI = O_OM + NO * PV, O_P = O_XI + (OUT ? NX * PK : 0),
-                         O_F = O_P + (OUT ? TILES * 3 * 512 : 0), LDS = O_F + (3 * C + 2 * NT + NW * C + NW) * 4;
+                         O_F = O_P + (OUT ? TILES * 3 * 512 : 0), LDS = O_F + (4 * C + 2 * NT + NW * C + NW) * 4;
     static_assert(NW >= NT, "a diagonal block's decays are formed by its own wavefront");
     static_assert(LDS <= 160 * 1024, "a workgroup's LDS");
 };
@@ -143,7 +141,8 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
     float* const fpre = reinterpret_cast<float*>(lds + P::O_F);  // gates from the block's start through t
     float* const fsuf = fpre + C;                                // gates after s through the block's end
     float* const fin = fsuf + C;                                 // b_s
-    float* const ftot = fin + C;                                 // a block's gates
+    float* const fo = fin + C;                                   // o_t
+    float* const ftot = fo + C;                                  // a block's gates
     float* const fdot = ftot + 2 * NT;                           // [NW][C]
     float* const fsum = fdot + NW * C;                           // [NW]
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), m16 = lane & 15, g4 = lane >> 4;
@@ -186,42 +185,47 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
     Piece<P::NK> pk[KP];
     Piece<P::NX> px[P::OUT ? KP : 1];
     Piece<P::NO> po[VP];
-    float pg = 1.f, pb = 0.f;
+    float pg = 1.f, pb = 0.f, po_ = 1.f;
     const int nch = (int)((hi - lo + C - 1) / C);
     auto span = [&](int ch, int64_t& t0, int& n) {  // the chunk's first token and length, in processing order
         const int64_t at = lo + (int64_t)(a.rev ? nch - 1 - ch : ch) * C;
         t0 = at;
         n = (int)(hi - at < C ? hi - at : C);
     };
+    // Rows are read through buffers that begin at the chunk's first token and end behind its
+    // last: a piece beyond it reads zeros, as does one beyond the row's width (offset OOB).
+    // Backwards, row j is the chunk's token n - 1 - j.
+    auto row = [&](int j, int n) { return a.rev ? n - 1 - j : j; };
+    auto rows = [&](const void* p, int64_t t0, int n, int width, uint32_t esz) {
+        return make_rsrc(static_cast<const char*>(p) + (row0 + t0) * width * esz, (int64_t)n * width * esz);
+    };
     auto fetch = [&](int ch) {
         int64_t t0;
         int n;
         span(ch, t0, n);
+        const rsrc_t rk = rows(a.kap, t0, n, a.DK, Piece<P::NK>::ESZ), ro = rows(a.omg, t0, n, a.DV, Piece<P::NO>::ESZ);
+        const rsrc_t rx = P::OUT ? rows(a.xi, t0, n, a.DK, Piece<P::NX>::ESZ) : rk;
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
             const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
-            pk[i].zero();
-            if (P::OUT) px[P::OUT ? i : 0].zero();
-            if (j < n && q < a.DK) {
-                const int64_t at = (row0 + (a.rev ? t0 + n - 1 - j : t0 + j)) * a.DK + q;
-                pk[i].load(a.kap, at);
-                if (P::OUT) px[P::OUT ? i : 0].load(a.xi, at);
-            }
+            const uint32_t at = (uint32_t)(row(j, n) * a.DK + q);
+            pk[i].load(rk, q < a.DK ? at * Piece<P::NK>::ESZ : OOB);
+            if (P::OUT) px[P::OUT ? i : 0].load(rx, q < a.DK ? at * Piece<P::NX>::ESZ : OOB);
         }
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
             const int e = tid + i * THR, j = e / (SV / 8), q = e % (SV / 8) * 8;
-            po[i].zero();
-            if (j < n && c0 + q < a.DV) po[i].load(a.omg, (row0 + (a.rev ? t0 + n - 1 - j : t0 + j)) * a.DV + c0 + q);
+            po[i].load(ro, c0 + q < a.DV ? (uint32_t)(row(j, n) * a.DV + c0 + q) * Piece<P::NO>::ESZ : OOB);
         }
         pg = 1.f;
         pb = 0.f;
         const int j = w * 16 + m16;
         if (w < NT && j < n) {
-            const int64_t t = a.rev ? t0 + n - 1 - j : t0 + j;
+            const int64_t t = t0 + row(j, n);
             if (!a.rev) pg = a.a[row0 + t];
             else if (t + 1 < a.T) pg = a.a[row0 + t + 1];
             pb = a.b ? a.b[row0 + t] : 1.f;
+            po_ = a.o ? a.o[row0 + t] : 1.f;
         }
     };
     fetch(0);
@@ -230,7 +234,6 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
         int64_t t0;
         int n;
         span(ch, t0, n);
-        auto token = [&](int j) { return a.rev ? t0 + n - 1 - j : t0 + j; };
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
@@ -257,6 +260,7 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
                 fpre[w * 16 + lane] = p;
                 fsuf[w * 16 + lane] = q;
                 fin[w * 16 + lane] = pb;
+                fo[w * 16 + lane] = po_;
                 if (lane == 15) ftot[w] = p;
             }
         }
@@ -269,6 +273,24 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
             total *= tot[b];
         }
         f32x4_t acc[P::OUT ? NT : 1][NCT];
+        float wi[P::DOT ? NT * 4 : 1][NCT];  // `with` at this lane's outputs
+        if constexpr (P::DOT) {
+            const uint32_t esz = a.with_bf16 ? 2 : 4;
+            const rsrc_t rw = rows(a.with, t0, n, a.DV, esz);
+#pragma unroll
+            for (int t = 0; t < NT * 4; ++t)
+#pragma unroll
+                for (int c = 0; c < NCT; ++c) {
+                    const int j = (t >> 2) * 16 + 4 * g4 + (t & 3);
+                    const uint32_t at = (uint32_t)(row(j, n) * a.DV + col[c]);
+                    if (a.with_bf16) {
+                        const uint32_t u = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rw, (int)(col[c] < a.DV ? at * 2u : OOB), 0, 0);
+                        wi[t][c] = bf_lo(u);
+                    } else {
+                        wi[t][c] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, (int)(col[c] < a.DV ? at * 4u : OOB), 0, 0));
+                    }
+                }
+        }
         if constexpr (P::OUT) {
             // P^T = kap xi^T, scaled: a tile (s block st, t block tt) by one wavefront, its planes
             // stored as the operand of the product with omg
@@ -345,21 +367,18 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
                 for (int c = 0; c < NCT; ++c)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[t][c][i] *= f[i];
-                if (a.dot) {  // what the chunk's start gives to xi_t X_t . with_t, summed over the chunk
+                if constexpr (P::DOT) {  // what the chunk's start gives to xi_t X_t . with_t, summed over the chunk
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = t * 16 + 4 * g4 + i;
-                        if (j >= n) continue;
-                        const int64_t at = row0 + token(j);
                         float d = 0.f;
 #pragma unroll
-                        for (int c = 0; c < NCT; ++c)
-                            if (col[c] < a.DV) d = fmaf(acc[t][c][i], load1(a.with, a.with_bf16, at * a.DV + col[c]), d);
-                        inter = fmaf(d, a.o ? a.o[at] : 1.f, inter);
+                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wi[t * 4 + i][c], d);
+                        inter = fmaf(d, fo[j], inter);
                     }
                 }
             }
-            if (a.dot) {
+            if constexpr (P::DOT) {
                 inter = wave_sum(inter);
                 if (lane == 0) fsum[w] = inter;
             }
@@ -441,31 +460,31 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
             }
         }
         if constexpr (P::OUT) {
+            const rsrc_t rout = rows(a.out, t0, n, a.DV, 4);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = t * 16 + 4 * g4 + i;
-                    const int64_t at = row0 + token(j < n ? j : 0);
-                    float d = 0.f;
+                    const float f = fo[j];
 #pragma unroll
                     for (int c = 0; c < NCT; ++c)
-                        if (j < n && col[c] < a.DV) {
-                            if (a.dot) d = fmaf(acc[t][c][i], load1(a.with, a.with_bf16, at * a.DV + col[c]), d);
-                            a.out[at * a.DV + col[c]] = a.o ? acc[t][c][i] * a.o[at] : acc[t][c][i];
-                        }
-                    if (a.dot) {
+                        st_f1(acc[t][c][i] * f, rout, col[c] < a.DV ? (uint32_t)(row(j, n) * a.DV + col[c]) * 4u : OOB, 0);
+                    if constexpr (P::DOT) {
+                        float d = 0.f;
+#pragma unroll
+                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wi[t * 4 + i][c], d);
                         d = ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(d))));
                         if (m16 == 0) fdot[w * C + j] = d;
                     }
                 }
-            if (a.dot) {
+            if constexpr (P::DOT) {
                 __syncthreads();
                 if (tid < n) {
                     float d = 0.f;
 #pragma unroll
                     for (int i = 0; i < NW; ++i) d += fdot[i * C + tid];
-                    a.dot[((int64_t)slab * a.NS + s) * a.T + token(tid)] = d;
+                    a.dot[((int64_t)slab * a.NS + s) * a.T + t0 + row(tid, n)] = d;
                 }
                 if (tid == 0) {
                     float d = 0.f;
@@ -504,17 +523,17 @@ hipError_t launch_dense_pass(DenseArgs a, hipStream_t st) {
 // the contracted width are then done once for all of them).
 constexpr int dense_slab(int dv) { return dv <= 64 ? 64 : 128; }
 
-template <int C, int NX, int NK, int NO, bool OUT>
+template <int C, int NX, int NK, int NO, bool OUT, bool DOT>
 hipError_t launch_dense_sized(const DenseArgs& a, hipStream_t st) {
     const bool wide = dense_slab(a.DV) == 128;
     if (a.DK <= 64)
-        return wide ? launch_dense_pass<DensePass<4, 2, 4, C, NX, NK, NO, OUT>>(a, st)
-                    : launch_dense_pass<DensePass<4, 1, 4, C, NX, NK, NO, OUT>>(a, st);
+        return wide ? launch_dense_pass<DensePass<4, 2, 4, C, NX, NK, NO, OUT, DOT>>(a, st)
+                    : launch_dense_pass<DensePass<4, 1, 4, C, NX, NK, NO, OUT, DOT>>(a, st);
     if (a.DK <= 128)
-        return wide ? launch_dense_pass<DensePass<8, 2, 4, C, NX, NK, NO, OUT>>(a, st)
-                    : launch_dense_pass<DensePass<8, 1, 4, C, NX, NK, NO, OUT>>(a, st);
-    return wide ? launch_dense_pass<DensePass<16, 1, 8, C, NX, NK, NO, OUT>>(a, st)
-                : launch_dense_pass<DensePass<16, 1, 4, C, NX, NK, NO, OUT>>(a, st);
+        return wide ? launch_dense_pass<DensePass<8, 1, 8, C, NX, NK, NO, OUT, DOT>>(a, st)
+                    : launch_dense_pass<DensePass<8, 1, 4, C, NX, NK, NO, OUT, DOT>>(a, st);
+    return wide ? launch_dense_pass<DensePass<16, 1, 8, C, NX, NK, NO, OUT, DOT>>(a, st)
+                : launch_dense_pass<DensePass<16, 1, 4, C, NX, NK, NO, OUT, DOT>>(a, st);
 }
 
 }  // namespace
