@@ -43,6 +43,10 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
+// An element offset whose byte offset, in 2- and in 4-byte elements and give or take a
+// chunk's rows, lies beyond every buffer (a buffer holds at most 64 KiB).
+constexpr uint32_t FAR = 0x28000000u;
+
 // two values' planes, packed: a's in the low half
 __device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) {
     const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
@@ -120,18 +124,21 @@ template <int DKT_, int NCT_, int NW_, int C_, int NX_, int NK_, int NO_, bool O
 struct DensePass {
     static constexpr int DKT = DKT_, NCT = NCT_, NW = NW_, C = C_, NX = NX_, NK = NK_, NO = NO_;
     static constexpr bool OUT = OUT_, DOT = DOT_;
+    static constexpr int WITH = NX == 3 && NK == 3 ? 3 : 1;  // planes of `with`: q and k, as the other operands
     static constexpr int DKP = DKT * 16, SV = 16 * NCT * NW, NT = C / 16, THR = NW * 64;
     static constexpr int RK = DKP * 2 + 16, RV = SV * 2 + 16;        // bytes of an LDS row
     static constexpr int PK = C * RK, PV = C * RV;                   // bytes of a plane
     static constexpr int TILES = NT * (NT + 1) / 2;
     static constexpr int O_KA = 0, O_OM = O_KA + NK * PK, O_XI = O_OM + NO * PV, O_P = O_XI + (OUT ? NX * PK : 0),
                          O_F = O_P + (OUT ? TILES * 3 * 512 : 0), LDS = O_F + (4 * C + 2 * NT + NW * C + NW) * 4;
+    // wavefronts per SIMD: two workgroups of 8 on a CU where X takes 32 registers a lane
+    static constexpr int OCC = NW == 8 && DKT <= 8 ? 4 : 2;
     static_assert(NW >= NT, "a diagonal block's decays are formed by its own wavefront");
     static_assert(LDS <= 160 * 1024, "a workgroup's LDS");
 };
 
 template <class P>
-__global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
+__global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a) {
     constexpr int DKT = P::DKT, NCT = P::NCT, C = P::C, NT = P::NT, THR = P::THR, DKP = P::DKP, SV = P::SV, NW = P::NW;
     extern __shared__ __align__(16) char lds[];
     char* const Ka = lds + P::O_KA;
@@ -193,29 +200,55 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
         n = (int)(hi - at < C ? hi - at : C);
     };
     // Rows are read through buffers that begin at the chunk's first token and end behind its
-    // last: a piece beyond it reads zeros, as does one beyond the row's width (offset OOB).
-    // Backwards, row j is the chunk's token n - 1 - j.
+    // last: a piece beyond it reads zeros, as does one beyond the row's width (offset FAR).
+    // Backwards, row j is the chunk's token n - 1 - j; the offsets are those of a full
+    // chunk, less the rows it lacks (negative ones wrap to beyond every buffer).
     auto row = [&](int j, int n) { return a.rev ? n - 1 - j : j; };
     auto rows = [&](const void* p, int64_t t0, int n, int width, uint32_t esz) {
         return make_rsrc(static_cast<const char*>(p) + (row0 + t0) * width * esz, (int64_t)n * width * esz);
     };
+    uint32_t ek[KP], ev[VP], eo[NCT];  // elements into the buffers, or FAR
+#pragma unroll
+    for (int i = 0; i < KP; ++i) {
+        const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
+        ek[i] = q < a.DK ? (uint32_t)(row(j, C) * a.DK + q) : FAR;
+    }
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+        const int e = tid + i * THR, j = e / (SV / 8), q = e % (SV / 8) * 8;
+        ev[i] = j < C && c0 + q < a.DV ? (uint32_t)(row(j, C) * a.DV + c0 + q) : FAR;
+    }
+#pragma unroll
+    for (int c = 0; c < NCT; ++c) eo[c] = col[c] < a.DV ? (uint32_t)(row(4 * g4, C) * a.DV + col[c]) : FAR;
+    const int step = a.rev ? -a.DV : a.DV;  // elements from one row of `out` to the next
+    float wi[P::DOT ? NT * 4 : 1][NCT];     // the next chunk's `with` at this lane's outputs
     auto fetch = [&](int ch) {
         int64_t t0;
         int n;
         span(ch, t0, n);
         const rsrc_t rk = rows(a.kap, t0, n, a.DK, Piece<P::NK>::ESZ), ro = rows(a.omg, t0, n, a.DV, Piece<P::NO>::ESZ);
         const rsrc_t rx = P::OUT ? rows(a.xi, t0, n, a.DK, Piece<P::NX>::ESZ) : rk;
+        const uint32_t lack = a.rev ? (uint32_t)(C - n) : 0u;
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
-            const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
-            const uint32_t at = (uint32_t)(row(j, n) * a.DK + q);
-            pk[i].load(rk, q < a.DK ? at * Piece<P::NK>::ESZ : OOB);
-            if (P::OUT) px[P::OUT ? i : 0].load(rx, q < a.DK ? at * Piece<P::NX>::ESZ : OOB);
+            const uint32_t at = ek[i] - lack * a.DK;
+            pk[i].load(rk, at * Piece<P::NK>::ESZ);
+            if (P::OUT) px[P::OUT ? i : 0].load(rx, at * Piece<P::NX>::ESZ);
         }
 #pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            const int e = tid + i * THR, j = e / (SV / 8), q = e % (SV / 8) * 8;
-            po[i].load(ro, c0 + q < a.DV ? (uint32_t)(row(j, n) * a.DV + c0 + q) * Piece<P::NO>::ESZ : OOB);
+        for (int i = 0; i < VP; ++i) po[i].load(ro, (ev[i] - lack * a.DV) * Piece<P::NO>::ESZ);
+        if constexpr (P::DOT) {
+            const rsrc_t rw = rows(a.with, t0, n, a.DV, P::WITH == 1 ? 2 : 4);
+#pragma unroll
+            for (int t = 0; t < NT * 4; ++t)
+#pragma unroll
+                for (int c = 0; c < NCT; ++c) {
+                    const uint32_t at = eo[c] + ((t >> 2) * 16 + (t & 3)) * step - lack * a.DV;
+                    if constexpr (P::WITH == 1)
+                        wi[t][c] = bf_lo((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rw, (int)(at * 2u), 0, 0));
+                    else
+                        wi[t][c] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, (int)(at * 4u), 0, 0));
+                }
         }
         pg = 1.f;
         pb = 0.f;
@@ -265,6 +298,12 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
             }
         }
         __syncthreads();
+        float wc[P::DOT ? NT * 4 : 1][NCT];
+        if constexpr (P::DOT)
+#pragma unroll
+            for (int t = 0; t < NT * 4; ++t)
+#pragma unroll
+                for (int c = 0; c < NCT; ++c) wc[t][c] = wi[t][c];
         if (ch + 1 < nch) fetch(ch + 1);
         float tot[NT], total = 1.f;
 #pragma unroll
@@ -273,24 +312,6 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
             total *= tot[b];
         }
         f32x4_t acc[P::OUT ? NT : 1][NCT];
-        float wi[P::DOT ? NT * 4 : 1][NCT];  // `with` at this lane's outputs
-        if constexpr (P::DOT) {
-            const uint32_t esz = a.with_bf16 ? 2 : 4;
-            const rsrc_t rw = rows(a.with, t0, n, a.DV, esz);
-#pragma unroll
-            for (int t = 0; t < NT * 4; ++t)
-#pragma unroll
-                for (int c = 0; c < NCT; ++c) {
-                    const int j = (t >> 2) * 16 + 4 * g4 + (t & 3);
-                    const uint32_t at = (uint32_t)(row(j, n) * a.DV + col[c]);
-                    if (a.with_bf16) {
-                        const uint32_t u = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rw, (int)(col[c] < a.DV ? at * 2u : OOB), 0, 0);
-                        wi[t][c] = bf_lo(u);
-                    } else {
-                        wi[t][c] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, (int)(col[c] < a.DV ? at * 4u : OOB), 0, 0));
-                    }
-                }
-        }
         if constexpr (P::OUT) {
             // P^T = kap xi^T, scaled: a tile (s block st, t block tt) by one wavefront, its planes
             // stored as the operand of the product with omg
@@ -373,7 +394,7 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
                         const int j = t * 16 + 4 * g4 + i;
                         float d = 0.f;
 #pragma unroll
-                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wi[t * 4 + i][c], d);
+                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wc[t * 4 + i][c], d);
                         inter = fmaf(d, fo[j], inter);
                     }
                 }
@@ -469,11 +490,11 @@ __global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
                     const float f = fo[j];
 #pragma unroll
                     for (int c = 0; c < NCT; ++c)
-                        st_f1(acc[t][c][i] * f, rout, col[c] < a.DV ? (uint32_t)(row(j, n) * a.DV + col[c]) * 4u : OOB, 0);
+                        st_f1(acc[t][c][i] * f, rout, (eo[c] + (t * 16 + i) * step - (a.rev ? C - n : 0) * a.DV) * 4u, 0);
                     if constexpr (P::DOT) {
                         float d = 0.f;
 #pragma unroll
-                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wi[t * 4 + i][c], d);
+                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wc[t * 4 + i][c], d);
                         d = ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(d))));
                         if (m16 == 0) fdot[w * C + j] = d;
                     }
