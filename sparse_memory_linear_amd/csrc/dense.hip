@@ -24,15 +24,6 @@
 
 namespace sdm {
 
-// the pass for these operands' types
-static hipError_t launch_dense(const DenseArgs& a, bool out, hipStream_t st) {
-    if (!a.kap_bf16 && (!out || !a.xi_bf16) && !a.omg_bf16) return out ? launch_dense_f32(a, st) : launch_dense_f32_state(a, st);
-    if (!out) return a.omg_bf16 ? launch_dense_bf16_state(a, st) : launch_dense_omg32_state(a, st);
-    if (!a.xi_bf16) return launch_dense_xi32(a, st);
-    if (!a.kap_bf16) return launch_dense_kap32(a, st);
-    return a.omg_bf16 ? launch_dense_bf16(a, st) : launch_dense_omg32(a, st);
-}
-
 namespace {
 
 // the running sums of the gates' gradients start anew at segments of at most this many tokens
@@ -70,7 +61,7 @@ __global__ __launch_bounds__(256) void dense_carry_kernel(CarryArgs a) {
 // chunks' own sums, which hold only what crosses their bounds.
 __global__ __launch_bounds__(256) void dense_gates_kernel(DenseGatesArgs a) {
     __shared__ float part[4];
-    __shared__ float diff[BWD_SEGMENT / DENSE_CHUNK_F32], at_end[BWD_SEGMENT / DENSE_CHUNK_F32];
+    __shared__ float diff[BWD_SEGMENT / DENSE_CHUNK], at_end[BWD_SEGMENT / DENSE_CHUNK];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int seg = (int)(blockIdx.x % a.nseg);
     const int64_t s = blockIdx.x / a.nseg;
@@ -130,54 +121,54 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t e) {
 // A few tokens a call (decoding): the state is read and written once, as rows
 // of 64 columns; thread (r, c) holds rows r + 16 i, columns 4c .. 4c + 3.
 template <int NR>
-__global__ __launch_bounds__(256) void dense_step_kernel(DenseArgs a) {
+__global__ __launch_bounds__(256) void dense_step_kernel(DenseFwdArgs a) {
     __shared__ float red[16][STEP_COLS];
     const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
-    const int slab = (int)(blockIdx.x % a.nslab);
-    const int64_t s = blockIdx.x / a.nslab;
+    const int nslab = (a.dv + STEP_COLS - 1) / STEP_COLS, slab = (int)(blockIdx.x % nslab);
+    const int64_t s = blockIdx.x / nslab;
     const int col = slab * STEP_COLS + 4 * c;
-    const bool col_ok = col < a.DV;
-    const int64_t st = s * (int64_t)a.DK * a.DV + col;
+    const bool col_ok = col < a.dv;
+    const int64_t st = s * (int64_t)a.dk * a.dv + col;
     float4 X[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         X[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (a.X0 && col_ok && r + 16 * i < a.DK) X[i] = *reinterpret_cast<const float4*>(a.X0 + st + (int64_t)(r + 16 * i) * a.DV);
+        if (a.S0 && col_ok && r + 16 * i < a.dk) X[i] = *reinterpret_cast<const float4*>(a.S0 + st + (int64_t)(r + 16 * i) * a.dv);
     }
     for (int64_t t = s * a.T; t < (s + 1) * a.T; ++t) {
-        const float g = a.a[t], b = a.b[t];
+        const float g = a.alpha[t], b = a.beta[t];
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f), y = v;
         if (col_ok) {
-            if (a.omg_bf16) {
-                const uint2 p = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.omg) + t * a.DV + col);
+            if (a.bf16) {
+                const uint2 p = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + t * a.dv + col);
                 v = make_float4(b * bf_lo(p.x), b * bf_hi(p.x), b * bf_lo(p.y), b * bf_hi(p.y));
             } else {
-                const float4 p = *reinterpret_cast<const float4*>(static_cast<const float*>(a.omg) + t * a.DV + col);
+                const float4 p = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + t * a.dv + col);
                 v = make_float4(b * p.x, b * p.y, b * p.z, b * p.w);
             }
         }
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            if (r + 16 * i >= a.DK) break;
-            const float k = load1(a.kap, a.kap_bf16, t * a.DK + r + 16 * i);
-            const float q = load1(a.xi, a.xi_bf16, t * a.DK + r + 16 * i);
+            if (r + 16 * i >= a.dk) break;
+            const float k = load1(a.k, a.bf16, t * a.dk + r + 16 * i);
+            const float q = load1(a.q, a.bf16, t * a.dk + r + 16 * i);
             X[i] = make_float4(fmaf(g, X[i].x, k * v.x), fmaf(g, X[i].y, k * v.y), fmaf(g, X[i].z, k * v.z), fmaf(g, X[i].w, k * v.w));
             y = make_float4(fmaf(q, X[i].x, y.x), fmaf(q, X[i].y, y.y), fmaf(q, X[i].z, y.z), fmaf(q, X[i].w, y.w));
         }
         __syncthreads();
         *reinterpret_cast<float4*>(&red[r][4 * c]) = y;
         __syncthreads();
-        if (tid < STEP_COLS && slab * STEP_COLS + tid < a.DV) {
+        if (tid < STEP_COLS && slab * STEP_COLS + tid < a.dv) {
             float o = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) o += red[i][tid];
-            a.out[t * a.DV + slab * STEP_COLS + tid] = o;
+            a.y[t * a.dv + slab * STEP_COLS + tid] = o;
         }
     }
-    if (a.Xend && col_ok)
+    if (a.S && col_ok)
 #pragma unroll
         for (int i = 0; i < NR; ++i)
-            if (r + 16 * i < a.DK) *reinterpret_cast<float4*>(a.Xend + st + (int64_t)(r + 16 * i) * a.DV) = X[i];
+            if (r + 16 * i < a.dk) *reinterpret_cast<float4*>(a.S + st + (int64_t)(r + 16 * i) * a.dv) = X[i];
 }
 
 hipError_t launch_carry(const CarryArgs& a, hipStream_t st) {
@@ -226,7 +217,7 @@ DenseBwdLayout backward_layout(int64_t NS, int64_t T, int dk, int dv) {
     y.decs = (y.nseg * NS * 4 + 255) / 256 * 256;
     y.slabs = (dk + dense_slab(dk) - 1) / dense_slab(dk);
     y.dots = (y.slabs * NS * T * 4 + 255) / 256 * 256;
-    y.nchunk = (T + DENSE_CHUNK_F32 - 1) / DENSE_CHUNK_F32;  // dy is fp32
+    y.nchunk = (T + DENSE_CHUNK - 1) / DENSE_CHUNK;
     y.inter = (y.slabs * NS * y.nchunk * 4 + 255) / 256 * 256;
     y.bytes = 2 * y.states + y.one + y.decs + 2 * y.dots + 2 * y.inter;
     return y;
@@ -241,36 +232,35 @@ int64_t dense_backward_workspace_bytes(int64_t NS, int64_t T, int dk, int dv) {
 
 hipError_t launch_dense_forward(const DenseFwdArgs& f, hipStream_t st) {
     const DenseLayout y = forward_layout(f.NS, f.T, f.dk, f.dv);
-    DenseArgs a{};
-    a.xi = f.q; a.kap = f.k; a.omg = f.v;
-    a.xi_bf16 = a.kap_bf16 = a.omg_bf16 = f.bf16;
-    a.a = f.alpha; a.b = f.beta; a.out = f.y;
-    a.NS = f.NS; a.T = f.T; a.L = y.L; a.nseg = (int)y.nseg;
-    a.DK = f.dk; a.DV = f.dv;
-    a.X0 = f.S0; a.x_row = f.dv; a.x_col = 1;
-    a.Xend = f.S;
     if (f.T <= STEP_TOKENS) {
-        a.nslab = (a.DV + STEP_COLS - 1) / STEP_COLS;
-        const dim3 grid((unsigned)(a.NS * a.nslab));
-        if (a.DK <= 64) hipLaunchKernelGGL(dense_step_kernel<4>, grid, dim3(256), 0, st, a);
-        else if (a.DK <= 128) hipLaunchKernelGGL(dense_step_kernel<8>, grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL(dense_step_kernel<16>, grid, dim3(256), 0, st, a);
+        const dim3 grid((unsigned)(f.NS * ((f.dv + STEP_COLS - 1) / STEP_COLS)));
+        if (f.dk <= 64) hipLaunchKernelGGL(dense_step_kernel<4>, grid, dim3(256), 0, st, f);
+        else if (f.dk <= 128) hipLaunchKernelGGL(dense_step_kernel<8>, grid, dim3(256), 0, st, f);
+        else hipLaunchKernelGGL(dense_step_kernel<16>, grid, dim3(256), 0, st, f);
         return hipGetLastError();
     }
-    if (y.nseg == 1) return launch_dense(a, true, st);
-    char* ws = static_cast<char*>(f.workspace);
-    float* states = reinterpret_cast<float*>(ws);
-    float* decs = reinterpret_cast<float*>(ws + y.states);
-    DenseArgs p = a;
-    p.X0 = nullptr; p.Xend = states; p.segdec = decs;
-    hipError_t e = launch_dense(p, false, st);
-    if (e != hipSuccess) return e;
-    CarryArgs c{};
-    c.ws = states; c.segdec = decs; c.X0 = f.S0; c.Xend = f.S;
-    c.NS = f.NS; c.per = (int64_t)f.dk * f.dv; c.nseg = (int)y.nseg;
-    if ((e = launch_carry(c, st)) != hipSuccess) return e;
-    a.X0 = states; a.X0_seg = true; a.Xend = nullptr;
-    return launch_dense(a, true, st);
+    DenseArgs a{};
+    a.a = f.alpha; a.beta = f.beta;
+    a.NS = f.NS; a.T = f.T; a.L = y.L; a.nseg = (int)y.nseg;
+    a.DK = f.dk; a.DV = f.dv;
+    a.kap = f.k; a.omg = f.v;
+    if (y.nseg > 1) {
+        char* ws = static_cast<char*>(f.workspace);
+        float* states = reinterpret_cast<float*>(ws);
+        DenseArgs p = a;
+        p.Xend = states; p.segdec = reinterpret_cast<float*>(ws + y.states);
+        hipError_t e = f.bf16 ? launch_dense_s(p, st) : launch_dense_s_f32(p, st);
+        if (e != hipSuccess) return e;
+        CarryArgs c{};
+        c.ws = states; c.segdec = p.segdec; c.X0 = f.S0; c.Xend = f.S;
+        c.NS = f.NS; c.per = (int64_t)f.dk * f.dv; c.nseg = (int)y.nseg;
+        if ((e = launch_carry(c, st)) != hipSuccess) return e;
+        a.X0 = states;
+    } else {
+        a.X0 = f.S0; a.Xend = f.S;
+    }
+    a.xi = f.q; a.out = f.y;
+    return f.bf16 ? launch_dense_y(a, st) : launch_dense_y_f32(a, st);
 }
 
 hipError_t launch_dense_pass_on(const float* X0, float* X, int64_t NS, int64_t per, hipStream_t st) {
@@ -294,47 +284,42 @@ hipError_t launch_dense_backward(const DenseBwdArgs& f, hipStream_t st) {
     const int64_t per = (int64_t)f.dk * f.dv;
     hipError_t e;
     DenseArgs base{};
-    base.a = f.alpha; base.NS = f.NS; base.T = f.T; base.L = y.L; base.nseg = (int)y.nseg;
+    base.a = f.alpha; base.beta = f.beta; base.NS = f.NS; base.T = f.T; base.L = y.L; base.nseg = (int)y.nseg;
     CarryArgs c{};
     c.segdec = decs; c.NS = f.NS; c.per = per; c.nseg = (int)y.nseg; c.T = f.T; c.gate = f.alpha;
 
     DenseArgs p = base;  // S at the segments' starts, and after the last
-    p.kap = f.k; p.omg = f.v; p.kap_bf16 = p.omg_bf16 = f.bf16; p.b = f.beta;
-    p.DK = f.dk; p.DV = f.dv; p.Xend = S; p.segdec = decs;
-    if ((e = launch_dense(p, false, st)) != hipSuccess) return e;
+    p.kap = f.k; p.omg = f.v; p.DK = f.dk; p.DV = f.dv; p.Xend = S; p.segdec = decs;
+    if ((e = f.bf16 ? launch_dense_s(p, st) : launch_dense_s_f32(p, st)) != hipSuccess) return e;
     c.ws = S; c.X0 = f.S0; c.Xend = ST;
     if ((e = launch_carry(c, st)) != hipSuccess) return e;
 
     p = base;            // G at the segments' ends, and what flows into S0
-    p.kap = f.q; p.kap_bf16 = f.bf16; p.omg = f.dy; p.rev = true;
-    p.DK = f.dk; p.DV = f.dv; p.Xend = G; p.segdec = decs;
-    if ((e = launch_dense(p, false, st)) != hipSuccess) return e;
+    p.kap = f.q; p.omg = f.dy; p.DK = f.dk; p.DV = f.dv; p.Xend = G; p.segdec = decs;
+    if ((e = f.bf16 ? launch_dense_g(p, st) : launch_dense_g_f32(p, st)) != hipSuccess) return e;
     c.ws = G; c.X0 = f.dS; c.Xend = f.dS0; c.rev = true;
     if ((e = launch_carry(c, st)) != hipSuccess) return e;
 
     p = base;            // dq, and q . dq
-    p.xi = f.dy; p.kap = f.v; p.kap_bf16 = f.bf16; p.omg = f.k; p.omg_bf16 = f.bf16; p.b = f.beta;
-    p.DK = f.dv; p.DV = f.dk; p.X0 = S; p.X0_seg = true; p.x_row = 1; p.x_col = f.dv;
-    p.out = f.dq; p.dot = qdq; p.inter = inter_q; p.with = f.q; p.with_bf16 = f.bf16;
-    if ((e = launch_dense(p, true, st)) != hipSuccess) return e;
+    p.xi = f.dy; p.kap = f.v; p.omg = f.k; p.DK = f.dv; p.DV = f.dk; p.X0 = S;
+    p.out = f.dq; p.dot = qdq; p.inter = inter_q; p.with = f.q;
+    if ((e = f.bf16 ? launch_dense_dq(p, st) : launch_dense_dq_f32(p, st)) != hipSuccess) return e;
 
     p = base;            // dk, and k . dk / beta
-    p.xi = f.v; p.xi_bf16 = f.bf16; p.kap = f.dy; p.omg = f.q; p.omg_bf16 = f.bf16; p.o = f.beta; p.rev = true;
-    p.DK = f.dv; p.DV = f.dk; p.X0 = G; p.X0_seg = true; p.x_row = 1; p.x_col = f.dv;
-    p.out = f.dk_out; p.dot = kdk; p.inter = inter_k; p.with = f.k; p.with_bf16 = f.bf16;
-    if ((e = launch_dense(p, true, st)) != hipSuccess) return e;
+    p.xi = f.v; p.kap = f.dy; p.omg = f.q; p.DK = f.dv; p.DV = f.dk; p.X0 = G;
+    p.out = f.dk_out; p.dot = kdk; p.inter = inter_k; p.with = f.k;
+    if ((e = f.bf16 ? launch_dense_dk(p, st) : launch_dense_dk_f32(p, st)) != hipSuccess) return e;
 
     p = base;            // dv
-    p.xi = f.k; p.xi_bf16 = f.bf16; p.kap = f.q; p.kap_bf16 = f.bf16; p.omg = f.dy; p.o = f.beta; p.rev = true;
-    p.DK = f.dk; p.DV = f.dv; p.X0 = G; p.X0_seg = true; p.x_row = f.dv; p.x_col = 1;
+    p.xi = f.k; p.kap = f.q; p.omg = f.dy; p.DK = f.dk; p.DV = f.dv; p.X0 = G;
     p.out = f.dv_out;
-    if ((e = launch_dense(p, true, st)) != hipSuccess) return e;
+    if ((e = f.bf16 ? launch_dense_dv(p, st) : launch_dense_dv_f32(p, st)) != hipSuccess) return e;
 
     DenseGatesArgs g{};
     g.G = G; g.S = S; g.ST = ST; g.qdq = qdq; g.kdk = kdk; g.alpha = f.alpha; g.beta = f.beta;
     g.dlog_alpha = f.dlog_alpha; g.dbeta = f.dbeta; g.has_dS = f.dS != nullptr;
     g.NS = f.NS; g.T = f.T; g.L = y.L; g.per = per; g.nseg = (int)y.nseg;
-    g.inter_q = inter_q; g.inter_k = inter_k; g.nchunk = y.nchunk; g.C = DENSE_CHUNK_F32; g.nslab = y.slabs;
+    g.inter_q = inter_q; g.inter_k = inter_k; g.nchunk = y.nchunk; g.C = DENSE_CHUNK; g.nslab = y.slabs;
     hipLaunchKernelGGL(dense_gates_kernel, dim3((unsigned)(f.NS * y.nseg)), dim3(256), 0, st, g);
     return hipGetLastError();
 }

@@ -4,7 +4,7 @@
 //   X_u = a_u X_{u-1} + b_u kap_u (x) omg_u,    out_u = o_u xi_u X_u
 //
 // A workgroup carries SV = 16 NCT NW columns of X in registers over a segment's
-// tokens, C at a time; a wavefront owns 16 NCT of them. Within a chunk, with
+// tokens, C = 32 at a time; a wavefront owns 16 NCT of them. Within a chunk, with
 // D_ts = a_{s+1} .. a_t,
 //   out = o (pre X_start + (tril(xi kap^T) . D . b) omg),   pre_t = a_c0 .. a_t
 //   X_end = total X_start + sum_s kap_s (x) (D_end,s b_s omg_s).
@@ -118,22 +118,31 @@ __device__ __forceinline__ uint2 read_tr(const char* p) {
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)p));
 }
 
-// NX, NK, NO: planes of xi, kap and omg (1: bf16 in memory, 3: fp32)
-// OUT: outputs (else only the segment's own state, from zero); DOT: also their products with `with`
-template <int DKT_, int NCT_, int NW_, int C_, int NX_, int NK_, int NO_, bool OUT_, bool DOT_>
+// NX, NK, NO: planes of xi, kap and omg (1: bf16 in memory, 3: fp32).
+// OUT: outputs (else only the segment's own state, from zero). REV: from the last
+// token to the first, with a_u = alpha_{t+1}, b = 1, o = beta (else alpha_t, beta, 1).
+// DOT: also the outputs' products with the rows `with`, and the starting states are
+// taken transposed (the gradients over the value rows: dq and dk).
+template <int DKT_, int NCT_, int NW_, int NX_, int NK_, int NO_, bool OUT_, bool REV_, bool DOT_>
 struct DensePass {
-    static constexpr int DKT = DKT_, NCT = NCT_, NW = NW_, C = C_, NX = NX_, NK = NK_, NO = NO_;
-    static constexpr bool OUT = OUT_, DOT = DOT_;
-    static constexpr int WITH = NX == 3 && NK == 3 ? 3 : 1;  // planes of `with`: q and k, as the other operands
+    static constexpr int DKT = DKT_, NCT = NCT_, NW = NW_, C = DENSE_CHUNK, NX = NX_, NK = NK_, NO = NO_;
+    static constexpr bool OUT = OUT_, REV = REV_, DOT = DOT_;
+    static constexpr int WITH = NX == 3 && NK == 3 ? 4 : 2;          // bytes of `with`: q and k, as the other rows
     static constexpr int DKP = DKT * 16, SV = 16 * NCT * NW, NT = C / 16, THR = NW * 64;
     static constexpr int RK = DKP * 2 + 16, RV = SV * 2 + 16;        // bytes of an LDS row
     static constexpr int PK = C * RK, PV = C * RV;                   // bytes of a plane
     static constexpr int TILES = NT * (NT + 1) / 2;
-    static constexpr int O_KA = 0, O_OM = O_KA + NK * PK, O_XI = O_OM + NO * PV, O_P = O_XI + (OUT ? NX * PK : 0),
-                         O_F = O_P + (OUT ? TILES * 3 * 512 : 0), LDS = O_F + (4 * C + 2 * NT + NW * C + NW) * 4;
+    static constexpr int O_KA = 0, O_OM = O_KA + NK * PK, O_XI = O_OM + NO * PV, ROWS = O_XI + (OUT ? NX * PK : 0);
+    // floats: two sets of a chunk's decays, outputs' products, their sums
+    static constexpr int DEC = 4 * C + 2 * NT, FLOATS = 2 * DEC + (DOT ? 2 * NW * (C + 1) : 0);
+    static constexpr int PBYTES = OUT ? TILES * 3 * 512 : 0;
+    // the rows twice (the next chunk's are stored while this one's are read), unless that
+    // keeps a second workgroup off the CU
+    static constexpr int BUF = 2 * ROWS + PBYTES + FLOATS * 4 <= 80 * 1024 ? 2 : 1;
+    static constexpr int O_P = BUF * ROWS, O_F = O_P + PBYTES, LDS = O_F + FLOATS * 4;
     // wavefronts per SIMD: two workgroups of 8 on a CU where X takes 32 registers a lane
     static constexpr int OCC = NW == 8 && DKT <= 8 ? 4 : 2;
-    static_assert(NW >= NT, "a diagonal block's decays are formed by its own wavefront");
+    static_assert(NT == 2, "tiles of P are numbered for 2 blocks");
     static_assert(LDS <= 160 * 1024, "a workgroup's LDS");
 };
 
@@ -141,17 +150,9 @@ template <class P>
 __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a) {
     constexpr int DKT = P::DKT, NCT = P::NCT, C = P::C, NT = P::NT, THR = P::THR, DKP = P::DKP, SV = P::SV, NW = P::NW;
     extern __shared__ __align__(16) char lds[];
-    char* const Ka = lds + P::O_KA;
-    char* const Om = lds + P::O_OM;
-    char* const Xi = lds + P::O_XI;
     char* const Pf = lds + P::O_P;
-    float* const fpre = reinterpret_cast<float*>(lds + P::O_F);  // gates from the block's start through t
-    float* const fsuf = fpre + C;                                // gates after s through the block's end
-    float* const fin = fsuf + C;                                 // b_s
-    float* const fo = fin + C;                                   // o_t
-    float* const ftot = fo + C;                                  // a block's gates
-    float* const fdot = ftot + 2 * NT;                           // [NW][C]
-    float* const fsum = fdot + NW * C;                           // [NW]
+    float* const dec = reinterpret_cast<float*>(lds + P::O_F);
+    float* const dots = dec + 2 * P::DEC;  // [2][NW][C + 1]: per wavefront, the rows' products, and their part from X_start
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), m16 = lane & 15, g4 = lane >> 4;
     int64_t us;
     int slab;
@@ -161,8 +162,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
     const int seg = (int)(us % a.nseg);
     const int64_t lo = (int64_t)seg * a.L, hi = lo + a.L < a.T ? lo + a.L : a.T;
     const int c0 = slab * SV;
-    const int64_t row0 = s * a.T, per = (int64_t)a.DK * a.DV;
-    const int64_t st_seg = (seg * a.NS + s) * per, st_one = s * per;
+    const int64_t row0 = s * a.T, state = (seg * a.NS + s) * (int64_t)a.DK * a.DV;
     int col[NCT];
 #pragma unroll
     for (int n = 0; n < NCT; ++n) col[n] = c0 + (w * NCT + n) * 16 + m16;
@@ -176,13 +176,12 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
             X[k][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
             const int r = 32 * (k >> 1) + 8 * g4 + 4 * (k & 1);
             if (P::OUT && a.X0 && r < a.DK && col[n] < a.DV) {  // DK a multiple of 8: 4 rows at once
-                const float* x = a.X0 + (a.X0_seg ? st_seg : st_one) + r * (int64_t)a.x_row + col[n] * (int64_t)a.x_col;
-                if (a.x_row == 1) {
-                    const float4 v = *reinterpret_cast<const float4*>(x);
+                if (P::DOT) {
+                    const float4 v = *reinterpret_cast<const float4*>(a.X0 + state + (int64_t)col[n] * a.DK + r);
                     X[k][n] = f32x4_t{v.x, v.y, v.z, v.w};
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) X[k][n][i] = x[i * (int64_t)a.x_row];
+                    for (int i = 0; i < 4; ++i) X[k][n][i] = a.X0[state + (int64_t)(r + i) * a.DV + col[n]];
                 }
             }
         }
@@ -192,18 +191,17 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
     Piece<P::NK> pk[KP];
     Piece<P::NX> px[P::OUT ? KP : 1];
     Piece<P::NO> po[VP];
-    float pg = 1.f, pb = 0.f, po_ = 1.f;
+    float pg = 1.f, pb = 0.f;
     const int nch = (int)((hi - lo + C - 1) / C);
     auto span = [&](int ch, int64_t& t0, int& n) {  // the chunk's first token and length, in processing order
-        const int64_t at = lo + (int64_t)(a.rev ? nch - 1 - ch : ch) * C;
-        t0 = at;
-        n = (int)(hi - at < C ? hi - at : C);
+        t0 = lo + (int64_t)(P::REV ? nch - 1 - ch : ch) * C;
+        n = (int)(hi - t0 < C ? hi - t0 : C);
     };
     // Rows are read through buffers that begin at the chunk's first token and end behind its
     // last: a piece beyond it reads zeros, as does one beyond the row's width (offset FAR).
     // Backwards, row j is the chunk's token n - 1 - j; the offsets are those of a full
     // chunk, less the rows it lacks (negative ones wrap to beyond every buffer).
-    auto row = [&](int j, int n) { return a.rev ? n - 1 - j : j; };
+    auto row = [&](int j, int n) { return P::REV ? n - 1 - j : j; };
     auto rows = [&](const void* p, int64_t t0, int n, int width, uint32_t esz) {
         return make_rsrc(static_cast<const char*>(p) + (row0 + t0) * width * esz, (int64_t)n * width * esz);
     };
@@ -220,31 +218,31 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
     }
 #pragma unroll
     for (int c = 0; c < NCT; ++c) eo[c] = col[c] < a.DV ? (uint32_t)(row(4 * g4, C) * a.DV + col[c]) : FAR;
-    const int step = a.rev ? -a.DV : a.DV;  // elements from one row of `out` to the next
-    float wi[P::DOT ? NT * 4 : 1][NCT];     // the next chunk's `with` at this lane's outputs
+    const int step = P::REV ? -a.DV : a.DV;  // elements from one row of `out` to the next
+    float wi[P::DOT ? NT * 4 : 1][NCT], wc[P::DOT ? NT * 4 : 1][NCT];  // `with` at this lane's outputs: fetched, and this chunk's
     auto fetch = [&](int ch) {
         int64_t t0;
         int n;
         span(ch, t0, n);
         const rsrc_t rk = rows(a.kap, t0, n, a.DK, Piece<P::NK>::ESZ), ro = rows(a.omg, t0, n, a.DV, Piece<P::NO>::ESZ);
-        const rsrc_t rx = P::OUT ? rows(a.xi, t0, n, a.DK, Piece<P::NX>::ESZ) : rk;
-        const uint32_t lack = a.rev ? (uint32_t)(C - n) : 0u;
+        const uint32_t lack = P::REV ? (uint32_t)(C - n) : 0u;
 #pragma unroll
-        for (int i = 0; i < KP; ++i) {
-            const uint32_t at = ek[i] - lack * a.DK;
-            pk[i].load(rk, at * Piece<P::NK>::ESZ);
-            if (P::OUT) px[P::OUT ? i : 0].load(rx, at * Piece<P::NX>::ESZ);
+        for (int i = 0; i < KP; ++i) pk[i].load(rk, (ek[i] - lack * a.DK) * Piece<P::NK>::ESZ);
+        if constexpr (P::OUT) {
+            const rsrc_t rx = rows(a.xi, t0, n, a.DK, Piece<P::NX>::ESZ);
+#pragma unroll
+            for (int i = 0; i < KP; ++i) px[i].load(rx, (ek[i] - lack * a.DK) * Piece<P::NX>::ESZ);
         }
 #pragma unroll
         for (int i = 0; i < VP; ++i) po[i].load(ro, (ev[i] - lack * a.DV) * Piece<P::NO>::ESZ);
         if constexpr (P::DOT) {
-            const rsrc_t rw = rows(a.with, t0, n, a.DV, P::WITH == 1 ? 2 : 4);
+            const rsrc_t rw = rows(a.with, t0, n, a.DV, P::WITH);
 #pragma unroll
             for (int t = 0; t < NT * 4; ++t)
 #pragma unroll
                 for (int c = 0; c < NCT; ++c) {
                     const uint32_t at = eo[c] + ((t >> 2) * 16 + (t & 3)) * step - lack * a.DV;
-                    if constexpr (P::WITH == 1)
+                    if constexpr (P::WITH == 2)
                         wi[t][c] = bf_lo((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rw, (int)(at * 2u), 0, 0));
                     else
                         wi[t][c] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, (int)(at * 4u), 0, 0));
@@ -255,32 +253,34 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
         const int j = w * 16 + m16;
         if (w < NT && j < n) {
             const int64_t t = t0 + row(j, n);
-            if (!a.rev) pg = a.a[row0 + t];
+            if (!P::REV) pg = a.a[row0 + t];
             else if (t + 1 < a.T) pg = a.a[row0 + t + 1];
-            pb = a.b ? a.b[row0 + t] : 1.f;
-            po_ = a.o ? a.o[row0 + t] : 1.f;
+            if (!P::REV || P::OUT) pb = a.beta[row0 + t];
         }
     };
-    fetch(0);
-    float segdec = 1.f;
-    for (int ch = 0; ch < nch; ++ch) {
-        int64_t t0;
-        int n;
-        span(ch, t0, n);
-        __syncthreads();
+    float dg[4] = {0.f, 0.f, 0.f, 0.f};  // D_ts of diagonal block w: t = m16, s = 4 g4 + i
+    // A chunk's decays, in set ch & 1: gates from the block's start through t, gates after s through its
+    // end, b_s, o_t, the blocks' gates
+    auto put = [&](int ch) {
+        char* const buf = lds + (P::BUF == 2 && (ch & 1) ? P::ROWS : 0);
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
             const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
-            pk[i].store(Ka + j * P::RK + q * 2, P::PK);
-            if constexpr (P::OUT) px[i].store(Xi + j * P::RK + q * 2, P::PK);
+            pk[i].store(buf + P::O_KA + j * P::RK + q * 2, P::PK);
+            if constexpr (P::OUT) px[i].store(buf + P::O_XI + j * P::RK + q * 2, P::PK);
         }
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
             const int e = tid + i * THR, j = e / (SV / 8), q = e % (SV / 8) * 8;
-            if (C * (SV / 8) % THR == 0 || j < C) po[i].store(Om + j * P::RV + q * 2, P::PV);
+            if (C * (SV / 8) % THR == 0 || j < C) po[i].store(buf + P::O_OM + j * P::RV + q * 2, P::PV);
         }
-        float dg[4] = {0.f, 0.f, 0.f, 0.f};  // D_ts of block w: t = m16, s = 4 g4 + i
+        if constexpr (P::DOT)
+#pragma unroll
+            for (int t = 0; t < NT * 4; ++t)
+#pragma unroll
+                for (int c = 0; c < NCT; ++c) wc[t][c] = wi[t][c];
         if (w < NT) {
+            float* const d = dec + (ch & 1) * P::DEC;
             float p = 1.f, q = 1.f;
 #pragma unroll
             for (int r = 15; r >= 0; --r) {
@@ -289,69 +289,85 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
                 p *= r <= m16 ? gr : 1.f;
                 q *= r > m16 ? gr : 1.f;
             }
+            int64_t t0;
+            int n;
+            span(ch, t0, n);
             if (lane < 16) {
-                fpre[w * 16 + lane] = p;
-                fsuf[w * 16 + lane] = q;
-                fin[w * 16 + lane] = pb;
-                fo[w * 16 + lane] = po_;
-                if (lane == 15) ftot[w] = p;
+                const int j = w * 16 + lane;
+                d[j] = p;
+                d[C + j] = q;
+                d[2 * C + j] = P::REV ? (j < n ? 1.f : 0.f) : pb;
+                d[3 * C + j] = P::REV ? pb : 1.f;
+                if (lane == 15) d[4 * C + w] = p;
             }
         }
-        __syncthreads();
-        float wc[P::DOT ? NT * 4 : 1][NCT];
-        if constexpr (P::DOT)
+    };
+    auto flush_dots = [&](int ch) {
+        int64_t t0;
+        int n;
+        span(ch, t0, n);
+        if (tid > C || (tid < C && tid >= n)) return;  // thread C: the sum of what the chunk's start gave
+        const float* const f = dots + (ch & 1) * NW * (C + 1) + tid;
+        float d = 0.f;
 #pragma unroll
-            for (int t = 0; t < NT * 4; ++t)
-#pragma unroll
-                for (int c = 0; c < NCT; ++c) wc[t][c] = wi[t][c];
-        if (ch + 1 < nch) fetch(ch + 1);
-        float tot[NT], total = 1.f;
-#pragma unroll
-        for (int b = 0; b < NT; ++b) {
-            tot[b] = ftot[b];
-            total *= tot[b];
-        }
+        for (int i = 0; i < NW; ++i) d += f[i * (C + 1)];
+        const int64_t u = (int64_t)slab * a.NS + s;
+        if (tid < C) a.dot[u * a.T + t0 + row(tid, n)] = d;
+        else a.inter[u * a.nchunk + t0 / C] = d;
+    };
+
+    fetch(0);
+    put(0);
+    if (nch > 1) fetch(1);
+    __syncthreads();
+    float segdec = 1.f;
+    for (int ch = 0; ch < nch; ++ch) {
+        const char* const buf = lds + (P::BUF == 2 && (ch & 1) ? P::ROWS : 0);
+        const char* const Ka = buf + P::O_KA;
+        const char* const Om = buf + P::O_OM;
+        const char* const Xi = buf + P::O_XI;
+        const float* const fpre = dec + (ch & 1) * P::DEC;
+        const float* const fsuf = fpre + C;
+        const float* const fin = fsuf + C;
+        const float* const fo = fin + C;
+        const float tot0 = fo[C], tot1 = fo[C + 1], total = tot0 * tot1;
         f32x4_t acc[P::OUT ? NT : 1][NCT];
         if constexpr (P::OUT) {
-            // P^T = kap xi^T, scaled: a tile (s block st, t block tt) by one wavefront, its planes
-            // stored as the operand of the product with omg
+            // P^T = kap xi^T, scaled: a tile (s block st, t block tt) a wavefront, its planes stored as
+            // the operand of the product with omg (wavefront b takes diagonal tile b, whose decays it has)
+            if (w < P::TILES) {
+                const int tt = w == 0 ? 0 : 1, st = w == 1 ? 1 : 0;
+                f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+                const char* const kr = Ka + (st * 16 + m16) * P::RK + g4 * 16;
+                const char* const xr = Xi + (tt * 16 + m16) * P::RK + g4 * 16;
 #pragma unroll
-            for (int tt = 0; tt < NT; ++tt)
+                for (int k2 = 0; k2 < DKP * 2; k2 += 64) {
+                    uint4 ka[P::NK], xb[P::NX];
 #pragma unroll
-                for (int st = 0; st <= tt; ++st) {
-                    const int owner = st == tt ? tt : (NT + tt * (tt - 1) / 2 + st) % NW;
-                    if (w != owner) continue;
-                    f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+                    for (int i = 0; i < P::NK; ++i) ka[i] = *reinterpret_cast<const uint4*>(kr + i * P::PK + k2);
 #pragma unroll
-                    for (int k = 0; k < DKP; k += 32) {
-                        uint4 ka[P::NK], xb[P::NX];
-#pragma unroll
-                        for (int i = 0; i < P::NK; ++i)
-                            ka[i] = *reinterpret_cast<const uint4*>(Ka + i * P::PK + (st * 16 + m16) * P::RK + k * 2 + g4 * 16);
-#pragma unroll
-                        for (int i = 0; i < P::NX; ++i)
-                            xb[i] = *reinterpret_cast<const uint4*>(Xi + i * P::PK + (tt * 16 + m16) * P::RK + k * 2 + g4 * 16);
-                        mma<P::NK, P::NX>(ka, xb, p);
-                    }
-                    const float4 in = *reinterpret_cast<const float4*>(fin + st * 16 + 4 * g4);
-                    float f[4] = {in.x, in.y, in.z, in.w};
-                    if (st == tt) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) f[i] *= dg[i];
-                    } else {
-                        const float4 sf = *reinterpret_cast<const float4*>(fsuf + st * 16 + 4 * g4);
-                        float pr = fpre[tt * 16 + m16];
-#pragma unroll
-                        for (int b = st + 1; b < tt; ++b) pr *= tot[b];
-                        f[0] *= sf.x * pr; f[1] *= sf.y * pr; f[2] *= sf.z * pr; f[3] *= sf.w * pr;
-                    }
-                    uint2 o[3];
-                    split2(p[0] * f[0], p[1] * f[1], o[0].x, o[1].x, o[2].x);
-                    split2(p[2] * f[2], p[3] * f[3], o[0].y, o[1].y, o[2].y);
-#pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        *reinterpret_cast<uint2*>(Pf + ((tt * (tt + 1) / 2 + st) * 3 + i) * 512 + lane * 8) = o[i];
+                    for (int i = 0; i < P::NX; ++i) xb[i] = *reinterpret_cast<const uint4*>(xr + i * P::PK + k2);
+                    mma<P::NK, P::NX>(ka, xb, p);
                 }
+                const float4 in = *reinterpret_cast<const float4*>(fin + st * 16 + 4 * g4);
+                float f[4] = {in.x, in.y, in.z, in.w};
+                if (w < NT) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] *= dg[i];
+                } else {
+                    const float4 sf = *reinterpret_cast<const float4*>(fsuf + st * 16 + 4 * g4);
+                    const float pr = fpre[tt * 16 + m16];
+                    f[0] *= sf.x * pr; f[1] *= sf.y * pr; f[2] *= sf.z * pr; f[3] *= sf.w * pr;
+                }
+                uint2 o[3];
+                split2(p[0] * f[0], p[1] * f[1], o[0].x, o[1].x, o[2].x);
+                split2(p[2] * f[2], p[3] * f[3], o[0].y, o[1].y, o[2].y);
+                char* const to = Pf + (tt + st) * 3 * 512 + lane * 8;  // tiles (0,0), (1,0), (1,1)
+#pragma unroll
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(to + i * 512) = o[i];
+            }
+            if constexpr (P::DOT)
+                if (ch > 0) flush_dots(ch - 1);
             // xi X_start
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -380,9 +396,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const float4 pr = *reinterpret_cast<const float4*>(fpre + t * 16 + 4 * g4);
-                float q = 1.f;
-#pragma unroll
-                for (int b = 0; b < t; ++b) q *= tot[b];
+                const float q = t ? tot0 : 1.f;
                 const float f[4] = {pr.x * q, pr.y * q, pr.z * q, pr.w * q};
 #pragma unroll
                 for (int c = 0; c < NCT; ++c)
@@ -391,17 +405,16 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
                 if constexpr (P::DOT) {  // what the chunk's start gives to xi_t X_t . with_t, summed over the chunk
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int j = t * 16 + 4 * g4 + i;
                         float d = 0.f;
 #pragma unroll
                         for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wc[t * 4 + i][c], d);
-                        inter = fmaf(d, fo[j], inter);
+                        inter = fmaf(d, fo[t * 16 + 4 * g4 + i], inter);
                     }
                 }
             }
             if constexpr (P::DOT) {
                 inter = wave_sum(inter);
-                if (lane == 0) fsum[w] = inter;
+                if (lane == 0) dots[((ch & 1) * NW + w) * (C + 1) + C] = inter;
             }
             __syncthreads();
         }
@@ -409,115 +422,105 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
         for (int k = 0; k < DKT; ++k)
 #pragma unroll
             for (int c = 0; c < NCT; ++c) X[k][c] *= total;
-        // over the tokens, two blocks of 16 at a time
+        // over the tokens
+        uint4 om[NCT][P::NO], ow[NCT][3];
+        float f[8];
 #pragma unroll
-        for (int b = 0; b < NT; b += 2) {
-            uint4 om[NCT][P::NO], ow[NCT][3];
-            float f[8];
+        for (int h = 0; h < 2; ++h) {
+            const float4 sf = *reinterpret_cast<const float4*>(fsuf + h * 16 + 4 * g4);
+            const float4 in = *reinterpret_cast<const float4*>(fin + h * 16 + 4 * g4);
+            const float q = h ? 1.f : tot1;
+            f[4 * h] = sf.x * in.x * q; f[4 * h + 1] = sf.y * in.y * q;
+            f[4 * h + 2] = sf.z * in.z * q; f[4 * h + 3] = sf.w * in.w * q;
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 sf = *reinterpret_cast<const float4*>(fsuf + (b + h) * 16 + 4 * g4);
-                const float4 in = *reinterpret_cast<const float4*>(fin + (b + h) * 16 + 4 * g4);
-                float q = 1.f;
+        for (int c = 0; c < NCT; ++c) {
 #pragma unroll
-                for (int e = b + h + 1; e < NT; ++e) q *= tot[e];
-                f[4 * h] = sf.x * in.x * q; f[4 * h + 1] = sf.y * in.y * q;
-                f[4 * h + 2] = sf.z * in.z * q; f[4 * h + 3] = sf.w * in.w * q;
+            for (int i = 0; i < P::NO; ++i) {
+                const char* o = Om + i * P::PV + (4 * g4 + (m16 >> 2)) * P::RV + ((w * NCT + c) * 16 + (m16 & 3) * 4) * 2;
+                const uint2 x = read_tr(o), y = read_tr(o + 16 * P::RV);
+                om[c][i] = make_uint4(x.x, x.y, y.x, y.y);
             }
+            const uint32_t u[4] = {om[c][0].x, om[c][0].y, om[c][0].z, om[c][0].w};
+            float v[8];
 #pragma unroll
-            for (int c = 0; c < NCT; ++c) {
-#pragma unroll
-                for (int i = 0; i < P::NO; ++i) {
-                    const char* o = Om + i * P::PV + (b * 16 + 4 * g4 + (m16 >> 2)) * P::RV + ((w * NCT + c) * 16 + (m16 & 3) * 4) * 2;
-                    const uint2 x = read_tr(o), y = read_tr(o + 16 * P::RV);
-                    om[c][i] = make_uint4(x.x, x.y, y.x, y.y);
-                }
-                const uint32_t u[4] = {om[c][0].x, om[c][0].y, om[c][0].z, om[c][0].w};
-                float v[8];
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bf_lo(u[i]);
+                v[2 * i + 1] = bf_hi(u[i]);
+            }
+            if constexpr (P::NO == 3) {  // the planes' sum is the value
+                const uint32_t m[4] = {om[c][1].x, om[c][1].y, om[c][1].z, om[c][1].w};
+                const uint32_t l[4] = {om[c][2].x, om[c][2].y, om[c][2].z, om[c][2].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[2 * i] = bf_lo(u[i]);
-                    v[2 * i + 1] = bf_hi(u[i]);
-                }
-                if constexpr (P::NO == 3) {  // the planes' sum is the value
-                    const uint32_t m[4] = {om[c][1].x, om[c][1].y, om[c][1].z, om[c][1].w};
-                    const uint32_t l[4] = {om[c][2].x, om[c][2].y, om[c][2].z, om[c][2].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[2 * i] += bf_lo(m[i]) + bf_lo(l[i]);
-                        v[2 * i + 1] += bf_hi(m[i]) + bf_hi(l[i]);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= f[i];
-                split8(v, ow[c]);
-            }
-            if constexpr (P::OUT) {
-#pragma unroll
-                for (int t = b; t < NT; ++t) {
-                    uint4 pa[3];
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const char* p = Pf + ((t * (t + 1) / 2 + b) * 3 + i) * 512 + lane * 8;
-                        const uint2 x = *reinterpret_cast<const uint2*>(p);
-                        const uint2 y = b < t ? *reinterpret_cast<const uint2*>(p + 3 * 512) : make_uint2(0u, 0u);
-                        pa[i] = make_uint4(x.x, x.y, y.x, y.y);
-                    }
-#pragma unroll
-                    for (int c = 0; c < NCT; ++c) mma<3, P::NO>(pa, om[c], acc[t][c]);
+                    v[2 * i] += bf_lo(m[i]) + bf_lo(l[i]);
+                    v[2 * i + 1] += bf_hi(m[i]) + bf_hi(l[i]);
                 }
             }
 #pragma unroll
-            for (int k = 0; k < DKT; ++k) {
-                uint4 ka[P::NK];
-#pragma unroll
-                for (int i = 0; i < P::NK; ++i) {
-                    const char* o = Ka + i * P::PK + (b * 16 + 4 * g4 + (m16 >> 2)) * P::RK + (32 * (k >> 1) + 8 * (m16 & 3) + 4 * (k & 1)) * 2;
-                    const uint2 x = read_tr(o), y = read_tr(o + 16 * P::RK);
-                    ka[i] = make_uint4(x.x, x.y, y.x, y.y);
-                }
-#pragma unroll
-                for (int c = 0; c < NCT; ++c) mma<P::NK, 3>(ka, ow[c], X[k][c]);
-            }
+            for (int i = 0; i < 8; ++i) v[i] *= f[i];
+            split8(v, ow[c]);
         }
         if constexpr (P::OUT) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                uint4 pa[3];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const char* p = Pf + (t * 3 + i) * 512 + lane * 8;
+                    const uint2 x = *reinterpret_cast<const uint2*>(p);
+                    const uint2 y = t ? *reinterpret_cast<const uint2*>(p + 3 * 512) : make_uint2(0u, 0u);
+                    pa[i] = make_uint4(x.x, x.y, y.x, y.y);
+                }
+#pragma unroll
+                for (int c = 0; c < NCT; ++c) mma<3, P::NO>(pa, om[c], acc[t][c]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < DKT; ++k) {
+            uint4 ka[P::NK];
+#pragma unroll
+            for (int i = 0; i < P::NK; ++i) {
+                const char* o = Ka + i * P::PK + (4 * g4 + (m16 >> 2)) * P::RK + (32 * (k >> 1) + 8 * (m16 & 3) + 4 * (k & 1)) * 2;
+                const uint2 x = read_tr(o), y = read_tr(o + 16 * P::RK);
+                ka[i] = make_uint4(x.x, x.y, y.x, y.y);
+            }
+#pragma unroll
+            for (int c = 0; c < NCT; ++c) mma<P::NK, 3>(ka, ow[c], X[k][c]);
+        }
+        if constexpr (P::OUT) {
+            int64_t t0;
+            int n;
+            span(ch, t0, n);
             const rsrc_t rout = rows(a.out, t0, n, a.DV, 4);
+            const int lack = P::REV ? (C - n) * a.DV : 0;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = t * 16 + 4 * g4 + i;
-                    const float f = fo[j];
 #pragma unroll
                     for (int c = 0; c < NCT; ++c)
-                        st_f1(acc[t][c][i] * f, rout, (eo[c] + (t * 16 + i) * step - (a.rev ? C - n : 0) * a.DV) * 4u, 0);
+                        st_f1(P::REV ? acc[t][c][i] * fo[j] : acc[t][c][i], rout, (eo[c] + (t * 16 + i) * step - lack) * 4u, 0);
                     if constexpr (P::DOT) {
                         float d = 0.f;
 #pragma unroll
                         for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wc[t * 4 + i][c], d);
                         d = ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(d))));
-                        if (m16 == 0) fdot[w * C + j] = d;
+                        if (m16 == 0) dots[((ch & 1) * NW + w) * (C + 1) + j] = d;
                     }
                 }
-            if constexpr (P::DOT) {
-                __syncthreads();
-                if (tid < n) {
-                    float d = 0.f;
-#pragma unroll
-                    for (int i = 0; i < NW; ++i) d += fdot[i * C + tid];
-                    a.dot[((int64_t)slab * a.NS + s) * a.T + t0 + row(tid, n)] = d;
-                }
-                if (tid == 0) {
-                    float d = 0.f;
-#pragma unroll
-                    for (int i = 0; i < NW; ++i) d += fsum[i];
-                    a.inter[((int64_t)slab * a.NS + s) * a.nchunk + t0 / C] = d;
-                }
-            }
         } else {
             segdec *= total;
         }
+        if (ch + 1 < nch) {
+            if (P::BUF == 1) __syncthreads();
+            put(ch + 1);
+            if (ch + 2 < nch) fetch(ch + 2);
+        }
+        __syncthreads();
     }
+    if constexpr (P::DOT) flush_dots(nch - 1);
     if (a.Xend) {
 #pragma unroll
         for (int k = 0; k < DKT; ++k)
@@ -526,7 +529,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = 32 * (k >> 1) + 8 * g4 + 4 * (k & 1) + i;
-                    if (r < a.DK && col[c] < a.DV) a.Xend[(P::OUT ? st_one : st_seg) + r * (int64_t)a.DV + col[c]] = X[k][c][i];
+                    if (r < a.DK && col[c] < a.DV) a.Xend[state + r * (int64_t)a.DV + col[c]] = X[k][c][i];
                 }
     }
     if (!P::OUT && slab == 0 && tid == 0) a.segdec[seg * a.NS + s] = segdec;
@@ -544,17 +547,17 @@ hipError_t launch_dense_pass(DenseArgs a, hipStream_t st) {
 // the contracted width are then done once for all of them).
 constexpr int dense_slab(int dv) { return dv <= 64 ? 64 : 128; }
 
-template <int C, int NX, int NK, int NO, bool OUT, bool DOT>
+template <int NX, int NK, int NO, bool OUT, bool REV, bool DOT>
 hipError_t launch_dense_sized(const DenseArgs& a, hipStream_t st) {
     const bool wide = dense_slab(a.DV) == 128;
     if (a.DK <= 64)
-        return wide ? launch_dense_pass<DensePass<4, 2, 4, C, NX, NK, NO, OUT, DOT>>(a, st)
-                    : launch_dense_pass<DensePass<4, 1, 4, C, NX, NK, NO, OUT, DOT>>(a, st);
+        return wide ? launch_dense_pass<DensePass<4, 2, 4, NX, NK, NO, OUT, REV, DOT>>(a, st)
+                    : launch_dense_pass<DensePass<4, 1, 4, NX, NK, NO, OUT, REV, DOT>>(a, st);
     if (a.DK <= 128)
-        return wide ? launch_dense_pass<DensePass<8, 1, 8, C, NX, NK, NO, OUT, DOT>>(a, st)
-                    : launch_dense_pass<DensePass<8, 1, 4, C, NX, NK, NO, OUT, DOT>>(a, st);
-    return wide ? launch_dense_pass<DensePass<16, 1, 8, C, NX, NK, NO, OUT, DOT>>(a, st)
-                : launch_dense_pass<DensePass<16, 1, 4, C, NX, NK, NO, OUT, DOT>>(a, st);
+        return wide ? launch_dense_pass<DensePass<8, (DOT ? 2 : 1), (DOT ? 4 : 8), NX, NK, NO, OUT, REV, DOT>>(a, st)
+                    : launch_dense_pass<DensePass<8, 1, 4, NX, NK, NO, OUT, REV, DOT>>(a, st);
+    return wide ? launch_dense_pass<DensePass<16, 1, 8, NX, NK, NO, OUT, REV, DOT>>(a, st)
+                : launch_dense_pass<DensePass<16, 1, 4, NX, NK, NO, OUT, REV, DOT>>(a, st);
 }
 
 }  // namespace

@@ -139,23 +139,18 @@ hipError_t launch_ypart_gate(const YGateArgs& a, hipStream_t st);
 // and omg [NS][T][DV], the state X [DK][DV] per stream.
 struct DenseArgs {
     const void* xi; const void* kap; const void* omg;
-    bool xi_bf16, kap_bf16, omg_bf16;
     const float* a;          // [NS][T] gates
-    const float* b;          // [NS][T] factor of the added product (nullptr: 1)
-    const float* o;          // [NS][T] factor of the output (nullptr: 1)
+    const float* beta;       // [NS][T]: factor of the added product, or backwards of the output
     float* out;              // [NS][T][DV]
-    const float* X0;         // starting state(s); nullptr: zeros
-    bool X0_seg;             // one per segment ([nseg][NS][..]) rather than one per stream
-    int x_row, x_col;        // X0's strides (a state may be taken transposed)
-    float* Xend;             // optional: the state after the stream (or, in the first pass, each segment's own)
+    const float* X0;         // [nseg][NS][..]: starting states; nullptr: zeros
+    float* Xend;             // optional, the same: the states at the segments' ends
     float* segdec;           // first pass: [nseg][NS] product of the segment's gates
-    const void* with; bool with_bf16;  // [NS][T][DV]: rows multiplied with the (unscaled) output
-    float* dot;              // optional [nslab][NS][T]: those products, per column slab, and
-    float* inter;            // [nslab][NS][nchunk]: the part (scaled by o) of the chunk's starting state, summed
+    const void* with;        // [NS][T][DV]: rows multiplied with the output (before beta)
+    float* dot;              // [nslab][NS][T]: those products, per column slab, and
+    float* inter;            // [nslab][NS][nchunk]: the part (after beta) of the chunk's starting state, summed
     int64_t NS, T, L;        // L: tokens per segment
     int64_t nchunk;          // chunks of a stream; set by the launcher
     int nseg, nslab, DK, DV;
-    bool rev;                // from the last token to the first
 };
 struct CarryArgs {
     float* ws;               // [nseg][NS][per]: own sums in, starting states out
@@ -178,17 +173,21 @@ struct DenseGatesArgs {
     int nseg, nslab, C;
     bool has_dS;
 };
-// Tokens per chunk: 64, or 32 where some rows are fp32 (three planes of each in LDS).
-constexpr int DENSE_CHUNK = 64, DENSE_CHUNK_F32 = 32;
-// The passes by their rows' types (those named are fp32, the others bf16; all of f32's)
-hipError_t launch_dense_bf16(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_bf16_state(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_xi32(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_kap32(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_omg32(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_omg32_state(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_f32(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_f32_state(const DenseArgs& a, hipStream_t st);
+// Tokens per chunk of the dense recurrence.
+constexpr int DENSE_CHUNK = 32;
+// Its passes, by what they give, over bf16 rows (dy's are fp32) or fp32 ones
+hipError_t launch_dense_y(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_y_f32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_s(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_s_f32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_g(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_g_f32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_dq(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_dq_f32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_dk(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_dk_f32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_dv(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_dv_f32(const DenseArgs& a, hipStream_t st);
 struct DenseFwdArgs {
     const void* q; const void* k; const void* v; bool bf16;
     const float* alpha; const float* beta;
