@@ -47,22 +47,52 @@ __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 
 // chunk's rows, lies beyond every buffer (a buffer holds at most 64 KiB).
 constexpr uint32_t FAR = 0x28000000u;
 
-// two values' planes, packed: a's in the low half
-__device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) {
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    h = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
-    const float ra = a - __uint_as_float(ua & 0xFFFF0000u), rb = b - __uint_as_float(ub & 0xFFFF0000u);
-    const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
-    m = __builtin_amdgcn_perm(vb, va, 0x07060302u);
-    const float sa = ra - __uint_as_float(va & 0xFFFF0000u), sb = rb - __uint_as_float(vb & 0xFFFF0000u);
-    l = __builtin_amdgcn_perm(__float_as_uint(sb), __float_as_uint(sa), 0x07060302u);
+// two values' planes, packed: a's in the low half. What a plane leaves over is taken by
+// the two-term bf16 dot product with (-1, 0) or (0, -1): one instruction a value in place of
+// masking and subtracting, and exact, as the difference is (checked on MI355X for 2^26 pairs of
+// random bits). The factors sit in registers: as an inline constant -1 would mean both halves' bits.
+struct Splitter {
+    uint32_t lo = 0x0000BF80u, hi = 0xBF800000u;
+    __device__ __forceinline__ Splitter() {
+        asm("" : "+s"(lo));
+        asm("" : "+s"(hi));
+    }
+    __device__ __forceinline__ void two(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) const {
+        typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+        auto less = [](uint32_t p, uint32_t f, float x) {
+            return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, p), __builtin_bit_cast(bf16x2_t, f), x, false);
+        };
+        auto top = [](float x, float y) { return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u); };
+        h = top(a, b);
+        a = less(h, lo, a); b = less(h, hi, b);
+        m = top(a, b);
+        a = less(m, lo, a); b = less(m, hi, b);
+        l = top(a, b);
+    }
+    // 8 values -> three operand planes
+    __device__ __forceinline__ void eight(const float (&v)[8], uint4 (&p)[3]) const {
+        two(v[0], v[1], p[0].x, p[1].x, p[2].x);
+        two(v[2], v[3], p[0].y, p[1].y, p[2].y);
+        two(v[4], v[5], p[0].z, p[1].z, p[2].z);
+        two(v[6], v[7], p[0].w, p[1].w, p[2].w);
+    }
+};
+
+// x times the values of the N lanes before (or behind) it in its row of 16; 1 beyond the row
+template <int N>
+__device__ __forceinline__ float times_before(float x) {
+    return x * __int_as_float(__builtin_amdgcn_update_dpp(0x3F800000, __float_as_int(x), 0x110 + N, 0xF, 0xF, false));
 }
-// 8 values -> three operand planes
-__device__ __forceinline__ void split8(const float (&v)[8], uint4 (&p)[3]) {
-    split2(v[0], v[1], p[0].x, p[1].x, p[2].x);
-    split2(v[2], v[3], p[0].y, p[1].y, p[2].y);
-    split2(v[4], v[5], p[0].z, p[1].z, p[2].z);
-    split2(v[6], v[7], p[0].w, p[1].w, p[2].w);
+template <int N>
+__device__ __forceinline__ float times_behind(float x) {
+    return x * __int_as_float(__builtin_amdgcn_update_dpp(0x3F800000, __float_as_int(x), 0x100 + N, 0xF, 0xF, false));
+}
+// products over the row's lanes up to and with this one, and from this one on
+__device__ __forceinline__ float product_to(float x) {
+    return times_before<8>(times_before<4>(times_before<2>(times_before<1>(x))));
+}
+__device__ __forceinline__ float product_from(float x) {
+    return times_behind<8>(times_behind<4>(times_behind<2>(times_behind<1>(x))));
 }
 
 // acc += A B over the operands' planes
@@ -92,7 +122,7 @@ struct Piece<1> {
         const int4 v = ld_i4(r, off, 0);
         x = make_uint4((uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w);
     }
-    __device__ __forceinline__ void store(char* lds, int) const { *reinterpret_cast<uint4*>(lds) = x; }
+    __device__ __forceinline__ void store(char* lds, int, const Splitter&) const { *reinterpret_cast<uint4*>(lds) = x; }
 };
 template <>
 struct Piece<3> {
@@ -102,10 +132,10 @@ struct Piece<3> {
         x = ld_f4(r, off, 0);
         y = ld_f4(r, off + 16u, 0);
     }
-    __device__ __forceinline__ void store(char* lds, int plane) const {
+    __device__ __forceinline__ void store(char* lds, int plane, const Splitter& sp) const {
         const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         uint4 p[3];
-        split8(v, p);
+        sp.eight(v, p);
 #pragma unroll
         for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(lds + i * plane) = p[i];
     }
@@ -167,6 +197,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
     for (int n = 0; n < NCT; ++n) col[n] = c0 + (w * NCT + n) * 16 + m16;
 
+    const Splitter sp;
     // rows 32p + 8 g4 + 4h + i in X[2p + h][..][i]
     f32x4_t X[DKT][NCT];
 #pragma unroll
@@ -266,13 +297,13 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
             const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
-            pk[i].store(buf + P::O_KA + j * P::RK + q * 2, P::PK);
-            if constexpr (P::OUT) px[i].store(buf + P::O_XI + j * P::RK + q * 2, P::PK);
+            pk[i].store(buf + P::O_KA + j * P::RK + q * 2, P::PK, sp);
+            if constexpr (P::OUT) px[i].store(buf + P::O_XI + j * P::RK + q * 2, P::PK, sp);
         }
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
             const int e = tid + i * THR, j = e / (SV / 8), q = e % (SV / 8) * 8;
-            if (C * (SV / 8) % THR == 0 || j < C) po[i].store(buf + P::O_OM + j * P::RV + q * 2, P::PV);
+            if (C * (SV / 8) % THR == 0 || j < C) po[i].store(buf + P::O_OM + j * P::RV + q * 2, P::PV, sp);
         }
         if constexpr (P::DOT)
 #pragma unroll
@@ -281,13 +312,17 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
                 for (int c = 0; c < NCT; ++c) wc[t][c] = wi[t][c];
         if (w < NT) {
             float* const d = dec + (ch & 1) * P::DEC;
-            float p = 1.f, q = 1.f;
+            const float p = product_to(pg);  // every row of 16 lanes holds the block's gates
+            const float q = product_from(__int_as_float(__builtin_amdgcn_update_dpp(0x3F800000, __float_as_int(pg), 0x101, 0xF, 0xF, false)));
+            if constexpr (P::OUT) {
+                // D_ts for s = 4 g4 + 3 is the product of the gates 4 g4 + 4 .. t; each smaller s takes one more
+                float e = product_to(m16 >= 4 * g4 + 4 ? pg : 1.f);
 #pragma unroll
-            for (int r = 15; r >= 0; --r) {
-                const float gr = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(pg), r));
-                if (P::OUT && g4 == r >> 2) dg[r & 3] = r <= m16 ? p : 0.f;
-                p *= r <= m16 ? gr : 1.f;
-                q *= r > m16 ? gr : 1.f;
+                for (int i = 3; i >= 0; --i) {
+                    dg[i] = m16 >= 4 * g4 + i ? e : 0.f;
+                    const float g = __shfl(pg, 4 * g4 + i, 16);
+                    e *= m16 >= 4 * g4 + i ? g : 1.f;
+                }
             }
             int64_t t0;
             int n;
@@ -360,8 +395,8 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
                     f[0] *= sf.x * pr; f[1] *= sf.y * pr; f[2] *= sf.z * pr; f[3] *= sf.w * pr;
                 }
                 uint2 o[3];
-                split2(p[0] * f[0], p[1] * f[1], o[0].x, o[1].x, o[2].x);
-                split2(p[2] * f[2], p[3] * f[3], o[0].y, o[1].y, o[2].y);
+                sp.two(p[0] * f[0], p[1] * f[1], o[0].x, o[1].x, o[2].x);
+                sp.two(p[2] * f[2], p[3] * f[3], o[0].y, o[1].y, o[2].y);
                 char* const to = Pf + (tt + st) * 3 * 512 + lane * 8;  // tiles (0,0), (1,0), (1,1)
 #pragma unroll
                 for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(to + i * 512) = o[i];
@@ -380,7 +415,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
                 for (int c = 0; c < NCT; ++c) {
                     const float v[8] = {X[2 * p][c][0], X[2 * p][c][1], X[2 * p][c][2], X[2 * p][c][3],
                                         X[2 * p + 1][c][0], X[2 * p + 1][c][1], X[2 * p + 1][c][2], X[2 * p + 1][c][3]};
-                    split8(v, xb[c]);
+                    sp.eight(v, xb[c]);
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
@@ -459,7 +494,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= f[i];
-            split8(v, ow[c]);
+            sp.eight(v, ow[c]);
         }
         if constexpr (P::OUT) {
 #pragma unroll
