@@ -123,6 +123,7 @@ struct Piece<1> {
         x = make_uint4((uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w);
     }
     __device__ __forceinline__ void store(char* lds, int, const Splitter&) const { *reinterpret_cast<uint4*>(lds) = x; }
+    __device__ __forceinline__ void store_raw(char* lds) const { *reinterpret_cast<uint4*>(lds) = x; }
 };
 template <>
 struct Piece<3> {
@@ -138,6 +139,10 @@ struct Piece<3> {
         sp.eight(v, p);
 #pragma unroll
         for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(lds + i * plane) = p[i];
+    }
+    __device__ __forceinline__ void store_raw(char* lds) const {
+        *reinterpret_cast<float4*>(lds) = x;
+        *reinterpret_cast<float4*>(lds + 16) = y;
     }
 };
 
@@ -162,7 +167,8 @@ struct DensePass {
     static constexpr int RK = DKP * 2 + 16, RV = SV * 2 + 16;        // bytes of an LDS row
     static constexpr int PK = C * RK, PV = C * RV;                   // bytes of a plane
     static constexpr int TILES = NT * (NT + 1) / 2;
-    static constexpr int O_KA = 0, O_OM = O_KA + NK * PK, O_XI = O_OM + NO * PV, ROWS = O_XI + (OUT ? NX * PK : 0);
+    static constexpr int O_KA = 0, O_OM = O_KA + NK * PK, O_XI = O_OM + NO * PV, O_WI = O_XI + (OUT ? NX * PK : 0),
+                         RW = SV * WITH + 16, ROWS = O_WI + (DOT ? C * RW : 0);
     // floats: two sets of a chunk's decays, outputs' products, their sums
     static constexpr int DEC = 4 * C + 2 * NT, FLOATS = 2 * DEC + (DOT ? 2 * NW * (C + 1) : 0);
     static constexpr int PBYTES = OUT ? TILES * 3 * 512 : 0;
@@ -222,6 +228,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
     Piece<P::NK> pk[KP];
     Piece<P::NX> px[P::OUT ? KP : 1];
     Piece<P::NO> po[VP];
+    Piece<P::WITH == 2 ? 1 : 3> pw[P::DOT ? VP : 1];
     float pg = 1.f, pb = 0.f;
     const int nch = (int)((hi - lo + C - 1) / C);
     auto span = [&](int ch, int64_t& t0, int& n) {  // the chunk's first token and length, in processing order
@@ -250,7 +257,6 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
     for (int c = 0; c < NCT; ++c) eo[c] = col[c] < a.DV ? (uint32_t)(row(4 * g4, C) * a.DV + col[c]) : FAR;
     const int step = P::REV ? -a.DV : a.DV;  // elements from one row of `out` to the next
-    float wi[P::DOT ? NT * 4 : 1][NCT], wc[P::DOT ? NT * 4 : 1][NCT];  // `with` at this lane's outputs: fetched, and this chunk's
     auto fetch = [&](int ch) {
         int64_t t0;
         int n;
@@ -269,15 +275,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
         if constexpr (P::DOT) {
             const rsrc_t rw = rows(a.with, t0, n, a.DV, P::WITH);
 #pragma unroll
-            for (int t = 0; t < NT * 4; ++t)
-#pragma unroll
-                for (int c = 0; c < NCT; ++c) {
-                    const uint32_t at = eo[c] + ((t >> 2) * 16 + (t & 3)) * step - lack * a.DV;
-                    if constexpr (P::WITH == 2)
-                        wi[t][c] = bf_lo((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rw, (int)(at * 2u), 0, 0));
-                    else
-                        wi[t][c] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, (int)(at * 4u), 0, 0));
-                }
+            for (int i = 0; i < VP; ++i) pw[i].load(rw, (ev[i] - lack * a.DV) * P::WITH);
         }
         pg = 1.f;
         pb = 0.f;
@@ -303,13 +301,11 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
             const int e = tid + i * THR, j = e / (SV / 8), q = e % (SV / 8) * 8;
-            if (C * (SV / 8) % THR == 0 || j < C) po[i].store(buf + P::O_OM + j * P::RV + q * 2, P::PV, sp);
+            if (C * (SV / 8) % THR == 0 || j < C) {
+                po[i].store(buf + P::O_OM + j * P::RV + q * 2, P::PV, sp);
+                if constexpr (P::DOT) pw[i].store_raw(buf + P::O_WI + j * P::RW + q * P::WITH);
+            }
         }
-        if constexpr (P::DOT)
-#pragma unroll
-            for (int t = 0; t < NT * 4; ++t)
-#pragma unroll
-                for (int c = 0; c < NCT; ++c) wc[t][c] = wi[t][c];
         if (w < NT) {
             float* const d = dec + (ch & 1) * P::DEC;
             const float p = product_to(pg);  // every row of 16 lanes holds the block's gates
@@ -366,6 +362,11 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
         const float* const fin = fsuf + C;
         const float* const fo = fin + C;
         const float tot0 = fo[C], tot1 = fo[C + 1], total = tot0 * tot1;
+        auto with = [&](int j, int c) {  // `with` at row j, this lane's column
+            const char* const p = buf + P::O_WI + j * P::RW + ((w * NCT + c) * 16 + m16) * P::WITH;
+            if constexpr (P::WITH == 2) return bf_lo(*reinterpret_cast<const uint16_t*>(p));
+            else return *reinterpret_cast<const float*>(p);
+        };
         f32x4_t acc[P::OUT ? NT : 1][NCT];
         if constexpr (P::OUT) {
             // P^T = kap xi^T, scaled: a tile (s block st, t block tt) a wavefront, its planes stored as
@@ -442,7 +443,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
                     for (int i = 0; i < 4; ++i) {
                         float d = 0.f;
 #pragma unroll
-                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wc[t * 4 + i][c], d);
+                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], with(t * 16 + 4 * g4 + i, c), d);
                         inter = fmaf(d, fo[t * 16 + 4 * g4 + i], inter);
                     }
                 }
@@ -540,7 +541,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
                     if constexpr (P::DOT) {
                         float d = 0.f;
 #pragma unroll
-                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], wc[t * 4 + i][c], d);
+                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], with(j, c), d);
                         d = ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(d))));
                         if (m16 == 0) dots[((ch & 1) * NW + w) * (C + 1) + j] = d;
                     }
