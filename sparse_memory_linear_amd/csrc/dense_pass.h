@@ -47,36 +47,22 @@ __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 
 // chunk's rows, lies beyond every buffer (a buffer holds at most 64 KiB).
 constexpr uint32_t FAR = 0x28000000u;
 
-// two values' planes, packed: a's in the low half. What a plane leaves over is taken by
-// the two-term bf16 dot product with (-1, 0) or (0, -1): one instruction a value in place of
-// masking and subtracting, and exact, as the difference is (checked on MI355X for 2^26 pairs of
-// random bits). The factors sit in registers: as an inline constant -1 would mean both halves' bits.
-struct Splitter {
-    uint32_t lo = 0x0000BF80u, hi = 0xBF800000u;
-    __device__ __forceinline__ Splitter() {
-        asm("" : "+s"(lo));
-        asm("" : "+s"(hi));
-    }
-    __device__ __forceinline__ void two(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) const {
-        typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-        auto less = [](uint32_t p, uint32_t f, float x) {
-            return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, p), __builtin_bit_cast(bf16x2_t, f), x, false);
-        };
-        auto top = [](float x, float y) { return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u); };
-        h = top(a, b);
-        a = less(h, lo, a); b = less(h, hi, b);
-        m = top(a, b);
-        a = less(m, lo, a); b = less(m, hi, b);
-        l = top(a, b);
-    }
-    // 8 values -> three operand planes
-    __device__ __forceinline__ void eight(const float (&v)[8], uint4 (&p)[3]) const {
-        two(v[0], v[1], p[0].x, p[1].x, p[2].x);
-        two(v[2], v[3], p[0].y, p[1].y, p[2].y);
-        two(v[4], v[5], p[0].z, p[1].z, p[2].z);
-        two(v[6], v[7], p[0].w, p[1].w, p[2].w);
-    }
-};
+// two values' planes, packed: a's in the low half
+__device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) {
+    auto rest = [](float x) { return x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); };  // exact
+    auto top = [](float x, float y) { return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u); };
+    h = top(a, b);
+    a = rest(a); b = rest(b);
+    m = top(a, b);
+    l = top(rest(a), rest(b));
+}
+// 8 values -> three operand planes
+__device__ __forceinline__ void split8(const float (&v)[8], uint4 (&p)[3]) {
+    split2(v[0], v[1], p[0].x, p[1].x, p[2].x);
+    split2(v[2], v[3], p[0].y, p[1].y, p[2].y);
+    split2(v[4], v[5], p[0].z, p[1].z, p[2].z);
+    split2(v[6], v[7], p[0].w, p[1].w, p[2].w);
+}
 
 // x times the values of the N lanes before (or behind) it in its row of 16; 1 beyond the row
 template <int N>
@@ -122,7 +108,7 @@ struct Piece<1> {
         const int4 v = ld_i4(r, off, 0);
         x = make_uint4((uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w);
     }
-    __device__ __forceinline__ void store(char* lds, int, const Splitter&) const { *reinterpret_cast<uint4*>(lds) = x; }
+    __device__ __forceinline__ void store(char* lds, int) const { *reinterpret_cast<uint4*>(lds) = x; }
     __device__ __forceinline__ void store_raw(char* lds) const { *reinterpret_cast<uint4*>(lds) = x; }
 };
 template <>
@@ -133,10 +119,10 @@ struct Piece<3> {
         x = ld_f4(r, off, 0);
         y = ld_f4(r, off + 16u, 0);
     }
-    __device__ __forceinline__ void store(char* lds, int plane, const Splitter& sp) const {
+    __device__ __forceinline__ void store(char* lds, int plane) const {
         const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         uint4 p[3];
-        sp.eight(v, p);
+        split8(v, p);
 #pragma unroll
         for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(lds + i * plane) = p[i];
     }
@@ -203,7 +189,6 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
     for (int n = 0; n < NCT; ++n) col[n] = c0 + (w * NCT + n) * 16 + m16;
 
-    const Splitter sp;
     // rows 32p + 8 g4 + 4h + i in X[2p + h][..][i]
     f32x4_t X[DKT][NCT];
 #pragma unroll
@@ -295,14 +280,14 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
             const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
-            pk[i].store(buf + P::O_KA + j * P::RK + q * 2, P::PK, sp);
-            if constexpr (P::OUT) px[i].store(buf + P::O_XI + j * P::RK + q * 2, P::PK, sp);
+            pk[i].store(buf + P::O_KA + j * P::RK + q * 2, P::PK);
+            if constexpr (P::OUT) px[i].store(buf + P::O_XI + j * P::RK + q * 2, P::PK);
         }
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
             const int e = tid + i * THR, j = e / (SV / 8), q = e % (SV / 8) * 8;
             if (C * (SV / 8) % THR == 0 || j < C) {
-                po[i].store(buf + P::O_OM + j * P::RV + q * 2, P::PV, sp);
+                po[i].store(buf + P::O_OM + j * P::RV + q * 2, P::PV);
                 if constexpr (P::DOT) pw[i].store_raw(buf + P::O_WI + j * P::RW + q * P::WITH);
             }
         }
@@ -396,8 +381,8 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
                     f[0] *= sf.x * pr; f[1] *= sf.y * pr; f[2] *= sf.z * pr; f[3] *= sf.w * pr;
                 }
                 uint2 o[3];
-                sp.two(p[0] * f[0], p[1] * f[1], o[0].x, o[1].x, o[2].x);
-                sp.two(p[2] * f[2], p[3] * f[3], o[0].y, o[1].y, o[2].y);
+                split2(p[0] * f[0], p[1] * f[1], o[0].x, o[1].x, o[2].x);
+                split2(p[2] * f[2], p[3] * f[3], o[0].y, o[1].y, o[2].y);
                 char* const to = Pf + (tt + st) * 3 * 512 + lane * 8;  // tiles (0,0), (1,0), (1,1)
 #pragma unroll
                 for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(to + i * 512) = o[i];
@@ -416,7 +401,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
                 for (int c = 0; c < NCT; ++c) {
                     const float v[8] = {X[2 * p][c][0], X[2 * p][c][1], X[2 * p][c][2], X[2 * p][c][3],
                                         X[2 * p + 1][c][0], X[2 * p + 1][c][1], X[2 * p + 1][c][2], X[2 * p + 1][c][3]};
-                    sp.eight(v, xb[c]);
+                    split8(v, xb[c]);
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
@@ -495,7 +480,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= f[i];
-            sp.eight(v, ow[c]);
+            split8(v, ow[c]);
         }
         if constexpr (P::OUT) {
 #pragma unroll
