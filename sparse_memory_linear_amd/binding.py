@@ -446,6 +446,34 @@ def sdm_state_init_backward(dM: torch.Tensor, out: Optional[torch.Tensor] = None
     return dM0
 
 
+# The calls below are short enough to be bound by their host side: addresses are
+# passed as plain integers, devices compared by index.
+
+def _gpu(t0: torch.Tensor, *ts: Optional[torch.Tensor]) -> torch.device:
+    """The tensors' device: all contiguous, on one GPU (None: not given)."""
+    i = t0.get_device()
+    if i < 0 or not t0.is_contiguous():
+        raise ValueError("tensors must be contiguous and on a GPU")
+    for t in ts:
+        if t is not None and (t.get_device() != i or not t.is_contiguous()):
+            raise ValueError("all tensors must be contiguous and on the same GPU")
+    return t0.device
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _out(t: Optional[torch.Tensor], like: torch.Tensor, shape, dtype: torch.dtype, name: str) -> torch.Tensor:
+    """A new tensor on ``like``'s device, or the given one after its checks."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} has the wrong shape or dtype")
+    _gpu(like, t)
+    return t
+
+
 def sdm_dense_scan_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int) -> int:
     n = lib().sdm_dense_scan_workspace_bytes(B, H, T, dk, dv)
     if n < 0:
@@ -454,7 +482,7 @@ def sdm_dense_scan_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int) -> 
 
 
 def _dense_inputs(fn, q, k, v, alpha, beta, states):
-    d = _dev(q, k, v, alpha, beta)
+    d = _gpu(q, k, v, alpha, beta)
     B, H, T, dk = q.shape
     dv = v.shape[3]
     for name, t, shp in (("k", k, (B, H, T, dk)), ("v", v, (B, H, T, dv)), ("alpha", alpha, (B, H, T)),
@@ -465,7 +493,7 @@ def _dense_inputs(fn, q, k, v, alpha, beta, states):
         raise ValueError(f"dtype mismatch in {fn}")
     for name, t in states:
         if t is not None:
-            _f32_out(t, (B, H, dk, dv), d, name)
+            _out(t, q, (B, H, dk, dv), torch.float32, name)
     return d, (B, H, T, dk, dv)
 
 
@@ -480,13 +508,13 @@ def sdm_dense_scan_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, al
     ``S`` and ``y`` may pass them preallocated, and S may be S0 (updated in place).
     """
     d, (B, H, T, dk, dv) = _dense_inputs("sdm_dense_scan_forward", q, k, v, alpha, beta, (("S0", S0), ("S", S)))
-    S = _f32_out(S, (B, H, dk, dv), d, "S")
-    y = _f32_out(y, (B, H, T, dv), d, "y")
+    S = _out(S, q, (B, H, dk, dv), torch.float32, "S")
+    y = _out(y, q, (B, H, T, dv), torch.float32, "y")
     n = sdm_dense_scan_workspace_bytes(B, H, T, dk, dv)
     ws = _workspace(workspace, n, d) if n or workspace is not None else None
     _check("sdm_dense_scan_forward", lib().sdm_dense_scan_forward(
-        _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(alpha), _ptr(beta), _ptr(S0), _ptr(S), _ptr(y),
-        B, H, T, dk, dv, _ptr(ws), ws.numel() if ws is not None else 0, _stream(d)))
+        _at(q), _at(k), _at(v), _dtype_code(q), _at(alpha), _at(beta), _at(S0), _at(S), _at(y),
+        B, H, T, dk, dv, _at(ws), ws.numel() if ws is not None else 0, _stream(d)))
     return y, S
 
 
@@ -508,17 +536,17 @@ def sdm_dense_scan_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a
     dS0 [B,H,dk,dv], all fp32; ``out`` may pass those tensors preallocated.
     """
     d, (B, H, T, dk, dv) = _dense_inputs("sdm_dense_scan_backward", q, k, v, alpha, beta, (("S0", S0), ("dS", dS)))
-    _f32_out(dy, (B, H, T, dv), d, "dy")
+    _out(dy, q, (B, H, T, dv), torch.float32, "dy")
     out = dict(out or {})
     shapes = {"dq": (B, H, T, dk), "dk": (B, H, T, dk), "dv": (B, H, T, dv), "dlog_alpha": (B, H, T),
               "dbeta": (B, H, T), "dS0": (B, H, dk, dv)}
     for name, shp in shapes.items():
-        out[name] = _f32_out(out.get(name), shp, d, name)
+        out[name] = _out(out.get(name), q, shp, torch.float32, name)
     workspace = _workspace(workspace, sdm_dense_scan_backward_workspace_bytes(B, H, T, dk, dv), d)
     _check("sdm_dense_scan_backward", lib().sdm_dense_scan_backward(
-        _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(alpha), _ptr(beta), _ptr(dy), _ptr(S0), _ptr(dS),
-        _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dlog_alpha"]), _ptr(out["dbeta"]),
-        _ptr(out["dS0"]), B, H, T, dk, dv, _ptr(workspace), workspace.numel(), _stream(d)))
+        _at(q), _at(k), _at(v), _dtype_code(q), _at(alpha), _at(beta), _at(dy), _at(S0), _at(dS),
+        _at(out["dq"]), _at(out["dk"]), _at(out["dv"]), _at(out["dlog_alpha"]), _at(out["dbeta"]),
+        _at(out["dS0"]), B, H, T, dk, dv, _at(workspace), workspace.numel(), _stream(d)))
     return out
 
 
@@ -536,7 +564,7 @@ def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.
     columns ([..., d / group]). Returns a dict with y, h (with res; in res's dtype) and
     scale (for e4m3); ``out`` may pass those tensors preallocated, h may be res or x.
     """
-    d_ = _dev(x, gamma, *(() if res is None else (res,)))
+    d_ = _gpu(x, gamma, res)
     if dtype not in NORM_OUT:
         raise ValueError(f"unknown output dtype {dtype!r}")
     if x.dim() < 1 or gamma.shape != x.shape[-1:] or gamma.dtype != torch.float32 \
@@ -545,7 +573,7 @@ def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.
     d = x.shape[-1]
     rows = x.numel() // d if d else 0
     code, yt = NORM_OUT[dtype]
-    out = dict(out or {})
+    out = dict(out) if out else {}
     want = {"y": (x.shape, yt)}
     if res is not None:
         want["h"] = (x.shape, res.dtype)
@@ -553,19 +581,14 @@ def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.
         if group < 0 or (group and d % group):
             raise ValueError("group must be 0 or divide d")
         want["scale"] = (x.shape[:-1] + (d // group if group else 1,), torch.float32)
-    if set(out) - set(want):
+    if out and set(out) - set(want):
         raise ValueError(f"no such output: {sorted(set(out) - set(want))}")
     for name, (shp, dt) in want.items():
-        t = out.get(name)
-        if t is None:
-            out[name] = torch.empty(shp, dtype=dt, device=d_)
-        elif t.shape != shp or t.dtype != dt:
-            raise ValueError(f"{name} has the wrong shape or dtype")
-        _dev(x, out[name])
+        out[name] = _out(out.get(name), x, shp, dt, name)
     h, scale = out.get("h"), out.get("scale")
     _check("sdm_residual_norm", lib().sdm_residual_norm(
-        _ptr(x), _dtype_code(x), _ptr(res), _ptr(h), _dtype_code(x if res is None else res), _ptr(gamma),
-        float(eps), rows, d, _ptr(out["y"]), code, _ptr(scale), group, _stream(d_)))
+        _at(x), _dtype_code(x), _at(res), _at(h), _dtype_code(x if res is None else res), _at(gamma),
+        float(eps), rows, d, _at(out["y"]), code, _at(scale), group, _stream(d_)))
     return out
 
 
@@ -578,27 +601,22 @@ def sdm_residual_norm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.T
     gamma [d] fp32. Returns a dict with dx (the gradient of x and of res, in dy's dtype) and
     dgamma [d] fp32; ``out`` may pass them preallocated.
     """
-    d_ = _dev(dy, h, gamma, *(() if dh is None else (dh,)))
+    d_ = _gpu(dy, h, gamma, dh)
     if dy.dim() < 1 or gamma.shape != dy.shape[-1:] or gamma.dtype != torch.float32 or h.shape != dy.shape \
             or (dh is not None and (dh.shape != dy.shape or dh.dtype != dy.dtype)):
         raise ValueError("shape or dtype mismatch in sdm_residual_norm_backward")
     d = dy.shape[-1]
     rows = dy.numel() // d if d else 0
     out = dict(out or {})
-    dx = out.get("dx")
-    if dx is None:
-        dx = torch.empty_like(dy)
-    elif dx.shape != dy.shape or dx.dtype != dy.dtype:
-        raise ValueError("dx has the wrong shape or dtype")
-    _dev(dy, dx)
-    dgamma = _f32_out(out.get("dgamma"), (d,), d_, "dgamma")
+    dx = _out(out.get("dx"), dy, dy.shape, dy.dtype, "dx")
+    dgamma = _out(out.get("dgamma"), dy, (d,), torch.float32, "dgamma")
     if rows == 0:
         dgamma.zero_()
     n = lib().sdm_residual_norm_backward_workspace_bytes(rows, d)
     ws = _workspace(workspace, max(n, 0), d_)
     _check("sdm_residual_norm_backward", lib().sdm_residual_norm_backward(
-        _ptr(dy), _ptr(dh), _dtype_code(dy), _ptr(h), _dtype_code(h), _ptr(gamma), float(eps), rows, d,
-        _ptr(dx), _ptr(dgamma), _ptr(ws), ws.numel(), _stream(d_)))
+        _at(dy), _at(dh), _dtype_code(dy), _at(h), _dtype_code(h), _at(gamma), float(eps), rows, d,
+        _at(dx), _at(dgamma), _at(ws), ws.numel(), _stream(d_)))
     return {"dx": dx, "dgamma": dgamma}
 
 
@@ -609,14 +627,12 @@ def sdm_balance_workspace_bytes(B: int, H: int, T: int, K: int, N: int) -> int:
     return n
 
 
-def _mask(mask, B, T, d):
+def _mask(mask, B, T, idx):
     if mask is None:
         return
     if tuple(mask.shape) != (B, T) or mask.dtype not in (torch.uint8, torch.bool):
         raise ValueError("mask must be [B, T], uint8 or bool")
-    _dev(mask)
-    if mask.device != d:
-        raise ValueError("all tensors must be on the same GPU")
+    _gpu(idx, mask)
 
 
 def sdm_balance_forward(idx: torch.Tensor, wt: torch.Tensor, N: int, mask: Optional[torch.Tensor] = None,
@@ -627,24 +643,19 @@ def sdm_balance_forward(idx: torch.Tensor, wt: torch.Tensor, N: int, mask: Optio
     bool (non-zero: kept) or None. Returns a dict with counts [H,N] int32, mass [H,N] fp32,
     tokens [1] int32 and loss [H] fp32 (1 when even); ``out`` may pass them preallocated.
     """
-    d = _dev(idx, wt)
+    d = _gpu(idx, wt)
     B, H, T, K = idx.shape
     if wt.shape != idx.shape or idx.dtype != torch.int32 or wt.dtype != torch.float32:
         raise ValueError("shape or dtype mismatch in sdm_balance_forward")
-    _mask(mask, B, T, d)
+    _mask(mask, B, T, idx)
     out = dict(out or {})
     for name, shp, dt in (("counts", (H, N), torch.int32), ("mass", (H, N), torch.float32),
                           ("tokens", (1,), torch.int32), ("loss", (H,), torch.float32)):
-        t = out.get(name)
-        if t is None:
-            out[name] = torch.empty(shp, dtype=dt, device=d)
-        elif tuple(t.shape) != shp or t.dtype != dt:
-            raise ValueError(f"{name} has the wrong shape or dtype")
-        _dev(idx, out[name])
+        out[name] = _out(out.get(name), idx, shp, dt, name)
     workspace = _workspace(workspace, sdm_balance_workspace_bytes(B, H, T, K, N), d)
     _check("sdm_balance_forward", lib().sdm_balance_forward(
-        _ptr(idx), _ptr(wt), _ptr(mask), B, H, T, K, N, _ptr(out["counts"]), _ptr(out["mass"]),
-        _ptr(out["tokens"]), _ptr(out["loss"]), _ptr(workspace), workspace.numel(), _stream(d)))
+        _at(idx), _at(wt), _at(mask), B, H, T, K, N, _at(out["counts"]), _at(out["mass"]),
+        _at(out["tokens"]), _at(out["loss"]), _at(workspace), workspace.numel(), _stream(d)))
     return out
 
 
@@ -652,15 +663,15 @@ def sdm_balance_backward(idx: torch.Tensor, counts: torch.Tensor, tokens: torch.
                          mask: Optional[torch.Tensor] = None, dwt: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The balance loss's gradient to the weights: dwt [B,H,T,K] fp32 from dloss [H] fp32 and the
     counts [H,N] and tokens [1] of sdm_balance_forward on the same idx and mask."""
-    d = _dev(idx, counts, tokens, dloss)
+    d = _gpu(idx, counts, tokens, dloss)
     B, H, T, K = idx.shape
     if idx.dtype != torch.int32 or counts.dtype != torch.int32 or tokens.dtype != torch.int32 \
             or dloss.dtype != torch.float32 or counts.dim() != 2 or counts.shape[0] != H \
             or tuple(tokens.shape) != (1,) or tuple(dloss.shape) != (H,):
         raise ValueError("shape or dtype mismatch in sdm_balance_backward")
-    _mask(mask, B, T, d)
-    dwt = _f32_out(dwt, (B, H, T, K), d, "dwt")
+    _mask(mask, B, T, idx)
+    dwt = _out(dwt, idx, (B, H, T, K), torch.float32, "dwt")
     _check("sdm_balance_backward", lib().sdm_balance_backward(
-        _ptr(idx), _ptr(mask), _ptr(counts), _ptr(tokens), _ptr(dloss), B, H, T, K, counts.shape[1],
-        _ptr(dwt), _stream(d)))
+        _at(idx), _at(mask), _at(counts), _at(tokens), _at(dloss), B, H, T, K, counts.shape[1],
+        _at(dwt), _stream(d)))
     return dwt

@@ -180,15 +180,19 @@ hipError_t launch_carry(const CarryArgs& a, hipStream_t st) {
 // Tokens of one call up to which the state is walked token by token.
 constexpr int64_t STEP_TOKENS = 8;
 
-// Segment length: enough workgroups for two per CU, segments of at least 256
-// tokens (a segment costs two passes over a state), a multiple of the chunk.
+// Tokens up to which a forward call is one segment a stream: one launch, where
+// segments take three.
+constexpr int64_t ONE_SEGMENT = 256;
+
+// Segment length: enough workgroups for two per CU (a state per segment and
+// stream, so some 512 of them whatever the length), of at least two chunks.
 int64_t segment_len(int64_t NS, int64_t T, int dv, int64_t most) {
     const int64_t slabs = (dv + dense_slab(dv) - 1) / dense_slab(dv);
-    int64_t want = (512 + NS * slabs - 1) / (NS * slabs);
+    const int64_t want = (512 + NS * slabs - 1) / (NS * slabs);
     int64_t L = (T + want - 1) / want;
-    if (L < 256) L = 256;
     if (L > most) L = most;
-    return (L + 63) / 64 * 64;
+    if (L < 2 * DENSE_CHUNK) L = 2 * DENSE_CHUNK;
+    return (L + DENSE_CHUNK - 1) / DENSE_CHUNK * DENSE_CHUNK;
 }
 
 struct DenseLayout {
@@ -196,9 +200,9 @@ struct DenseLayout {
 };
 DenseLayout forward_layout(int64_t NS, int64_t T, int dk, int dv) {
     DenseLayout y{};
-    y.L = segment_len(NS, T, dv, T);
+    y.L = T <= ONE_SEGMENT ? T : segment_len(NS, T, dv, T);
     y.nseg = (T + y.L - 1) / y.L;
-    if (T <= STEP_TOKENS || y.nseg == 1) return DenseLayout{y.L, 1, 0, 0, 0};
+    if (y.nseg == 1) return DenseLayout{T, 1, 0, 0, 0};
     y.states = y.nseg * NS * (int64_t)dk * dv * 4;
     y.decs = (y.nseg * NS * 4 + 255) / 256 * 256;
     y.bytes = y.states + y.decs;

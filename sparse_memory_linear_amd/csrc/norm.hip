@@ -286,19 +286,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
     }
 }
 
-// dgamma = the sum of the blocks' rows: 64 columns a workgroup, 16 wavefronts
-// each adding every 16th row, then the 16 sums in order.
+// dgamma = the sum of the blocks' rows: 16 columns a workgroup, 64 groups of 16
+// lanes each adding every 64th row, then the 64 sums pairwise.
 __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* part, float* dgamma, int blocks, int d) {
-    __shared__ float s[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+    __shared__ float s[64][17];
+    const int l = threadIdx.x & 15, w = threadIdx.x >> 4, c = blockIdx.x * 16 + l;
     float x = 0.f;
     if (c < d)
-        for (int b = w; b < blocks; b += 16) x += part[(int64_t)b * d + c];
-    s[w][lane] = x;
-    __syncthreads();
-    if (w || c >= d) return;
-    for (int i = 1; i < 16; ++i) x += s[i][lane];
-    dgamma[c] = x;
+#pragma unroll 4
+        for (int b = w; b < blocks; b += 64) x += part[(int64_t)b * d + c];
+    s[w][l] = x;
+    for (int n = 32; n > 0; n >>= 1) {
+        __syncthreads();
+        if (w < n) s[w][l] = x += s[w + n][l];
+    }
+    if (w == 0 && c < d) dgamma[c] = x;
 }
 
 template <int VEC, int TPR, int NV>
@@ -359,7 +361,7 @@ hipError_t launch_norm_backward(NormBwdArgs a, hipStream_t st) {
     a.blocks = (int)norm_bwd_blocks(a.rows, a.d);
     hipError_t e = norm_any(a, st);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((a.d + 63) / 64)), dim3(1024), 0, st, a.part, a.dgamma,
+    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((a.d + 15) / 16)), dim3(1024), 0, st, a.part, a.dgamma,
                        a.blocks, a.d);
     return hipGetLastError();
 }
