@@ -17,35 +17,54 @@
 namespace sdm {
 namespace {
 
+// A thread's piece: VEC consecutive elements of a row, n of which lie in it. Rows
+// need not begin at a multiple of the piece's bytes (d odd): the vector types
+// carry the elements' alignment only, which global memory accesses allow.
+typedef uint32_t u32x4a __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2a __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32a __attribute__((aligned(1)));
+typedef uint32_t u32x2b __attribute__((ext_vector_type(2), aligned(1)));
+
 template <int VEC>
-__device__ __forceinline__ void load_vec(const void* p, bool bf16, int64_t e, float (&v)[VEC]) {
+__device__ __forceinline__ void load_vec(const void* p, bool bf16, int64_t e, int n, float (&v)[VEC]) {
     if (bf16) {
         const uint16_t* b = static_cast<const uint16_t*>(p) + e;
-        uint32_t u[(VEC + 1) / 2];
-        if constexpr (VEC == 8) {
-            const uint4 x = *reinterpret_cast<const uint4*>(b);
-            u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
-        } else if constexpr (VEC == 4) {
-            const uint2 x = *reinterpret_cast<const uint2*>(b);
-            u[0] = x.x; u[1] = x.y;
-        } else {
-            u[0] = *b;
-        }
+        if (n >= VEC) {
+            uint32_t u[VEC / 2];
+            if constexpr (VEC == 8) {
+                const u32x4a x = *reinterpret_cast<const u32x4a*>(b);
+                u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+            } else {
+                const u32x2a x = *reinterpret_cast<const u32x2a*>(b);
+                u[0] = x.x; u[1] = x.y;
+            }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+            for (int i = 0; i < VEC; ++i)
+                v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = i < n ? __uint_as_float((uint32_t)b[i] << 16) : 0.f;
+        }
     } else {
         const float* f = static_cast<const float*>(p) + e;
-        if constexpr (VEC == 1) {
-            v[0] = *f;
-        } else {
+        if (n >= VEC) {
 #pragma unroll
             for (int i = 0; i < VEC; i += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(f + i);
+                const f32x4a x = *reinterpret_cast<const f32x4a*>(f + i);
                 v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = i < n ? f[i] : 0.f;
         }
     }
+}
+
+// elements of the row from column c on: rows of 8 (VEC 8) have no partial piece
+template <int VEC>
+__device__ __forceinline__ int left(int d, int c) {
+    return VEC == 8 ? VEC : d - c;
 }
 
 // nearest even; a NaN stays one
@@ -56,42 +75,50 @@ __device__ __forceinline__ uint32_t to_bf16(float f) {
 }
 
 template <int VEC>
-__device__ __forceinline__ void store_vec(void* p, bool bf16, int64_t e, const float (&v)[VEC]) {
+__device__ __forceinline__ void store_vec(void* p, bool bf16, int64_t e, int n, const float (&v)[VEC]) {
     if (bf16) {
         uint16_t* b = static_cast<uint16_t*>(p) + e;
-        uint32_t u[(VEC + 1) / 2];
+        if (n >= VEC) {
+            uint32_t u[VEC / 2];
 #pragma unroll
-        for (int i = 0; i < VEC; i += 2) u[i / 2] = to_bf16(v[i]) | (VEC > 1 ? to_bf16(v[i + (VEC > 1)]) << 16 : 0u);
-        if constexpr (VEC == 8) *reinterpret_cast<uint4*>(b) = make_uint4(u[0], u[1], u[2], u[3]);
-        else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(b) = make_uint2(u[0], u[1]);
-        else *b = (uint16_t)u[0];
-    } else {
-        float* f = static_cast<float*>(p) + e;
-        if constexpr (VEC == 1) {
-            *f = v[0];
+            for (int i = 0; i < VEC; i += 2) u[i / 2] = to_bf16(v[i]) | to_bf16(v[i + 1]) << 16;
+            if constexpr (VEC == 8) *reinterpret_cast<u32x4a*>(b) = u32x4a{u[0], u[1], u[2], u[3]};
+            else *reinterpret_cast<u32x2a*>(b) = u32x2a{u[0], u[1]};
         } else {
 #pragma unroll
-            for (int i = 0; i < VEC; i += 4)
-                *reinterpret_cast<float4*>(f + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int i = 0; i < VEC; ++i)
+                if (i < n) b[i] = (uint16_t)to_bf16(v[i]);
+        }
+    } else {
+        float* f = static_cast<float*>(p) + e;
+        if (n >= VEC) {
+#pragma unroll
+            for (int i = 0; i < VEC; i += 4) *reinterpret_cast<f32x4a*>(f + i) = f32x4a{v[i], v[i + 1], v[i + 2], v[i + 3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (i < n) f[i] = v[i];
         }
     }
 }
 
 // v / scale in e4m3 (nearest even), by the scale's reciprocal; |v| <= 448 scale
 template <int VEC>
-__device__ __forceinline__ void store_e4m3(void* p, int64_t e, const float (&v)[VEC], float inv) {
+__device__ __forceinline__ void store_e4m3(void* p, int64_t e, int n, const float (&v)[VEC], float inv) {
     uint8_t* b = static_cast<uint8_t*>(p) + e;
-    if constexpr (VEC == 1) {
-        *b = (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, 0.f, 0, false) & 0xFF);
-    } else {
-        uint32_t u[VEC / 4];
+    uint32_t u[VEC / 4];
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) {
-            int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inv, v[4 * i + 1] * inv, 0, false);
-            u[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, q, true);
-        }
-        if constexpr (VEC == 8) *reinterpret_cast<uint2*>(b) = make_uint2(u[0], u[1]);
-        else *reinterpret_cast<uint32_t*>(b) = u[0];
+    for (int i = 0; i < VEC / 4; ++i) {
+        const int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inv, v[4 * i + 1] * inv, 0, false);
+        u[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, q, true);
+    }
+    if (n >= VEC) {
+        if constexpr (VEC == 8) *reinterpret_cast<u32x2b*>(b) = u32x2b{u[0], u[1]};
+        else *reinterpret_cast<u32a*>(b) = u[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (i < n) b[i] = (uint8_t)(u[i / 4] >> (8 * (i % 4)));
     }
 }
 
@@ -110,7 +137,6 @@ __device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*buf)[2
     }
     if constexpr (TPR > 64) {
         const int w = threadIdx.x >> 6;
-        __syncthreads();  // the last row's values have been read
         if ((threadIdx.x & 63) == 0) { buf[w][0] = sum; buf[w][1] = mx; }
         __syncthreads();
         sum = 0.f; mx = 0.f;
@@ -128,65 +154,65 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + lane) * VEC;
-        if (c < a.d) load_vec<VEC>(a.gamma, false, c, ga[j]);
+        if (c < a.d) load_vec<VEC>(a.gamma, false, c, left<VEC>(a.d, c), ga[j]);
     }
-    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
-        float v[NV][VEC];
-        const int64_t at = row * a.d;
-        float ss = 0.f, mx = 0.f;
+    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (row >= a.rows) return;  // TPR > 64: all of the workgroup's threads have this row
+    float v[NV][VEC];
+    const int64_t at = row * a.d;
+    float ss = 0.f, mx = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + lane) * VEC;
-            if (c >= a.d) break;
-            load_vec<VEC>(a.x, a.x_bf16, at + c, v[j]);
-            if (a.res) {
-                float r[VEC];
-                load_vec<VEC>(a.res, a.h_bf16, at + c, r);
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + lane) * VEC;
+        if (c >= a.d) break;
+        load_vec<VEC>(a.x, a.x_bf16, at + c, left<VEC>(a.d, c), v[j]);
+        if (a.res) {
+            float r[VEC];
+            load_vec<VEC>(a.res, a.h_bf16, at + c, left<VEC>(a.d, c), r);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) v[j][i] += r[i];
+            for (int i = 0; i < VEC; ++i) v[j][i] += r[i];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + lane) * VEC;
+        if (c >= a.d) break;
+        if (a.res) store_vec<VEC>(a.h, a.h_bf16, at + c, left<VEC>(a.d, c), v[j]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            ss = fmaf(v[j][i], v[j][i], ss);
+            v[j][i] *= ga[j][i];
+            mx = fmaxf(mx, fabsf(v[j][i]));
+        }
+    }
+    row_reduce<TPR>(ss, mx, buf);
+    const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+    float scale = 0.f, inv = 0.f;
+    if (a.y_type == NORM_E4M3 && a.group == 0) {
+        scale = e4m3_scale(mx * r);
+        inv = scale > 0.f ? 1.f / scale : 0.f;
+        if (lane == 0) a.scale[row] = scale;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + lane) * VEC;
+        if constexpr (VEC == 8) {
+            if (a.y_type == NORM_E4M3 && a.group) {  // group / 8 neighbouring lanes share a scale
+                float m = 0.f;
+                if (c < a.d)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(v[j][i] * r));
+                for (int k = 1; k < a.group / 8; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
+                scale = e4m3_scale(m);
+                inv = scale > 0.f ? 1.f / scale : 0.f;
+                if (c < a.d && c % a.group == 0) a.scale[row * (a.d / a.group) + c / a.group] = scale;
             }
         }
+        if (c >= a.d) continue;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + lane) * VEC;
-            if (c >= a.d) break;
-            if (a.res) store_vec<VEC>(a.h, a.h_bf16, at + c, v[j]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                ss = fmaf(v[j][i], v[j][i], ss);
-                v[j][i] *= ga[j][i];
-                mx = fmaxf(mx, fabsf(v[j][i]));
-            }
-        }
-        row_reduce<TPR>(ss, mx, buf);
-        const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
-        float scale = 0.f, inv = 0.f;
-        if (a.y_type == NORM_E4M3 && a.group == 0) {
-            scale = e4m3_scale(mx * r);
-            inv = scale > 0.f ? 1.f / scale : 0.f;
-            if (lane == 0) a.scale[row] = scale;
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + lane) * VEC;
-            if constexpr (VEC == 8) {
-                if (a.y_type == NORM_E4M3 && a.group) {  // group / 8 neighbouring lanes share a scale
-                    float m = 0.f;
-                    if (c < a.d)
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(v[j][i] * r));
-                    for (int k = 1; k < a.group / 8; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
-                    scale = e4m3_scale(m);
-                    inv = scale > 0.f ? 1.f / scale : 0.f;
-                    if (c < a.d && c % a.group == 0) a.scale[row * (a.d / a.group) + c / a.group] = scale;
-                }
-            }
-            if (c >= a.d) continue;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[j][i] *= r;
-            if (a.y_type == NORM_E4M3) store_e4m3<VEC>(a.y, at + c, v[j], inv);
-            else store_vec<VEC>(a.y, a.y_type == NORM_BF16, at + c, v[j]);
-        }
+        for (int i = 0; i < VEC; ++i) v[j][i] *= r;
+        if (a.y_type == NORM_E4M3) store_e4m3<VEC>(a.y, at + c, left<VEC>(a.d, c), v[j], inv);
+        else store_vec<VEC>(a.y, a.y_type == NORM_BF16, at + c, left<VEC>(a.d, c), v[j]);
     }
 }
 
@@ -203,7 +229,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + lane) * VEC;
-        if (c < a.d) load_vec<VEC>(a.gamma, false, c, ga[j]);
+        if (c < a.d) load_vec<VEC>(a.gamma, false, c, left<VEC>(a.d, c), ga[j]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
     }
@@ -215,8 +241,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + lane) * VEC;
             if (c >= a.d) break;
-            load_vec<VEC>(a.h, a.h_bf16, at + c, h[j]);
-            load_vec<VEC>(a.dy, a.g_bf16, at + c, dy[j]);
+            load_vec<VEC>(a.h, a.h_bf16, at + c, left<VEC>(a.d, c), h[j]);
+            load_vec<VEC>(a.dy, a.g_bf16, at + c, left<VEC>(a.d, c), dy[j]);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -255,11 +281,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
             }
             if (a.dh) {
                 float t[VEC];
-                load_vec<VEC>(a.dh, a.g_bf16, at + c, t);
+                load_vec<VEC>(a.dh, a.g_bf16, at + c, left<VEC>(a.d, c), t);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) o[i] += t[i];
             }
-            store_vec<VEC>(a.dx, a.g_bf16, at + c, o);
+            store_vec<VEC>(a.dx, a.g_bf16, at + c, left<VEC>(a.d, c), o);
         }
     }
     float* part = a.part + (int64_t)blockIdx.x * a.d;
@@ -271,7 +297,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
                     const int c = (j * TPR + lane) * VEC;
                     if (c >= a.d) break;
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) dg[c + i] = w ? dg[c + i] + acc[j][i] : acc[j][i];
+                    for (int i = 0; i < VEC; ++i)
+                        if (c + i < a.d) dg[c + i] = w ? dg[c + i] + acc[j][i] : acc[j][i];
                 }
             __syncthreads();
         }
@@ -281,7 +308,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + lane) * VEC;
             if (c >= a.d) break;
-            store_vec<VEC>(part, false, c, acc[j]);
+            store_vec<VEC>(part, false, c, left<VEC>(a.d, c), acc[j]);
         }
     }
 }
@@ -306,8 +333,7 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* part, fl
 template <int VEC, int TPR, int NV>
 void norm_launch(const NormArgs& a, hipStream_t st) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1, THR = TPR < 256 ? 256 : TPR;
-    const int64_t need = (a.rows + RPB - 1) / RPB, most = 256 * (2048 / THR);
-    hipLaunchKernelGGL((norm_kernel<VEC, TPR, NV>), dim3((unsigned)(need < most ? need : most)), dim3(THR), 0, st, a);
+    hipLaunchKernelGGL((norm_kernel<VEC, TPR, NV>), dim3((unsigned)((a.rows + RPB - 1) / RPB)), dim3(THR), 0, st, a);
 }
 template <int VEC, int TPR, int NV>
 void norm_launch(const NormBwdArgs& a, hipStream_t st) {
@@ -326,24 +352,17 @@ hipError_t norm_dispatch(const A& a, hipStream_t st) {
     else if (n <= 512) norm_launch<VEC, 256, 2>(a, st);
     else if (n <= 1024) norm_launch<VEC, 256, 4>(a, st);
     else if (n <= 2048) norm_launch<VEC, 256, 8>(a, st);
-    else if constexpr (VEC < 8) {
-        if (n <= 4096) norm_launch<VEC, 1024, 4>(a, st);
-        else if constexpr (VEC < 4) {
-            if (n <= 8192) norm_launch<VEC, 1024, 8>(a, st);
-            else norm_launch<VEC, 1024, 16>(a, st);
-        }
-    }
+    else if constexpr (VEC < 8) norm_launch<VEC, 1024, 4>(a, st);
     return hipGetLastError();
 }
 template <typename A>
 hipError_t norm_any(const A& a, hipStream_t st) {
     if (a.d % 8 == 0) return norm_dispatch<8>(a, st);
-    if (a.d % 4 == 0) return norm_dispatch<4>(a, st);
-    return norm_dispatch<1>(a, st);
+    return norm_dispatch<4>(a, st);
 }
 
 int row_threads(int d) {
-    const int n = d % 8 == 0 ? d / 8 : d % 4 == 0 ? d / 4 : d;
+    const int n = d % 8 == 0 ? d / 8 : (d + 3) / 4;
     return n <= 256 ? 64 : n <= 2048 ? 256 : 1024;
 }
 
