@@ -17,28 +17,21 @@
 namespace sdm {
 namespace {
 
+constexpr int VEC = 8;
+
 // A thread's piece: VEC consecutive elements of a row, n of which lie in it. Rows
 // need not begin at a multiple of the piece's bytes (d odd): the vector types
 // carry the elements' alignment only, which global memory accesses allow.
 typedef uint32_t u32x4a __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u32x2a __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u32a __attribute__((aligned(1)));
 typedef uint32_t u32x2b __attribute__((ext_vector_type(2), aligned(1)));
 
-template <int VEC>
 __device__ __forceinline__ void load_vec(const void* p, bool bf16, int64_t e, int n, float (&v)[VEC]) {
     if (bf16) {
         const uint16_t* b = static_cast<const uint16_t*>(p) + e;
         if (n >= VEC) {
-            uint32_t u[VEC / 2];
-            if constexpr (VEC == 8) {
-                const u32x4a x = *reinterpret_cast<const u32x4a*>(b);
-                u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
-            } else {
-                const u32x2a x = *reinterpret_cast<const u32x2a*>(b);
-                u[0] = x.x; u[1] = x.y;
-            }
+            const u32x4a x = *reinterpret_cast<const u32x4a*>(b);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
                 v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
@@ -61,10 +54,10 @@ __device__ __forceinline__ void load_vec(const void* p, bool bf16, int64_t e, in
     }
 }
 
-// elements of the row from column c on: rows of 8 (VEC 8) have no partial piece
-template <int VEC>
+// elements of the row from column c on (TAIL false: d a multiple of VEC, no partial pieces)
+template <bool TAIL>
 __device__ __forceinline__ int left(int d, int c) {
-    return VEC == 8 ? VEC : d - c;
+    return TAIL ? d - c : VEC;
 }
 
 // nearest even; a NaN stays one
@@ -74,7 +67,6 @@ __device__ __forceinline__ uint32_t to_bf16(float f) {
     return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
-template <int VEC>
 __device__ __forceinline__ void store_vec(void* p, bool bf16, int64_t e, int n, const float (&v)[VEC]) {
     if (bf16) {
         uint16_t* b = static_cast<uint16_t*>(p) + e;
@@ -82,8 +74,7 @@ __device__ __forceinline__ void store_vec(void* p, bool bf16, int64_t e, int n, 
             uint32_t u[VEC / 2];
 #pragma unroll
             for (int i = 0; i < VEC; i += 2) u[i / 2] = to_bf16(v[i]) | to_bf16(v[i + 1]) << 16;
-            if constexpr (VEC == 8) *reinterpret_cast<u32x4a*>(b) = u32x4a{u[0], u[1], u[2], u[3]};
-            else *reinterpret_cast<u32x2a*>(b) = u32x2a{u[0], u[1]};
+            *reinterpret_cast<u32x4a*>(b) = u32x4a{u[0], u[1], u[2], u[3]};
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
@@ -103,7 +94,6 @@ __device__ __forceinline__ void store_vec(void* p, bool bf16, int64_t e, int n, 
 }
 
 // v / scale in e4m3 (nearest even), by the scale's reciprocal; |v| <= 448 scale
-template <int VEC>
 __device__ __forceinline__ void store_e4m3(void* p, int64_t e, int n, const float (&v)[VEC], float inv) {
     uint8_t* b = static_cast<uint8_t*>(p) + e;
     uint32_t u[VEC / 4];
@@ -113,8 +103,7 @@ __device__ __forceinline__ void store_e4m3(void* p, int64_t e, int n, const floa
         u[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, q, true);
     }
     if (n >= VEC) {
-        if constexpr (VEC == 8) *reinterpret_cast<u32x2b*>(b) = u32x2b{u[0], u[1]};
-        else *reinterpret_cast<u32a*>(b) = u[0];
+        *reinterpret_cast<u32x2b*>(b) = u32x2b{u[0], u[1]};
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
@@ -131,7 +120,7 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
 // Sum and maximum over the TPR threads that own a row (the same on all of them)
 template <int TPR>
 __device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*buf)[2]) {
-    for (int m = 1; m < 64; m <<= 1) {
+    for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) {
         sum += __shfl_xor(sum, m);
         mx = fmaxf(mx, __shfl_xor(mx, m));
     }
@@ -145,16 +134,16 @@ __device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*buf)[2
     }
 }
 
-template <int VEC, int TPR, int NV>
+template <int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-    __shared__ float buf[TPR / 64][2];
+    __shared__ float buf[TPR < 64 ? 1 : TPR / 64][2];
     const int lane = threadIdx.x % TPR;
     float ga[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + lane) * VEC;
-        if (c < a.d) load_vec<VEC>(a.gamma, false, c, left<VEC>(a.d, c), ga[j]);
+        if (c < a.d) load_vec(a.gamma, false, c, left<TAIL>(a.d, c), ga[j]);
     }
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
     if (row >= a.rows) return;  // TPR > 64: all of the workgroup's threads have this row
@@ -165,10 +154,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + lane) * VEC;
         if (c >= a.d) break;
-        load_vec<VEC>(a.x, a.x_bf16, at + c, left<VEC>(a.d, c), v[j]);
+        load_vec(a.x, a.x_bf16, at + c, left<TAIL>(a.d, c), v[j]);
         if (a.res) {
             float r[VEC];
-            load_vec<VEC>(a.res, a.h_bf16, at + c, left<VEC>(a.d, c), r);
+            load_vec(a.res, a.h_bf16, at + c, left<TAIL>(a.d, c), r);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[j][i] += r[i];
         }
@@ -177,7 +166,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + lane) * VEC;
         if (c >= a.d) break;
-        if (a.res) store_vec<VEC>(a.h, a.h_bf16, at + c, left<VEC>(a.d, c), v[j]);
+        if (a.res) store_vec(a.h, a.h_bf16, at + c, left<TAIL>(a.d, c), v[j]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             ss = fmaf(v[j][i], v[j][i], ss);
@@ -196,7 +185,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + lane) * VEC;
-        if constexpr (VEC == 8) {
+        if constexpr (!TAIL) {  // (groups divide d, and are multiples of 8)
             if (a.y_type == NORM_E4M3 && a.group) {  // group / 8 neighbouring lanes share a scale
                 float m = 0.f;
                 if (c < a.d)
@@ -211,25 +200,25 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
         if (c >= a.d) continue;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[j][i] *= r;
-        if (a.y_type == NORM_E4M3) store_e4m3<VEC>(a.y, at + c, left<VEC>(a.d, c), v[j], inv);
-        else store_vec<VEC>(a.y, a.y_type == NORM_BF16, at + c, left<VEC>(a.d, c), v[j]);
+        if (a.y_type == NORM_E4M3) store_e4m3(a.y, at + c, left<TAIL>(a.d, c), v[j], inv);
+        else store_vec(a.y, a.y_type == NORM_BF16, at + c, left<TAIL>(a.d, c), v[j]);
     }
 }
 
 // A block's rows' share of dgamma stays in registers, its wavefronts' shares are
 // added in order in LDS, and the blocks' rows of `part` by norm_dgamma_kernel:
 // the order of all sums follows from the sizes alone.
-template <int VEC, int TPR, int NV>
+template <int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwdArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     extern __shared__ float dg[];  // [d] (TPR < 256)
-    __shared__ float buf[TPR / 64][2];
+    __shared__ float buf[TPR < 64 ? 1 : TPR / 64][2];
     const int lane = threadIdx.x % TPR;
     float ga[NV][VEC], acc[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + lane) * VEC;
-        if (c < a.d) load_vec<VEC>(a.gamma, false, c, left<VEC>(a.d, c), ga[j]);
+        if (c < a.d) load_vec(a.gamma, false, c, left<TAIL>(a.d, c), ga[j]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
     }
@@ -241,8 +230,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + lane) * VEC;
             if (c >= a.d) break;
-            load_vec<VEC>(a.h, a.h_bf16, at + c, left<VEC>(a.d, c), h[j]);
-            load_vec<VEC>(a.dy, a.g_bf16, at + c, left<VEC>(a.d, c), dy[j]);
+            load_vec(a.h, a.h_bf16, at + c, left<TAIL>(a.d, c), h[j]);
+            load_vec(a.dy, a.g_bf16, at + c, left<TAIL>(a.d, c), dy[j]);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -254,7 +243,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
                 dot = fmaf(dy[j][i] * ga[j][i], h[j][i], dot);
             }
         }
-        for (int m = 1; m < 64; m <<= 1) {
+        for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) {
             ss += __shfl_xor(ss, m);
             dot += __shfl_xor(dot, m);
         }
@@ -281,11 +270,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
             }
             if (a.dh) {
                 float t[VEC];
-                load_vec<VEC>(a.dh, a.g_bf16, at + c, left<VEC>(a.d, c), t);
+                load_vec(a.dh, a.g_bf16, at + c, left<TAIL>(a.d, c), t);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) o[i] += t[i];
             }
-            store_vec<VEC>(a.dx, a.g_bf16, at + c, left<VEC>(a.d, c), o);
+            store_vec(a.dx, a.g_bf16, at + c, left<TAIL>(a.d, c), o);
         }
     }
     float* part = a.part + (int64_t)blockIdx.x * a.d;
@@ -308,7 +297,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + lane) * VEC;
             if (c >= a.d) break;
-            store_vec<VEC>(part, false, c, left<VEC>(a.d, c), acc[j]);
+            store_vec(part, false, c, left<TAIL>(a.d, c), acc[j]);
         }
     }
 }
@@ -330,47 +319,45 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* part, fl
     if (w == 0 && c < d) dgamma[c] = x;
 }
 
-template <int VEC, int TPR, int NV>
+template <int TPR, int NV, bool TAIL>
 void norm_launch(const NormArgs& a, hipStream_t st) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1, THR = TPR < 256 ? 256 : TPR;
-    hipLaunchKernelGGL((norm_kernel<VEC, TPR, NV>), dim3((unsigned)((a.rows + RPB - 1) / RPB)), dim3(THR), 0, st, a);
+    hipLaunchKernelGGL((norm_kernel<TPR, NV, TAIL>), dim3((unsigned)((a.rows + RPB - 1) / RPB)), dim3(THR), 0, st, a);
 }
-template <int VEC, int TPR, int NV>
+template <int TPR, int NV, bool TAIL>
 void norm_launch(const NormBwdArgs& a, hipStream_t st) {
     constexpr int THR = TPR < 256 ? 256 : TPR;
-    hipLaunchKernelGGL((norm_bwd_kernel<VEC, TPR, NV>), dim3((unsigned)a.blocks), dim3(THR), TPR < 256 ? a.d * 4 : 0, st, a);
+    hipLaunchKernelGGL((norm_bwd_kernel<TPR, NV, TAIL>), dim3((unsigned)a.blocks), dim3(THR), TPR < 256 ? a.d * 4 : 0, st, a);
 }
 
-// Threads a row: a wavefront while its pieces fit 4 a lane (no LDS exchange),
-// else 256 or 1024 threads.
-template <int VEC, typename A>
+// Threads a row: as many as it has pieces up to a wavefront (16 and 32 for the
+// narrow ones; no LDS exchange), then 256 or 1024, so that a row takes few
+// registers of each. (Backward of 2^25 elements in bf16, in TB/s, with 64 threads of
+// 4 pieces, 256 of 4 and of 8 / as here: d = 1536: 2.9 / 3.8, 8192: 2.7 / 3.8, 16384: 1.5 / 3.9.)
+int row_threads(int n) { return n <= 16 ? 16 : n <= 32 ? 32 : n <= 128 ? 64 : n <= 512 ? 256 : 1024; }
+
+template <bool TAIL, typename A>
 hipError_t norm_dispatch(const A& a, hipStream_t st) {
     const int n = (a.d + VEC - 1) / VEC;
-    if (n <= 64) norm_launch<VEC, 64, 1>(a, st);
-    else if (n <= 128) norm_launch<VEC, 64, 2>(a, st);
-    else if (n <= 256) norm_launch<VEC, 64, 4>(a, st);
-    else if (n <= 512) norm_launch<VEC, 256, 2>(a, st);
-    else if (n <= 1024) norm_launch<VEC, 256, 4>(a, st);
-    else if (n <= 2048) norm_launch<VEC, 256, 8>(a, st);
-    else if constexpr (VEC < 8) norm_launch<VEC, 1024, 4>(a, st);
+    switch (row_threads(n)) {
+        case 16: norm_launch<16, 1, TAIL>(a, st); break;
+        case 32: norm_launch<32, 1, TAIL>(a, st); break;
+        case 64: n <= 64 ? norm_launch<64, 1, TAIL>(a, st) : norm_launch<64, 2, TAIL>(a, st); break;
+        case 256: n <= 256 ? norm_launch<256, 1, TAIL>(a, st) : norm_launch<256, 2, TAIL>(a, st); break;
+        default: n <= 1024 ? norm_launch<1024, 1, TAIL>(a, st) : norm_launch<1024, 2, TAIL>(a, st);
+    }
     return hipGetLastError();
 }
 template <typename A>
 hipError_t norm_any(const A& a, hipStream_t st) {
-    if (a.d % 8 == 0) return norm_dispatch<8>(a, st);
-    return norm_dispatch<4>(a, st);
-}
-
-int row_threads(int d) {
-    const int n = d % 8 == 0 ? d / 8 : (d + 3) / 4;
-    return n <= 256 ? 64 : n <= 2048 ? 256 : 1024;
+    return a.d % VEC ? norm_dispatch<true>(a, st) : norm_dispatch<false>(a, st);
 }
 
 }  // namespace
 
 int64_t norm_bwd_blocks(int64_t rows, int d) {
-    const int tpr = row_threads(d), rpb = tpr < 256 ? 256 / tpr : 1;
-    const int64_t need = (rows + rpb - 1) / rpb, most = 256 * (tpr == 1024 ? 1 : 4);
+    const int tpr = row_threads((d + VEC - 1) / VEC), rpb = tpr < 256 ? 256 / tpr : 1;
+    const int64_t need = (rows + rpb - 1) / rpb, most = 256 * (tpr == 1024 ? 1 : 4);  // what the CUs hold at once
     return need < most ? need : most;
 }
 
