@@ -460,6 +460,14 @@ def _gpu(t0: torch.Tensor, *ts: Optional[torch.Tensor]) -> torch.device:
     return t0.device
 
 
+def _call(fn: str, d: torch.device, *args):
+    """Library call ``fn`` on the device's current stream, whatever device is current."""
+    if torch.cuda.current_device() != d.index:
+        with torch.cuda.device(d):
+            return _call(fn, d, *args)
+    _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(d).cuda_stream))
+
+
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -512,9 +520,9 @@ def sdm_dense_scan_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, al
     y = _out(y, q, (B, H, T, dv), torch.float32, "y")
     n = sdm_dense_scan_workspace_bytes(B, H, T, dk, dv)
     ws = _workspace(workspace, n, d) if n or workspace is not None else None
-    _check("sdm_dense_scan_forward", lib().sdm_dense_scan_forward(
+    _call("sdm_dense_scan_forward", d,
         _at(q), _at(k), _at(v), _dtype_code(q), _at(alpha), _at(beta), _at(S0), _at(S), _at(y),
-        B, H, T, dk, dv, _at(ws), ws.numel() if ws is not None else 0, _stream(d)))
+        B, H, T, dk, dv, _at(ws), ws.numel() if ws is not None else 0)
     return y, S
 
 
@@ -543,10 +551,10 @@ def sdm_dense_scan_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a
     for name, shp in shapes.items():
         out[name] = _out(out.get(name), q, shp, torch.float32, name)
     workspace = _workspace(workspace, sdm_dense_scan_backward_workspace_bytes(B, H, T, dk, dv), d)
-    _check("sdm_dense_scan_backward", lib().sdm_dense_scan_backward(
+    _call("sdm_dense_scan_backward", d,
         _at(q), _at(k), _at(v), _dtype_code(q), _at(alpha), _at(beta), _at(dy), _at(S0), _at(dS),
         _at(out["dq"]), _at(out["dk"]), _at(out["dv"]), _at(out["dlog_alpha"]), _at(out["dbeta"]),
-        _at(out["dS0"]), B, H, T, dk, dv, _at(workspace), workspace.numel(), _stream(d)))
+        _at(out["dS0"]), B, H, T, dk, dv, _at(workspace), workspace.numel())
     return out
 
 
@@ -586,9 +594,9 @@ def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.
     for name, (shp, dt) in want.items():
         out[name] = _out(out.get(name), x, shp, dt, name)
     h, scale = out.get("h"), out.get("scale")
-    _check("sdm_residual_norm", lib().sdm_residual_norm(
+    _call("sdm_residual_norm", d_,
         _at(x), _dtype_code(x), _at(res), _at(h), _dtype_code(x if res is None else res), _at(gamma),
-        float(eps), rows, d, _at(out["y"]), code, _at(scale), group, _stream(d_)))
+        float(eps), rows, d, _at(out["y"]), code, _at(scale), group)
     return out
 
 
@@ -614,9 +622,9 @@ def sdm_residual_norm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.T
         dgamma.zero_()
     n = lib().sdm_residual_norm_backward_workspace_bytes(rows, d)
     ws = _workspace(workspace, max(n, 0), d_)
-    _check("sdm_residual_norm_backward", lib().sdm_residual_norm_backward(
+    _call("sdm_residual_norm_backward", d_,
         _at(dy), _at(dh), _dtype_code(dy), _at(h), _dtype_code(h), _at(gamma), float(eps), rows, d,
-        _at(dx), _at(dgamma), _at(ws), ws.numel(), _stream(d_)))
+        _at(dx), _at(dgamma), _at(ws), ws.numel())
     return {"dx": dx, "dgamma": dgamma}
 
 
@@ -653,9 +661,9 @@ def sdm_balance_forward(idx: torch.Tensor, wt: torch.Tensor, N: int, mask: Optio
                           ("tokens", (1,), torch.int32), ("loss", (H,), torch.float32)):
         out[name] = _out(out.get(name), idx, shp, dt, name)
     workspace = _workspace(workspace, sdm_balance_workspace_bytes(B, H, T, K, N), d)
-    _check("sdm_balance_forward", lib().sdm_balance_forward(
+    _call("sdm_balance_forward", d,
         _at(idx), _at(wt), _at(mask), B, H, T, K, N, _at(out["counts"]), _at(out["mass"]),
-        _at(out["tokens"]), _at(out["loss"]), _at(workspace), workspace.numel(), _stream(d)))
+        _at(out["tokens"]), _at(out["loss"]), _at(workspace), workspace.numel())
     return out
 
 
@@ -671,7 +679,7 @@ def sdm_balance_backward(idx: torch.Tensor, counts: torch.Tensor, tokens: torch.
         raise ValueError("shape or dtype mismatch in sdm_balance_backward")
     _mask(mask, B, T, idx)
     dwt = _out(dwt, idx, (B, H, T, K), torch.float32, "dwt")
-    _check("sdm_balance_backward", lib().sdm_balance_backward(
+    _call("sdm_balance_backward", d,
         _at(idx), _at(mask), _at(counts), _at(tokens), _at(dloss), B, H, T, K, counts.shape[1],
-        _at(dwt), _stream(d)))
+        _at(dwt))
     return dwt
