@@ -489,7 +489,7 @@ int64_t sdm_balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t K, 
  * Selections outside [0, N) are left out; a kept weight that is NaN or beyond 2
  * in magnitude makes its head's mass and loss NaN. Masked tokens are not
  * looked at. Weights are added in fixed point (to 2^-40, or with more than 2^21
- * selections B*H*T*K to 2^-(61 - ceil(log2 B*H*T*K))), so results do not
+ * selections a head, n = B*T*K, to 2^-(61 - ceil(log2 n))), so results do not
  * depend on the order of the additions. Without tokens (B or T = 0) the outputs are zeros.
  * Supported: N <= 2^18, K <= 256, H <= 4096, B*T*K < 2^31.
  */

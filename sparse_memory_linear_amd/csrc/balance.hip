@@ -6,7 +6,7 @@
 //
 // Weights are added as whole numbers (fixed point with 2^shift to one, 64
 // bits), so the sums do not depend on the order in which they arrive. The shift
-// leaves room for as many weights of magnitude 2 as the call has entries. A
+// leaves room for as many weights of magnitude 2 as a head has selections. A
 // weight becomes one by an fp64 addition: w + 1.5 2^(52 - shift) holds the
 // rounded w 2^shift in its low bits, so the raw bits are added, and the constant's
 // are taken off count times at the end (modulo 2^64).
@@ -280,7 +280,7 @@ hipError_t launch_balance(BalanceArgs a, hipStream_t st) {
     a.part = reinterpret_cast<double*>(p += y.kept);
     a.nrange = (int)y.nrange; a.range = (int)y.range; a.nshare = y.nshare; a.share = y.share; a.nblk = (int)y.nblk;
     int bits = 0;
-    while ((int64_t)1 << bits < a.B * a.H * a.T * a.K) ++bits;
+    while ((int64_t)1 << bits < a.B * a.T * a.K) ++bits;
     a.shift = 61 - bits < 40 ? 61 - bits : 40;
     const dim3 grid((unsigned)unit_grid(a.H * a.nshare, a.nrange));
     const int bytes = a.range * 12;

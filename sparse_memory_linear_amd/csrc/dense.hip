@@ -110,7 +110,8 @@ __global__ __launch_bounds__(256) void dense_gates_kernel(DenseGatesArgs a) {
             const float y = __shfl_up(x, m);
             if (lane >= m) x += y;
         }
-        if (t >= c0) a.dlog_alpha[s * a.T + t] = at_end[c] + x;
+        // nothing passes a gate of 0: exactly 0 there, not what the sums round to
+        if (t >= c0) a.dlog_alpha[s * a.T + t] = a.alpha[s * a.T + t] == 0.f ? 0.f : at_end[c] + x;
     }
 }
 

@@ -84,6 +84,17 @@ def test_one_slot_takes_everything_and_even_use():
     assert check(even, torch.full((1, 1, 16, 4), 0.25), 64, None, torch.ones(1))["loss"][0] == 1.0
 
 
+def test_counts_beyond_16_bits_and_the_largest_table():
+    idx = torch.full((2, 2, 9000, 8), 17, dtype=torch.int32)
+    idx[0, 0, :, 0] = 3
+    got = check(idx, torch.full((2, 2, 9000, 8), 0.125), 64, None, torch.ones(2))
+    assert got["counts"][0, 17] == 2 * 9000 * 8 - 9000
+    idx, wt, m = make(1, 16, 10300, 64, 81920, 9, "some")  # 81920 counts of 16 bits: all of a CU's LDS
+    check(idx, wt, 81920, m, torch.ones(16))
+    idx, wt, m = make(1, 16, 10300, 64, 81921, 9)
+    check(idx, wt, 81921, None, torch.ones(16))
+
+
 def test_selections_out_of_range_are_left_out():
     idx, wt, m = make(2, 2, 50, 8, 100, 3, "some")
     idx[0, 0, :, 0] = 100
