@@ -33,7 +33,8 @@ constexpr int STEP_COLS = 64;  // columns of X a workgroup of the few-token form
 // The segments' own sums -> their starting states, and the state after the last
 // one. Backwards, the segments run from the last, and the end is what flows
 // into the state before token 0 (decayed by its gate).
-__global__ __launch_bounds__(256) void dense_carry_kernel(CarryArgs a) {
+__global__ __launch_bounds__(256) void dense_carry_kernel(CarryArgs s0, CarryArgs s1) {
+    const CarryArgs& a = blockIdx.y ? s1 : s0;
     const int64_t per = a.per, i4 = ((int64_t)blockIdx.x * 256 + threadIdx.x);
     if (i4 >= a.NS * per / 4) return;
     const int64_t s = i4 / (per / 4), e = i4 % (per / 4);
@@ -72,7 +73,8 @@ __global__ __launch_bounds__(256) void dense_gates_kernel(DenseGatesArgs a) {
     if (!last || a.has_dS) {
         const float4* G = reinterpret_cast<const float4*>(a.G + (seg * a.NS + s) * a.per);
         const float4* S = reinterpret_cast<const float4*>(last ? a.ST + s * a.per : a.S + ((seg + 1) * a.NS + s) * a.per);
-        for (int64_t e = tid; e < a.per / 4; e += 256) d += dot4(G[e], S[e]);
+#pragma unroll 8
+        for (int e = tid; e < (int)(a.per / 4); e += 256) d += dot4(G[e], S[e]);
         d *= last ? 1.f : a.alpha[s * a.T + hi];
     }
     d = wave_sum(d);
@@ -172,9 +174,10 @@ __global__ __launch_bounds__(256) void dense_step_kernel(DenseFwdArgs a) {
             if (r + 16 * i < a.dk) *reinterpret_cast<float4*>(a.S + st + (int64_t)(r + 16 * i) * a.dv) = X[i];
 }
 
-hipError_t launch_carry(const CarryArgs& a, hipStream_t st) {
+// b: another set of the same sizes in the same launch, or nullptr
+hipError_t launch_carry(const CarryArgs& a, const CarryArgs* b, hipStream_t st) {
     const int64_t n = a.NS * a.per / 4;
-    hipLaunchKernelGGL(dense_carry_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(dense_carry_kernel, dim3((unsigned)((n + 255) / 256), b ? 2 : 1), dim3(256), 0, st, a, b ? *b : a);
     return hipGetLastError();
 }
 
@@ -224,7 +227,7 @@ DenseBwdLayout backward_layout(int64_t NS, int64_t T, int dk, int dv) {
     y.dots = (y.slabs * NS * T * 4 + 255) / 256 * 256;
     y.nchunk = (T + DENSE_CHUNK - 1) / DENSE_CHUNK;
     y.inter = (y.slabs * NS * y.nchunk * 4 + 255) / 256 * 256;
-    y.bytes = 2 * y.states + y.one + y.decs + 2 * y.dots + 2 * y.inter;
+    y.bytes = 2 * y.states + y.one + 2 * y.decs + 2 * y.dots + 2 * y.inter;
     return y;
 }
 
@@ -259,7 +262,7 @@ hipError_t launch_dense_forward(const DenseFwdArgs& f, hipStream_t st) {
         CarryArgs c{};
         c.ws = states; c.segdec = p.segdec; c.X0 = f.S0; c.Xend = f.S;
         c.NS = f.NS; c.per = (int64_t)f.dk * f.dv; c.nseg = (int)y.nseg;
-        if ((e = launch_carry(c, st)) != hipSuccess) return e;
+        if ((e = launch_carry(c, nullptr, st)) != hipSuccess) return e;
         a.X0 = states;
     } else {
         a.X0 = f.S0; a.Xend = f.S;
@@ -271,7 +274,7 @@ hipError_t launch_dense_forward(const DenseFwdArgs& f, hipStream_t st) {
 hipError_t launch_dense_pass_on(const float* X0, float* X, int64_t NS, int64_t per, hipStream_t st) {
     CarryArgs c{};
     c.X0 = X0; c.Xend = X; c.NS = NS; c.per = per;
-    return launch_carry(c, st);
+    return launch_carry(c, nullptr, st);
 }
 
 hipError_t launch_dense_backward(const DenseBwdArgs& f, hipStream_t st) {
@@ -280,8 +283,9 @@ hipError_t launch_dense_backward(const DenseBwdArgs& f, hipStream_t st) {
     float* S = reinterpret_cast<float*>(ws);
     float* G = reinterpret_cast<float*>(ws + y.states);
     float* ST = reinterpret_cast<float*>(ws + 2 * y.states);
-    float* decs = reinterpret_cast<float*>(ws + 2 * y.states + y.one);
-    char* dots = ws + 2 * y.states + y.one + y.decs;
+    float* decS = reinterpret_cast<float*>(ws + 2 * y.states + y.one);
+    float* decG = reinterpret_cast<float*>(ws + 2 * y.states + y.one + y.decs);
+    char* dots = ws + 2 * y.states + y.one + 2 * y.decs;
     float* qdq = reinterpret_cast<float*>(dots);
     float* kdk = reinterpret_cast<float*>(dots + y.dots);
     float* inter_q = reinterpret_cast<float*>(dots + 2 * y.dots);
@@ -290,35 +294,26 @@ hipError_t launch_dense_backward(const DenseBwdArgs& f, hipStream_t st) {
     hipError_t e;
     DenseArgs base{};
     base.a = f.alpha; base.beta = f.beta; base.NS = f.NS; base.T = f.T; base.L = y.L; base.nseg = (int)y.nseg;
-    CarryArgs c{};
-    c.segdec = decs; c.NS = f.NS; c.per = per; c.nseg = (int)y.nseg; c.T = f.T; c.gate = f.alpha;
+    // S at the segments' starts and after the last, G at their ends and what flows into S0
+    DenseArgs ps = base, pg = base;
+    ps.kap = f.k; ps.omg = f.v; ps.DK = f.dk; ps.DV = f.dv; ps.Xend = S; ps.segdec = decS;
+    pg.kap = f.q; pg.omg = f.dy; pg.DK = f.dk; pg.DV = f.dv; pg.Xend = G; pg.segdec = decG;
+    if ((e = f.bf16 ? launch_dense_sg(ps, pg, st) : launch_dense_sg_f32(ps, pg, st)) != hipSuccess) return e;
+    CarryArgs cs{}, cg{};
+    cs.ws = S; cs.segdec = decS; cs.X0 = f.S0; cs.Xend = ST;
+    cs.NS = f.NS; cs.per = per; cs.nseg = (int)y.nseg; cs.T = f.T; cs.gate = f.alpha;
+    cg = cs;
+    cg.ws = G; cg.segdec = decG; cg.X0 = f.dS; cg.Xend = f.dS0; cg.rev = true;
+    if ((e = launch_carry(cs, &cg, st)) != hipSuccess) return e;
 
-    DenseArgs p = base;  // S at the segments' starts, and after the last
-    p.kap = f.k; p.omg = f.v; p.DK = f.dk; p.DV = f.dv; p.Xend = S; p.segdec = decs;
-    if ((e = f.bf16 ? launch_dense_s(p, st) : launch_dense_s_f32(p, st)) != hipSuccess) return e;
-    c.ws = S; c.X0 = f.S0; c.Xend = ST;
-    if ((e = launch_carry(c, st)) != hipSuccess) return e;
-
-    p = base;            // G at the segments' ends, and what flows into S0
-    p.kap = f.q; p.omg = f.dy; p.DK = f.dk; p.DV = f.dv; p.Xend = G; p.segdec = decs;
-    if ((e = f.bf16 ? launch_dense_g(p, st) : launch_dense_g_f32(p, st)) != hipSuccess) return e;
-    c.ws = G; c.X0 = f.dS; c.Xend = f.dS0; c.rev = true;
-    if ((e = launch_carry(c, st)) != hipSuccess) return e;
-
-    p = base;            // dq, and q . dq
-    p.xi = f.dy; p.kap = f.v; p.omg = f.k; p.DK = f.dv; p.DV = f.dk; p.X0 = S;
-    p.out = f.dq; p.dot = qdq; p.inter = inter_q; p.with = f.q;
-    if ((e = f.bf16 ? launch_dense_dq(p, st) : launch_dense_dq_f32(p, st)) != hipSuccess) return e;
-
-    p = base;            // dk, and k . dk / beta
-    p.xi = f.v; p.kap = f.dy; p.omg = f.q; p.DK = f.dv; p.DV = f.dk; p.X0 = G;
-    p.out = f.dk_out; p.dot = kdk; p.inter = inter_k; p.with = f.k;
-    if ((e = f.bf16 ? launch_dense_dk(p, st) : launch_dense_dk_f32(p, st)) != hipSuccess) return e;
-
-    p = base;            // dv
-    p.xi = f.k; p.kap = f.q; p.omg = f.dy; p.DK = f.dk; p.DV = f.dv; p.X0 = G;
-    p.out = f.dv_out;
-    if ((e = f.bf16 ? launch_dense_dv(p, st) : launch_dense_dv_f32(p, st)) != hipSuccess) return e;
+    DenseArgs pq = base, pk = base, pv = base;
+    pq.xi = f.dy; pq.kap = f.v; pq.omg = f.k; pq.DK = f.dv; pq.DV = f.dk; pq.X0 = S;  // dq, and q . dq
+    pq.out = f.dq; pq.dot = qdq; pq.inter = inter_q; pq.with = f.q;
+    pk.xi = f.v; pk.kap = f.dy; pk.omg = f.q; pk.DK = f.dv; pk.DV = f.dk; pk.X0 = G;  // dk, and k . dk / beta
+    pk.out = f.dk_out; pk.dot = kdk; pk.inter = inter_k; pk.with = f.k;
+    pv.xi = f.k; pv.kap = f.q; pv.omg = f.dy; pv.DK = f.dk; pv.DV = f.dv; pv.X0 = G;  // dv
+    pv.out = f.dv_out;
+    if ((e = f.bf16 ? launch_dense_grads(pq, pk, pv, st) : launch_dense_grads_f32(pq, pk, pv, st)) != hipSuccess) return e;
 
     DenseGatesArgs g{};
     g.G = G; g.S = S; g.ST = ST; g.qdq = qdq; g.kdk = kdk; g.alpha = f.alpha; g.beta = f.beta;

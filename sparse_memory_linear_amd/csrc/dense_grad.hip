@@ -1,11 +1,10 @@
-// dense_grad.hip -- the dense recurrence's passes that mix bf16 rows with the fp32 rows of dy.
+// dense_grad.hip -- the dense recurrence's passes for the gradients, over bf16 rows (dy's are fp32).
 #include "dense_pass.h"
 
 namespace sdm {
 
-hipError_t launch_dense_dq(const DenseArgs& a, hipStream_t st) { return launch_dense_sized<3, 1, 1, true, false, true>(a, st); }
-hipError_t launch_dense_dk(const DenseArgs& a, hipStream_t st) { return launch_dense_sized<1, 3, 1, true, true, true>(a, st); }
-hipError_t launch_dense_dv(const DenseArgs& a, hipStream_t st) { return launch_dense_sized<1, 1, 3, true, true, false>(a, st); }
-hipError_t launch_dense_g(const DenseArgs& a, hipStream_t st) { return launch_dense_sized<1, 1, 3, false, true, false>(a, st); }
+hipError_t launch_dense_grads(const DenseArgs& q, const DenseArgs& k, const DenseArgs& v, hipStream_t st) {
+    return dense_grads<1>(q, k, v, st);
+}
 
 }  // namespace sdm

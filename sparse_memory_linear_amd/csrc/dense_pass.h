@@ -30,6 +30,8 @@
 // kap xi^T is written by the wavefront that computes it in the order in which the
 // others read it.
 #pragma once
+#include <type_traits>
+
 #include "sdm_buffer.h"
 #include "sdm_internal.h"
 
@@ -163,23 +165,19 @@ struct DensePass {
     static constexpr int BUF = 2 * ROWS + PBYTES + FLOATS * 4 <= 80 * 1024 ? 2 : 1;
     static constexpr int O_P = BUF * ROWS, O_F = O_P + PBYTES, LDS = O_F + FLOATS * 4;
     // wavefronts per SIMD: two workgroups of 8 on a CU where X takes 32 registers a lane
-    static constexpr int OCC = NW == 8 && DKT <= 8 ? 4 : 2;
+    static constexpr int OCC = NW == 8 && DKT <= 8 && !(DOT || NX == 3 || NO == 3 && OUT) ? 4 : 2;
     static_assert(NT == 2, "tiles of P are numbered for 2 blocks");
     static_assert(LDS <= 160 * 1024, "a workgroup's LDS");
 };
 
+// One workgroup's pass: stream and segment us, column slab `slab`.
 template <class P>
-__global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a) {
+__device__ __forceinline__ void dense_pass(const DenseArgs& a, int64_t us, int slab, char* const lds) {
     constexpr int DKT = P::DKT, NCT = P::NCT, C = P::C, NT = P::NT, THR = P::THR, DKP = P::DKP, SV = P::SV, NW = P::NW;
-    extern __shared__ __align__(16) char lds[];
     char* const Pf = lds + P::O_P;
     float* const dec = reinterpret_cast<float*>(lds + P::O_F);
     float* const dots = dec + 2 * P::DEC;  // [2][NW][C + 1]: per wavefront, the rows' products, and their part from X_start
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), m16 = lane & 15, g4 = lane >> 4;
-    int64_t us;
-    int slab;
-    block_unit((int)blockIdx.x, a.NS * a.nseg, a.nslab, us, slab);
-    if (us >= a.NS * a.nseg) return;
     const int64_t s = us / a.nseg;  // stream
     const int seg = (int)(us % a.nseg);
     const int64_t lo = (int64_t)seg * a.L, hi = lo + a.L < a.T ? lo + a.L : a.T;
@@ -208,8 +206,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
             }
         }
 
-    constexpr int KP = C * (DKP / 8) / THR, VP = (C * (SV / 8) + THR - 1) / THR;  // pieces a thread
-    static_assert(C * (DKP / 8) % THR == 0, "whole pieces");
+    constexpr int KP = (C * (DKP / 8) + THR - 1) / THR, VP = (C * (SV / 8) + THR - 1) / THR;  // pieces a thread
     Piece<P::NK> pk[KP];
     Piece<P::NX> px[P::OUT ? KP : 1];
     Piece<P::NO> po[VP];
@@ -232,7 +229,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
         const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
-        ek[i] = q < a.DK ? (uint32_t)(row(j, C) * a.DK + q) : FAR;
+        ek[i] = j < C && q < a.DK ? (uint32_t)(row(j, C) * a.DK + q) : FAR;
     }
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
@@ -280,6 +277,7 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
             const int e = tid + i * THR, j = e / (DKP / 8), q = e % (DKP / 8) * 8;
+            if (C * (DKP / 8) % THR != 0 && j >= C) continue;
             pk[i].store(buf + P::O_KA + j * P::RK + q * 2, P::PK);
             if constexpr (P::OUT) px[i].store(buf + P::O_XI + j * P::RK + q * 2, P::PK);
         }
@@ -556,11 +554,68 @@ __global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a)
     if (!P::OUT && slab == 0 && tid == 0) a.segdec[seg * a.NS + s] = segdec;
 }
 
+// Workgroups of the same stream and segment go to one XCD, one after the other
+// (their rows are largely the same).
 template <class P>
-hipError_t launch_dense_pass(DenseArgs a, hipStream_t st) {
+__global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a) {
+    extern __shared__ __align__(16) char lds[];
+    int64_t us;
+    int slab;
+    block_unit((int)blockIdx.x, a.NS * a.nseg, a.nslab, us, slab);
+    if (us < a.NS * a.nseg) dense_pass<P>(a, us, slab, lds);
+}
+
+constexpr int max2(int a, int b) { return a > b ? a : b; }
+
+// Two or three passes in one launch: a's slabs, then b's, then c's.
+template <class P1, class P2>
+__global__ __launch_bounds__(P1::THR, P1::OCC) void dense_two_kernel(DenseArgs a, DenseArgs b) {
+    static_assert(P1::THR == P2::THR && P1::OCC == P2::OCC, "one launch");
+    extern __shared__ __align__(16) char lds[];
+    int64_t us;
+    int u;
+    block_unit((int)blockIdx.x, a.NS * a.nseg, a.nslab + b.nslab, us, u);
+    if (us >= a.NS * a.nseg) return;
+    if (u < a.nslab) dense_pass<P1>(a, us, u, lds);
+    else dense_pass<P2>(b, us, u - a.nslab, lds);
+}
+template <class P1, class P2, class P3>
+__global__ __launch_bounds__(P1::THR, P1::OCC) void dense_three_kernel(DenseArgs a, DenseArgs b, DenseArgs c) {
+    static_assert(P1::THR == P2::THR && P1::THR == P3::THR && P1::OCC == P2::OCC && P1::OCC == P3::OCC, "one launch");
+    extern __shared__ __align__(16) char lds[];
+    int64_t us;
+    int u;
+    block_unit((int)blockIdx.x, a.NS * a.nseg, a.nslab + b.nslab + c.nslab, us, u);
+    if (us >= a.NS * a.nseg) return;
+    if (u < a.nslab) dense_pass<P1>(a, us, u, lds);
+    else if (u < a.nslab + b.nslab) dense_pass<P2>(b, us, u - a.nslab, lds);
+    else dense_pass<P3>(c, us, u - a.nslab - b.nslab, lds);
+}
+
+template <class P>
+DenseArgs dense_slabs(DenseArgs a) {
     a.nslab = (a.DV + P::SV - 1) / P::SV;
     a.nchunk = (a.T + P::C - 1) / P::C;
+    return a;
+}
+template <class P>
+hipError_t launch_passes(const DenseArgs& a0, hipStream_t st) {
+    const DenseArgs a = dense_slabs<P>(a0);
     hipLaunchKernelGGL(dense_pass_kernel<P>, dim3((unsigned)unit_grid(a.NS * a.nseg, a.nslab)), dim3(P::THR), P::LDS, st, a);
+    return hipGetLastError();
+}
+template <class P1, class P2>
+hipError_t launch_passes(const DenseArgs& a0, const DenseArgs& b0, hipStream_t st) {
+    const DenseArgs a = dense_slabs<P1>(a0), b = dense_slabs<P2>(b0);
+    hipLaunchKernelGGL((dense_two_kernel<P1, P2>), dim3((unsigned)unit_grid(a.NS * a.nseg, a.nslab + b.nslab)), dim3(P1::THR),
+                       max2(P1::LDS, P2::LDS), st, a, b);
+    return hipGetLastError();
+}
+template <class P1, class P2, class P3>
+hipError_t launch_passes(const DenseArgs& a0, const DenseArgs& b0, const DenseArgs& c0, hipStream_t st) {
+    const DenseArgs a = dense_slabs<P1>(a0), b = dense_slabs<P2>(b0), c = dense_slabs<P3>(c0);
+    hipLaunchKernelGGL((dense_three_kernel<P1, P2, P3>), dim3((unsigned)unit_grid(a.NS * a.nseg, a.nslab + b.nslab + c.nslab)),
+                       dim3(P1::THR), max2(P1::LDS, max2(P2::LDS, P3::LDS)), st, a, b, c);
     return hipGetLastError();
 }
 
@@ -568,17 +623,53 @@ hipError_t launch_dense_pass(DenseArgs a, hipStream_t st) {
 // the contracted width are then done once for all of them).
 constexpr int dense_slab(int dv) { return dv <= 64 ? 64 : 128; }
 
-template <int NX, int NK, int NO, bool OUT, bool REV, bool DOT>
-hipError_t launch_dense_sized(const DenseArgs& a, hipStream_t st) {
-    const bool wide = dense_slab(a.DV) == 128;
-    if (a.DK <= 64)
-        return wide ? launch_dense_pass<DensePass<4, 2, 4, NX, NK, NO, OUT, REV, DOT>>(a, st)
-                    : launch_dense_pass<DensePass<4, 1, 4, NX, NK, NO, OUT, REV, DOT>>(a, st);
-    if (a.DK <= 128)
-        return wide ? launch_dense_pass<DensePass<8, (DOT ? 2 : 1), (DOT ? 4 : 8), NX, NK, NO, OUT, REV, DOT>>(a, st)
-                    : launch_dense_pass<DensePass<8, 1, 4, NX, NK, NO, OUT, REV, DOT>>(a, st);
-    return wide ? launch_dense_pass<DensePass<16, 1, 8, NX, NK, NO, OUT, REV, DOT>>(a, st)
-                : launch_dense_pass<DensePass<16, 1, 4, NX, NK, NO, OUT, REV, DOT>>(a, st);
+// f(contracted width's tiles, column tiles a wavefront, wavefronts), for a pass of its own
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <class F>
+hipError_t dense_sized(int DK, int DV, F f) {
+    const bool wide = dense_slab(DV) == 128;
+    if (DK <= 64) return wide ? f(Int<4>{}, Int<2>{}, Int<4>{}) : f(Int<4>{}, Int<1>{}, Int<4>{});
+    if (DK <= 128) return wide ? f(Int<8>{}, Int<1>{}, Int<8>{}) : f(Int<8>{}, Int<1>{}, Int<4>{});
+    return wide ? f(Int<16>{}, Int<1>{}, Int<8>{}) : f(Int<16>{}, Int<1>{}, Int<4>{});
+}
+
+template <int NX, int NK, int NO>
+hipError_t dense_y(const DenseArgs& a, hipStream_t st) {
+    return dense_sized(a.DK, a.DV, [&](auto t, auto c, auto w) {
+        return launch_passes<DensePass<t(), c(), w(), NX, NK, NO, true, false, false>>(a, st);
+    });
+}
+template <int NK, int NO>
+hipError_t dense_s(const DenseArgs& a, hipStream_t st) {
+    return dense_sized(a.DK, a.DV, [&](auto t, auto c, auto w) {
+        return launch_passes<DensePass<t(), c(), w(), 1, NK, NO, false, false, false>>(a, st);
+    });
+}
+// the segments' own S and G (kap planes NK, and omg planes of S and of G)
+template <int NK, int NOS, int NOG>
+hipError_t dense_sg(const DenseArgs& s, const DenseArgs& g, hipStream_t st) {
+    return dense_sized(s.DK, s.DV, [&](auto t, auto c, auto w) {
+        return launch_passes<DensePass<t(), c(), w(), 1, NK, NOS, false, false, false>,
+                             DensePass<t(), c(), w(), 1, NK, NOG, false, true, false>>(s, g, st);
+    });
+}
+// dq, dk and dv: NR planes of the rows q, k and v, three of dy's. dq and dk contract the
+// value width (tiles TV) and put out the key width; dv the other way round (tiles TK). In one
+// launch all have 4 wavefronts, or 8 where a width passes 128.
+template <int NR, int TK, int TV>
+hipError_t dense_grads_t(const DenseArgs& q, const DenseArgs& k, const DenseArgs& v, hipStream_t st) {
+    constexpr int W = TK == 16 || TV == 16 ? 8 : 4;
+    constexpr int CK = W == 8 || TK == 4 ? 1 : 2, CV = W == 8 || TV == 4 ? 1 : 2;  // column tiles a wavefront
+    return launch_passes<DensePass<TV, CK, W, 3, NR, NR, true, false, true>, DensePass<TV, CK, W, NR, 3, NR, true, true, true>,
+                         DensePass<TK, CV, W, NR, NR, 3, true, true, false>>(q, k, v, st);
+}
+template <int NR>
+hipError_t dense_grads(const DenseArgs& q, const DenseArgs& k, const DenseArgs& v, hipStream_t st) {
+    auto tiles = [](int d, auto f) { return d <= 64 ? f(Int<4>{}) : d <= 128 ? f(Int<8>{}) : f(Int<16>{}); };
+    return tiles(v.DK, [&](auto tk) {
+        return tiles(q.DK, [&](auto tv) { return dense_grads_t<NR, tk(), tv()>(q, k, v, st); });
+    });
 }
 
 }  // namespace

@@ -175,19 +175,16 @@ struct DenseGatesArgs {
 };
 // Tokens per chunk of the dense recurrence.
 constexpr int DENSE_CHUNK = 32;
-// Its passes, by what they give, over bf16 rows (dy's are fp32) or fp32 ones
+// Its passes, by what they give (S's and G's segments, and all the gradients, in one
+// launch), over bf16 rows (dy's are fp32) or fp32 ones
 hipError_t launch_dense_y(const DenseArgs& a, hipStream_t st);
 hipError_t launch_dense_y_f32(const DenseArgs& a, hipStream_t st);
 hipError_t launch_dense_s(const DenseArgs& a, hipStream_t st);
 hipError_t launch_dense_s_f32(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_g(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_g_f32(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_dq(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_dq_f32(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_dk(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_dk_f32(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_dv(const DenseArgs& a, hipStream_t st);
-hipError_t launch_dense_dv_f32(const DenseArgs& a, hipStream_t st);
+hipError_t launch_dense_sg(const DenseArgs& s, const DenseArgs& g, hipStream_t st);
+hipError_t launch_dense_sg_f32(const DenseArgs& s, const DenseArgs& g, hipStream_t st);
+hipError_t launch_dense_grads(const DenseArgs& q, const DenseArgs& k, const DenseArgs& v, hipStream_t st);
+hipError_t launch_dense_grads_f32(const DenseArgs& q, const DenseArgs& k, const DenseArgs& v, hipStream_t st);
 struct DenseFwdArgs {
     const void* q; const void* k; const void* v; bool bf16;
     const float* alpha; const float* beta;
