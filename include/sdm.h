@@ -366,7 +366,8 @@ int sdm_output_gate(const float* y, const float* gamma, const void* g, int g_dty
 
 /*
  * sdm_dense_scan_workspace_bytes -- device workspace sdm_dense_scan_forward
- * needs (0: none, e.g. when there is no work or T <= 8; -1: invalid sizes).
+ * needs (0: none, as when there is no work, for short calls or many streams; -1:
+ * invalid sizes).
  */
 int64_t sdm_dense_scan_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
 

@@ -121,8 +121,10 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t e) {
     return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[e] << 16) : static_cast<const float*>(p)[e];
 }
 
-// A few tokens a call (decoding): the state is read and written once, as rows
-// of 64 columns; thread (r, c) holds rows r + 16 i, columns 4c .. 4c + 3.
+// One token (decoding): the state is read and written once, as rows of 64
+// columns; thread (r, c) takes rows r + 16 i, columns 4c .. 4c + 3. HBM-bound: 2048
+// states of 128 x 128 in 54 us, 5.0 TB/s with part of them in the memory-side cache. (The
+// chunked form takes 60 us there and 57 for two tokens, where walking them took 67.)
 template <int NR>
 __global__ __launch_bounds__(256) void dense_step_kernel(DenseFwdArgs a) {
     __shared__ float red[16][STEP_COLS];
@@ -132,46 +134,39 @@ __global__ __launch_bounds__(256) void dense_step_kernel(DenseFwdArgs a) {
     const int col = slab * STEP_COLS + 4 * c;
     const bool col_ok = col < a.dv;
     const int64_t st = s * (int64_t)a.dk * a.dv + col;
+    const float g = a.alpha[s], b = a.beta[s];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), y = v;
+    if (col_ok) {
+        if (a.bf16) {
+            const uint2 p = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + s * a.dv + col);
+            v = make_float4(b * bf_lo(p.x), b * bf_hi(p.x), b * bf_lo(p.y), b * bf_hi(p.y));
+        } else {
+            v = f4_scale(b, *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + s * a.dv + col));
+        }
+    }
     float4 X[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         X[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (a.S0 && col_ok && r + 16 * i < a.dk) X[i] = *reinterpret_cast<const float4*>(a.S0 + st + (int64_t)(r + 16 * i) * a.dv);
     }
-    for (int64_t t = s * a.T; t < (s + 1) * a.T; ++t) {
-        const float g = a.alpha[t], b = a.beta[t];
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), y = v;
-        if (col_ok) {
-            if (a.bf16) {
-                const uint2 p = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + t * a.dv + col);
-                v = make_float4(b * bf_lo(p.x), b * bf_hi(p.x), b * bf_lo(p.y), b * bf_hi(p.y));
-            } else {
-                const float4 p = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + t * a.dv + col);
-                v = make_float4(b * p.x, b * p.y, b * p.z, b * p.w);
-            }
-        }
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            if (r + 16 * i >= a.dk) break;
-            const float k = load1(a.k, a.bf16, t * a.dk + r + 16 * i);
-            const float q = load1(a.q, a.bf16, t * a.dk + r + 16 * i);
-            X[i] = make_float4(fmaf(g, X[i].x, k * v.x), fmaf(g, X[i].y, k * v.y), fmaf(g, X[i].z, k * v.z), fmaf(g, X[i].w, k * v.w));
-            y = make_float4(fmaf(q, X[i].x, y.x), fmaf(q, X[i].y, y.y), fmaf(q, X[i].z, y.z), fmaf(q, X[i].w, y.w));
-        }
-        __syncthreads();
-        *reinterpret_cast<float4*>(&red[r][4 * c]) = y;
-        __syncthreads();
-        if (tid < STEP_COLS && slab * STEP_COLS + tid < a.dv) {
-            float o = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o += red[i][tid];
-            a.y[t * a.dv + slab * STEP_COLS + tid] = o;
-        }
+    for (int i = 0; i < NR; ++i) {
+        const int row = r + 16 * i;
+        if (row >= a.dk) break;
+        const float k = load1(a.k, a.bf16, s * a.dk + row), q = load1(a.q, a.bf16, s * a.dk + row);
+        X[i] = make_float4(fmaf(g, X[i].x, k * v.x), fmaf(g, X[i].y, k * v.y), fmaf(g, X[i].z, k * v.z), fmaf(g, X[i].w, k * v.w));
+        y = f4_fma(q, X[i], y);
+        if (a.S && col_ok) *reinterpret_cast<float4*>(a.S + st + (int64_t)row * a.dv) = X[i];
     }
-    if (a.S && col_ok)
+    *reinterpret_cast<float4*>(&red[r][4 * c]) = y;
+    __syncthreads();
+    if (tid < STEP_COLS && slab * STEP_COLS + tid < a.dv) {
+        float o = 0.f;
 #pragma unroll
-        for (int i = 0; i < NR; ++i)
-            if (r + 16 * i < a.dk) *reinterpret_cast<float4*>(a.S + st + (int64_t)(r + 16 * i) * a.dv) = X[i];
+        for (int i = 0; i < 16; ++i) o += red[i][tid];
+        a.y[s * a.dv + slab * STEP_COLS + tid] = o;
+    }
 }
 
 // b: another set of the same sizes in the same launch, or nullptr
@@ -180,13 +175,6 @@ hipError_t launch_carry(const CarryArgs& a, const CarryArgs* b, hipStream_t st) 
     hipLaunchKernelGGL(dense_carry_kernel, dim3((unsigned)((n + 255) / 256), b ? 2 : 1), dim3(256), 0, st, a, b ? *b : a);
     return hipGetLastError();
 }
-
-// Tokens of one call up to which the state is walked token by token.
-constexpr int64_t STEP_TOKENS = 8;
-
-// Tokens up to which a forward call is one segment a stream: one launch, where
-// segments take three.
-constexpr int64_t ONE_SEGMENT = 256;
 
 // Segment length: enough workgroups for two per CU (a state per segment and
 // stream, so some 512 of them whatever the length), of at least two chunks.
@@ -204,9 +192,15 @@ struct DenseLayout {
 };
 DenseLayout forward_layout(int64_t NS, int64_t T, int dk, int dv) {
     DenseLayout y{};
-    y.L = T <= ONE_SEGMENT ? T : segment_len(NS, T, dv, T);
+    y.L = segment_len(NS, T, dv, T);
     y.nseg = (T + y.L - 1) / y.L;
-    if (y.nseg == 1) return DenseLayout{T, 1, 0, 0, 0};
+    // One segment a stream (one launch) unless segments are quicker. In us: a chunk takes 2.5, in the
+    // first pass some 0.6 of that; two more launches 6; a segment's state is moved four times at 4.75
+    // TB/s. (Measured, one / segments: 8 streams of 128 x 128, T = 128: 15 / 17, 256: 25 / 18; 64 streams,
+    // 384: 36 / 36, 1024: 84 / 54; of 256 x 256, 512: 65 / 99, 1024: 123 / 144.)
+    const double one = 2.5 * T / DENSE_CHUNK;
+    const double many = 4.0 * y.L / DENSE_CHUNK + 6 + 16e-6 * y.nseg * NS * dk * dv / 4.75;
+    if (y.nseg == 1 || one <= many) return DenseLayout{T, 1, 0, 0, 0};
     y.states = y.nseg * NS * (int64_t)dk * dv * 4;
     y.decs = (y.nseg * NS * 4 + 255) / 256 * 256;
     y.bytes = y.states + y.decs;
@@ -240,7 +234,7 @@ int64_t dense_backward_workspace_bytes(int64_t NS, int64_t T, int dk, int dv) {
 
 hipError_t launch_dense_forward(const DenseFwdArgs& f, hipStream_t st) {
     const DenseLayout y = forward_layout(f.NS, f.T, f.dk, f.dv);
-    if (f.T <= STEP_TOKENS) {
+    if (f.T == 1) {
         const dim3 grid((unsigned)(f.NS * ((f.dv + STEP_COLS - 1) / STEP_COLS)));
         if (f.dk <= 64) hipLaunchKernelGGL(dense_step_kernel<4>, grid, dim3(256), 0, st, f);
         else if (f.dk <= 128) hipLaunchKernelGGL(dense_step_kernel<8>, grid, dim3(256), 0, st, f);
