@@ -164,8 +164,6 @@ struct DensePass {
     // keeps a second workgroup off the CU
     static constexpr int BUF = 2 * ROWS + PBYTES + FLOATS * 4 <= 80 * 1024 ? 2 : 1;
     static constexpr int O_P = BUF * ROWS, O_F = O_P + PBYTES, LDS = O_F + FLOATS * 4;
-    // wavefronts per SIMD: two workgroups of 8 on a CU where X takes 32 registers a lane
-    static constexpr int OCC = NW == 8 && DKT <= 8 && !(DOT || NX == 3 || NO == 3 && OUT) ? 4 : 2;
     static_assert(NT == 2, "tiles of P are numbered for 2 blocks");
     static_assert(LDS <= 160 * 1024, "a workgroup's LDS");
 };
@@ -557,7 +555,7 @@ __device__ __forceinline__ void dense_pass(const DenseArgs& a, int64_t us, int s
 // Workgroups of the same stream and segment go to one XCD, one after the other
 // (their rows are largely the same).
 template <class P>
-__global__ __launch_bounds__(P::THR, P::OCC) void dense_pass_kernel(DenseArgs a) {
+__global__ __launch_bounds__(P::THR, 2) void dense_pass_kernel(DenseArgs a) {
     extern __shared__ __align__(16) char lds[];
     int64_t us;
     int slab;
@@ -569,8 +567,8 @@ constexpr int max2(int a, int b) { return a > b ? a : b; }
 
 // Two or three passes in one launch: a's slabs, then b's, then c's.
 template <class P1, class P2>
-__global__ __launch_bounds__(P1::THR, P1::OCC) void dense_two_kernel(DenseArgs a, DenseArgs b) {
-    static_assert(P1::THR == P2::THR && P1::OCC == P2::OCC, "one launch");
+__global__ __launch_bounds__(P1::THR, 2) void dense_two_kernel(DenseArgs a, DenseArgs b) {
+    static_assert(P1::THR == P2::THR, "one launch");
     extern __shared__ __align__(16) char lds[];
     int64_t us;
     int u;
@@ -580,8 +578,8 @@ __global__ __launch_bounds__(P1::THR, P1::OCC) void dense_two_kernel(DenseArgs a
     else dense_pass<P2>(b, us, u - a.nslab, lds);
 }
 template <class P1, class P2, class P3>
-__global__ __launch_bounds__(P1::THR, P1::OCC) void dense_three_kernel(DenseArgs a, DenseArgs b, DenseArgs c) {
-    static_assert(P1::THR == P2::THR && P1::THR == P3::THR && P1::OCC == P2::OCC && P1::OCC == P3::OCC, "one launch");
+__global__ __launch_bounds__(P1::THR, 2) void dense_three_kernel(DenseArgs a, DenseArgs b, DenseArgs c) {
+    static_assert(P1::THR == P2::THR && P1::THR == P3::THR, "one launch");
     extern __shared__ __align__(16) char lds[];
     int64_t us;
     int u;
@@ -623,14 +621,17 @@ hipError_t launch_passes(const DenseArgs& a0, const DenseArgs& b0, const DenseAr
 // the contracted width are then done once for all of them).
 constexpr int dense_slab(int dv) { return dv <= 64 ? 64 : 128; }
 
-// f(contracted width's tiles, column tiles a wavefront, wavefronts), for a pass of its own
+// f(contracted width's tiles, column tiles a wavefront, wavefronts), for a pass of its own.
+// Four wavefronts of 32 columns read each operand half as often as eight of 16, and hold
+// twice the state (4x8x8192 tokens, 128 x 128, bf16: y in 85 / 86 us, T = 131072 in one sequence
+// 472 / 484 in all); from 128 to 256 rows of state a lane's registers allow 16 columns.
 template <int N>
 using Int = std::integral_constant<int, N>;
 template <class F>
 hipError_t dense_sized(int DK, int DV, F f) {
     const bool wide = dense_slab(DV) == 128;
     if (DK <= 64) return wide ? f(Int<4>{}, Int<2>{}, Int<4>{}) : f(Int<4>{}, Int<1>{}, Int<4>{});
-    if (DK <= 128) return wide ? f(Int<8>{}, Int<1>{}, Int<8>{}) : f(Int<8>{}, Int<1>{}, Int<4>{});
+    if (DK <= 128) return wide ? f(Int<8>{}, Int<2>{}, Int<4>{}) : f(Int<8>{}, Int<1>{}, Int<4>{});
     return wide ? f(Int<16>{}, Int<1>{}, Int<8>{}) : f(Int<16>{}, Int<1>{}, Int<4>{});
 }
 
@@ -656,10 +657,12 @@ hipError_t dense_sg(const DenseArgs& s, const DenseArgs& g, hipStream_t st) {
 }
 // dq, dk and dv: NR planes of the rows q, k and v, three of dy's. dq and dk contract the
 // value width (tiles TV) and put out the key width; dv the other way round (tiles TK). In one
-// launch all have 4 wavefronts, or 8 where a width passes 128.
+// launch all have 4 wavefronts, or 8 where a width passes 128, or where fp32 rows of 128 leave
+// room for one workgroup on a CU (2x8x4096 tokens, 128 x 128, fp32, all of the backward: 263 us
+// with 8, 301 with 4; of 64 x 128: 127 with 8, 98 with 4).
 template <int NR, int TK, int TV>
 hipError_t dense_grads_t(const DenseArgs& q, const DenseArgs& k, const DenseArgs& v, hipStream_t st) {
-    constexpr int W = TK == 16 || TV == 16 ? 8 : 4;
+    constexpr int W = TK == 16 || TV == 16 || (NR == 3 && TK == 8 && TV == 8) ? 8 : 4;
     constexpr int CK = W == 8 || TK == 4 ? 1 : 2, CV = W == 8 || TV == 4 ? 1 : 2;  // column tiles a wavefront
     return launch_passes<DensePass<TV, CK, W, 3, NR, NR, true, false, true>, DensePass<TV, CK, W, NR, 3, NR, true, true, true>,
                          DensePass<TK, CV, W, NR, NR, 3, true, true, false>>(q, k, v, st);
