@@ -74,7 +74,8 @@ __global__ __launch_bounds__(ADD_THREADS) void balance_add_kernel(BalanceArgs a)
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 const uint32_t e = e0 + k * ADD_THREADS;
-                const bool in = e < n / W && on(e * W);
+                const bool in = e < n / W;
+                const bool kept = in && on(e * W);  // (loaded beside the selections, not in front of them)
                 if constexpr (VEC) {
                     int4 x = make_int4(-1, -1, -1, -1);
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -82,10 +83,12 @@ __global__ __launch_bounds__(ADD_THREADS) void balance_add_kernel(BalanceArgs a)
                         x = reinterpret_cast<const int4*>(a.idx + at)[e];
                         y = reinterpret_cast<const float4*>(a.wt + at)[e];
                     }
+                    if (!kept) x = make_int4(-1, -1, -1, -1);
                     i[k][0] = x.x; i[k][1] = x.y; i[k][2] = x.z; i[k][3] = x.w;
                     w[k][0] = y.x; w[k][1] = y.y; w[k][2] = y.z; w[k][3] = y.w;
                 } else {
                     i[k][0] = in ? a.idx[at + e] : -1;
+                    if (!kept) i[k][0] = -1;
                     w[k][0] = in ? a.wt[at + e] : 0.f;
                 }
             }

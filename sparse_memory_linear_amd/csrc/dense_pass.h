@@ -343,10 +343,16 @@ __device__ __forceinline__ void dense_pass(const DenseArgs& a, int64_t us, int s
         const float* const fin = fsuf + C;
         const float* const fo = fin + C;
         const float tot0 = fo[C], tot1 = fo[C + 1], total = tot0 * tot1;
-        auto with = [&](int j, int c) {  // `with` at row j, this lane's column
-            const char* const p = buf + P::O_WI + j * P::RW + ((w * NCT + c) * 16 + m16) * P::WITH;
-            if constexpr (P::WITH == 2) return bf_lo(*reinterpret_cast<const uint16_t*>(p));
-            else return *reinterpret_cast<const float*>(p);
+        // `with` at rows 16 t + 4 g4 + i of this lane's column (bf16: by a transposing read)
+        auto with = [&](int t, int c, float (&v)[4]) {
+            const char* const p = buf + P::O_WI + (t * 16 + 4 * g4) * P::RW + (w * NCT + c) * 16 * P::WITH;
+            if constexpr (P::WITH == 2) {
+                const uint2 u = read_tr(p + (m16 >> 2) * P::RW + (m16 & 3) * 8);
+                v[0] = bf_lo(u.x); v[1] = bf_hi(u.x); v[2] = bf_lo(u.y); v[3] = bf_hi(u.y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float*>(p + i * P::RW + m16 * 4);
+            }
         };
         f32x4_t acc[P::OUT ? NT : 1][NCT];
         if constexpr (P::OUT) {
@@ -420,12 +426,14 @@ __device__ __forceinline__ void dense_pass(const DenseArgs& a, int64_t us, int s
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[t][c][i] *= f[i];
                 if constexpr (P::DOT) {  // what the chunk's start gives to xi_t X_t . with_t, summed over the chunk
+                    const float4 o4 = *reinterpret_cast<const float4*>(fo + t * 16 + 4 * g4);
+                    const float o[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float d = 0.f;
+                    for (int c = 0; c < NCT; ++c) {
+                        float v[4];
+                        with(t, c, v);
 #pragma unroll
-                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], with(t * 16 + 4 * g4 + i, c), d);
-                        inter = fmaf(d, fo[t * 16 + 4 * g4 + i], inter);
+                        for (int i = 0; i < 4; ++i) inter = fmaf(P::REV ? acc[t][c][i] * o[i] : acc[t][c][i], v[i], inter);
                     }
                 }
             }
@@ -512,21 +520,27 @@ __device__ __forceinline__ void dense_pass(const DenseArgs& a, int64_t us, int s
             const rsrc_t rout = rows(a.out, t0, n, a.DV, 4);
             const int lack = P::REV ? (C - n) * a.DV : 0;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t) {
+                const float4 o4 = *reinterpret_cast<const float4*>(fo + t * 16 + 4 * g4);
+                const float o[4] = {o4.x, o4.y, o4.z, o4.w};
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = t * 16 + 4 * g4 + i;
+                for (int c = 0; c < NCT; ++c) {
+                    float v[4];
+                    if constexpr (P::DOT) with(t, c, v);
 #pragma unroll
-                    for (int c = 0; c < NCT; ++c)
-                        st_f1(P::REV ? acc[t][c][i] * fo[j] : acc[t][c][i], rout, (eo[c] + (t * 16 + i) * step - lack) * 4u, 0);
-                    if constexpr (P::DOT) {
-                        float d = 0.f;
-#pragma unroll
-                        for (int c = 0; c < NCT; ++c) d = fmaf(acc[t][c][i], with(j, c), d);
-                        d = ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(d))));
-                        if (m16 == 0) dots[((ch & 1) * NW + w) * (C + 1) + j] = d;
+                    for (int i = 0; i < 4; ++i) {
+                        st_f1(P::REV ? acc[t][c][i] * o[i] : acc[t][c][i], rout, (eo[c] + (t * 16 + i) * step - lack) * 4u, 0);
+                        if constexpr (P::DOT) d[i] = fmaf(acc[t][c][i], v[i], d[i]);
                     }
                 }
+                if constexpr (P::DOT)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        d[i] = ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(d[i]))));
+                        if (m16 == 0) dots[((ch & 1) * NW + w) * (C + 1) + t * 16 + 4 * g4 + i] = d[i];
+                    }
+            }
         } else {
             segdec *= total;
         }
