@@ -1,6 +1,7 @@
 """SDM (Sparse Delta Memory) hot path on MI355X: product-key addressing and the
 sparse gated delta scan as hand-written HIP kernels behind a C ABI
-(include/sdm.h). This package holds the Python binding (``binding``), the
+(include/sdm.h), and the operators that a stack of such layers puts around them
+(dense gated recurrence, residual norm, balance loss). This package holds the Python binding (``binding``), the
 in-tree build (``build``) and the seeded synthetic inputs (``inputs``)."""
 from . import inputs  # noqa: F401
 from .binding import (SDM_BF16, SDM_DELTA_EQ4, SDM_DELTA_FIG2, SDM_E4M3, SDM_F32,  # noqa: F401

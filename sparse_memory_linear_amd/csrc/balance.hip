@@ -17,6 +17,12 @@
 // one XCD at about the same time, so all but the first read them from its L2.
 // Shares split the tokens until there is a workgroup per CU. The second kernel
 // adds the shares' tables.
+//
+// Measured: 16.8 M selections (4 x 8 x 8192 tokens of 64), 65536 slots, forward and
+// backward 116 us: adding 59 (134 MB, 28 us at a copy's 4.75 TB/s; bound by the vector
+// instructions that look at every selection once per range, 5 times here), tables and loss 13,
+// backward 37 (134 MB). 64-bit atomics in memory in place of the tables in LDS took 2.0 ms in
+// all. Dealing the slots to the ranges in turn, which evens out skewed use, took as long.
 #include "sdm_buffer.h"
 #include "sdm_internal.h"
 
@@ -231,7 +237,8 @@ __global__ __launch_bounds__(TABLE ? 1024 : 256) void balance_bwd_kernel(Balance
 template <bool VEC>
 void balance_bwd_launch(BalanceBwdArgs a, hipStream_t st) {
     // The table pays where a workgroup per CU has at least half as many selections as
-    // slots to load, and holds up to 80 K slots.
+    // slots to load, and holds up to 80 K slots (16.8 M selections, 65536 slots, as
+    // many a workgroup as slots: 37 us, and 65 without).
     const int64_t sel = a.B * a.T * a.K, wgs = a.H < 256 ? 256 / a.H : 1;
     const bool table = a.N <= 80 * 1024 && sel / wgs >= a.N / 2;
     a.piece = table ? (a.B * a.T + wgs - 1) / wgs : (BALANCE_PIECE + a.K - 1) / a.K;
@@ -242,7 +249,8 @@ void balance_bwd_launch(BalanceBwdArgs a, hipStream_t st) {
 
 // Shares of the tokens: a workgroup per CU (an LDS range fills one), but no
 // share with fewer selections than a quarter of the slots: a share's table is
-// written and read once more.
+// written and read once more (504 K selections over 262144 slots: 48 us with 7
+// shares, 80 with 12).
 struct BalanceLayout {
     int64_t nrange, range, nshare, share, nblk, fixed, counts, bad, kept, bytes;
 };

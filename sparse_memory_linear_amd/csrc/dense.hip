@@ -19,7 +19,14 @@
 //
 // Segments: with few streams the tokens are split into segments; a pass leaves
 // each segment's own sum, a second adds them up over the segments (giving each
-// one's starting state), and the last computes the outputs.
+// one's starting state), and the last computes the outputs. The backward does so
+// for S and G in one launch, and for dq, dk and dv in one.
+//
+// Measured at 4 x 8 streams, T = 8192, 128 x 128, bf16 rows (32 streams, 16
+// segments of 512 tokens each): forward 136 us in all (segments' sums 38, carry 14, y 84;
+// 342 MB that it cannot do without: 72 us at a copy's 4.75 TB/s), backward 491 us (sums 92,
+// carry 23, gradients 397, gates 25; 749 MB, 158 us). The passes are bound by vector
+// instructions (dense_pass.h), the carry by HBM.
 #include "dense_pass.h"
 
 namespace sdm {
@@ -28,7 +35,7 @@ namespace {
 
 // the running sums of the gates' gradients start anew at segments of at most this many tokens
 constexpr int64_t BWD_SEGMENT = 512;
-constexpr int STEP_COLS = 64;  // columns of X a workgroup of the few-token form
+constexpr int STEP_COLS = 64;  // columns of X a workgroup of the one-token form
 
 // The segments' own sums -> their starting states, and the state after the last
 // one. Backwards, the segments run from the last, and the end is what flows

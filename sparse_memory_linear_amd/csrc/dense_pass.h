@@ -29,6 +29,15 @@
 // token order (4 (lane / 16) + i of two tiles of 16) is the accumulators', so P^T =
 // kap xi^T is written by the wavefront that computes it in the order in which the
 // others read it.
+//
+// What bounds it (4 x 8 streams, T = 8192, 128 x 128, bf16; per SIMD, in thousands of cycles):
+// the y pass takes 160, of them 96 of vector instructions, 57 of matrix ones and, per CU, 82 of LDS;
+// the three gradient passes 718, 350, 232 and 258. Nearly half of the vector instructions cut X into
+// planes: with that left out (wrong results) y takes 73 us in place of 87, with two of the three matrix
+// products left out 93. Two planes would do with a relative error of 3e-6; three keep fp32's. Tried and
+// dropped: chunks of 64 tokens (half the cutting, but spilled registers: 117 us against 90), fp32
+// matrix instructions (819 us for the forward against 287 for the first form of this one), residues
+// of the planes by the bf16 dot instruction (its wait states cost what it saved: 92 us against 87).
 #pragma once
 #include <type_traits>
 
