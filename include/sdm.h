@@ -400,7 +400,7 @@ int sdm_dense_scan_forward(const void* q, const void* k, const void* v, int in_d
 /*
  * sdm_dense_scan_backward_workspace_bytes -- device workspace
  * sdm_dense_scan_backward needs: the states S and G at the bounds of segments
- * of at most 512 tokens, and two numbers a token (0: no work, -1: invalid sizes).
+ * of at most 512 tokens, and a few numbers a token (0: no work, -1: invalid sizes).
  */
 int64_t sdm_dense_scan_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
 

@@ -24,7 +24,8 @@
 // 16 bytes so that 16 rows' pieces fall into different banks. A lane of the 16x16x32
 // instruction takes 8 consecutive k; X's tiles are numbered so that the 8 rows that
 // a lane's accumulators hold in tiles 2p and 2p+1 are 32p + 8 (lane / 16) + 0..7,
-// so X goes from accumulator to operand without leaving its registers. kap^T and omg as
+// so X goes from accumulator to operand without leaving its registers (a pass
+// without outputs numbers them plainly, which spares the transposing reads bank conflicts). kap^T and omg as
 // operands over the tokens come from the same rows by transposing LDS reads; their
 // token order (4 (lane / 16) + i of two tiles of 16) is the accumulators', so P^T =
 // kap xi^T is written by the wavefront that computes it in the order in which the
@@ -161,11 +162,13 @@ struct DensePass {
     static constexpr bool OUT = OUT_, REV = REV_, DOT = DOT_;
     static constexpr int WITH = NX == 3 && NK == 3 ? 4 : 2;          // bytes of `with`: q and k, as the other rows
     static constexpr int DKP = DKT * 16, SV = 16 * NCT * NW, NT = C / 16, THR = NW * 64;
-    static constexpr int RK = DKP * 2 + 16, RV = SV * 2 + 16;        // bytes of an LDS row
+    // bytes of an LDS row: rows read as operands are 16 apart of the banks' width, rows that
+    // only transposing reads take (4 rows of 32 bytes at a time) 32
+    static constexpr int RK = DKP * 2 + (OUT ? 16 : 32), RV = SV * 2 + 32;
     static constexpr int PK = C * RK, PV = C * RV;                   // bytes of a plane
     static constexpr int TILES = NT * (NT + 1) / 2;
     static constexpr int O_KA = 0, O_OM = O_KA + NK * PK, O_XI = O_OM + NO * PV, O_WI = O_XI + (OUT ? NX * PK : 0),
-                         RW = SV * WITH + 16, ROWS = O_WI + (DOT ? C * RW : 0);
+                         RW = SV * WITH + 32, ROWS = O_WI + (DOT ? C * RW : 0);
     // floats: two sets of a chunk's decays, outputs' products, their sums
     static constexpr int DEC = 4 * C + 2 * NT, FLOATS = 2 * DEC + (DOT ? 2 * NW * (C + 1) : 0);
     static constexpr int PBYTES = OUT ? TILES * 3 * 512 : 0;
@@ -515,7 +518,7 @@ __device__ __forceinline__ void dense_pass(const DenseArgs& a, int64_t us, int s
             uint4 ka[P::NK];
 #pragma unroll
             for (int i = 0; i < P::NK; ++i) {
-                const char* o = Ka + i * P::PK + (4 * g4 + (m16 >> 2)) * P::RK + (32 * (k >> 1) + 8 * (m16 & 3) + 4 * (k & 1)) * 2;
+                const char* o = Ka + i * P::PK + (4 * g4 + (m16 >> 2)) * P::RK + (P::OUT ? 32 * (k >> 1) + 8 * (m16 & 3) + 4 * (k & 1) : 16 * k + 4 * (m16 & 3)) * 2;
                 const uint2 x = read_tr(o), y = read_tr(o + 16 * P::RK);
                 ka[i] = make_uint4(x.x, x.y, y.x, y.y);
             }
@@ -568,7 +571,7 @@ __device__ __forceinline__ void dense_pass(const DenseArgs& a, int64_t us, int s
             for (int c = 0; c < NCT; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = 32 * (k >> 1) + 8 * g4 + 4 * (k & 1) + i;
+                    const int r = (P::OUT ? 32 * (k >> 1) + 8 * g4 + 4 * (k & 1) : 16 * k + 4 * g4) + i;
                     if (r < a.DK && col[c] < a.DV) a.Xend[state + r * (int64_t)a.DV + col[c]] = X[k][c][i];
                 }
     }
