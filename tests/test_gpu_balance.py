@@ -130,6 +130,21 @@ def test_many_selections_repeat_bit_for_bit():
             assert torch.equal(a[name], b[name]), name
 
 
+def test_offsets_beyond_32_bits():
+    """2.3 G selections in all (17 heads): the last head as a call of its own."""
+    H, T, K, N = 17, 2_100_000, 64, 4096
+    idx = torch.empty((1, H, T, K), dtype=torch.int32, device=DEV).random_(0, N)
+    wt = torch.empty((1, H, T, K), device=DEV).fill_(1 / 64)
+    dl = torch.ones(H, device=DEV)
+    a = sdm.sdm_balance_forward(idx, wt, N)
+    d = sdm.sdm_balance_backward(idx, a["counts"], a["tokens"], dl)
+    i, w = idx[:, -1:].clone(), wt[:, -1:].clone()
+    b = sdm.sdm_balance_forward(i, w, N)
+    assert torch.equal(a["counts"][-1:], b["counts"]) and torch.equal(a["mass"][-1:], b["mass"])
+    assert (a["counts"].sum(-1) == T * K).all() and torch.equal(a["loss"][-1:], b["loss"])
+    assert torch.equal(d[:, -1:], sdm.sdm_balance_backward(i, b["counts"], b["tokens"], dl[:1]))
+
+
 def test_no_tokens():
     z = sdm.sdm_balance_forward(torch.empty((0, 2, 5, 4), dtype=torch.int32, device=DEV), torch.empty((0, 2, 5, 4), device=DEV), 9)
     assert (z["counts"] == 0).all() and (z["mass"] == 0).all() and (z["loss"] == 0).all() and int(z["tokens"]) == 0

@@ -107,7 +107,7 @@ GRADS = ("dq", "dk", "dv", "dlog_alpha", "dbeta", "dS0")
 SIZES = [  # B, H, T, dk, dv: one token to several segments, tiles filled and not
     (1, 1, 1, 8, 8), (3, 2, 1, 128, 128), (2, 2, 3, 256, 72), (1, 3, 8, 64, 40), (1, 1, 9, 16, 8),
     (2, 1, 31, 40, 24), (1, 2, 64, 64, 64), (2, 2, 65, 72, 136), (1, 2, 300, 128, 128),
-    (1, 1, 517, 256, 256), (1, 1, 256, 64, 72), (1, 1, 257, 72, 64), (2, 1, 1100, 96, 80), (1, 2, 577, 200, 64), (1, 1, 1537, 32, 128),
+    (1, 1, 517, 256, 256), (1, 1, 130, 64, 256), (1, 1, 140, 128, 200), (1, 1, 256, 64, 72), (1, 1, 257, 72, 64), (2, 1, 1100, 96, 80), (1, 2, 577, 200, 64), (1, 1, 1537, 32, 128),
 ]
 
 
@@ -160,6 +160,28 @@ def test_no_tokens_pass_the_states_on():
     assert torch.equal(backward(z)["dS0"], x["dS"])
     z["S0"] = None
     assert (forward(z)["S"] == 0).all()
+
+
+def test_states_that_are_not_wanted():
+    """Through the C ABI: no last state, and no gradient of the first."""
+    from sparse_memory_linear_amd import binding
+    lib, p = binding.lib(), lambda t: t.data_ptr()  # noqa: E731
+    for T in (1, 40, 1500):
+        g = dev(make(2, 2, T, 64, 96, BF, T))
+        want, grads = forward(g), backward(g)
+        ws = torch.empty(max(16, sdm.sdm_dense_scan_workspace_bytes(2, 2, T, 64, 96)), dtype=torch.uint8, device=DEV)
+        y = torch.empty_like(want["y"])
+        st = torch.cuda.current_stream().cuda_stream
+        args = [p(g[m]) for m in ("q", "k", "v")] + [1, p(g["alpha"]), p(g["beta"])]
+        assert lib.sdm_dense_scan_forward(*args, p(g["S0"]), None, p(y), 2, 2, T, 64, 96, p(ws), ws.numel(), st) == 0
+        ws = torch.empty(sdm.sdm_dense_scan_backward_workspace_bytes(2, 2, T, 64, 96), dtype=torch.uint8, device=DEV)
+        out = {m: torch.empty_like(grads[m]) for m in GRADS[:-1]}
+        assert lib.sdm_dense_scan_backward(*args, p(g["dy"]), p(g["S0"]), p(g["dS"]), *(p(out[m]) for m in GRADS[:-1]), None,
+                                           2, 2, T, 64, 96, p(ws), ws.numel(), st) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(y, want["y"])
+        for m in out:
+            assert torch.equal(out[m], grads[m]), m
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])

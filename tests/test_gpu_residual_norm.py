@@ -157,6 +157,45 @@ def test_in_place_mixed_types_and_shapes():
     assert torch.equal(u["dx"], d2) and torch.equal(u["dgamma"], v["dgamma"])
 
 
+def test_h_over_x_and_all_type_pairs():
+    for xt in (BF, F32):
+        for ht in (BF, F32):
+            x, r, gamma = make(7, 300, F32, 12)
+            x, r, gamma = x.to(xt).to(DEV), r.to(ht).to(DEV), gamma.to(DEV)
+            a = sdm.sdm_residual_norm(x, gamma, r, EPS, "f32")
+            h, y = reference(x.cpu(), r.cpu(), gamma.cpu())
+            mag = (x.double().abs() + r.double().abs()).cpu()
+            assert ((a["h"].cpu().double() - h).abs() <= HALF[ht] * h.abs() * (1 + 1e-6) + 2.0 ** -24 * mag).all()
+            ymag = mag / (h.square().mean(-1, keepdim=True) + EPS).sqrt() * gamma.cpu().double().abs()
+            assert ((a["y"].cpu().double() - y).abs() <= 308 * 2.0 ** -24 * ymag * (1 + 1e-3)).all()
+            if xt == ht:
+                x2 = x.clone()
+                b = sdm.sdm_residual_norm(x2, gamma, r, EPS, "f32", out={"h": x2})
+                assert b["h"].data_ptr() == x2.data_ptr() and torch.equal(x2, a["h"]) and torch.equal(a["y"], b["y"])
+            # gradients of either type over a stream of either type
+            dy = torch.randn(7, 300, device=DEV).to(xt)
+            g = sdm.sdm_residual_norm_backward(dy, a["h"], gamma, None, EPS)
+            H, DY, GA = a["h"].cpu().double(), dy.cpu().double(), gamma.cpu().double()
+            rr = 1 / (H.square().mean(-1, keepdim=True) + EPS).sqrt()
+            n = H * rr
+            w = rr * (GA * DY - n * (GA * DY * n).mean(-1, keepdim=True))
+            m = rr * ((GA * DY).abs() + n.abs() * (GA * DY * n).abs().mean(-1, keepdim=True))
+            assert g["dx"].dtype == xt
+            assert ((g["dx"].cpu().double() - w).abs() <= HALF[xt] * w.abs() + 916 * 2.0 ** -24 * m).all()
+
+
+def test_offsets_beyond_32_bits():
+    rows, d = 2_200_003, 1024
+    x = torch.empty((rows, d), dtype=BF, device=DEV).normal_()
+    gamma = torch.ones(d, device=DEV)
+    a = sdm.sdm_residual_norm(x, gamma, None, EPS, "e4m3", 128)
+    b = sdm.sdm_residual_norm(x[-9:].clone(), gamma, None, EPS, "e4m3", 128)
+    assert torch.equal(a["y"][-9:].view(torch.uint8), b["y"].view(torch.uint8)) and torch.equal(a["scale"][-9:], b["scale"])
+    g = sdm.sdm_residual_norm_backward(x, x, gamma, x)
+    h = sdm.sdm_residual_norm_backward(x[-9:].clone(), x[-9:].clone(), gamma, x[-9:].clone())
+    assert torch.equal(g["dx"][-9:], h["dx"])
+
+
 def test_no_rows():
     x = torch.empty((0, 64), dtype=BF, device=DEV)
     gamma = torch.ones(64, device=DEV)
