@@ -24,9 +24,9 @@
 //
 // Measured at 4 x 8 streams, T = 8192, 128 x 128, bf16 rows (32 streams, 16
 // segments of 512 tokens each): forward 136 us in all (segments' sums 38, carry 14, y 84;
-// 342 MB that it cannot do without: 72 us at a copy's 4.75 TB/s), backward 491 us (sums 92,
-// carry 23, gradients 397, gates 25; 749 MB, 158 us). The passes are bound by vector
-// instructions (dense_pass.h), the carry by HBM.
+// 342 MB that it cannot do without: 72 us at a copy's 4.75 TB/s), backward 491 us (traced
+// one by one: sums 98, carry 23, gradients 376, gates 25; 749 MB, 158 us). The passes are
+// bound by vector instructions (dense_pass.h), the carry by HBM.
 #include "dense_pass.h"
 
 namespace sdm {

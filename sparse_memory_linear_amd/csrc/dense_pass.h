@@ -32,8 +32,8 @@
 // others read it.
 //
 // What bounds it (4 x 8 streams, T = 8192, 128 x 128, bf16; per SIMD, in thousands of cycles):
-// the y pass takes 160, of them 96 of vector instructions, 57 of matrix ones and, per CU, 82 of LDS;
-// the three gradient passes 718, 350, 232 and 258. Nearly half of the vector instructions cut X into
+// the y pass takes 163, of them 89 of vector instructions, 57 of matrix ones and, per CU, 49 of LDS;
+// the three gradient passes 693, 354, 232 and 238. Nearly half of the vector instructions cut X into
 // planes: with that left out (wrong results) y takes 73 us in place of 87, with two of the three matrix
 // products left out 93. Two planes would do with a relative error of 3e-6; three keep fp32's. Tried and
 // dropped: chunks of 64 tokens (half the cutting, but spilled registers: 117 us against 90), fp32
