@@ -25,7 +25,7 @@
 // Measured at 4 x 8 streams, T = 8192, 128 x 128, bf16 rows (32 streams, 16
 // segments of 512 tokens each): forward 136 us in all (segments' sums 38, carry 14, y 84;
 // 342 MB that it cannot do without: 72 us at a copy's 4.75 TB/s), backward 491 us (traced
-// one by one: sums 98, carry 23, gradients 376, gates 25; 749 MB, 158 us). The passes are
+// one by one: sums 98, carry 23, gradients 376, gates 22; 749 MB, 158 us). The passes are
 // bound by vector instructions (dense_pass.h), the carry by HBM.
 #include "dense_pass.h"
 
@@ -61,21 +61,25 @@ __global__ __launch_bounds__(256) void dense_carry_kernel(CarryArgs s0, CarryArg
     }
 }
 
-// Gates' gradients: a workgroup per (stream, segment). With e the value of
-// <alpha_{t+1} G_{t+1}, S_t> at a chunk's end: at the segment's end it is that
-// product of the two states; over a chunk it changes by what the two passes found to
-// flow into and out of the chunk, and within one E_t = e + the sum over u >= t of
-// q_u . dq_u - k_u . dk_u. So a rounding reaches no further than a chunk, but for the
-// chunks' own sums, which hold only what crosses their bounds.
+// Gates' gradients: a workgroup per (stream, segment), a row of 32 lanes a chunk, its last
+// token in lane 0. With e the value of <alpha_{t+1} G_{t+1}, S_t> at a chunk's end: at the
+// segment's end it is that product of the two states; over a chunk it changes by what the two
+// passes found to flow into and out of the chunk, and within one E_t = e + the sum over u >= t
+// of q_u . dq_u - k_u . dk_u. So a rounding reaches no further than a chunk, but for the chunks'
+// own sums, which hold only what crosses their bounds. Nothing passes a gate of 0: E is exactly
+// 0 there and the sums begin anew, so that a sequence's rounding stays out of the one before it.
 __global__ __launch_bounds__(256) void dense_gates_kernel(DenseGatesArgs a) {
+    constexpr int C = DENSE_CHUNK, NI = BWD_SEGMENT / 256;
+    static_assert(C == 32 && BWD_SEGMENT % 256 == 0, "a chunk is half a wavefront");
     __shared__ float part[4];
-    __shared__ float diff[BWD_SEGMENT / DENSE_CHUNK], at_end[BWD_SEGMENT / DENSE_CHUNK];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    __shared__ float diff[BWD_SEGMENT / C], at_end[BWD_SEGMENT / C];
+    __shared__ bool anew[BWD_SEGMENT / C];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, in = tid & (C - 1);
     const int seg = (int)(blockIdx.x % a.nseg);
     const int64_t s = blockIdx.x / a.nseg;
     const int64_t lo = (int64_t)seg * a.L, hi = lo + a.L < a.T ? lo + a.L : a.T;
     const bool last = seg + 1 == a.nseg;
-    const int nch = (int)((hi - lo + a.C - 1) / a.C);
+    const int nch = (int)((hi - lo + C - 1) / C);
     float d = 0.f;
     if (!last || a.has_dS) {
         const float4* G = reinterpret_cast<const float4*>(a.G + (seg * a.NS + s) * a.per);
@@ -86,42 +90,61 @@ __global__ __launch_bounds__(256) void dense_gates_kernel(DenseGatesArgs a) {
     }
     d = wave_sum(d);
     if (lane == 0) part[w] = d;
-    if (tid < nch) {
-        float x = 0.f;
-        for (int p = 0; p < a.nslab; ++p) {
-            const int64_t at = (p * a.NS + s) * a.nchunk + lo / a.C + tid;
-            x += a.inter_q[at] - a.inter_k[at];
+    float x[NI];
+    int shut[NI];  // a gate of 0 at this token or behind it in the chunk
+    int64_t t[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int c = (i * 256 + tid) / C;
+        const int64_t c0 = lo + (int64_t)c * C, c1 = c0 + C < hi ? c0 + C : hi;
+        t[i] = c1 - 1 - in;
+        x[i] = 0.f;
+        shut[i] = 0;
+        if (c >= nch || t[i] < c0) {
+            t[i] = -1;
+        } else {
+            float qdq = 0.f, db = 0.f;
+            for (int p = 0; p < a.nslab; ++p) {
+                qdq += a.qdq[(p * a.NS + s) * a.T + t[i]];
+                db += a.kdk[(p * a.NS + s) * a.T + t[i]];
+            }
+            a.dbeta[s * a.T + t[i]] = db;
+            shut[i] = a.alpha[s * a.T + t[i]] == 0.f;
+            x[i] = shut[i] ? 0.f : qdq - a.beta[s * a.T + t[i]] * db;
         }
-        diff[tid] = x;
+        for (int m = 1; m < C; m <<= 1) {
+            const float y = __shfl_up(x[i], m, C);
+            const int z = __shfl_up(shut[i], m, C);
+            if (in >= m) {
+                if (!shut[i]) x[i] += y;
+                shut[i] |= z;
+            }
+        }
+        if (c < nch && t[i] == c0) {  // over the chunk
+            float v = x[i];
+            if (!shut[i]) {
+                v = 0.f;
+                for (int p = 0; p < a.nslab; ++p) {
+                    const int64_t at = (p * a.NS + s) * a.nchunk + c0 / C;
+                    v += a.inter_q[at] - a.inter_k[at];
+                }
+            }
+            diff[c] = v;
+            anew[c] = shut[i] != 0;
+        }
     }
     __syncthreads();
     if (tid == 0) {
         float e = (part[0] + part[1]) + (part[2] + part[3]);
         for (int c = nch - 1; c >= 0; --c) {
             at_end[c] = e;
-            e += diff[c];
+            e = anew[c] ? diff[c] : e + diff[c];
         }
     }
     __syncthreads();
-    for (int c = w; c < nch; c += 4) {  // a wavefront a chunk, the last token in lane 0
-        const int64_t c0 = lo + (int64_t)c * a.C, c1 = c0 + a.C < hi ? c0 + a.C : hi, t = c1 - 1 - lane;
-        float x = 0.f;
-        if (t >= c0) {
-            float qdq = 0.f, db = 0.f;
-            for (int p = 0; p < a.nslab; ++p) {
-                qdq += a.qdq[(p * a.NS + s) * a.T + t];
-                db += a.kdk[(p * a.NS + s) * a.T + t];
-            }
-            a.dbeta[s * a.T + t] = db;
-            x = qdq - a.beta[s * a.T + t] * db;
-        }
-        for (int m = 1; m < 64; m <<= 1) {
-            const float y = __shfl_up(x, m);
-            if (lane >= m) x += y;
-        }
-        // nothing passes a gate of 0: exactly 0 there, not what the sums round to
-        if (t >= c0) a.dlog_alpha[s * a.T + t] = a.alpha[s * a.T + t] == 0.f ? 0.f : at_end[c] + x;
-    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+        if (t[i] >= 0) a.dlog_alpha[s * a.T + t[i]] = shut[i] ? x[i] : at_end[(i * 256 + tid) / C] + x[i];
 }
 
 __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t e) {
@@ -320,7 +343,7 @@ hipError_t launch_dense_backward(const DenseBwdArgs& f, hipStream_t st) {
     g.G = G; g.S = S; g.ST = ST; g.qdq = qdq; g.kdk = kdk; g.alpha = f.alpha; g.beta = f.beta;
     g.dlog_alpha = f.dlog_alpha; g.dbeta = f.dbeta; g.has_dS = f.dS != nullptr;
     g.NS = f.NS; g.T = f.T; g.L = y.L; g.per = per; g.nseg = (int)y.nseg;
-    g.inter_q = inter_q; g.inter_k = inter_k; g.nchunk = y.nchunk; g.C = DENSE_CHUNK; g.nslab = y.slabs;
+    g.inter_q = inter_q; g.inter_k = inter_k; g.nchunk = y.nchunk; g.nslab = y.slabs;
     hipLaunchKernelGGL(dense_gates_kernel, dim3((unsigned)(f.NS * y.nseg)), dim3(256), 0, st, g);
     return hipGetLastError();
 }

@@ -170,7 +170,7 @@ struct DenseGatesArgs {
     const float* alpha; const float* beta;
     float* dlog_alpha; float* dbeta;
     int64_t NS, T, L, per, nchunk;
-    int nseg, nslab, C;
+    int nseg, nslab;
     bool has_dS;
 };
 // Tokens per chunk of the dense recurrence.

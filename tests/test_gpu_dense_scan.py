@@ -131,6 +131,22 @@ def test_extreme_gates_and_missing_states(B, H, T, dk, dv, dtype, states):
     check(backward(g), want, mag, n, GRADS)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T0,T1", [(64, 40), (70, 90), (17, 3), (600, 700), (512, 512)])
+def test_a_gate_of_zero_keeps_two_sequences_apart(T0, T1, dtype):
+    """The second sequence's rows are 2^10 times larger, its gradients' products 2^40 times: a
+    rounding of them that passed the gate would be far beyond the first one's bound."""
+    x, z = make(1, 2, T0, 64, 40, dtype, T0, states=False), make(1, 2, T1, 64, 40, dtype, T1, states=False)
+    z["alpha"][:, :, 0] = 0.0
+    both = {n: None if x[n] is None else torch.cat([x[n], z[n] * (1024 if n in ("q", "k", "v", "dy") else 1)], 2) for n in x}
+    want, mag, n = walk(x), walk(x, True), roundings(T0 + T1, 64, 40)
+    g = dev(both)
+    got, y = backward(g), forward(g)["y"]
+    first = {m: got[m][:, :, :T0] for m in GRADS if m != "dS0"}
+    check({**first, "dS0": got["dS0"], "y": y[:, :, :T0]}, want, mag, n, ("y",) + GRADS)
+    assert (got["dlog_alpha"][:, :, T0] == 0).all()
+
+
 def test_state_in_place_and_preallocated_outputs():
     for T in (1, 4, 40, 1500):
         g = dev(make(2, 2, T, 64, 96, BF, T))
