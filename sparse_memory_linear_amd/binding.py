@@ -462,10 +462,13 @@ def _gpu(t0: torch.Tensor, *ts: Optional[torch.Tensor]) -> torch.device:
 
 def _call(fn: str, d: torch.device, *args):
     """Library call ``fn`` on the device's current stream, whatever device is current."""
-    if torch.cuda.current_device() != d.index:
-        with torch.cuda.device(d):
+    i = d.index
+    if torch.cuda.current_device() != i:
+        with torch.cuda.device(i):
             return _call(fn, d, *args)
-    _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(d).cuda_stream))
+    rc = getattr(lib(), fn)(*args, torch.cuda.current_stream(i).cuda_stream)
+    if rc:
+        _check(fn, rc)
 
 
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -475,7 +478,7 @@ def _at(t: Optional[torch.Tensor]) -> Optional[int]:
 def _out(t: Optional[torch.Tensor], like: torch.Tensor, shape, dtype: torch.dtype, name: str) -> torch.Tensor:
     """A new tensor on ``like``'s device, or the given one after its checks."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} has the wrong shape or dtype")
     _gpu(like, t)
@@ -582,13 +585,14 @@ def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.
     rows = x.numel() // d if d else 0
     code, yt = NORM_OUT[dtype]
     out = dict(out) if out else {}
-    want = {"y": (x.shape, yt)}
+    shape = x.shape
+    want = {"y": (shape, yt)}
     if res is not None:
-        want["h"] = (x.shape, res.dtype)
+        want["h"] = (shape, res.dtype)
     if dtype == "e4m3":
         if group < 0 or (group and d % group):
             raise ValueError("group must be 0 or divide d")
-        want["scale"] = (x.shape[:-1] + (d // group if group else 1,), torch.float32)
+        want["scale"] = ((*shape[:-1], d // group if group else 1), torch.float32)
     if out and set(out) - set(want):
         raise ValueError(f"no such output: {sorted(set(out) - set(want))}")
     for name, (shp, dt) in want.items():
