@@ -32,6 +32,7 @@ namespace {
 constexpr int RANGE = 13312;   // slots a workgroup: 12 bytes each, 156 KiB of LDS
 constexpr int ADD_THREADS = 1024;
 constexpr int MERGE_SLOTS = 512;
+constexpr int64_t MOST = 1 << 23;  // tokens walked at a time: MOST K (2^40 / K + 1) < 2^64
 
 // fp64 whose unit in the last place is 2^-shift
 __device__ __forceinline__ double fix_base(int shift) { return ldexp(1.5, 52 - shift); }
@@ -53,7 +54,7 @@ __global__ __launch_bounds__(ADD_THREADS) void balance_add_kernel(BalanceArgs a)
     if (tid == 0) { bad = 0; kept = 0; }
     __syncthreads();
     const double base = fix_base(a.shift);
-    const uint64_t kdiv = ((1ull << 40) / (uint64_t)a.K) + 1;  // e / K = e kdiv >> 40 for e < 2^32, K <= 256
+    const uint64_t kdiv = ((1ull << 40) / (uint64_t)a.K) + 1;  // e / K = e kdiv >> 40 for e < MOST K, K <= 256
     auto take = [&](int32_t slot, float w) {
         const uint32_t i = (uint32_t)slot - lo;
         if (i < len) {
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(ADD_THREADS) void balance_add_kernel(BalanceArgs a)
     const int64_t u0 = share * a.share, u1 = u0 + a.share < ntok ? u0 + a.share : ntok;
     for (int64_t u = u0; u < u1;) {  // one sequence's tokens at a time: contiguous selections
         const int64_t b = u / a.T, t = u - b * a.T;
-        const int64_t m = a.T - t < u1 - u ? a.T - t : u1 - u;
+        const int64_t m = min(min(a.T - t, u1 - u), MOST);
         const int64_t at = ((b * a.H + h) * a.T + t) * a.K;
         const uint8_t* keep = a.mask ? a.mask + b * a.T + t : nullptr;
         const uint32_t n = (uint32_t)(m * a.K);  // < 2^31 (host)
@@ -198,7 +199,7 @@ __global__ __launch_bounds__(TABLE ? 1024 : 256) void balance_bwd_kernel(Balance
         for (uint32_t i = threadIdx.x; i < N; i += THR) table[i] = (uint16_t)min(counts[i], 65535);
         __syncthreads();
     }
-    const uint64_t kdiv = ((1ull << 40) / (uint64_t)a.K) + 1;  // e / K = e kdiv >> 40 for e < 2^32, K <= 256
+    const uint64_t kdiv = ((1ull << 40) / (uint64_t)a.K) + 1;  // e / K = e kdiv >> 40 for e < MOST K, K <= 256
     auto grad = [&](int32_t slot) {
         if ((uint32_t)slot >= N) return 0.f;
         int k;
@@ -214,7 +215,7 @@ __global__ __launch_bounds__(TABLE ? 1024 : 256) void balance_bwd_kernel(Balance
     const int64_t u0 = piece * a.piece, u1 = u0 + a.piece < ntok ? u0 + a.piece : ntok;
     for (int64_t u = u0; u < u1;) {  // one sequence's tokens at a time: contiguous selections
         const int64_t b = u / a.T, t = u - b * a.T;
-        const int64_t m = a.T - t < u1 - u ? a.T - t : u1 - u;
+        const int64_t m = min(min(a.T - t, u1 - u), MOST);
         const int64_t at = ((b * a.H + h) * a.T + t) * a.K;
         const uint8_t* keep = a.mask ? a.mask + b * a.T + t : nullptr;
         const uint32_t e1 = (uint32_t)(m * a.K);

@@ -145,6 +145,30 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(d[:, -1:], sdm.sdm_balance_backward(i, b["counts"], b["tokens"], dl[:1]))
 
 
+def test_one_sequence_of_more_than_2_to_24_masked_tokens():
+    T, N = (1 << 24) + 5001, 1 << 18
+    mask = (torch.arange(T, device=DEV) % 7 < 3).to(torch.uint8)[None]
+    mask[0, 1 << 24:] = 1 - mask[0, 1 << 24:]
+    keep = mask[0] != 0
+    # 13 heads of 20 ranges: a workgroup walks the whole sequence
+    idx = torch.randint(0, N, (1, 13, T, 1), device=DEV, dtype=torch.int32)
+    wt = torch.ones((1, 13, T, 1), device=DEV)
+    got = sdm.sdm_balance_forward(idx, wt, N, mask)
+    assert int(got["tokens"]) == int(keep.sum())
+    for h in (0, 12):
+        want = torch.bincount(idx[0, h, keep, 0], minlength=N)
+        assert torch.equal(got["counts"][h].long(), want)
+        assert torch.equal(got["mass"][h], want.float())  # whole numbers below 2^24
+    del idx, wt, got
+    # 129 heads of 16 slots: so does the gradient's, with its counts in LDS
+    idx = torch.zeros((1, 129, T, 1), device=DEV, dtype=torch.int32)
+    n = int(keep.sum())
+    counts = torch.full((129, 16), n, device=DEV, dtype=torch.int32)
+    d = sdm.sdm_balance_backward(idx, counts, torch.tensor([n], device=DEV, dtype=torch.int32),
+                                 torch.ones(129, device=DEV), mask)
+    assert torch.equal((d != 0)[0, :, :, 0], keep[None].expand(129, T))
+
+
 def test_no_tokens():
     z = sdm.sdm_balance_forward(torch.empty((0, 2, 5, 4), dtype=torch.int32, device=DEV), torch.empty((0, 2, 5, 4), device=DEV), 9)
     assert (z["counts"] == 0).all() and (z["mass"] == 0).all() and (z["loss"] == 0).all() and int(z["tokens"]) == 0
