@@ -390,7 +390,8 @@ int64_t sdm_dense_scan_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t 
  * be split over several calls. Inputs must be finite: tokens are worked in
  * tiles, and a NaN or infinity may reach earlier tokens of its tile. T = 0
  * passes the state on (S = S0).
- * Supported: dk, dv multiples of 8 up to 256; B*H*ceil(T/64)*8 < 2^31.
+ * Supported: dk, dv multiples of 8 up to 256; B*H*ceil(T/64)*8 < 2^31,
+ * B*H*ceil(T/512)*ceil(max(dk,dv)/64) < 2^21, B*H*dk*dv < 2^34 - 2^10.
  */
 int sdm_dense_scan_forward(const void* q, const void* k, const void* v, int in_dtype,
                            const float* alpha, const float* beta, const float* S0, float* S, float* y,

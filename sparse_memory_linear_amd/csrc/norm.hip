@@ -148,7 +148,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
         const int c = (j * TPR + lane) * VEC;
         if (c < a.d) load_vec(a.gamma, false, c, left<TAIL>(a.d, c), ga[j]);
     }
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RPB + threadIdx.x / TPR;
     if (row >= a.rows) return;  // TPR > 64: all of the workgroup's threads have this row
     float v[NV][VEC];
     const int64_t at = row * a.d;
@@ -325,7 +325,9 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* part, fl
 template <int TPR, int NV, bool TAIL>
 void norm_launch(const NormArgs& a, hipStream_t st) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1, THR = TPR < 256 ? 256 : TPR;
-    hipLaunchKernelGGL((norm_kernel<TPR, NV, TAIL>), dim3((unsigned)((a.rows + RPB - 1) / RPB)), dim3(THR), 0, st, a);
+    const int64_t n = (a.rows + RPB - 1) / RPB, most = 1 << 21;  // a grid's side: fewer than 2^32 threads
+    const dim3 grid((unsigned)(n < most ? n : most), (unsigned)((n + most - 1) / most));
+    hipLaunchKernelGGL((norm_kernel<TPR, NV, TAIL>), grid, dim3(THR), 0, st, a);
 }
 template <int TPR, int NV, bool TAIL>
 void norm_launch(const NormBwdArgs& a, hipStream_t st) {

@@ -529,7 +529,10 @@ int check_dense(const char* fn, int in_dtype, int64_t B, int64_t H, int64_t T, i
                     (long long)dv);
     // B, H and T below 2^31 each, so that the products below stay in 64 bits
     if (B > 0x7FFFFFFFll || H > 0x7FFFFFFFll || T > 0x7FFFFFFFll || B * H > 0x7FFFFFFFll ||
-        B * H * 8 * ((T + 63) / 64) > 0x7FFFFFFFll || B * H * (dk * dv / 4) / 256 >= 0x7FFFFFFFll)
+        B * H * 8 * ((T + 63) / 64) > 0x7FFFFFFFll ||
+        // fewer than 2^32 threads a launch: three passes of 512 a segment and slab; 4 elements a thread
+        B * H * ((T + 511) / 512) * (((dk > dv ? dk : dv) + 63) / 64) >= 1ll << 21 ||
+        B * H * dk * dv >= (1ll << 34) - 1024)
         return fail(SDM_ERR_UNSUPPORTED, "%s: too many streams or tokens for one launch", fn);
     return B == 0 || H == 0 ? NO_WORK : 0;
 }

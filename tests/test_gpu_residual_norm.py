@@ -196,6 +196,14 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(g["dx"][-9:], h["dx"])
 
 
+def test_more_rows_than_one_side_of_a_grid():
+    rows = (1 << 28) + 37
+    x = torch.full((rows, 1), -3.0, dtype=BF, device=DEV)
+    x[1 << 28:] = 5.0
+    y = sdm.sdm_residual_norm(x, torch.full((1,), 2.0, device=DEV), None, 0.0)["y"]
+    assert (y[:1 << 28] == -2.0).all() and (y[1 << 28:] == 2.0).all()  # h / |h| gamma
+
+
 def test_no_rows():
     x = torch.empty((0, 64), dtype=BF, device=DEV)
     gamma = torch.ones(64, device=DEV)

@@ -56,6 +56,13 @@ def test_dense_scan_backward_checks(lib):
     assert lib.sdm_dense_scan_backward_workspace_bytes(2, 2, 100, 64, 512) == -1
 
 
+@pytest.mark.parametrize("B,H,T,dk,dv", [(1 << 21, 1, 1, 8, 8), (64, 1 << 14, 512, 8, 72), (1 << 20, 1, 1, 128, 128),
+                                         (1 << 14, 16, 0, 256, 256), (512, 2, 1 << 20, 8, 8)])
+def test_dense_sizes_beyond_a_launch_are_refused(lib, B, H, T, dk, dv):
+    assert lib.sdm_dense_scan_forward(*[FAKE] * 3, 1, *[FAKE] * 5, B, H, T, dk, dv, FAKE, 1 << 60, None) == 5
+    assert lib.sdm_dense_scan_backward(*[FAKE] * 3, 1, *[FAKE] * 11, B, H, T, dk, dv, FAKE, 1 << 60, None) == 5
+
+
 def test_residual_norm_checks(lib):
     x, r, h, y = P(4096), P(8192), P(12288), P(16384)
     base = dict(x=x, xd=1, r=r, h=h, hd=1, g=FAKE, eps=F(1e-6), rows=4, d=256, y=y, yd=2, s=FAKE, grp=128, st=None)
