@@ -249,3 +249,20 @@ def test_refusals():
                  lambda: sdm.sdm_residual_norm(torch.zeros(1, 16400, device=DEV), torch.zeros(16400, device=DEV))):
         with pytest.raises(sdm.SdmError):
             call()
+
+
+@pytest.mark.parametrize("group", [0, 32, 128, 512])
+def test_codes_are_the_rounded_quotients(group):
+    """The fp32 output holds the y that the 8-bit one is made of: its scale is the fp32 quotient
+    max |y| / 448 (at least 2^-126) and its codes the fp32 quotients y / scale, to nearest even, bit
+    for bit; also for rows so small that eps decides and y / scale passes through denormal numbers."""
+    for rows, d in ((700, 1024), (9, 8192), (3, 512)) + (((400, 1919), (5000, 40)) if group == 0 else ()):
+        for size in (1.0, 1e-30, 1e-35, 1e-39):
+            x, res, gamma = make(rows, d, F32 if size < 1 else BF, group + rows)
+            x, res, gamma = (x * size).to(DEV), (res * size).to(DEV), gamma.to(DEV)
+            y = sdm.sdm_residual_norm(x, gamma, res, EPS, "f32")["y"].cpu().view(rows, -1, group or d)
+            got = sdm.sdm_residual_norm(x, gamma, res, EPS, "e4m3", group)
+            scale = (y.abs().amax(-1) / 448.0).clamp_min(2.0 ** -126)
+            assert torch.equal(got["scale"].cpu(), scale)
+            codes = (y / scale[..., None]).to(F8).view(rows, d)
+            assert torch.equal(got["y"].cpu().view(torch.uint8), codes.view(torch.uint8))
