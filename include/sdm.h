@@ -440,7 +440,7 @@ int sdm_dense_scan_backward(const void* q, const void* k, const void* v, int in_
  *   scale (out, fp32; else unused, may be NULL): with group = 0 one per row, [rows, 1]; else
  *   one per `group` columns, [rows, d / group]. scale = max |y| / 448 over its columns (0
  *   where all are 0, else at least 2^-126), and y holds the fp32 quotients y / scale, rounded
- *   to nearest even
+ *   to nearest even; where a y is NaN or infinite, so is the scale, and all of its y are NaN
  * The norm is that of the fp32 sum; h is stored rounded to its dtype. h may
  * be res, or x in x's dtype (in place); y may not alias x, res or h.
  * Supported: 1 <= d <= 16384; group 0, or a power of two from 32 to 512 that

@@ -128,17 +128,21 @@ __device__ __forceinline__ void store_e4m3(void* p, int64_t e, int n, const floa
 }
 
 // The scale that maps the largest magnitude onto e4m3's largest value, 448. It
-// stays a normal number; 0 for a row of zeros.
+// stays a normal number; 0 for a row of zeros, NaN or infinite where the largest is.
 __device__ __forceinline__ float e4m3_scale(float amax) {
-    return amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 0.f;
+    const float s = amax / 448.f;
+    return amax == 0.f ? 0.f : s < 1.17549435e-38f ? 1.17549435e-38f : s;
 }
+
+// the larger of m >= 0 and |x|; a NaN of either stays (fmaxf drops it, and a row of NaN then has a scale of 0)
+__device__ __forceinline__ float larger(float m, float x) { return __builtin_elementwise_maximum(m, fabsf(x)); }
 
 // Sum and maximum over the TPR threads that own a row (the same on all of them)
 template <int TPR>
 __device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*buf)[2]) {
     for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) {
         sum += __shfl_xor(sum, m);
-        mx = fmaxf(mx, __shfl_xor(mx, m));
+        mx = larger(mx, __shfl_xor(mx, m));
     }
     if constexpr (TPR > 64) {
         const int w = threadIdx.x >> 6;
@@ -146,7 +150,7 @@ __device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*buf)[2
         __syncthreads();
         sum = 0.f; mx = 0.f;
 #pragma unroll
-        for (int i = 0; i < TPR / 64; ++i) { sum += buf[i][0]; mx = fmaxf(mx, buf[i][1]); }
+        for (int i = 0; i < TPR / 64; ++i) { sum += buf[i][0]; mx = larger(mx, buf[i][1]); }
     }
 }
 
@@ -187,7 +191,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
         for (int i = 0; i < VEC; ++i) {
             ss = fmaf(v[j][i], v[j][i], ss);
             v[j][i] *= ga[j][i];
-            mx = fmaxf(mx, fabsf(v[j][i]));
+            mx = larger(mx, v[j][i]);
         }
     }
     row_reduce<TPR>(ss, mx, buf);
@@ -205,8 +209,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
                 float m = 0.f;
                 if (c < a.d)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(v[j][i] * r));
-                for (int k = 1; k < a.group / 8; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
+                    for (int i = 0; i < VEC; ++i) m = larger(m, v[j][i] * r);
+                for (int k = 1; k < a.group / 8; k <<= 1) m = larger(m, __shfl_xor(m, k));
                 scale = e4m3_scale(m);
                 if (c < a.d && c % a.group == 0) a.scale[row * (a.d / a.group) + c / a.group] = scale;
             }

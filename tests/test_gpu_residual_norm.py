@@ -266,3 +266,25 @@ def test_codes_are_the_rounded_quotients(group):
             assert torch.equal(got["scale"].cpu(), scale)
             codes = (y / scale[..., None]).to(F8).view(rows, d)
             assert torch.equal(got["y"].cpu().view(torch.uint8), codes.view(torch.uint8))
+
+
+@pytest.mark.parametrize("d", [512, 1919, 8192])
+def test_scales_of_rows_that_are_not_finite(d):
+    """A scale is 0 only over zeros: over a NaN, or an infinity (whose y, infinity / infinity, is one), it is a NaN."""
+    x, _, gamma = make(6, d, F32, d)
+    x[1, 7], x[2, d - 1], x[3, 300], x[4] = float("nan"), float("inf"), -float("inf"), 0.0
+    for group in (0,) if d % 128 else (0, 128):
+        n = d // (group or d)
+        got = sdm.sdm_residual_norm(x.to(DEV), gamma.to(DEV), None, EPS, "e4m3", group)
+        s, y = got["scale"].cpu(), got["y"].cpu().float().view(6, n, -1)
+        want = torch.zeros(6, n, dtype=torch.bool)
+        want[1] = True                                       # the norm of a row with a NaN is one
+        want[2, -1] = want[3, 300 // (group or d)] = True    # beside an infinity all else is 0
+        assert torch.equal(torch.isnan(s), want) and torch.equal(torch.isnan(y).all(-1), want)
+        assert torch.equal(torch.isnan(y).any(-1), want)
+        s[want], y[want] = 0.0, 0.0
+        assert (s[1:5] == 0).all() and (y[1:5] == 0).all() and (s[0] > 0).all() and (s[5] > 0).all()
+        g = gamma.clone()
+        g[5] = float("nan")                                  # and so is that of a column
+        s = sdm.sdm_residual_norm(x[:1].to(DEV), g.to(DEV), None, EPS, "e4m3", group)["scale"].cpu()
+        assert torch.isnan(s[0, 0]) and (s[0, 1:] > 0).all()
