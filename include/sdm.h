@@ -367,7 +367,7 @@ int sdm_output_gate(const float* y, const float* gamma, const void* g, int g_dty
 /*
  * sdm_dense_scan_workspace_bytes -- device workspace sdm_dense_scan_forward
  * needs (0: none, as when there is no work, for short calls or many streams; -1:
- * invalid sizes).
+ * sizes that the call refuses).
  */
 int64_t sdm_dense_scan_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
 
@@ -401,7 +401,8 @@ int sdm_dense_scan_forward(const void* q, const void* k, const void* v, int in_d
 /*
  * sdm_dense_scan_backward_workspace_bytes -- device workspace
  * sdm_dense_scan_backward needs: the states S and G at the bounds of segments
- * of at most 512 tokens, and a few numbers a token (0: no work, -1: invalid sizes).
+ * of at most 512 tokens, and a few numbers a token (0: no work, -1: sizes that the
+ * call refuses).
  */
 int64_t sdm_dense_scan_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
 

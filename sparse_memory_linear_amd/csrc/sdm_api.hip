@@ -537,18 +537,14 @@ int check_dense(const char* fn, int in_dtype, int64_t B, int64_t H, int64_t T, i
     return B == 0 || H == 0 ? NO_WORK : 0;
 }
 
-bool dense_sizes_ok(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
-    return B >= 0 && H >= 0 && T >= 0 && B <= 0x7FFFFFFFll && H <= 0x7FFFFFFFll && T <= 0x7FFFFFFFll &&
-           B * H <= 0x7FFFFFFFll && dk >= 8 && dv >= 8 && dk <= 256 && dv <= 256 && dk % 8 == 0 && dv % 8 == 0;
-}
-
 }  // namespace
 
 extern "C" {
 
 int64_t sdm_dense_scan_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
-    if (!dense_sizes_ok(B, H, T, dk, dv)) return -1;
-    if (B == 0 || H == 0 || T == 0) return 0;
+    const int rc = check_dense("sdm_dense_scan_workspace_bytes", SDM_F32, B, H, T, dk, dv);
+    if (rc == NO_WORK || (rc == 0 && T == 0)) return 0;
+    if (rc) return -1;
     return sdm::dense_workspace_bytes(B * H, T, (int)dk, (int)dv);
 }
 
@@ -581,8 +577,9 @@ int sdm_dense_scan_forward(const void* q, const void* k, const void* v, int in_d
 }
 
 int64_t sdm_dense_scan_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
-    if (!dense_sizes_ok(B, H, T, dk, dv)) return -1;
-    if (B == 0 || H == 0 || T == 0) return 0;
+    const int rc = check_dense("sdm_dense_scan_backward_workspace_bytes", SDM_F32, B, H, T, dk, dv);
+    if (rc == NO_WORK || (rc == 0 && T == 0)) return 0;
+    if (rc) return -1;
     return sdm::dense_backward_workspace_bytes(B * H, T, (int)dk, (int)dv);
 }
 

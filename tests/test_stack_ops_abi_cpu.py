@@ -124,3 +124,14 @@ def test_binding_refuses_cpu_tensors(lib):
                  lambda: binding.sdm_balance_forward(i, w, 4)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv", [(1 << 21, 1, 1, 8, 8), (64, 1 << 14, 512, 8, 72), (1 << 20, 1, 1, 128, 128),
+                                         (512, 2, 1 << 20, 8, 8), ((1 << 31) - 1, 1, (1 << 31) - 1, 256, 256),
+                                         (1 << 29, 1, 1 << 24, 256, 256), (32768, 65534, (1 << 31) - 1, 256, 256)])
+def test_refused_dense_sizes_have_no_workspace(lib, B, H, T, dk, dv):
+    assert lib.sdm_dense_scan_workspace_bytes(B, H, T, dk, dv) == -1
+    assert lib.sdm_dense_scan_backward_workspace_bytes(B, H, T, dk, dv) == -1
+    for f in (binding.sdm_dense_scan_workspace_bytes, binding.sdm_dense_scan_backward_workspace_bytes):
+        with pytest.raises(ValueError):
+            f(B, H, T, dk, dv)
