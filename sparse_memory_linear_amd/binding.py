@@ -485,6 +485,12 @@ def _out(t: Optional[torch.Tensor], like: torch.Tensor, shape, dtype: torch.dtyp
     return t
 
 
+def _known(out: dict, names):
+    """Refuses preallocated tensors under names that the call does not write."""
+    if not out.keys() <= set(names):
+        raise ValueError(f"no such output: {sorted(out.keys() - set(names))}")
+
+
 def sdm_dense_scan_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int) -> int:
     n = lib().sdm_dense_scan_workspace_bytes(B, H, T, dk, dv)
     if n < 0:
@@ -551,6 +557,7 @@ def sdm_dense_scan_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a
     out = dict(out or {})
     shapes = {"dq": (B, H, T, dk), "dk": (B, H, T, dk), "dv": (B, H, T, dv), "dlog_alpha": (B, H, T),
               "dbeta": (B, H, T), "dS0": (B, H, dk, dv)}
+    _known(out, shapes)
     for name, shp in shapes.items():
         out[name] = _out(out.get(name), q, shp, torch.float32, name)
     workspace = _workspace(workspace, sdm_dense_scan_backward_workspace_bytes(B, H, T, dk, dv), d)
@@ -593,8 +600,7 @@ def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.
         if group < 0 or (group and d % group):
             raise ValueError("group must be 0 or divide d")
         want["scale"] = ((*shape[:-1], d // group if group else 1), torch.float32)
-    if out and set(out) - set(want):
-        raise ValueError(f"no such output: {sorted(set(out) - set(want))}")
+    _known(out, want)
     for name, (shp, dt) in want.items():
         out[name] = _out(out.get(name), x, shp, dt, name)
     h, scale = out.get("h"), out.get("scale")
@@ -620,6 +626,7 @@ def sdm_residual_norm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.T
     d = dy.shape[-1]
     rows = dy.numel() // d if d else 0
     out = dict(out or {})
+    _known(out, ("dx", "dgamma"))
     dx = _out(out.get("dx"), dy, dy.shape, dy.dtype, "dx")
     dgamma = _out(out.get("dgamma"), dy, (d,), torch.float32, "dgamma")
     if rows == 0:
@@ -661,8 +668,10 @@ def sdm_balance_forward(idx: torch.Tensor, wt: torch.Tensor, N: int, mask: Optio
         raise ValueError("shape or dtype mismatch in sdm_balance_forward")
     _mask(mask, B, T, idx)
     out = dict(out or {})
-    for name, shp, dt in (("counts", (H, N), torch.int32), ("mass", (H, N), torch.float32),
-                          ("tokens", (1,), torch.int32), ("loss", (H,), torch.float32)):
+    want = {"counts": ((H, N), torch.int32), "mass": ((H, N), torch.float32),
+            "tokens": ((1,), torch.int32), "loss": ((H,), torch.float32)}
+    _known(out, want)
+    for name, (shp, dt) in want.items():
         out[name] = _out(out.get(name), idx, shp, dt, name)
     workspace = _workspace(workspace, sdm_balance_workspace_bytes(B, H, T, K, N), d)
     _call("sdm_balance_forward", d,

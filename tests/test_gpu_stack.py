@@ -142,3 +142,17 @@ def test_decoding_continues_a_prompt():
         ys.append(y)
     assert (torch.cat(ys, 2) - whole).abs().max() <= TOL * whole.abs().max()
     assert (S - last).abs().max() <= TOL * last.abs().max()
+
+
+def test_outputs_of_other_names_are_refused():
+    """A preallocated tensor under a name that a call does not know would go unused."""
+    x = {k: v.to(DEV) for k, v in layer(T=8).items()}
+    q, al = torch.zeros((2, 2, 8, 16), device=DEV), torch.ones((2, 2, 8), device=DEV)
+    i, w, t = torch.zeros((2, 2, 8, 4), dtype=torch.int32, device=DEV), torch.ones((2, 2, 8, 4), device=DEV), q.new_empty(1)
+    for name, call in (("dS", lambda o: sdm.sdm_dense_scan_backward(q, q, q, al, al, q, out=o)),
+                       ("dh", lambda o: sdm.sdm_residual_norm_backward(x["c"], x["x"], x["gamma"], out=o)),
+                       ("count", lambda o: sdm.sdm_balance_forward(i, w, 16, out=o)),
+                       ("scale", lambda o: sdm.sdm_residual_norm(x["x"], x["gamma"], out=o))):
+        with pytest.raises(ValueError):
+            call({name: t})
+        call({})
