@@ -494,7 +494,8 @@ int64_t sdm_balance_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t K, 
  * in magnitude makes its head's mass and loss NaN. Masked tokens are not
  * looked at. Weights are added in fixed point (to 2^-40, or with more than 2^21
  * selections a head, n = B*T*K, to 2^-(61 - ceil(log2 n))), so results do not
- * depend on the order of the additions. Without tokens (B or T = 0) the outputs are zeros.
+ * depend on the order of the additions. Without tokens (B or T = 0) the outputs are zeros;
+ * H = 0 is empty work (tokens is not written).
  * Supported: N <= 2^18, K <= 256, H <= 4096, B*T*K < 2^31.
  */
 int sdm_balance_forward(const int32_t* idx, const float* wt, const uint8_t* mask,

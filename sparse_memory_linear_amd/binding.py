@@ -673,6 +673,8 @@ def sdm_balance_forward(idx: torch.Tensor, wt: torch.Tensor, N: int, mask: Optio
     _known(out, want)
     for name, (shp, dt) in want.items():
         out[name] = _out(out.get(name), idx, shp, dt, name)
+    if H == 0:
+        out["tokens"].zero_()
     workspace = _workspace(workspace, sdm_balance_workspace_bytes(B, H, T, K, N), d)
     _call("sdm_balance_forward", d,
         _at(idx), _at(wt), _at(mask), B, H, T, K, N, _at(out["counts"]), _at(out["mass"]),

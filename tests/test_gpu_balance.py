@@ -230,3 +230,11 @@ def test_refusals():
         sdm.sdm_balance_backward(idx, got["counts"][:1].contiguous(), got["tokens"], torch.ones(2, device=DEV))
     with pytest.raises(sdm.SdmError):
         sdm.sdm_balance_forward(idx, wt, 16, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+def test_no_heads():
+    """No head, no selection: nothing is counted, so no token either."""
+    used = torch.full((1,), 7, dtype=torch.int32, device=DEV)
+    z = sdm.sdm_balance_forward(torch.empty((2, 0, 5, 4), dtype=torch.int32, device=DEV), torch.empty((2, 0, 5, 4), device=DEV), 9,
+                                out={"tokens": used})
+    assert z["counts"].shape == (0, 9) and z["loss"].shape == (0,) and int(z["tokens"]) == 0
