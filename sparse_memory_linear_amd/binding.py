@@ -501,7 +501,7 @@ def sdm_dense_scan_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int) -> 
 def _dense_inputs(fn, q, k, v, alpha, beta, states):
     d = _gpu(q, k, v, alpha, beta)
     B, H, T, dk = q.shape
-    dv = v.shape[3]
+    dv = v.shape[-1] if v.dim() else 0
     for name, t, shp in (("k", k, (B, H, T, dk)), ("v", v, (B, H, T, dv)), ("alpha", alpha, (B, H, T)),
                          ("beta", beta, (B, H, T))):
         if tuple(t.shape) != shp:

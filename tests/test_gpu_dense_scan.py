@@ -343,3 +343,12 @@ def test_refusals():
     long = dev(make(1, 2, 2000, 16, 8, BF, 1))
     with pytest.raises(sdm.SdmError):
         forward(long, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
+def test_values_of_other_ranks_are_refused():
+    g = dev(make(1, 2, 9, 16, 8, BF, 1))
+    for v in (g["v"][..., 0].contiguous(), g["v"][..., None].contiguous()):
+        with pytest.raises(ValueError):
+            sdm.sdm_dense_scan_forward(g["q"], g["k"], v, g["alpha"], g["beta"])
+        with pytest.raises(ValueError):
+            sdm.sdm_dense_scan_backward(g["q"], g["k"], v, g["alpha"], g["beta"], g["dy"])
