@@ -387,8 +387,9 @@ int64_t sdm_dense_scan_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t 
  *   workspace    >= sdm_dense_scan_workspace_bytes bytes, 16-byte aligned (may be
  *                NULL where that is 0)
  * Products and sums are fp32 for both input types, states fp32. A sequence may
- * be split over several calls. Inputs must be finite: tokens are worked in
- * tiles, and a NaN or infinity may reach earlier tokens of its tile. T = 0
+ * be split over several calls. Inputs and states must be finite, fp32 ones below 2^127 in
+ * magnitude: tokens are worked in tiles, and a NaN or infinity may reach earlier tokens
+ * of its tile. T = 0
  * passes the state on (S = S0).
  * Supported: dk, dv multiples of 8 up to 256; B*H*ceil(T/64)*8 < 2^31,
  * B*H*ceil(T/512)*ceil(max(dk,dv)/64) < 2^21, B*H*dk*dv < 2^34 - 2^10.
