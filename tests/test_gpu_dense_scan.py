@@ -374,3 +374,90 @@ def test_single_products_keep_all_of_fp32():
     off = (y.cpu().double() - want) / want / EPS
     assert off.abs().max() <= 3.1, off.abs().max().item()
     assert off.mean().abs() <= 0.1, off.mean().item()
+
+
+# Segments of 512 tokens (16 chunks; many streams) and errors in the mean.
+CHUNK = 32
+
+
+def magnitudes(x):
+    return walk({m: None if t is None else t.double().abs() for m, t in x.items()})
+
+
+def dot_magnitudes(x, o, mag):
+    """dlog_alpha's terms, in magnitude: its sums begin anew every CHUNK tokens. Up to its chunk's end a token
+    adds q.dq and k.dk; E at a chunk's end is that at the segment's end (a product of the two states) and, per
+    chunk between, what crosses its bounds: never more than E's own terms there, each taken three times at
+    most (from its product or the chunk behind, the chunk before, and the sum)."""
+    B, H, T = x["alpha"].shape
+    E = torch.nn.functional.pad(o["dlog_alpha"], (0, 1))
+    if x["dS"] is not None:
+        E[..., T] = (x["dS"].double().abs() * o["S"]).sum((-1, -2)) if mag else (x["dS"].double() * o["S"]).sum((-1, -2))
+    a = lambda t: t.double().abs() if mag else t.double()  # noqa: E731
+    terms = [(a(x[m]) * o["d" + m]).sum(-1) for m in ("q", "k")]
+    f, g = (lambda z: z, lambda z: z) if mag else (torch.square, torch.sqrt)
+    out = torch.zeros_like(o["dlog_alpha"])
+    for t0 in range(0, T, CHUNK):
+        t1, last = min(T, t0 + CHUNK), min(T, (t0 // SEGMENT + 1) * SEGMENT)
+        for c in terms:
+            out[:, :, t0:t1] += f(c[:, :, t0:t1]).flip(-1).cumsum(-1).flip(-1)
+        for b in {*range(t1, last, CHUNK), last}:
+            out[:, :, t0:t1] += 3 * f(E[:, :, b, None])
+    return g(out)
+
+
+def in_the_mean(got, want, x, T, dk, dv):
+    """Errors against the outputs in the mean square. A sum's roundings are of either sign, and its partial
+    sums no larger than the result in the mean, so m of them leave sqrt(m) times one: at most 2 half steps
+    over sqrt(3) where a matrix instruction rounds to either neighbour. m: 6 plane products per 32 of a width
+    for each of two contractions, 7 per chunk that the state crosses, 30 for decays, products and sums. A
+    plane that is lost is 2^-17 of its operand: some 30 half steps in the mean of its products."""
+    m = 12 * ((max(dk, dv) + 31) // 32) + 7 * ((T + CHUNK - 1) // CHUNK) + 30
+    rms = lambda t: t.square().mean().sqrt().item()  # noqa: E731
+    for name in ("y", "S") + GRADS:
+        size = rms(dot_magnitudes(x, want, False) if name == "dlog_alpha" else want[name])
+        e = rms(got[name].cpu().double() - want[name])
+        assert e <= (4 * m / 3) ** 0.5 * EPS * size, (name, e / size / EPS, (4 * m / 3) ** 0.5)
+
+
+def check_streams(x, streams, mean=True):
+    """All streams in one call, some of them against the walk."""
+    g = dev(x)
+    got = {**forward(g), **backward(g)}
+    pick = lambda z: {m: None if t is None else t.flatten(0, 1)[streams][:, None] for m, t in z.items()}  # noqa: E731
+    x, got = pick(x), pick(got)
+    (T, dk), dv = x["q"].shape[2:], x["v"].shape[3]
+    want, mag = walk(x), magnitudes(x)
+    mag["dlog_alpha"] = dot_magnitudes(x, mag, True)
+    check(got, want, mag, roundings(T, dk, dv), ("y", "S") + GRADS)
+    if mean:
+        in_the_mean(got, want, x, T, dk, dv)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,H,T,dk,dv", [(1, 2, 300, 128, 128), (2, 1, 130, 256, 256), (1, 1, 577, 200, 64), (2, 2, 96, 64, 40)])
+def test_errors_in_the_mean(B, H, T, dk, dv, dtype):
+    check_streams(make(B, H, T, dk, dv, dtype, T + dv), list(range(B * H)))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("gates", ["mid", "extreme", "near one"])
+@pytest.mark.parametrize("B,H,T,dk,dv,streams", [(64, 8, 1100, 8, 16, [0, 7, 300, 511]), (8, 32, 1100, 72, 136, [3, 255]),
+                                                 (8, 8, 2085, 128, 128, [63])])
+def test_segments_of_many_chunks(B, H, T, dk, dv, streams, gates, dtype):
+    """With 512 streams and column slabs a segment takes 512 tokens, with 64 streams of 2085 tokens 288 (the last one fewer)."""
+    x = make(B, H, T, dk, dv, dtype, T + dk, gates="extreme" if gates == "extreme" else "mid")
+    if gates == "near one":
+        x["alpha"] = 1 - (1 - x["alpha"]) / 64
+    check_streams(x, streams, gates != "extreme")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_roundings_of_a_large_token_stay_in_its_chunk(dtype):
+    """Token 400 has rows 2^10 times the others', products 2^40 times; around it gates of 1/2 let nothing
+    of that reach beyond a chunk or two. A sum over the whole segment would carry roundings of 2^16 on."""
+    x = make(64, 8, 1030, 16, 8, dtype, 4)
+    x["alpha"][:, :, 300:430] = 0.5
+    for m in ("q", "k", "v", "dy"):
+        x[m][:, :, 400] *= 1024
+    check_streams(x, [0, 200, 511], False)
