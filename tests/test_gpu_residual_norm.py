@@ -288,3 +288,73 @@ def test_scales_of_rows_that_are_not_finite(d):
         g[5] = float("nan")                                  # and so is that of a column
         s = sdm.sdm_residual_norm(x[:1].to(DEV), g.to(DEV), None, EPS, "e4m3", group)["scale"].cpu()
         assert torch.isnan(s[0, 0]) and (s[0, 1:] > 0).all()
+
+
+# Rows in turn: 9001 x 512 and below take 16 to 64 threads a row (4 to 16 rows a workgroup, 1024
+# workgroups), 1536 to 4096 columns 256 threads, more 1024 threads (256 workgroups).
+LOOPS = [(40000, 40, 16, 1024), (20000, 200, 8, 1024), (9001, 512, 4, 1024), (9001, 1001, 4, 1024), (2600, 1536, 1, 1024),
+         (2600, 3001, 1, 1024), (700, 8192, 1, 256), (700, 12001, 1, 256)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,d,together,blocks", LOOPS)
+def test_backward_of_several_rows_a_thread_group(rows, d, together, blocks, dtype):
+    """dgamma's sums are chains of a thread group's rows, of a workgroup's groups, of 1 in 64 workgroups,
+    and 6 levels of pairs: a rounding of each is of at most the sum of the magnitudes."""
+    h, dy, gamma = make(rows, d, dtype, rows + 5 * d)
+    H, DY, GA = h.double(), dy.double(), gamma.double()
+    r = 1 / (H.square().mean(-1, keepdim=True) + EPS).sqrt()
+    n = H * r
+    want = r * (GA * DY - n * (GA * DY * n).mean(-1, keepdim=True))
+    mag = r * ((GA * DY).abs() + n.abs() * (GA * DY * n).abs().mean(-1, keepdim=True))
+    got = sdm.sdm_residual_norm_backward(dy.to(DEV), h.to(DEV), gamma.to(DEV), None, EPS)
+    assert ((got["dx"].cpu().double() - want).abs() <= HALF[dtype] * want.abs() + (3 * d + 16) * 2.0 ** -24 * mag + 1e-37).all()
+    # the squares' sum of a row: a thread's pieces of 8, 10 levels over its threads; half of that in its root
+    own = 8 + 10 + 6
+    chain = (rows + together * blocks - 1) // (together * blocks) + together + (blocks + 63) // 64 + 6
+    tol = (own + chain) * 2.0 ** -24 * (DY * n).abs().sum(0)
+    assert ((got["dgamma"].cpu().double() - (DY * n).sum(0)).abs() <= tol + 1e-37).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,d", [c[:2] for c in LOOPS] + [(9001, 40), (5000, 256), (1500, 1024)])
+def test_no_row_is_lost_or_added_twice(rows, d, dtype):
+    """Rows of +-1 without eps have a norm of 1, and whole gradients: dgamma is a sum of whole numbers below 2^24, and exact."""
+    g = torch.Generator().manual_seed(rows)
+    h = torch.randint(0, 2, (rows, d), generator=g).mul_(2).sub_(1).to(dtype)
+    dy = torch.randint(-9, 10, (rows, d), generator=g).to(dtype)
+    got = sdm.sdm_residual_norm_backward(dy.to(DEV), h.to(DEV), torch.ones(d, device=DEV), None, 0.0)
+    assert torch.equal(got["dgamma"].cpu().double(), (dy.double() * h.double()).sum(0))
+
+
+@pytest.mark.parametrize("rows,d", [(5, 300), (7, 1024), (2600, 1536), (700, 8200)])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_dx_over_dy_and_over_h(rows, d, dtype):
+    h, dy, gamma = (t.to(DEV) for t in make(rows, d, dtype, d))
+    dh = torch.flip(dy, (0, 1)).contiguous()
+    for behind in (None, dh):
+        want = sdm.sdm_residual_norm_backward(dy, h, gamma, behind, EPS)
+        for over in ("dy", "h") + (("dh",) if behind is not None else ()):
+            a = {"dy": dy.clone(), "h": h.clone(), "dh": None if behind is None else behind.clone()}
+            got = sdm.sdm_residual_norm_backward(a["dy"], a["h"], gamma, a["dh"], EPS, out={"dx": a[over]})
+            assert got["dx"].data_ptr() == a[over].data_ptr()
+            assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dgamma"], want["dgamma"]), over
+
+
+def test_gradient_of_a_bf16_stream():
+    """The norm is that of the fp32 sum, its gradient's that of the stored one, half a bf16 step (2^-8) off an
+    element: n is off by 2^-8 |n| from that and, through r, by at most as much again, so dx in fp32 is by 2 * 2^-8
+    times each of r's three uses in its terms, 6 * 2^-8 of their magnitudes (dgamma: 2 * 2^-8), and a little in second order."""
+    x, res, gamma = make(50, 1000, BF, 21)
+    dy = torch.randn((50, 1000), generator=torch.Generator().manual_seed(8))
+    X, R, GA = (t.double().requires_grad_() for t in (x, res, gamma))
+    y = reference(X, R, GA)[1]
+    dx, _, dgamma = torch.autograd.grad((y * dy.double()).sum(), [X, R, GA])
+    f = sdm.sdm_residual_norm(x.to(DEV), gamma.to(DEV), res.to(DEV), EPS, "bf16")
+    got = sdm.sdm_residual_norm_backward(dy.to(DEV), f["h"], gamma.to(DEV), None, EPS)
+    h = x.double() + res.double()
+    r = 1 / (h.square().mean(-1, keepdim=True) + EPS).sqrt()
+    n, gd = (h * r).abs(), (gamma * dy).double().abs()
+    mag = r * (gd + n * (gd * n).mean(-1, keepdim=True))
+    assert ((got["dx"].cpu().double() - dx).abs() <= 6.1 * 2.0 ** -8 * mag).all()
+    assert ((got["dgamma"].cpu().double() - dgamma).abs() <= 2.1 * 2.0 ** -8 * (n * dy.double().abs()).sum(0)).all()
