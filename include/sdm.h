@@ -360,8 +360,10 @@ int sdm_output_gate(const float* y, const float* gamma, const void* g, int g_dty
 
 /*
  * The dense gated recurrence: the layers that a stack puts beside its sparse
- * ones, with the scan's gates, v and y ([SDM] §2.1 Eq. (1) with the gates of
- * §2.4: a state of dk rows, all of them decayed and written by every token).
+ * ones, with the scan's gates, v and y ([SDM] §2.1 Eq. (1) without its normalised
+ * read, with the gates of §2.4: a state of dk rows, all of them decayed and written
+ * by every token). A write adds beta k (x) v as it is; it is not the delta rule, which
+ * first takes off what the state holds for k (Eq. (2)).
  */
 
 /*
@@ -414,7 +416,9 @@ int64_t sdm_dense_scan_backward_workspace_bytes(int64_t B, int64_t H, int64_t T,
  *   dlog_alpha_t = alpha_t dL/dalpha_t = <G_t, alpha_t S_{t-1}>
  * The decay's gradient is the one to ln alpha: it is finite for alpha = 0, and
  * with alpha = exp(-A softplus(z)) the gate's inputs follow as
- * dz = -A sigmoid(z) dlog_alpha, dA = -softplus(z) dlog_alpha.
+ * dz = -A sigmoid(z) dlog_alpha, dA = -softplus(z) dlog_alpha. It is formed as a running
+ * difference of q.dq and k.dk: its error is some 2^-20 of those and of the neighbouring
+ * tokens' values, not of its own, so do not divide it by a tiny alpha.
  *   q, k, v, in_dtype, alpha, beta, S0: as given to the forward call
  *   dy [B, H, T, dv] fp32: dL/dy;  dS [B, H, dk, dv] fp32: dL/dS, or NULL (zeros)
  *   dq, dk_out [B, H, T, dk], dv_out [B, H, T, dv], dlog_alpha, dbeta [B, H, T]: fp32 (out)
@@ -444,7 +448,9 @@ int sdm_dense_scan_backward(const void* q, const void* k, const void* v, int in_
  *   where all are 0, else at least 2^-126), and y holds the fp32 quotients y / scale, rounded
  *   to nearest even; where a y is NaN or infinite, so is the scale, and all of its y are NaN
  * The norm is that of the fp32 sum; h is stored rounded to its dtype. h may
- * be res, or x in x's dtype (in place); y may not alias x, res or h.
+ * be res, or x in x's dtype (in place); y may not alias x, res or h. The squares are
+ * summed in fp32: their sum must stay below 2^128 (y is 0 beyond), and above 0 where
+ * eps = 0 (a row of zeros gives NaN then).
  * Supported: 1 <= d <= 16384; group 0, or a power of two from 32 to 512 that
  * divides d; rows < 2^31. rows = 0 is empty work.
  */

@@ -518,7 +518,7 @@ def sdm_dense_scan_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, al
                            beta: torch.Tensor, S0: Optional[torch.Tensor] = None,
                            S: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                            workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Dense gated recurrence S_t = alpha_t S_{t-1} + beta_t k_t (x) v_t, y_t = q_t S_t.
+    """Dense gated recurrence S_t = alpha_t S_{t-1} + beta_t k_t (x) v_t, y_t = q_t S_t (no delta rule).
 
     q, k [B,H,T,dk], v [B,H,T,dv] (one dtype, fp32 or bf16), alpha, beta [B,H,T] fp32,
     S0 [B,H,dk,dv] fp32 or None (zeros). Returns (y [B,H,T,dv] fp32, S the last state);
@@ -579,8 +579,9 @@ def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.
 
     x [..., d], res the same shape or None, gamma [d] fp32. ``dtype`` is y's: "f32",
     "bf16" or "e4m3", the last with fp32 scales per row (group 0: [..., 1]) or per ``group``
-    columns ([..., d / group]). Returns a dict with y, h (with res; in res's dtype) and
-    scale (for e4m3); ``out`` may pass those tensors preallocated, h may be res or x.
+    columns ([..., d / group]); a row or group with a NaN or infinity has such a scale. Returns
+    a dict with y, h (with res; in res's dtype) and scale (for e4m3); ``out`` may pass those
+    tensors preallocated, h may be res or x.
     """
     d_ = _gpu(x, gamma, res)
     if dtype not in NORM_OUT:
@@ -617,7 +618,7 @@ def sdm_residual_norm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.T
 
     dy, dh [..., d] of one dtype (dh: what arrives at h from behind, or None), h [..., d],
     gamma [d] fp32. Returns a dict with dx (the gradient of x and of res, in dy's dtype) and
-    dgamma [d] fp32; ``out`` may pass them preallocated.
+    dgamma [d] fp32; ``out`` may pass them preallocated, dx may be dy, dh or h.
     """
     d_ = _gpu(dy, h, gamma, dh)
     if dy.dim() < 1 or gamma.shape != dy.shape[-1:] or gamma.dtype != torch.float32 or h.shape != dy.shape \

@@ -1,7 +1,9 @@
 // dense.hip -- the dense gated recurrence on gfx950: a d_k x d_v state per head
 // in which every token decays all rows and adds one outer product,
 //   S_t = alpha_t S_{t-1} + beta_t k_t (x) v_t,     y_t = q_t S_t,
-// and its gradients. The sparse scan's dense counterpart: same gates, v and y.
+// and its gradients: linear attention with a forget and an input gate, the same gates,
+// v and y as the sparse scan's. (Its rule adds beta k (x) v as it is; the scan's takes
+// off what the rows hold before it adds, and nothing here normalises the read.)
 //
 // One recurrence serves the forward and every gradient. With rows xi, kap (DK
 // wide) and omg (DV wide), processed forwards or backwards in t,
@@ -23,10 +25,13 @@
 // for S and G in one launch, and for dq, dk and dv in one.
 //
 // Measured at 4 x 8 streams, T = 8192, 128 x 128, bf16 rows (32 streams, 16
-// segments of 512 tokens each): forward 136 us in all (segments' sums 38, carry 14, y 84;
-// 342 MB that it cannot do without: 72 us at a copy's 4.75 TB/s), backward 491 us (traced
-// one by one: sums 98, carry 23, gradients 376, gates 22; 749 MB, 158 us). The passes are
-// bound by vector instructions (dense_pass.h), the carry by HBM.
+// segments of 512 tokens each): forward 141 us in all (segments' sums 36, carry 14, y 84;
+// 342 MB that it cannot do without: 72 us at a copy's 4.75 TB/s), backward 494 us (sums 97,
+// carry 23, gradients 358, gates 22; 749 MB, 158 us). The forward moves 604 MB, k and v twice
+// and the states four times: the sums 168 MB at 4.6 TB/s, the carry 67 at 4.9, y 369 at 4.4,
+// where the vector units are busy for half of the time too (dense_pass.h). The gradients are
+// bound by vector and matrix instructions. With few streams the carry is a chain of loads: 0.4 us
+// a segment.
 #include "dense_pass.h"
 
 namespace sdm {
@@ -153,8 +158,10 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, int64_t e) {
 
 // One token (decoding): the state is read and written once, as rows of 64
 // columns; thread (r, c) takes rows r + 16 i, columns 4c .. 4c + 3. HBM-bound: 2048
-// states of 128 x 128 in 54 us, 5.0 TB/s with part of them in the memory-side cache. (The
-// chunked form takes 60 us there and 57 for two tokens, where walking them took 67.)
+// states of 128 x 128 in 62.6 us over three sets in turn, 4.3 TB/s (41.5 over one, part of
+// which stays in the memory-side cache). The chunked pass takes 62.6 (50.9) for one token and 62.9
+// for two there, but 31 us against 23 for 4096 states of 64 x 64, and 195 against 112 for
+// 4096 of 128 x 128 with fp32 rows.
 template <int NR>
 __global__ __launch_bounds__(256) void dense_step_kernel(DenseFwdArgs a) {
     __shared__ float red[16][STEP_COLS];
@@ -226,8 +233,10 @@ DenseLayout forward_layout(int64_t NS, int64_t T, int dk, int dv) {
     y.nseg = (T + y.L - 1) / y.L;
     // One segment a stream (one launch) unless segments are quicker. In us: a chunk takes 2.5, in the
     // first pass some 0.6 of that; two more launches 6; a segment's state is moved four times at 4.75
-    // TB/s. (Measured, one / segments: 8 streams of 128 x 128, T = 128: 15 / 17, 256: 25 / 18; 64 streams,
-    // 384: 36 / 36, 1024: 84 / 54; of 256 x 256, 512: 65 / 99, 1024: 123 / 144.)
+    // TB/s. (Measured, one / segments: 8 streams of 128 x 128, T = 128: 17 / 21, 256: 27 / 21; 64 streams,
+    // 384: 39 / 38, 1024: 91 / 56; of 256 x 256, 512: 71 / 101, 1024: 134 / 152; 256 streams of 64 x 64, 512:
+    // 29 / 37, 1024: 52 / 61. The chunk's time is that of bf16 rows and 128 x 128; with fp32 rows the same
+    // are 26 / 26, 46 / 27; 68 / 55, 178 / 99; 141 / 154, 270 / 253; 45 / 58, 84 / 102.)
     const double one = 2.5 * T / DENSE_CHUNK;
     const double many = 4.0 * y.L / DENSE_CHUNK + 6 + 16e-6 * y.nseg * NS * dk * dv / 4.75;
     if (y.nseg == 1 || one <= many) return DenseLayout{T, 1, 0, 0, 0};

@@ -36,13 +36,14 @@
 // others read it.
 //
 // What bounds it (4 x 8 streams, T = 8192, 128 x 128, bf16; per SIMD, in thousands of cycles):
-// the y pass takes 163, of them 89 of vector instructions, 57 of matrix ones and, per CU, 49 of LDS;
-// the three gradient passes 693, 354, 232 and 238. Nearly half of the vector instructions cut X into
-// planes: with that left out (wrong results) y takes 73 us in place of 87, with two of the three matrix
-// products left out 93. Two planes would do with a relative error of 3e-6; three keep fp32's. Tried and
-// dropped: chunks of 64 tokens (half the cutting, but spilled registers: 117 us against 90), fp32
-// matrix instructions (819 us for the forward against 287 for the first form of this one), residues
-// of the planes by the bf16 dot instruction (its wait states cost what it saved: 92 us against 87).
+// the y pass takes 173, of them 89 of vector instructions, 57 of matrix ones and, per CU, 49 of LDS,
+// and moves its bytes at 4.4 TB/s; the three gradient passes 711, 354, 232 and 238. Nearly half of
+// the vector instructions cut X into planes: with that left out (wrong results) y took 73 us in place of
+// 87, with two of the three matrix products left out 93. Two planes would do with a relative error of
+// 3e-6; three keep fp32's. Tried and dropped: chunks of 64 tokens (half the cutting, but spilled
+// registers: 117 us against 90), fp32 matrix instructions (819 us for the forward against 287 for the
+// first form of this one), residues of the planes by the bf16 dot instruction (its wait states cost what
+// it saved: 92 us against 87).
 #pragma once
 #include <type_traits>
 
@@ -652,8 +653,8 @@ constexpr int dense_slab(int dv) { return dv <= 64 ? 64 : 128; }
 
 // f(contracted width's tiles, column tiles a wavefront, wavefronts), for a pass of its own.
 // Four wavefronts of 32 columns read each operand half as often as eight of 16, and hold
-// twice the state (4x8x8192 tokens, 128 x 128, bf16: y in 85 / 86 us, T = 131072 in one sequence
-// 472 / 484 in all); from 128 to 256 rows of state a lane's registers allow 16 columns.
+// twice the state (128 x 128, bf16: 4x8x8192 tokens 147 / 157 us, 1x8x131072 506 / 533; with fp32
+// rows 291 / 282, 1x8x32768 302 / 294); from 128 to 256 rows of state a lane's registers allow 16 columns.
 template <int N>
 using Int = std::integral_constant<int, N>;
 template <class F>
@@ -687,8 +688,8 @@ hipError_t dense_sg(const DenseArgs& s, const DenseArgs& g, hipStream_t st) {
 // dq, dk and dv: NR planes of the rows q, k and v, three of dy's. dq and dk contract the
 // value width (tiles TV) and put out the key width; dv the other way round (tiles TK). In one
 // launch all have 4 wavefronts, or 8 where a width passes 128, or where fp32 rows of 128 leave
-// room for one workgroup on a CU (2x8x4096 tokens, 128 x 128, fp32, all of the backward: 263 us
-// with 8, 301 with 4; of 64 x 128: 127 with 8, 98 with 4).
+// room for one workgroup on a CU (2x8x4096 tokens, fp32, all of the backward, with 4 / 8: 128 x 128
+// 304 / 261 us, 64 x 128 201 / 217, 64 x 64 100 / 144).
 template <int NR, int TK, int TV>
 hipError_t dense_grads_t(const DenseArgs& q, const DenseArgs& k, const DenseArgs& v, hipStream_t st) {
     constexpr int W = TK == 16 || TV == 16 || (NR == 3 && TK == 8 && TV == 8) ? 8 : 4;

@@ -8,7 +8,7 @@
 // Both read each input once and write each output once: a row stays in the
 // registers of the TPR threads that own it (NV pieces of VEC elements each),
 // between its sums and its outputs. HBM-bound: 32768 rows of 1024 in bf16 with a
-// residual, to bf16 and e4m3 with a scale per 128 columns, 236 MB in 49 us (4.8 TB/s; a
+// residual, to bf16 and e4m3 with a scale per 128 columns, 236 MB in 50 us (4.7 TB/s; a
 // copy of 1 GB reaches 4.75); the backward, 268 MB, in 58 us (4.6 TB/s). One row a thread
 // group and no loop over rows: with 4 rows in turn the forward took 57 us in rotation, against 48.
 //
