@@ -97,8 +97,8 @@ __device__ __forceinline__ void store_vec(void* p, bool bf16, int64_t e, int n, 
 }
 
 // v / scale in e4m3 (nearest even) with |v| <= 448 scale; 0 for a scale of 0. The codes are those of
-// the fp32 quotient: a product with the scale's reciprocal is off by up to two steps, and 1 value in
-// 10^5 near the border of two codes then falls to the other side. Each correction by the exact rest of
+// the fp32 quotient: a product with the scale's reciprocal is off by up to two steps, and a value in
+// some 10^6, near the border of two codes, then falls to the other side. Each correction by the exact rest of
 // the division leaves the nearest value to a quotient at most a step off (Markstein's theorem, for a
 // reciprocal rounded to nearest); the first takes the product that near. (32768 x 1024, groups of 128:
 // 44 us by the reciprocal alone, 45 so, 47 by divisions; 8192 x 8192, a scale a row: 89, 94, 100.)
@@ -127,7 +127,8 @@ __device__ __forceinline__ void store_e4m3(void* p, int64_t e, int n, const floa
     }
 }
 
-// The scale that maps the largest magnitude onto e4m3's largest value, 448. It
+// The scale that maps the largest magnitude onto e4m3's largest value, 448 (a product with
+// 1 / 448 is a step off the quotient for more than half of all magnitudes). It
 // stays a normal number; 0 for a row of zeros, NaN or infinite where the largest is.
 __device__ __forceinline__ float e4m3_scale(float amax) {
     const float s = amax / 448.f;
