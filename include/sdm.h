@@ -46,7 +46,7 @@ typedef enum sdm_status {
 } sdm_status;
 
 /* SDM_E4M3 (8-bit floats of 4 exponent and 3 mantissa bits, largest value 448)
- * is an output type of sdm_residual_norm only. */
+ * is an output type of sdm_residual_norm and sdm_residual_layer_norm only. */
 typedef enum sdm_dtype { SDM_F32 = 0, SDM_BF16 = 1, SDM_E4M3 = 2 } sdm_dtype;
 
 /* The two write rules the notes keep side by side ([SDM] §2.4-§2.5):
@@ -520,6 +520,145 @@ int sdm_balance_forward(const int32_t* idx, const float* wt, const uint8_t* mask
 int sdm_balance_backward(const int32_t* idx, const uint8_t* mask, const int32_t* counts, const int32_t* tokens,
                          const float* dloss, int64_t B, int64_t H, int64_t T, int64_t K, int64_t N, float* dwt,
                          void* stream);
+
+/*
+ * A selective state-space layer's operators: the layers of a state per channel that a stack puts
+ * beside its sparse and dense ones. The convolution is also what a dense layer has on its q, k and v.
+ *
+ * Tensors said to be "by strides" are rows of consecutive channels at any address that their elements'
+ * size divides; their strides (in elements, not negative) are an array in host memory, or NULL for a
+ * contiguous tensor. Everything else follows the conventions above.
+ *
+ * start [B, T] bytes or NULL: non-zero where a sequence begins (packed sequences): a token sees nothing
+ * in front of it. lengths [B] int32 or NULL: only the first lengths[b] tokens are there (padded
+ * sequences; taken into [0, T]); the others are not looked at, outputs and gradients there are 0, and the last state
+ * is the one behind the last token that is there. Both: any alignment that their elements allow.
+ */
+
+/* Activations behind the convolution. */
+typedef enum sdm_act { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1 } sdm_act;
+
+/*
+ * sdm_causal_conv_forward -- the short causal convolution over time of every channel:
+ *     y_t = act(bias + sum_j w_j x_{t-K+1+j}),   j = 0 .. K-1
+ *   x       [B, H, T, d]    dtype (SDM_F32 or SDM_BF16), by strides [3]: batch, head, token (heads out of a
+ *                           projection [B, T, H, d] need no copy; H = 1 for a layer without heads)
+ *   w       [H, d, K], bias [H, d] fp32 (bias may be NULL)
+ *   S0      [B, H, K-1, d]  dtype: the K-1 inputs in front of token 0, oldest first, or NULL (zeros)
+ *   S       [B, H, K-1, d]  dtype (out): those behind the last token, or NULL (not wanted); may be S0
+ *                           (decoding). Rows in front of the last sequence's first token are 0
+ *   y       [B, H, T, d]    dtype (out); may not overlap x, S0 or S
+ * Products and sums are fp32. T = 0 passes the state on.
+ * Supported: K from 2 to 8; B*H*ceil(T/32)*d < 2^31, H*d <= 2^23.
+ */
+int sdm_causal_conv_forward(const void* x, int dtype, const int64_t* x_strides, const float* w, const float* bias,
+                            int act, const void* S0, void* S, const uint8_t* start, const int32_t* lengths, void* y,
+                            int64_t B, int64_t H, int64_t T, int64_t d, int64_t K, void* stream);
+
+/*
+ * sdm_causal_conv_backward_workspace_bytes -- device workspace sdm_causal_conv_backward needs (0: no work;
+ * -1: sizes that the call refuses).
+ */
+int64_t sdm_causal_conv_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t d, int64_t K);
+
+/*
+ * sdm_causal_conv_backward -- its gradients; nothing is kept from the forward call.
+ *   dy [B, H, T, d] dtype: dL/dy;  x, w, bias, act, S0, start, lengths as given to the forward call
+ *   dS [B, H, K-1, d] dtype: dL/dS, or NULL (zeros)
+ *   dx [B, H, T, d] dtype (out), by strides [3] (so that it may be a part of a projection's gradient); its
+ *   elements may not share an address, nor overlap an input
+ *   dw [H, d, K], dbias [H, d] fp32 (out; dbias may be NULL), summed over all tokens in an order that
+ *   follows from the sizes alone;  dS0 [B, H, K-1, d] dtype (out), or NULL; may be dS only where T = 0
+ *   workspace >= sdm_causal_conv_backward_workspace_bytes bytes, 16-byte aligned
+ * Same support as the forward. B = 0 is empty work (dw and dbias are not written).
+ */
+int sdm_causal_conv_backward(const void* dy, const void* x, int dtype, const int64_t* x_strides, const float* w,
+                             const float* bias, int act, const void* S0, const void* dS, const uint8_t* start,
+                             const int32_t* lengths, void* dx, const int64_t* dx_strides, float* dw, float* dbias,
+                             void* dS0, int64_t B, int64_t H, int64_t T, int64_t d, int64_t K, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/*
+ * sdm_selective_scan_workspace_bytes -- device workspace sdm_selective_scan_forward needs (0: none; -1: sizes
+ * that the call refuses).
+ */
+int64_t sdm_selective_scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);
+
+/*
+ * sdm_selective_scan_forward -- for every channel d (of group g = d / (D / G)) and state n:
+ *     delta_t = softplus(dt_t + dt_bias)               (or dt_t + dt_bias, softplus = 0)
+ *     h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t
+ *     y_t = (sum_n C_t h_t + D x_t) z_t sigmoid(z_t)   (without the last factors where z is NULL)
+ *   x, dt, z  [B, T, D]     in_dtype (SDM_F32 or SDM_BF16), by strides (z may be NULL)
+ *   Bm, Cm    [B, T, G, N]  in_dtype, by strides
+ *   strides   [12]: x's batch and token, dt's, z's, then Bm's batch, token and group, and Cm's
+ *   A [D, N], Dskip [D] (or NULL), dt_bias [D] (or NULL) fp32
+ *   S0        [B, D, N]     fp32: the state before token 0, or NULL (zeros)
+ *   S         [B, D, N]     fp32 (out): the state behind the last token, or NULL; may be S0 (decoding)
+ *   y         [B, T, D]     in_dtype (out); may not overlap an input
+ *   workspace >= sdm_selective_scan_workspace_bytes bytes, 16-byte aligned (may be NULL where that is 0)
+ * Products, sums and states are fp32. Meant for delta A <= 0; inputs and states must be finite (a NaN or
+ * infinity in one channel's x, dt, z or state stays in that channel). T = 0 passes the state on.
+ * Supported: N <= 64, D <= 2^20 with G dividing it, B*G*ceil(D/G/64) < 2^21.
+ */
+int sdm_selective_scan_forward(const void* x, const void* dt, const void* z, const void* Bm, const void* Cm,
+                               int in_dtype, const int64_t* strides, const float* A, const float* Dskip,
+                               const float* dt_bias, int softplus, const float* S0, float* S, const uint8_t* start,
+                               const int32_t* lengths, void* y, int64_t B, int64_t T, int64_t D, int64_t G, int64_t N,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * sdm_selective_scan_backward_workspace_bytes -- device workspace sdm_selective_scan_backward needs: a state
+ * every 8 tokens and rows of partial sums (0: no work; -1: sizes that the call refuses).
+ */
+int64_t sdm_selective_scan_backward_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);
+
+/*
+ * sdm_selective_scan_backward -- its gradients; nothing is kept from the forward call.
+ *   dy [B, T, D] in_dtype, by strides: dL/dy;  strides [14]: the forward call's, then dy's batch and token
+ *   dS [B, D, N] fp32: dL/dS, or NULL (zeros); the other inputs as given to the forward call
+ *   dx, ddt, dz [B, T, D] in_dtype (out; dz NULL where z is)
+ *   dA [D, N], dB, dC [B, T, G, N], dD, ddt_bias [D], dS0 [B, D, N] fp32 (out; dD, ddt_bias and dS0 may be
+ *   NULL; dS0 may be dS)
+ *   workspace >= sdm_selective_scan_backward_workspace_bytes bytes, 16-byte aligned
+ * The order of all sums follows from the sizes alone. Same support as the forward, and
+ * B*T*G*ceil(N/16) < 2^27, G*ceil(D/G/64)*ceil(N/16) < 2^17.
+ * B = 0 is empty work (dA, dD and ddt_bias are not written).
+ */
+int sdm_selective_scan_backward(const void* dy, const void* x, const void* dt, const void* z, const void* Bm,
+                                const void* Cm, int in_dtype, const int64_t* strides, const float* A,
+                                const float* Dskip, const float* dt_bias, int softplus, const float* S0,
+                                const float* dS, const uint8_t* start, const int32_t* lengths, void* dx, void* ddt,
+                                void* dz, float* dA, float* dB, float* dC, float* dD, float* ddt_bias, float* dS0,
+                                int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+
+/*
+ * sdm_residual_layer_norm -- sdm_residual_norm with the mean taken off and a bias, per row:
+ *   h = x + res,   m = mean_j h_j,   y = (h - m) / sqrt(mean_j (h_j - m)^2 + eps) * gamma + bias
+ *   bias [d] fp32, or NULL (zeros); everything else, e4m3 outputs with their scales among it, as there
+ * The mean and the squares about it are summed in fp32, over the fp32 sums h.
+ */
+int sdm_residual_layer_norm(const void* x, int x_dtype, const void* res, void* h, int h_dtype, const float* gamma,
+                            const float* bias, float eps, int64_t rows, int64_t d, void* y, int y_dtype, float* scale,
+                            int64_t group, void* stream);
+
+/*
+ * sdm_residual_layer_norm_backward_workspace_bytes -- device workspace
+ * sdm_residual_layer_norm_backward needs (0: no work, -1: invalid sizes).
+ */
+int64_t sdm_residual_layer_norm_backward_workspace_bytes(int64_t rows, int64_t d);
+
+/*
+ * sdm_residual_layer_norm_backward -- its gradients, from the stored h (x where there was no residual), with
+ * r = 1 / sqrt(mean (h - m)^2 + eps) and n = (h - m) r:
+ *   dx = dh + r (gamma dy - mean_j(gamma dy) - n mean_j(gamma dy n))
+ *   dgamma = sum over rows of dy n,   dbias = sum over rows of dy (may be NULL)
+ * Arguments, aliases and support as sdm_residual_norm_backward.
+ */
+int sdm_residual_layer_norm_backward(const void* dy, const void* dh, int g_dtype, const void* h, int h_dtype,
+                                     const float* gamma, float eps, int64_t rows, int64_t d, void* dx, float* dgamma,
+                                     float* dbias, void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,7 +1,8 @@
 """SDM (Sparse Delta Memory) hot path on MI355X: product-key addressing and the
 sparse gated delta scan as hand-written HIP kernels behind a C ABI
 (include/sdm.h), and the operators that a stack of such layers puts around them
-(dense gated recurrence, residual norm, balance loss). This package holds the Python binding (``binding``), the
+(dense gated recurrence, residual norm, balance loss; a selective state-space
+layer's causal convolution, scan and layer norm). This package holds the Python binding (``binding``), the
 in-tree build (``build``) and the seeded synthetic inputs (``inputs``)."""
 from . import inputs  # noqa: F401
 from .binding import (SDM_BF16, SDM_DELTA_EQ4, SDM_DELTA_FIG2, SDM_E4M3, SDM_F32,  # noqa: F401
@@ -14,4 +15,8 @@ from .binding import (SDM_BF16, SDM_DELTA_EQ4, SDM_DELTA_FIG2, SDM_E4M3, SDM_F32
                       sdm_balance_backward, sdm_balance_forward, sdm_balance_workspace_bytes,
                       sdm_dense_scan_backward, sdm_dense_scan_backward_workspace_bytes,
                       sdm_dense_scan_forward, sdm_dense_scan_workspace_bytes,
-                      sdm_residual_norm, sdm_residual_norm_backward)
+                      sdm_residual_norm, sdm_residual_norm_backward,
+                      sdm_causal_conv_backward, sdm_causal_conv_backward_workspace_bytes, sdm_causal_conv_forward,
+                      sdm_residual_layer_norm, sdm_residual_layer_norm_backward,
+                      sdm_selective_scan_backward, sdm_selective_scan_backward_workspace_bytes,
+                      sdm_selective_scan_forward, sdm_selective_scan_workspace_bytes)

@@ -64,6 +64,18 @@ _SIGS = {
     "sdm_balance_workspace_bytes": (_I64, [_I64, _I64, _I64, _I64, _I64]),
     "sdm_balance_forward": (_I, [_P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P]),
     "sdm_balance_backward": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P]),
+    "sdm_causal_conv_forward": (_I, [_P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P] + [_I64] * 5 + [_P]),
+    "sdm_causal_conv_backward_workspace_bytes": (_I64, [_I64] * 5),
+    "sdm_causal_conv_backward": (_I, [_P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P] + [_I64] * 5
+                                 + [_P, _I64, _P]),
+    "sdm_selective_scan_workspace_bytes": (_I64, [_I64] * 5),
+    "sdm_selective_scan_forward": (_I, [_P] * 5 + [_I, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P] + [_I64] * 5 + [_P, _I64, _P]),
+    "sdm_selective_scan_backward_workspace_bytes": (_I64, [_I64] * 5),
+    "sdm_selective_scan_backward": (_I, [_P] * 6 + [_I, _P, _P, _P, _P, _I] + [_P] * 13 + [_I64] * 5 + [_P, _I64, _P]),
+    "sdm_residual_layer_norm": (_I, [_P, _I, _P, _P, _I, _P, _P, ctypes.c_float, _I64, _I64, _P, _I, _P, _I64, _P]),
+    "sdm_residual_layer_norm_backward_workspace_bytes": (_I64, [_I64, _I64]),
+    "sdm_residual_layer_norm_backward": (_I, [_P, _P, _I, _P, _I, _P, ctypes.c_float, _I64, _I64, _P, _P, _P,
+                                              _P, _I64, _P]),
 }
 
 _lib = None
@@ -583,12 +595,18 @@ def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.
     a dict with y, h (with res; in res's dtype) and scale (for e4m3); ``out`` may pass those
     tensors preallocated, h may be res or x.
     """
-    d_ = _gpu(x, gamma, res)
+    return _norm("sdm_residual_norm", x, gamma, (), res, eps, dtype, group, out)
+
+
+def _norm(fn, x, gamma, more, res, eps, dtype, group, out):
+    """``more``: the parameters that the call takes behind gamma, [d] fp32 or None."""
+    d_ = _gpu(x, gamma, res, *more)
     if dtype not in NORM_OUT:
         raise ValueError(f"unknown output dtype {dtype!r}")
     if x.dim() < 1 or gamma.shape != x.shape[-1:] or gamma.dtype != torch.float32 \
-            or (res is not None and res.shape != x.shape):
-        raise ValueError("shape or dtype mismatch in sdm_residual_norm")
+            or (res is not None and res.shape != x.shape) \
+            or any(p is not None and (p.shape != gamma.shape or p.dtype != torch.float32) for p in more):
+        raise ValueError(f"shape or dtype mismatch in {fn}")
     d = x.shape[-1]
     rows = x.numel() // d if d else 0
     code, yt = NORM_OUT[dtype]
@@ -605,9 +623,9 @@ def sdm_residual_norm(x: torch.Tensor, gamma: torch.Tensor, res: Optional[torch.
     for name, (shp, dt) in want.items():
         out[name] = _out(out.get(name), x, shp, dt, name)
     h, scale = out.get("h"), out.get("scale")
-    _call("sdm_residual_norm", d_,
+    _call(fn, d_,
         _at(x), _dtype_code(x), _at(res), _at(h), _dtype_code(x if res is None else res), _at(gamma),
-        float(eps), rows, d, _at(out["y"]), code, _at(scale), group)
+        *map(_at, more), float(eps), rows, d, _at(out["y"]), code, _at(scale), group)
     return out
 
 
@@ -620,24 +638,47 @@ def sdm_residual_norm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.T
     gamma [d] fp32. Returns a dict with dx (the gradient of x and of res, in dy's dtype) and
     dgamma [d] fp32; ``out`` may pass them preallocated, dx may be dy, dh or h.
     """
+    return _norm_backward("sdm_residual_norm_backward", ("dgamma",), dy, h, gamma, dh, eps, out, workspace)
+
+
+def _norm_backward(fn, sums, dy, h, gamma, dh, eps, out, workspace):
     d_ = _gpu(dy, h, gamma, dh)
     if dy.dim() < 1 or gamma.shape != dy.shape[-1:] or gamma.dtype != torch.float32 or h.shape != dy.shape \
             or (dh is not None and (dh.shape != dy.shape or dh.dtype != dy.dtype)):
-        raise ValueError("shape or dtype mismatch in sdm_residual_norm_backward")
+        raise ValueError(f"shape or dtype mismatch in {fn}")
     d = dy.shape[-1]
     rows = dy.numel() // d if d else 0
     out = dict(out or {})
-    _known(out, ("dx", "dgamma"))
-    dx = _out(out.get("dx"), dy, dy.shape, dy.dtype, "dx")
-    dgamma = _out(out.get("dgamma"), dy, (d,), torch.float32, "dgamma")
-    if rows == 0:
-        dgamma.zero_()
-    n = lib().sdm_residual_norm_backward_workspace_bytes(rows, d)
+    _known(out, ("dx", *sums))
+    got = {"dx": _out(out.get("dx"), dy, dy.shape, dy.dtype, "dx")}
+    for name in sums:
+        got[name] = _out(out.get(name), dy, (d,), torch.float32, name)
+        if rows == 0:
+            got[name].zero_()
+    n = getattr(lib(), fn + "_workspace_bytes")(rows, d)
     ws = _workspace(workspace, max(n, 0), d_)
-    _call("sdm_residual_norm_backward", d_,
+    _call(fn, d_,
         _at(dy), _at(dh), _dtype_code(dy), _at(h), _dtype_code(h), _at(gamma), float(eps), rows, d,
-        _at(dx), _at(dgamma), _at(ws), ws.numel())
-    return {"dx": dx, "dgamma": dgamma}
+        *map(_at, got.values()), _at(ws), ws.numel())
+    return got
+
+
+def sdm_residual_layer_norm(x: torch.Tensor, gamma: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                            res: Optional[torch.Tensor] = None, eps: float = 1e-5, dtype: str = "bf16", group: int = 0,
+                            out: Optional[dict] = None) -> dict:
+    """h = x + res and its layer norm y = (h - mean h) / sqrt(var h + eps) * gamma + bias, per row.
+
+    bias [d] fp32 or None; everything else, outputs among it, as in sdm_residual_norm.
+    """
+    return _norm("sdm_residual_layer_norm", x, gamma, (bias,), res, eps, dtype, group, out)
+
+
+def sdm_residual_layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor,
+                                     dh: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                                     out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of sdm_residual_layer_norm from the stored h: dx, dgamma and dbias [d] fp32 (as
+    sdm_residual_norm_backward)."""
+    return _norm_backward("sdm_residual_layer_norm_backward", ("dgamma", "dbias"), dy, h, gamma, dh, eps, out, workspace)
 
 
 def sdm_balance_workspace_bytes(B: int, H: int, T: int, K: int, N: int) -> int:
@@ -699,3 +740,231 @@ def sdm_balance_backward(idx: torch.Tensor, counts: torch.Tensor, tokens: torch.
         _at(idx), _at(mask), _at(counts), _at(tokens), _at(dloss), B, H, T, K, counts.shape[1],
         _at(dwt))
     return dwt
+
+
+# Rows by strides: consecutive channels, the other dimensions at any stride.
+
+ACTS = {None: 0, "silu": 1}
+
+
+def _rows(name: str, t: torch.Tensor, like: torch.Tensor, shape):
+    """Checks a tensor by strides (batch, head or token, token or group first, channels last)."""
+    if t.get_device() != like.get_device() or t.get_device() < 0:
+        raise ValueError("all tensors must be on the same GPU")
+    if t.shape != shape or t.dtype != like.dtype:
+        raise ValueError(f"{name} has the wrong shape or dtype")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the channels of {name} must be consecutive")
+
+
+def _sequences(start, lengths, B, T, like):
+    if start is not None:
+        if start.shape != (B, T) or start.dtype not in (torch.uint8, torch.bool):
+            raise ValueError("start must be [B, T], uint8 or bool")
+        _gpu(like, start)
+    if lengths is not None:
+        if lengths.shape != (B,) or lengths.dtype != torch.int32:
+            raise ValueError("lengths must be [B], int32")
+        _gpu(like, lengths)
+
+
+def _conv_inputs(fn, x, w, bias, act, S0, S, start, lengths):
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    if x.dim() == 4:
+        (B, H, T, d), lead = x.shape, x.shape[:2]
+        s = (x.stride(0), x.stride(1), x.stride(2))
+    elif x.dim() == 3:
+        (B, T, d), H, lead = x.shape, 1, x.shape[:1]
+        s = (x.stride(0), 0, x.stride(1))
+    else:
+        raise ValueError("x must be [B, T, d] or [B, H, T, d]")
+    _rows("x", x, x, x.shape)
+    if w.dim() != x.dim() - 1 or w.shape[:-1] != (*lead[1:], d) or w.dtype != torch.float32 \
+            or (bias is not None and (bias.shape != w.shape[:-1] or bias.dtype != torch.float32)):
+        raise ValueError(f"shape or dtype mismatch in {fn}")
+    K = w.shape[-1]
+    if K < 2:
+        raise ValueError("w must hold at least 2 taps")
+    dev = _gpu(w, bias)
+    state = (*lead, K - 1, d)
+    for name, t in (("S0", S0), ("S", S)):
+        if t is not None:
+            _out(t, w, state, x.dtype, name)
+    if x.get_device() != w.get_device():
+        raise ValueError("all tensors must be on the same GPU")
+    _sequences(start, lengths, B, T, w)
+    return dev, (B, H, T, d, K), state, (ctypes.c_int64 * 3)(*s)
+
+
+def sdm_causal_conv_forward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                            act: Optional[str] = "silu", S0: Optional[torch.Tensor] = None,
+                            S: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
+                            lengths: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None
+                            ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Short causal convolution y_t = act(bias + sum_j w_j x_{t-K+1+j}) over time of every channel.
+
+    x [B,T,d] or [B,H,T,d] (fp32 or bf16; channels consecutive, the rest at any stride: a part of a
+    projection or its heads transposed need no copy), w [d,K] or [H,d,K] and bias [d] or [H,d] fp32,
+    act "silu" or None. S0: the K-1 inputs in front, [B,K-1,d] or [B,H,K-1,d] in x's dtype, or None
+    (zeros). start [B,T] uint8 or bool: tokens that begin a sequence; lengths [B] int32: the tokens that
+    are there (y is 0 behind them). Returns (y, S): y contiguous in x's shape and dtype, S the last K-1
+    inputs; both may be passed preallocated, and S may be S0 (updated in place).
+    """
+    d_, sizes, state, xs = _conv_inputs("sdm_causal_conv_forward", x, w, bias, act, S0, S, start, lengths)
+    if S is None:
+        S = x.new_empty(state)
+    y = _out(y, w, x.shape, x.dtype, "y")
+    _call("sdm_causal_conv_forward", d_,
+        _at(x), _dtype_code(x), xs, _at(w), _at(bias), ACTS[act], _at(S0), _at(S), _at(start), _at(lengths), _at(y), *sizes)
+    return y, S
+
+
+def sdm_causal_conv_backward_workspace_bytes(B: int, H: int, T: int, d: int, K: int) -> int:
+    n = lib().sdm_causal_conv_backward_workspace_bytes(B, H, T, d, K)
+    if n < 0:
+        raise ValueError("invalid sizes for the convolution's backward workspace")
+    return n
+
+
+def sdm_causal_conv_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                             act: Optional[str] = "silu", S0: Optional[torch.Tensor] = None,
+                             dS: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
+                             lengths: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                             workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of one sdm_causal_conv_forward call (nothing is kept from it).
+
+    dy contiguous in x's shape and dtype; dS, the gradient of the last state, or None. Returns a dict with
+    dx (x's dtype, in x's order of dimensions), dw, dbias (fp32) and dS0 (x's dtype); ``out`` may pass those
+    preallocated, dx at any strides with consecutive channels (a part of a projection's gradient).
+    """
+    d_, sizes, state, xs = _conv_inputs("sdm_causal_conv_backward", x, w, bias, act, S0, dS, start, lengths)
+    B, H, T, d, K = sizes
+    _out(dy, w, x.shape, x.dtype, "dy")
+    out = dict(out or {})
+    _known(out, ("dx", "dw", "dbias", "dS0"))
+    dx = out.get("dx")
+    if dx is None:
+        dx = torch.empty_like(x)
+    _rows("dx", dx, x, x.shape)
+    gs = (dx.stride(0), dx.stride(1) if x.dim() == 4 else 0, dx.stride(-2))
+    dw = _out(out.get("dw"), w, w.shape, torch.float32, "dw")
+    dbias = _out(out.get("dbias"), w, w.shape[:-1], torch.float32, "dbias")
+    dS0 = _out(out.get("dS0"), w, state, x.dtype, "dS0")
+    if B == 0:
+        dw.zero_()
+        dbias.zero_()
+    ws = _workspace(workspace, sdm_causal_conv_backward_workspace_bytes(*sizes), d_)
+    _call("sdm_causal_conv_backward", d_,
+        _at(dy), _at(x), _dtype_code(x), xs, _at(w), _at(bias), ACTS[act], _at(S0), _at(dS), _at(start), _at(lengths),
+        _at(dx), (ctypes.c_int64 * 3)(*gs), _at(dw), _at(dbias), _at(dS0), *sizes, _at(ws), ws.numel())
+    return {"dx": dx, "dw": dw, "dbias": dbias, "dS0": dS0}
+
+
+def sdm_selective_scan_workspace_bytes(B: int, T: int, D: int, G: int, N: int) -> int:
+    n = lib().sdm_selective_scan_workspace_bytes(B, T, D, G, N)
+    if n < 0:
+        raise ValueError("invalid sizes for the selective scan workspace")
+    return n
+
+
+def _selective_inputs(fn, x, dt, A, Bm, Cm, D, z, dt_bias, states, start, lengths, dy=None):
+    if x.dim() != 3 or Bm.dim() not in (3, 4) or A.dim() != 2:
+        raise ValueError("x must be [B, T, D], A [D, N], Bm and Cm [B, T, N] or [B, T, G, N]")
+    B, T, n = x.shape
+    G, N = (Bm.shape[2] if Bm.dim() == 4 else 1), A.shape[1]
+    groups = (B, T, G, N) if Bm.dim() == 4 else (B, T, N)
+    s = []
+    for name, t in (("x", x), ("dt", dt), ("z", z)):
+        if t is None:
+            s += (0, 0)
+            continue
+        _rows(name, t, x, x.shape)
+        s += t.stride()[:2]
+    for name, t in (("Bm", Bm), ("Cm", Cm)):
+        _rows(name, t, x, groups)
+        s += t.stride()[:3] if Bm.dim() == 4 else (*t.stride()[:2], 0)
+    if dy is not None:
+        _rows("dy", dy, x, x.shape)
+        s += dy.stride()[:2]
+    if G < 1 or n % G or A.shape[0] != n or A.dtype != torch.float32 \
+            or any(p is not None and (p.shape != (n,) or p.dtype != torch.float32) for p in (D, dt_bias)):
+        raise ValueError(f"shape or dtype mismatch in {fn}")
+    dev = _gpu(A, D, dt_bias)
+    if x.get_device() != A.get_device():
+        raise ValueError("all tensors must be on the same GPU")
+    for name, t in states:
+        if t is not None:
+            _out(t, A, (B, n, N), torch.float32, name)
+    _sequences(start, lengths, B, T, A)
+    return dev, (B, T, n, G, N), (ctypes.c_int64 * len(s))(*s)
+
+
+def sdm_selective_scan_forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+                               D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                               dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                               S0: Optional[torch.Tensor] = None, S: Optional[torch.Tensor] = None,
+                               start: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                               y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                               ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Selective state-space scan: delta = softplus(dt + dt_bias) (or dt + dt_bias), h_t = exp(delta_t A) h_{t-1} +
+    delta_t x_t B_t, y_t = (C_t h_t + D x_t) silu(z_t).
+
+    x, dt, z [B,T,D] and Bm, Cm [B,T,N] or [B,T,G,N] (channels in G groups), one dtype (fp32 or bf16; last
+    dimension consecutive, the rest at any stride), A [D,N], D and dt_bias [D] fp32, S0 [B,D,N] fp32 or None
+    (zeros). start and lengths as in sdm_causal_conv_forward. Returns (y [B,T,D] in x's dtype, S the last
+    state); both may be passed preallocated, and S may be S0 (updated in place).
+    """
+    d_, sizes, s = _selective_inputs("sdm_selective_scan_forward", x, dt, A, Bm, Cm, D, z, dt_bias,
+                                     (("S0", S0), ("S", S)), start, lengths)
+    B, T, n, G, N = sizes
+    if S is None:
+        S = A.new_empty((B, n, N))
+    y = _out(y, A, x.shape, x.dtype, "y")
+    need = sdm_selective_scan_workspace_bytes(*sizes)
+    ws = _workspace(workspace, need, d_) if need or workspace is not None else None
+    _call("sdm_selective_scan_forward", d_,
+        _at(x), _at(dt), _at(z), _at(Bm), _at(Cm), _dtype_code(x), s, _at(A), _at(D), _at(dt_bias), int(softplus),
+        _at(S0), _at(S), _at(start), _at(lengths), _at(y), *sizes, _at(ws), ws.numel() if ws is not None else 0)
+    return y, S
+
+
+def sdm_selective_scan_backward_workspace_bytes(B: int, T: int, D: int, G: int, N: int) -> int:
+    n = lib().sdm_selective_scan_backward_workspace_bytes(B, T, D, G, N)
+    if n < 0:
+        raise ValueError("invalid sizes for the selective scan's backward workspace")
+    return n
+
+
+def sdm_selective_scan_backward(dy: torch.Tensor, x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor,
+                                Cm: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                                dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                                S0: Optional[torch.Tensor] = None, dS: Optional[torch.Tensor] = None,
+                                start: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                                out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of one sdm_selective_scan_forward call (nothing is kept from it).
+
+    dy [B,T,D] in x's dtype, at any stride; dS [B,D,N] fp32, the gradient of the last state, or None. Returns
+    a dict with dx, ddt, dz (with z) in x's dtype, dA, dB, dC, dD, ddt_bias and dS0 in fp32, named after the
+    formula's letters and shaped as the inputs; ``out`` may pass those tensors preallocated.
+    """
+    d_, sizes, s = _selective_inputs("sdm_selective_scan_backward", x, dt, A, Bm, Cm, D, z, dt_bias,
+                                     (("S0", S0), ("dS", dS)), start, lengths, dy)
+    B, T, n, G, N = sizes
+    out = dict(out or {})
+    want = {"dx": (x.shape, x.dtype), "ddt": (x.shape, x.dtype), "dz": (x.shape, x.dtype), "dA": (A.shape, torch.float32),
+            "dB": (Bm.shape, torch.float32), "dC": (Bm.shape, torch.float32), "dD": ((n,), torch.float32),
+            "ddt_bias": ((n,), torch.float32), "dS0": ((B, n, N), torch.float32)}
+    if z is None:
+        del want["dz"]
+    _known(out, want)
+    for name, (shp, dtype) in want.items():
+        out[name] = _out(out.get(name), A, shp, dtype, name)
+        if B == 0:
+            out[name].zero_()
+    ws = _workspace(workspace, sdm_selective_scan_backward_workspace_bytes(*sizes), d_)
+    _call("sdm_selective_scan_backward", d_,
+        _at(dy), _at(x), _at(dt), _at(z), _at(Bm), _at(Cm), _dtype_code(x), s, _at(A), _at(D), _at(dt_bias), int(softplus),
+        _at(S0), _at(dS), _at(start), _at(lengths), *(_at(out.get(k)) for k in ("dx", "ddt", "dz", "dA", "dB", "dC", "dD", "ddt_bias", "dS0")),
+        *sizes, _at(ws), ws.numel())
+    return out

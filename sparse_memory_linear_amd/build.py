@@ -13,7 +13,7 @@ LIB = os.path.join(PKG, "libsdm.so")
 OBJ = os.path.join(PKG, "_build")
 SOURCES = ["sdm_api.hip", "address.hip", "scan.hip", "scan_bwd.hip", "state_init.hip", "glue.hip",
            "dense.hip", "dense_bf16.hip", "dense_grad.hip", "dense_f32.hip",
-           "dense_grad_f32.hip", "norm.hip", "balance.hip"]
+           "dense_grad_f32.hip", "norm.hip", "balance.hip", "conv.hip", "selective.hip", "selective_bwd.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

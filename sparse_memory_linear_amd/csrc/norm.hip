@@ -1,9 +1,13 @@
-// norm.hip -- RMS-Norm of a token's row with the residual's addition, and its
+// norm.hip -- RMS-Norm and layer norm of a token's row with the residual's addition, and their
 // gradients, on gfx950:
 //   h = x + res,   y = h / sqrt(mean(h^2) + eps) * gamma,
 // y in fp32, bf16 or e4m3 with fp32 scales (per row, or per group of columns).
 // Backward, with r = 1 / sqrt(mean(h^2) + eps) and n = h r:
 //   dx = dh + r (gamma dy - n mean(gamma dy n)),   dgamma = sum over rows of dy n.
+// The layer norm (MEAN) takes the row's mean off first, m = mean(h), c = h - m:
+//   y = c / sqrt(mean(c^2) + eps) * gamma + bias,
+//   dx = dh + r (gamma dy - mean(gamma dy) - n mean(gamma dy n)),   n = c r,   dbias = sum over rows of dy;
+// its variance is the mean of the squares about the mean, a second sum over the registers.
 //
 // Both read each input once and write each output once: a row stays in the
 // registers of the TPR threads that own it (NV pieces of VEC elements each),
@@ -16,6 +20,7 @@
 // and the backward works from the stored h, so that it reads no statistics.
 #include "sdm_buffer.h"
 #include "sdm_internal.h"
+#include "sdm_rows.h"
 
 namespace sdm {
 namespace {
@@ -96,6 +101,11 @@ __device__ __forceinline__ void store_vec(void* p, bool bf16, int64_t e, int n, 
     }
 }
 
+__device__ __forceinline__ void clear_vec(float (&v)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+}
+
 // v / scale in e4m3 (nearest even) with |v| <= 448 scale; 0 for a scale of 0. The codes are those of
 // the fp32 quotient: a product with the scale's reciprocal is off by up to two steps, and a value in
 // some 10^6, near the border of two codes, then falls to the other side. Each correction by the exact rest of
@@ -155,7 +165,24 @@ __device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*buf)[2
     }
 }
 
-template <int TPR, int NV, bool TAIL>
+// Sums of x and y over them; buf is free on entry, and may be used again behind the next barrier
+template <int TPR>
+__device__ __forceinline__ void row_sums(float& x, float& y, float (*buf)[2]) {
+    for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) {
+        x += __shfl_xor(x, m);
+        y += __shfl_xor(y, m);
+    }
+    if constexpr (TPR > 64) {
+        const int w = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) { buf[w][0] = x; buf[w][1] = y; }
+        __syncthreads();
+        x = 0.f; y = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) { x += buf[i][0]; y += buf[i][1]; }
+    }
+}
+
+template <int TPR, int NV, bool TAIL, bool MEAN>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     __shared__ float buf[TPR < 64 ? 1 : TPR / 64][2];
@@ -183,20 +210,63 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
             for (int i = 0; i < VEC; ++i) v[j][i] += r[i];
         }
     }
+    float r;
+    if constexpr (!MEAN) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + lane) * VEC;
-        if (c >= a.d) break;
-        if (a.res) store_vec(a.h, a.h_bf16, at + c, left<TAIL>(a.d, c), v[j]);
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+            if (a.res) store_vec(a.h, a.h_bf16, at + c, left<TAIL>(a.d, c), v[j]);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            ss = fmaf(v[j][i], v[j][i], ss);
-            v[j][i] *= ga[j][i];
-            mx = larger(mx, v[j][i]);
+            for (int i = 0; i < VEC; ++i) {
+                ss = fmaf(v[j][i], v[j][i], ss);
+                v[j][i] *= ga[j][i];
+                mx = larger(mx, v[j][i]);
+            }
         }
+        row_reduce<TPR>(ss, mx, buf);
+        r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+    } else {
+        __shared__ float buf2[TPR < 64 ? 1 : TPR / 64][2], buf3[TPR < 64 ? 1 : TPR / 64][2];
+        float sum = 0.f, none = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+            if (a.res) store_vec(a.h, a.h_bf16, at + c, left<TAIL>(a.d, c), v[j]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) sum += v[j][i];  // 0 behind the row's end
+        }
+        row_sums<TPR>(sum, none, buf2);
+        const float m = sum / (float)a.d;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                v[j][i] = i < left<TAIL>(a.d, c) ? v[j][i] - m : 0.f;
+                ss = fmaf(v[j][i], v[j][i], ss);
+            }
+        }
+        row_sums<TPR>(ss, none, buf3);
+        r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+            float be[VEC];
+            clear_vec(be);
+            if (a.bias) load_vec(a.bias, false, c, left<TAIL>(a.d, c), be);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                v[j][i] = fmaf(v[j][i] * r, ga[j][i], be[i]);
+                mx = larger(mx, v[j][i]);
+            }
+        }
+        if (a.y_type == NORM_E4M3 && a.group == 0) row_reduce<TPR>(none, mx, buf);
+        r = 1.f;  // y is whole
     }
-    row_reduce<TPR>(ss, mx, buf);
-    const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
     float scale = 0.f;
     if (a.y_type == NORM_E4M3 && a.group == 0) {
         scale = e4m3_scale(mx * r);
@@ -227,19 +297,22 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
 // A block's rows' share of dgamma stays in registers, its wavefronts' shares are
 // added in order in LDS, and the blocks' rows of `part` by norm_dgamma_kernel:
 // the order of all sums follows from the sizes alone.
-template <int TPR, int NV, bool TAIL>
+template <int TPR, int NV, bool TAIL, bool MEAN>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwdArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     extern __shared__ float dg[];  // [d] (TPR < 256)
     __shared__ float buf[TPR < 64 ? 1 : TPR / 64][2];
     const int lane = threadIdx.x % TPR;
-    float ga[NV][VEC], acc[NV][VEC];
+    float ga[NV][VEC], acc[NV][VEC], accb[MEAN ? NV : 1][VEC];  // accb: dbias
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + lane) * VEC;
         if (c < a.d) load_vec(a.gamma, false, c, left<TAIL>(a.d, c), ga[j]);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
+        for (int i = 0; i < VEC; ++i) {
+            acc[j][i] = 0.f;
+            if constexpr (MEAN) accb[j][i] = 0.f;
+        }
     }
     for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
         float h[NV][VEC], dy[NV][VEC];
@@ -251,6 +324,31 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
             if (c >= a.d) break;
             load_vec(a.h, a.h_bf16, at + c, left<TAIL>(a.d, c), h[j]);
             load_vec(a.dy, a.g_bf16, at + c, left<TAIL>(a.d, c), dy[j]);
+        }
+        float mg = 0.f;  // mean of gamma dy
+        if constexpr (MEAN) {
+            __shared__ float buf2[TPR < 64 ? 1 : TPR / 64][2];
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * TPR + lane) * VEC;
+                if (c >= a.d) break;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    m += h[j][i];
+                    mg = fmaf(dy[j][i], ga[j][i], mg);
+                }
+            }
+            row_sums<TPR>(m, mg, buf2);  // (buf's two barriers lie between this row's use of buf2 and the next one's)
+            m /= (float)a.d;
+            mg /= (float)a.d;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * TPR + lane) * VEC;
+                if (c >= a.d) break;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) h[j][i] = i < left<TAIL>(a.d, c) ? h[j][i] - m : 0.f;
+            }
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -285,7 +383,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 acc[j][i] = fmaf(dy[j][i], h[j][i] * r, acc[j][i]);
-                o[i] = r * (dy[j][i] * ga[j][i] - h[j][i] * k);
+                if constexpr (MEAN) accb[j][i] += dy[j][i];
+                o[i] = r * ((MEAN ? dy[j][i] * ga[j][i] - mg : dy[j][i] * ga[j][i]) - h[j][i] * k);
             }
             if (a.dh) {
                 float t[VEC];
@@ -296,28 +395,36 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
             store_vec(a.dx, a.g_bf16, at + c, left<TAIL>(a.d, c), o);
         }
     }
-    float* part = a.part + (int64_t)blockIdx.x * a.d;
-    if constexpr (TPR < 256) {
-        for (int w = 0; w < RPB; ++w) {
-            if (threadIdx.x / TPR == w)
+    // the wavefronts' shares of one of the sums, in order, into the block's row of part
+    auto leave = [&](float (&acc)[NV][VEC], float* part) {
+        if constexpr (TPR < 256) {
+            for (int w = 0; w < RPB; ++w) {
+                if (threadIdx.x / TPR == w)
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const int c = (j * TPR + lane) * VEC;
-                    if (c >= a.d) break;
+                    for (int j = 0; j < NV; ++j) {
+                        const int c = (j * TPR + lane) * VEC;
+                        if (c >= a.d) break;
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        if (c + i < a.d) dg[c + i] = w ? dg[c + i] + acc[j][i] : acc[j][i];
-                }
-            __syncthreads();
+                        for (int i = 0; i < VEC; ++i)
+                            if (c + i < a.d) dg[c + i] = w ? dg[c + i] + acc[j][i] : acc[j][i];
+                    }
+                __syncthreads();
+            }
+            for (int c = threadIdx.x; c < a.d; c += 256) part[c] = dg[c];
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * TPR + lane) * VEC;
+                if (c >= a.d) break;
+                store_vec(part, false, c, left<TAIL>(a.d, c), acc[j]);
+            }
         }
-        for (int c = threadIdx.x; c < a.d; c += 256) part[c] = dg[c];
-    } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + lane) * VEC;
-            if (c >= a.d) break;
-            store_vec(part, false, c, left<TAIL>(a.d, c), acc[j]);
-        }
+    };
+    float* part = a.part + (int64_t)blockIdx.x * a.d * (MEAN ? 2 : 1);
+    leave(acc, part);
+    if constexpr (MEAN) {
+        __syncthreads();
+        leave(accb, part + a.d);
     }
 }
 
@@ -338,17 +445,30 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* part, fl
     if (w == 0 && c < d) dgamma[c] = x;
 }
 
+// dgamma and dbias of the columns [2][d]
+struct NormSums {
+    float* dgamma; float* dbias;
+    int d;
+    __device__ void operator()(int64_t i, float v) const {
+        if (i < d) dgamma[i] = v;
+        else if (dbias) dbias[i - d] = v;
+    }
+};
+
 template <int TPR, int NV, bool TAIL>
 void norm_launch(const NormArgs& a, hipStream_t st) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1, THR = TPR < 256 ? 256 : TPR;
     const int64_t n = (a.rows + RPB - 1) / RPB, most = 1 << 21;  // a grid's side: fewer than 2^32 threads
     const dim3 grid((unsigned)(n < most ? n : most), (unsigned)((n + most - 1) / most));
-    hipLaunchKernelGGL((norm_kernel<TPR, NV, TAIL>), grid, dim3(THR), 0, st, a);
+    if (a.mean) hipLaunchKernelGGL((norm_kernel<TPR, NV, TAIL, true>), grid, dim3(THR), 0, st, a);
+    else hipLaunchKernelGGL((norm_kernel<TPR, NV, TAIL, false>), grid, dim3(THR), 0, st, a);
 }
 template <int TPR, int NV, bool TAIL>
 void norm_launch(const NormBwdArgs& a, hipStream_t st) {
     constexpr int THR = TPR < 256 ? 256 : TPR;
-    hipLaunchKernelGGL((norm_bwd_kernel<TPR, NV, TAIL>), dim3((unsigned)a.blocks), dim3(THR), TPR < 256 ? a.d * 4 : 0, st, a);
+    const dim3 grid((unsigned)a.blocks);
+    if (a.mean) hipLaunchKernelGGL((norm_bwd_kernel<TPR, NV, TAIL, true>), grid, dim3(THR), TPR < 256 ? a.d * 4 : 0, st, a);
+    else hipLaunchKernelGGL((norm_bwd_kernel<TPR, NV, TAIL, false>), grid, dim3(THR), TPR < 256 ? a.d * 4 : 0, st, a);
 }
 
 // Threads a row: as many as it has pieces up to a wavefront (16 and 32 for the
@@ -388,6 +508,7 @@ hipError_t launch_norm_backward(NormBwdArgs a, hipStream_t st) {
     a.blocks = (int)norm_bwd_blocks(a.rows, a.d);
     hipError_t e = norm_any(a, st);
     if (e != hipSuccess) return e;
+    if (a.mean) return sum_columns(a.part, a.blocks, 2 * a.d, NormSums{a.dgamma, a.dbias, a.d}, st);
     hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((a.d + 15) / 16)), dim3(1024), 0, st, a.part, a.dgamma,
                        a.blocks, a.d);
     return hipGetLastError();

@@ -629,12 +629,11 @@ int check_norm_sizes(const char* fn, int64_t rows, int64_t d, float eps) {
 
 }  // namespace
 
-extern "C" {
+namespace {
 
-int sdm_residual_norm(const void* x, int x_dtype, const void* res, void* h, int h_dtype, const float* gamma,
-                      float eps, int64_t rows, int64_t d, void* y, int y_dtype, float* scale, int64_t group,
-                      void* stream) {
-    const char* fn = "sdm_residual_norm";
+int norm_impl(const char* fn, bool mean, const void* x, int x_dtype, const void* res, void* h, int h_dtype,
+              const float* gamma, const float* bias, float eps, int64_t rows, int64_t d, void* y, int y_dtype,
+              float* scale, int64_t group, void* stream) {
     if (x_dtype != SDM_F32 && x_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown x dtype %d", fn, x_dtype);
     if (h_dtype != SDM_F32 && h_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown h dtype %d", fn, h_dtype);
     if (y_dtype != SDM_F32 && y_dtype != SDM_BF16 && y_dtype != SDM_E4M3)
@@ -651,6 +650,7 @@ int sdm_residual_norm(const void* x, int x_dtype, const void* res, void* h, int 
     if ((rc = check_buffers(fn, {x, gamma, y}))) return rc;
     if ((res == nullptr) != (h == nullptr)) return fail(SDM_ERR_NULL, "%s: res and h go together", fn);
     if (res && (rc = check_buffers(fn, {res, h}))) return rc;
+    if (bias && (rc = check_buffers(fn, {bias}))) return rc;
     if (y_dtype == SDM_E4M3 && (rc = check_buffers(fn, {scale}))) return rc;
     if (y == x || y == h || (res && y == res)) return fail(SDM_ERR_SHAPE, "%s: y may not alias x, res or h", fn);
     if (h && h == x && x_dtype != h_dtype) return fail(SDM_ERR_SHAPE, "%s: h may alias x only in the same dtype", fn);
@@ -659,19 +659,19 @@ int sdm_residual_norm(const void* x, int x_dtype, const void* res, void* h, int 
     a.rows = rows; a.d = (int)d; a.group = (int)group; a.eps = eps;
     a.y_type = y_dtype == SDM_E4M3 ? sdm::NORM_E4M3 : y_dtype == SDM_BF16 ? sdm::NORM_BF16 : sdm::NORM_F32;
     a.x_bf16 = x_dtype == SDM_BF16; a.h_bf16 = h_dtype == SDM_BF16;
+    a.bias = bias; a.mean = mean;
     hipError_t e = sdm::launch_norm(a, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, fn);
 }
 
-int64_t sdm_residual_norm_backward_workspace_bytes(int64_t rows, int64_t d) {
+int64_t norm_backward_bytes(bool mean, int64_t rows, int64_t d) {
     if (rows < 0 || d < 1 || d > 16384 || rows > 0x7FFFFFFFll) return -1;
-    return rows == 0 ? 0 : sdm::norm_bwd_blocks(rows, (int)d) * d * 4;
+    return rows == 0 ? 0 : sdm::norm_bwd_blocks(rows, (int)d) * d * (mean ? 8 : 4);
 }
 
-int sdm_residual_norm_backward(const void* dy, const void* dh, int g_dtype, const void* h, int h_dtype,
-                               const float* gamma, float eps, int64_t rows, int64_t d, void* dx, float* dgamma,
-                               void* workspace, int64_t workspace_bytes, void* stream) {
-    const char* fn = "sdm_residual_norm_backward";
+int norm_backward_impl(const char* fn, bool mean, const void* dy, const void* dh, int g_dtype, const void* h,
+                       int h_dtype, const float* gamma, float eps, int64_t rows, int64_t d, void* dx, float* dgamma,
+                       float* dbias, void* workspace, int64_t workspace_bytes, void* stream) {
     if (g_dtype != SDM_F32 && g_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown gradient dtype %d", fn, g_dtype);
     if (h_dtype != SDM_F32 && h_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown h dtype %d", fn, h_dtype);
     int rc = check_norm_sizes(fn, rows, d, eps);
@@ -679,15 +679,55 @@ int sdm_residual_norm_backward(const void* dy, const void* dh, int g_dtype, cons
     if (rows == 0) return ok();
     if ((rc = check_buffers(fn, {dy, h, gamma, dx, dgamma}))) return rc;
     if (dh && !aligned16(dh)) return fail(SDM_ERR_ALIGN, "%s: dh not 16-byte aligned", fn);
+    if (dbias && !aligned16(dbias)) return fail(SDM_ERR_ALIGN, "%s: dbias not 16-byte aligned", fn);
     if (dx == h && g_dtype != h_dtype) return fail(SDM_ERR_SHAPE, "%s: dx may alias h only in the same dtype", fn);
-    if ((rc = check_workspace(workspace, workspace_bytes, sdm::norm_bwd_blocks(rows, (int)d) * d * 4))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, norm_backward_bytes(mean, rows, d)))) return rc;
     sdm::NormBwdArgs a{};
     a.dy = dy; a.dh = dh; a.h = h; a.gamma = gamma; a.dx = dx; a.dgamma = dgamma;
     a.part = static_cast<float*>(workspace);
     a.rows = rows; a.d = (int)d; a.eps = eps;
     a.g_bf16 = g_dtype == SDM_BF16; a.h_bf16 = h_dtype == SDM_BF16;
+    a.dbias = dbias; a.mean = mean;
     hipError_t e = sdm::launch_norm_backward(a, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+}  // namespace
+
+extern "C" {
+
+int sdm_residual_norm(const void* x, int x_dtype, const void* res, void* h, int h_dtype, const float* gamma,
+                      float eps, int64_t rows, int64_t d, void* y, int y_dtype, float* scale, int64_t group,
+                      void* stream) {
+    return norm_impl("sdm_residual_norm", false, x, x_dtype, res, h, h_dtype, gamma, nullptr, eps, rows, d, y, y_dtype,
+                     scale, group, stream);
+}
+
+int64_t sdm_residual_norm_backward_workspace_bytes(int64_t rows, int64_t d) { return norm_backward_bytes(false, rows, d); }
+
+int sdm_residual_norm_backward(const void* dy, const void* dh, int g_dtype, const void* h, int h_dtype,
+                               const float* gamma, float eps, int64_t rows, int64_t d, void* dx, float* dgamma,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+    return norm_backward_impl("sdm_residual_norm_backward", false, dy, dh, g_dtype, h, h_dtype, gamma, eps, rows, d, dx,
+                              dgamma, nullptr, workspace, workspace_bytes, stream);
+}
+
+int sdm_residual_layer_norm(const void* x, int x_dtype, const void* res, void* h, int h_dtype, const float* gamma,
+                            const float* bias, float eps, int64_t rows, int64_t d, void* y, int y_dtype, float* scale,
+                            int64_t group, void* stream) {
+    return norm_impl("sdm_residual_layer_norm", true, x, x_dtype, res, h, h_dtype, gamma, bias, eps, rows, d, y, y_dtype,
+                     scale, group, stream);
+}
+
+int64_t sdm_residual_layer_norm_backward_workspace_bytes(int64_t rows, int64_t d) {
+    return norm_backward_bytes(true, rows, d);
+}
+
+int sdm_residual_layer_norm_backward(const void* dy, const void* dh, int g_dtype, const void* h, int h_dtype,
+                                     const float* gamma, float eps, int64_t rows, int64_t d, void* dx, float* dgamma,
+                                     float* dbias, void* workspace, int64_t workspace_bytes, void* stream) {
+    return norm_backward_impl("sdm_residual_layer_norm_backward", true, dy, dh, g_dtype, h, h_dtype, gamma, eps, rows, d,
+                              dx, dgamma, dbias, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
@@ -747,6 +787,284 @@ int sdm_balance_backward(const int32_t* idx, const uint8_t* mask, const int32_t*
     a.idx = idx; a.mask = mask; a.counts = counts; a.tokens = tokens; a.dloss = dloss; a.dwt = dwt;
     a.B = B; a.H = H; a.T = T; a.K = K; a.N = N;
     hipError_t e = sdm::launch_balance_backward(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t MOST = 0x7FFFFFFFll;
+
+// Strides (elements) of a tensor by strides: not negative, and its last element within 64 bits
+int check_strides(const char* fn, const char* name, std::initializer_list<int64_t> sizes,
+                  std::initializer_list<int64_t> strides) {
+    __int128 last = 0;
+    const int64_t* n = sizes.begin();
+    for (int64_t s : strides) {
+        if (s < 0) return fail(SDM_ERR_SHAPE, "%s: negative stride of %s", fn, name);
+        last += (__int128)(*n > 0 ? *n - 1 : 0) * s;
+        ++n;
+    }
+    return last < ((__int128)1 << 59) ? 0 : fail(SDM_ERR_UNSUPPORTED, "%s: strides of %s pass 64 bits", fn, name);
+}
+
+int check_address(const char* fn, const char* name, const void* p, int64_t bytes) {
+    if (!p) return fail(SDM_ERR_NULL, "%s: %s is NULL", fn, name);
+    return (uintptr_t)p % bytes == 0 ? 0 : fail(SDM_ERR_ALIGN, "%s: %s not aligned to its elements", fn, name);
+}
+
+// The largest power of two up to 8 elements that divides all of them (addresses in elements of `bytes`)
+int common_align(std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> counts, int64_t bytes) {
+    uint64_t all = 8;
+    for (const void* p : ptrs) all |= p ? (uintptr_t)p / bytes : 0;
+    for (int64_t n : counts) all |= (uint64_t)n;
+    return (int)(all & (~all + 1));
+}
+
+int check_conv(const char* fn, int dtype, int act, int64_t B, int64_t H, int64_t T, int64_t d, int64_t K) {
+    if (dtype != SDM_F32 && dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown dtype %d", fn, dtype);
+    if (act != SDM_ACT_NONE && act != SDM_ACT_SILU) return fail(SDM_ERR_DTYPE, "%s: unknown activation %d", fn, act);
+    if (B < 0 || H < 0 || T < 0 || d < 1 || K < 1) return fail(SDM_ERR_SHAPE, "%s: invalid sizes", fn);
+    if (K < 2 || K > 8) return fail(SDM_ERR_UNSUPPORTED, "%s: K=%lld: from 2 to 8 taps", fn, (long long)K);
+    // each factor below 2^31 first, so that the products stay in 64 bits
+    const int64_t tiles = T > sdm::CONV_TILE_MIN ? (T + sdm::CONV_TILE_MIN - 1) / sdm::CONV_TILE_MIN : 1;
+    if (B > MOST || H > MOST || T > MOST || d > MOST || B * H > MOST || H * d > MOST || B * H * tiles > MOST ||
+        B * H * tiles * d > MOST || H * d > 1 << 23)
+        return fail(SDM_ERR_UNSUPPORTED, "%s: too many tokens and channels for one launch", fn);
+    return B == 0 || H == 0 ? NO_WORK : 0;
+}
+
+// Rows by strides that a call writes: no element twice
+int check_apart(const char* fn, const char* name, int64_t row, std::initializer_list<int64_t> sizes,
+                std::initializer_list<int64_t> strides) {
+    __int128 extent = row;  // of the dimensions so far, the nearest ones first
+    bool used[3] = {};
+    for (size_t k = 0; k < sizes.size(); ++k) {
+        int at = -1;
+        for (int i = 0; i < (int)sizes.size(); ++i)
+            if (!used[i] && (at < 0 || strides.begin()[i] < strides.begin()[at])) at = i;
+        used[at] = true;
+        const int64_t n = sizes.begin()[at], s = strides.begin()[at];
+        if (n <= 1) continue;
+        if (s < extent) return fail(SDM_ERR_SHAPE, "%s: elements of %s share an address", fn, name);
+        extent += (__int128)(n - 1) * s;
+    }
+    return 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sdm_causal_conv_forward(const void* x, int dtype, const int64_t* x_strides, const float* w, const float* bias,
+                            int act, const void* S0, void* S, const uint8_t* start, const int32_t* lengths, void* y,
+                            int64_t B, int64_t H, int64_t T, int64_t d, int64_t K, void* stream) {
+    const char* fn = "sdm_causal_conv_forward";
+    int rc = check_conv(fn, dtype, act, B, H, T, d, K);
+    if (rc == NO_WORK) return ok();
+    if (rc) return rc;
+    const int64_t flat[3] = {H * T * d, T * d, d}, *xs = x_strides ? x_strides : flat, es = dtype == SDM_BF16 ? 2 : 4;
+    if ((rc = check_strides(fn, "x", {B, H, T}, {xs[0], xs[1], xs[2]}))) return rc;
+    if (T > 0 && ((rc = check_address(fn, "x", x, es)) || (rc = check_buffers(fn, {y})))) return rc;
+    if ((rc = check_buffers(fn, {w}))) return rc;
+    const void* opt[] = {bias, S0, S};
+    for (const void* p : opt)
+        if (p && !aligned16(p)) return fail(SDM_ERR_ALIGN, "%s: pointer %p not 16-byte aligned", fn, p);
+    if (lengths && (rc = check_address(fn, "lengths", lengths, 4))) return rc;
+    if (T > 0 && (y == x || y == S0 || y == S)) return fail(SDM_ERR_SHAPE, "%s: y may not alias x, S0 or S", fn);
+    sdm::ConvArgs a{};
+    a.x = x; a.w = w; a.bias = bias; a.S0 = S0; a.S = S; a.start = start; a.lengths = lengths; a.y = y;
+    a.x_b = xs[0]; a.x_h = xs[1]; a.x_t = xs[2];
+    a.B = B; a.H = H; a.T = T; a.d = (int)d; a.K = (int)K;
+    a.align = common_align({x}, {d, xs[0], xs[1], xs[2]}, es);
+    a.bf16 = dtype == SDM_BF16; a.silu = act == SDM_ACT_SILU;
+    hipError_t e = sdm::launch_conv(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+int64_t sdm_causal_conv_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t d, int64_t K) {
+    const int rc = check_conv("sdm_causal_conv_backward_workspace_bytes", SDM_F32, SDM_ACT_NONE, B, H, T, d, K);
+    if (rc == NO_WORK) return 0;
+    return rc ? -1 : sdm::conv_backward_workspace_bytes(B, H, T, d, (int)K);
+}
+
+int sdm_causal_conv_backward(const void* dy, const void* x, int dtype, const int64_t* x_strides, const float* w,
+                             const float* bias, int act, const void* S0, const void* dS, const uint8_t* start,
+                             const int32_t* lengths, void* dx, const int64_t* dx_strides, float* dw, float* dbias,
+                             void* dS0, int64_t B, int64_t H, int64_t T, int64_t d, int64_t K, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+    const char* fn = "sdm_causal_conv_backward";
+    int rc = check_conv(fn, dtype, act, B, H, T, d, K);
+    if (rc == NO_WORK) return ok();
+    if (rc) return rc;
+    const int64_t flat[3] = {H * T * d, T * d, d}, es = dtype == SDM_BF16 ? 2 : 4;
+    const int64_t *xs = x_strides ? x_strides : flat, *gs = dx_strides ? dx_strides : flat;
+    if ((rc = check_strides(fn, "x", {B, H, T}, {xs[0], xs[1], xs[2]}))) return rc;
+    if ((rc = check_strides(fn, "dx", {B, H, T}, {gs[0], gs[1], gs[2]}))) return rc;
+    if ((rc = check_apart(fn, "dx", d, {B, H, T}, {gs[0], gs[1], gs[2]}))) return rc;
+    if (T > 0) {
+        if ((rc = check_address(fn, "x", x, es)) || (rc = check_address(fn, "dx", dx, es)) || (rc = check_buffers(fn, {dy})))
+            return rc;
+        if (dx == x || dx == dy || (dS0 && (dS0 == dS || dS0 == S0 || dS0 == dx)))
+            return fail(SDM_ERR_SHAPE, "%s: dx and dS0 may not alias an input or each other", fn);
+    }
+    if ((rc = check_buffers(fn, {w, dw}))) return rc;
+    const void* opt[] = {bias, S0, dS, dbias, dS0};
+    for (const void* p : opt)
+        if (p && !aligned16(p)) return fail(SDM_ERR_ALIGN, "%s: pointer %p not 16-byte aligned", fn, p);
+    if (lengths && (rc = check_address(fn, "lengths", lengths, 4))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, sdm::conv_backward_workspace_bytes(B, H, T, d, (int)K)))) return rc;
+    sdm::ConvBwdArgs a{};
+    a.dy = dy; a.x = x; a.w = w; a.bias = bias; a.S0 = S0; a.dS = dS; a.start = start; a.lengths = lengths;
+    a.dx = dx; a.dw = dw; a.dbias = dbias; a.dS0 = dS0;
+    a.part = static_cast<float*>(workspace);
+    a.x_b = xs[0]; a.x_h = xs[1]; a.x_t = xs[2];
+    a.dx_b = gs[0]; a.dx_h = gs[1]; a.dx_t = gs[2];
+    a.B = B; a.H = H; a.T = T; a.d = (int)d; a.K = (int)K;
+    a.align = common_align({x, dx}, {d, xs[0], xs[1], xs[2], gs[0], gs[1], gs[2]}, es);
+    a.bf16 = dtype == SDM_BF16; a.silu = act == SDM_ACT_SILU;
+    hipError_t e = sdm::launch_conv_backward(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_selective(const char* fn, int in_dtype, int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
+    if (in_dtype != SDM_F32 && in_dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "%s: unknown dtype %d", fn, in_dtype);
+    if (B < 0 || T < 0 || D < 1 || G < 1 || N < 1 || D % G != 0)
+        return fail(SDM_ERR_SHAPE, "%s: invalid sizes (G has to divide D)", fn);
+    if (N > 64) return fail(SDM_ERR_UNSUPPORTED, "%s: N=%lld: at most 64 states a channel", fn, (long long)N);
+    if (D > (1 << 20)) return fail(SDM_ERR_UNSUPPORTED, "%s: D=%lld: at most 2^20 channels", fn, (long long)D);
+    // fewer than 2^21 tiles, in at most 2^11 segments; each factor is bounded first
+    if (B > MOST || T > MOST || B * G >= 1 << 21 || sdm::sel_tiles(B, (int)G, (int)D) >= 1 << 21)
+        return fail(SDM_ERR_UNSUPPORTED, "%s: too many sequences and channels for one launch", fn);
+    return B == 0 ? NO_WORK : 0;
+}
+int check_selective_backward(const char* fn, int in_dtype, int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
+    const int rc = check_selective(fn, in_dtype, B, T, D, G, N);
+    // fewer than 2^32 threads for the sums: 32 a token, group and tile of states; 32768 a tile's gradient of A
+    if (rc == 0 && (B * G * T * ((N + 15) / 16) >= 1 << 27 || sdm::sel_tiles(1, (int)G, (int)D) * ((N + 15) / 16) >= 1 << 17))
+        return fail(SDM_ERR_UNSUPPORTED, "%s: too many tokens or groups for one launch", fn);
+    return rc;
+}
+
+struct SelTensor {
+    const char* name;
+    const void* p;
+    const int64_t* s;  // batch, token (group)
+    bool bc;
+};
+int check_selective_tensors(const char* fn, std::initializer_list<SelTensor> ts, int64_t es, int64_t B, int64_t T, int64_t G) {
+    int rc;
+    for (const SelTensor& t : ts) {
+        if (T > 0 && (rc = check_address(fn, t.name, t.p, es))) return rc;
+        rc = t.bc ? check_strides(fn, t.name, {B, T, G}, {t.s[0], t.s[1], t.s[2]}) : check_strides(fn, t.name, {B, T}, {t.s[0], t.s[1]});
+        if (rc) return rc;
+    }
+    return 0;
+}
+
+template <typename Args>
+void selective_args(Args& a, const void* x, const void* dt, const void* z, const void* Bm, const void* Cm, int in_dtype,
+                    const int64_t* s, const float* A, const float* Dskip, const float* dt_bias, int softplus,
+                    const float* S0, const uint8_t* start, const int32_t* lengths, int64_t B, int64_t T, int64_t D,
+                    int64_t G, int64_t N, void* workspace) {
+    a.x = x; a.dt = dt; a.z = z; a.Bm = Bm; a.Cm = Cm; a.bf16 = in_dtype == SDM_BF16;
+    a.x_b = s[0]; a.x_t = s[1]; a.dt_b = s[2]; a.dt_t = s[3]; a.z_b = s[4]; a.z_t = s[5];
+    a.B_b = s[6]; a.B_t = s[7]; a.B_g = s[8]; a.C_b = s[9]; a.C_t = s[10]; a.C_g = s[11];
+    a.A = A; a.Dskip = Dskip; a.bias = dt_bias; a.softplus = softplus != 0; a.S0 = S0;
+    a.start = start; a.lengths = lengths;
+    a.B = B; a.T = T; a.D = (int)D; a.G = (int)G; a.N = (int)N;
+    a.workspace = workspace;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sdm_selective_scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
+    const int rc = check_selective("sdm_selective_scan_workspace_bytes", SDM_F32, B, T, D, G, N);
+    if (rc == NO_WORK) return 0;
+    return rc ? -1 : sdm::selective_workspace_bytes(B, T, (int)G, (int)D, (int)N);
+}
+
+int sdm_selective_scan_forward(const void* x, const void* dt, const void* z, const void* Bm, const void* Cm,
+                               int in_dtype, const int64_t* strides, const float* A, const float* Dskip,
+                               const float* dt_bias, int softplus, const float* S0, float* S, const uint8_t* start,
+                               const int32_t* lengths, void* y, int64_t B, int64_t T, int64_t D, int64_t G, int64_t N,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+    const char* fn = "sdm_selective_scan_forward";
+    int rc = check_selective(fn, in_dtype, B, T, D, G, N);
+    if (rc == NO_WORK) return ok();
+    if (rc) return rc;
+    const int64_t td = T * D, tg = T * G * N, gn = G * N, es = in_dtype == SDM_BF16 ? 2 : 4;
+    const int64_t flat[12] = {td, D, td, D, td, D, tg, gn, N, tg, gn, N}, *s = strides ? strides : flat;
+    if ((rc = check_selective_tensors(fn, {{"x", x, s, false}, {"dt", dt, s + 2, false}, {"Bm", Bm, s + 6, true}, {"Cm", Cm, s + 9, true}},
+                                      es, B, T, G)))
+        return rc;
+    if (z && (rc = check_selective_tensors(fn, {{"z", z, s + 4, false}}, es, B, T, G))) return rc;
+    if ((rc = check_buffers(fn, {A})) || (T > 0 && (rc = check_buffers(fn, {y})))) return rc;
+    const void* opt[] = {Dskip, dt_bias, S0, S};
+    for (const void* p : opt)
+        if (p && !aligned16(p)) return fail(SDM_ERR_ALIGN, "%s: pointer %p not 16-byte aligned", fn, p);
+    if (lengths && (rc = check_address(fn, "lengths", lengths, 4))) return rc;
+    if (T > 0 && (y == x || y == dt || y == z || y == Bm || y == Cm || y == S0 || y == S))
+        return fail(SDM_ERR_SHAPE, "%s: y may not alias an input or S", fn);
+    const int64_t need = sdm::selective_workspace_bytes(B, T, (int)G, (int)D, (int)N);
+    if (need > 0 && (rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+    sdm::SelArgs a{};
+    selective_args(a, x, dt, z, Bm, Cm, in_dtype, s, A, Dskip, dt_bias, softplus, S0, start, lengths, B, T, D, G, N, workspace);
+    a.S = S; a.y = y;
+    hipError_t e = sdm::launch_selective(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, fn);
+}
+
+int64_t sdm_selective_scan_backward_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
+    const int rc = check_selective_backward("sdm_selective_scan_backward_workspace_bytes", SDM_F32, B, T, D, G, N);
+    if (rc == NO_WORK) return 0;
+    return rc ? -1 : sdm::selective_backward_workspace_bytes(B, T, (int)G, (int)D, (int)N);
+}
+
+int sdm_selective_scan_backward(const void* dy, const void* x, const void* dt, const void* z, const void* Bm,
+                                const void* Cm, int in_dtype, const int64_t* strides, const float* A,
+                                const float* Dskip, const float* dt_bias, int softplus, const float* S0,
+                                const float* dS, const uint8_t* start, const int32_t* lengths, void* dx, void* ddt,
+                                void* dz, float* dA, float* dB, float* dC, float* dD, float* ddt_bias, float* dS0,
+                                int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
+    const char* fn = "sdm_selective_scan_backward";
+    int rc = check_selective_backward(fn, in_dtype, B, T, D, G, N);
+    if (rc == NO_WORK) return ok();
+    if (rc) return rc;
+    const int64_t td = T * D, tg = T * G * N, gn = G * N, es = in_dtype == SDM_BF16 ? 2 : 4;
+    const int64_t flat[14] = {td, D, td, D, td, D, tg, gn, N, tg, gn, N, td, D}, *s = strides ? strides : flat;
+    if ((rc = check_selective_tensors(fn, {{"x", x, s, false}, {"dt", dt, s + 2, false}, {"Bm", Bm, s + 6, true}, {"Cm", Cm, s + 9, true},
+                                           {"dy", dy, s + 12, false}}, es, B, T, G)))
+        return rc;
+    if (z && (rc = check_selective_tensors(fn, {{"z", z, s + 4, false}}, es, B, T, G))) return rc;
+    if ((rc = check_buffers(fn, {A, dA}))) return rc;
+    if (T > 0 && ((rc = check_buffers(fn, {dx, ddt, dB, dC})) || (z && (rc = check_buffers(fn, {dz}))))) return rc;
+    const void* opt[] = {Dskip, dt_bias, S0, dS, dD, ddt_bias, dS0};
+    for (const void* p : opt)
+        if (p && !aligned16(p)) return fail(SDM_ERR_ALIGN, "%s: pointer %p not 16-byte aligned", fn, p);
+    if (lengths && (rc = check_address(fn, "lengths", lengths, 4))) return rc;
+    if (T > 0) {
+        const void *outs[] = {dx, ddt, z ? dz : nullptr, dB, dC}, *ins[] = {x, dt, z, Bm, Cm, dy, S0, dS};
+        for (const void* o : outs)
+            for (const void* i : ins)
+                if (o && o == i) return fail(SDM_ERR_SHAPE, "%s: a gradient may not alias an input", fn);
+    }
+    if ((rc = check_workspace(workspace, workspace_bytes,
+                              sdm::selective_backward_workspace_bytes(B, T, (int)G, (int)D, (int)N))))
+        return rc;
+    sdm::SelBwdArgs a{};
+    selective_args(a, x, dt, z, Bm, Cm, in_dtype, s, A, Dskip, dt_bias, softplus, S0, start, lengths, B, T, D, G, N, workspace);
+    a.dy = dy; a.dS = dS; a.dy_b = s[12]; a.dy_t = s[13];
+    a.dx = dx; a.ddt = ddt; a.dz = z ? dz : nullptr; a.dA = dA; a.dB = dB; a.dC = dC; a.dD = dD; a.dbias = ddt_bias; a.dS0 = dS0;
+    hipError_t e = sdm::launch_selective_backward(a, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, fn);
 }
 

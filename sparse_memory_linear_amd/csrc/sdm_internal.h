@@ -218,19 +218,111 @@ struct NormArgs {
     int d, group, y_type;
     float eps;
     bool x_bf16, h_bf16;
+    const float* bias = nullptr;
+    bool mean = false;       // layer norm: the mean taken off, the bias added
 };
 hipError_t launch_norm(const NormArgs& a, hipStream_t st);
 struct NormBwdArgs {
     const void* dy; const void* h; const void* dh; const float* gamma;
     void* dx; float* dgamma;
-    float* part;             // [blocks][d]
+    float* part;             // [blocks][d]; layer norm: [blocks][2][d]
     int64_t rows;
     int d, blocks;
     float eps;
     bool g_bf16, h_bf16;     // dy, dh, dx; h
+    float* dbias = nullptr;
+    bool mean = false;
 };
 int64_t norm_bwd_blocks(int64_t rows, int d);
 hipError_t launch_norm_backward(NormBwdArgs a, hipStream_t st);
+
+// The causal convolution: x [B,H,T,d] by strides, everything else contiguous.
+struct ConvArgs {
+    const void* x; const float* w; const float* bias; const void* S0; void* S;
+    const uint8_t* start; const int32_t* lengths;
+    void* y;
+    int64_t x_b, x_h, x_t;   // elements between sequences, heads, tokens
+    int64_t B, H, T;
+    int d, K;
+    int align;               // elements: a power of two that divides d, the strides and the tensors' addresses
+    bool bf16, silu;
+    // set by the launcher
+    int64_t threads, ntile;
+    int tile, nvec, vec;
+};
+hipError_t launch_conv(ConvArgs a, hipStream_t st);
+struct ConvBwdArgs {
+    const void* dy; const void* x; const float* w; const float* bias; const void* S0; const void* dS;
+    const uint8_t* start; const int32_t* lengths;
+    void* dx; float* dw; float* dbias; void* dS0;
+    float* part;             // [B * ntile][K + 1][H * d]
+    int64_t x_b, x_h, x_t, dx_b, dx_h, dx_t;
+    int64_t B, H, T;
+    int d, K;
+    int align;
+    bool bf16, silu;
+    int64_t threads, ntile;
+    int tile, nvec, vec;
+};
+constexpr int CONV_TILE_MIN = 32;  // tokens a thread at least, of more than that: bounds the launches' threads
+int64_t conv_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t d, int K);
+hipError_t launch_conv_backward(ConvBwdArgs a, hipStream_t st);
+
+// The selective state-space scan: x, dt, z [B,T,D], Bm, Cm [B,T,G,N] and dy by strides, everything else
+// contiguous. A tile is 64 channels of a group in one sequence (by 16 states: a wavefront's).
+inline int sel_ctiles(int G, int D) { return (D / G + 63) / 64; }
+inline int sel_ntiles(int N) { return (N + 15) / 16; }
+inline int64_t sel_tiles(int64_t B, int G, int D) { return B * G * sel_ctiles(G, D); }
+struct SelArgs {
+    const void* x; const void* dt; const void* z; const void* Bm; const void* Cm;
+    const float* A; const float* Dskip; const float* bias;
+    const float* S0; float* S;
+    const uint8_t* start; const int32_t* lengths;
+    void* y;
+    int64_t x_b, x_t, dt_b, dt_t, z_b, z_t, B_b, B_t, B_g, C_b, C_t, C_g;
+    int64_t B, T;
+    int D, G, N;
+    bool bf16, softplus;
+    void* workspace;
+    // set by the launcher
+    float* ends;             // [nseg][tiles][ntiles][1024]: what a segment adds, then where it starts
+    float* steps;            // [nseg][tiles][64]: its sum of steps
+    int64_t L, tiles;        // tokens per segment
+    int nseg, ctiles, ntiles;
+};
+int64_t selective_workspace_bytes(int64_t B, int64_t T, int G, int D, int N);
+hipError_t launch_selective(SelArgs a, hipStream_t st);
+struct SelBwdArgs {
+    const void* dy; const void* x; const void* dt; const void* z; const void* Bm; const void* Cm;
+    const float* A; const float* Dskip; const float* bias;
+    const float* S0; const float* dS;
+    const uint8_t* start; const int32_t* lengths;
+    void* dx; void* ddt; void* dz;
+    float* dA; float* dB; float* dC; float* dD; float* dbias; float* dS0;
+    int64_t x_b, x_t, dt_b, dt_t, z_b, z_t, B_b, B_t, B_g, C_b, C_t, C_g, dy_b, dy_t;
+    int64_t B, T;
+    int D, G, N;
+    bool bf16, softplus;
+    void* workspace;
+    // set by the launcher; with the forward's ends and steps
+    float* ends; float* gends; float* steps;  // gends: what a segment passes back, then what arrives at its end
+    float* marks; float* msteps;  // [chunk][tiles][ntiles][1024], [chunk][tiles][64]: the segment's own state and sum of
+                                  // steps in front of every chunk
+    float* part_bc;          // [ctiles][B][G][T][ntiles][2][16]
+    float* part_A;           // [nseg][tiles][ntiles][1024]
+    float* part_D;           // [nseg][ntiles][tiles][2][64]
+    int64_t L, tiles;
+    int nseg, ctiles, ntiles;
+};
+int64_t selective_backward_workspace_bytes(int64_t B, int64_t T, int G, int D, int N);
+hipError_t launch_selective_backward(SelBwdArgs a, hipStream_t st);
+struct SelCarryArgs {
+    float* ends; const float* steps; const float* A;
+    const float* from;       // [B][D][N] or nullptr (zeros)
+    int64_t tiles;
+    int nseg, ntiles, ctiles, G, D, N;
+    bool rev;
+};
 
 struct BalanceArgs {
     const int32_t* idx; const float* wt;  // [B,H,T,K]

@@ -1,0 +1,232 @@
+// selective.h -- what the passes of the selective state-space scan share (selective.hip, selective_bwd.hip).
+//
+// A wavefront carries the states of 64 channels (one a lane in what a channel has once a token) by 16 states
+// n. The tile lies in the registers as v_mfma_f32_16x16x1 (4 blocks) gives it: h[4 blk + r] of lane 16 q + j is
+// state 4 q + r of channel 16 blk + j. That instruction adds a token's u (x) B to the decayed tile, from B_n
+// in lane j = n and u in the channels' own lanes, in fp32 and beside the vector units, which bound these
+// kernels: a state costs a product and an exponential (four issue slots) for the decay and one product to
+// apply it. Sums over n are over r in a lane and over q by two permlane swaps, which put channel c's sum in lane c.
+#pragma once
+#include "sdm_internal.h"
+#include "sdm_rows.h"
+
+namespace sdm {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int SC = 8;               // tokens per chunk
+constexpr float GONE = -INFINITY;   // in place of a sum of steps: a sequence began since, nothing crosses
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t raw(const void* p, uint32_t i) {
+    if constexpr (BF16) return static_cast<const uint16_t*>(p)[i];
+    else return static_cast<const uint32_t*>(p)[i];
+}
+template <bool BF16>
+__device__ __forceinline__ float value(uint32_t u) {
+    return BF16 ? bf16_f(u) : __uint_as_float(u);
+}
+template <bool BF16>
+__device__ __forceinline__ void put(void* p, uint32_t i, float f) {
+    if constexpr (BF16) static_cast<uint16_t*>(p)[i] = (uint16_t)f_bf16(f);
+    else static_cast<float*>(p)[i] = f;
+}
+// the row at element e (the same for the wavefront)
+template <bool BF16>
+__device__ __forceinline__ const char* row(const void* p, int64_t e) {
+    return static_cast<const char*>(p) + e * (BF16 ? 2 : 4);
+}
+
+// log(1 + e^v) = max(v, 0) + log(1 + e^-|v|); the logarithm of 1 + e as 2 artanh(s), s = e / (2 + e) <= 1/3, by a
+// polynomial in s^2 (fitted at Chebyshev points; 4e-9 off): exact to some steps for tiny e too, where 1 + e is not
+__device__ __forceinline__ float softplus(float v) {
+    const float e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(v));
+    const float s = e * __builtin_amdgcn_rcpf(2.f + e), w = s * s;
+    float p = fmaf(0.28174657f, w, 0.27961418f);
+    p = fmaf(p, w, 0.40024853f);
+    p = fmaf(p, w, 0.66666317f);
+    p = fmaf(p, w, 2.f);
+    return fmaf(s, p, fmaxf(v, 0.f));
+}
+
+// v's four rows of 16 lanes, each in all rows
+__device__ __forceinline__ void spread(float v, float (&o)[4]) {
+    const uint32_t u = __float_as_uint(v);
+    const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    o[0] = __uint_as_float(a[0]); o[1] = __uint_as_float(a[1]);
+    o[2] = __uint_as_float(b[0]); o[3] = __uint_as_float(b[1]);
+}
+// lane 16 blk + j: the sum of p[blk] over the lanes j, 16 + j, 32 + j, 48 + j
+__device__ __forceinline__ float gather_sum(const float (&p)[4]) {
+    auto add = [](auto h) { return __uint_as_float(h[0]) + __uint_as_float(h[1]); };
+    const float s02 = add(__builtin_amdgcn_permlane32_swap(__float_as_uint(p[0]), __float_as_uint(p[2]), false, false));
+    const float s13 = add(__builtin_amdgcn_permlane32_swap(__float_as_uint(p[1]), __float_as_uint(p[3]), false, false));
+    return add(__builtin_amdgcn_permlane16_swap(__float_as_uint(s02), __float_as_uint(s13), false, false));
+}
+
+__device__ __forceinline__ f32x16 outer_add(float n, float c, f32x16 t) {
+    return __builtin_amdgcn_mfma_f32_16x16x1f32(n, c, t, 0, 0, 0);
+}
+
+// Where a wavefront works
+struct SelAt {
+    int lane, q, j, nt;          // nt: tile of 16 states
+    int64_t b, tile;             // tile: of channels, over all sequences and groups
+    int g, c0, dg, seg;          // c0: first channel in its group
+    bool in;                     // the lane's channel is there
+    uint32_t c;                  // the lane's channel (the group's last one where it is not)
+    int64_t t0, t1, end;         // tokens of the segment, and those of them that are there
+};
+template <typename Args>
+__device__ __forceinline__ SelAt sel_at(const Args& a) {
+    SelAt w;
+    w.lane = threadIdx.x & 63;
+    w.q = w.lane >> 4;
+    w.j = w.lane & 15;
+    w.nt = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    w.tile = blockIdx.x;
+    uint32_t i = blockIdx.x;
+    w.c0 = (int)(i % (uint32_t)a.ctiles) * 64;
+    i /= (uint32_t)a.ctiles;
+    w.g = (int)(i % (uint32_t)a.G);
+    w.b = i / (uint32_t)a.G;
+    w.dg = a.D / a.G;
+    w.in = w.c0 + w.lane < w.dg;
+    w.c = (uint32_t)(w.g * w.dg + (w.in ? w.c0 + w.lane : w.dg - 1));
+    w.seg = blockIdx.y;
+    w.t0 = (int64_t)w.seg * a.L;
+    w.t1 = w.t0 + a.L < a.T ? w.t0 + a.L : a.T;
+    int64_t n = a.T;
+    if (a.lengths) {
+        n = a.lengths[w.b];
+        n = n < 0 ? 0 : n > a.T ? a.T : n;
+    }
+    w.end = n < w.t1 ? n : w.t1;
+    return w;
+}
+
+// A tile out of [D][N] (of sequence b where there are several), zeros outside, times f
+template <typename Args>
+__device__ __forceinline__ f32x16 load_dn(const Args& a, const SelAt& w, const float* p, float f) {
+    f32x16 v;
+    const int n = 16 * w.nt + 4 * w.q;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = w.c0 + 16 * k + w.j;
+        const float* e = p + (int64_t)(w.g * w.dg + c) * a.N + n;
+        if (a.N % 4 == 0) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < w.dg && n < a.N) x = *reinterpret_cast<const float4*>(e);
+            v[4 * k] = x.x * f; v[4 * k + 1] = x.y * f; v[4 * k + 2] = x.z * f; v[4 * k + 3] = x.w * f;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[4 * k + r] = c < w.dg && n + r < a.N ? e[r] * f : 0.f;
+        }
+    }
+    return v;
+}
+template <typename Args>
+__device__ __forceinline__ void store_dn(const Args& a, const SelAt& w, float* p, const f32x16& v) {
+    const int n = 16 * w.nt + 4 * w.q;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = w.c0 + 16 * k + w.j;
+        if (c >= w.dg) continue;
+        float* e = p + (int64_t)(w.g * w.dg + c) * a.N + n;
+        if (a.N % 4 == 0) {
+            if (n < a.N) *reinterpret_cast<float4*>(e) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (n + r < a.N) e[r] = v[4 * k + r];
+        }
+    }
+}
+
+// Tiles in the workspace: 1024 floats as the registers hold them
+__device__ __forceinline__ f32x16 load_tile(const float* p, int lane) {
+    f32x16 v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float4 x = reinterpret_cast<const float4*>(p)[64 * k + lane];
+        v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
+    }
+    return v;
+}
+__device__ __forceinline__ void store_tile(float* p, int lane, const f32x16& v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        reinterpret_cast<float4*>(p)[64 * k + lane] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+}
+
+// exp(delta A): a2 = A log2(e)
+__device__ __forceinline__ f32x16 decays(float delta, const f32x16& a2) {
+    float d[4];
+    spread(delta, d);
+    f32x16 v;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __builtin_amdgcn_exp2f(d[i / 4] * a2[i]);
+    return v;
+}
+__device__ __forceinline__ f32x16 zeros16() {
+    f32x16 v;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    return v;
+}
+
+// Bit k: a sequence begins at token t + k (k < 8, t + k < end)
+__device__ __forceinline__ uint32_t starts(const uint8_t* start, int64_t t, int64_t end, int lane) {
+    if (!start) return 0u;
+    const bool on = lane < SC && t + lane < end && start[t + lane] != 0;
+    return (uint32_t)__ballot(on);
+}
+
+// Values of B or C: lane 16 q + j gets state j's of token t + q (0 past the end or the last state)
+template <bool BF16>
+__device__ __forceinline__ float load_bc(const char* p, int64_t stride, int64_t t, const SelAt& w, int N) {
+    const int n = 16 * w.nt + w.j;
+    return t + w.q < w.end && n < N ? value<BF16>(raw<BF16>(row<BF16>(p, (t + w.q) * stride), n)) : 0.f;
+}
+
+// Tiles' ends carried through the segments: out[s] holds what a segment adds (start state 0) and gets what
+// arrives at it. One float4 a thread.
+__global__ __launch_bounds__(256) void sel_carry_kernel(SelCarryArgs a0, SelCarryArgs a1) {
+    const SelCarryArgs& a = blockIdx.y ? a1 : a0;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // [tile][nt][blk][lane]
+    const int e = (int)(i & 255), lane = e & 63, blk = e >> 6, j = lane & 15, q = lane >> 4;
+    const int64_t w = i >> 8, tile = w / a.ntiles;
+    if (tile >= a.tiles) return;
+    const int nt = (int)(w % a.ntiles);
+    const int64_t bg = tile / a.ctiles, b = bg / a.G;
+    const int g = (int)(bg % a.G), dg = a.D / a.G, c = (int)(tile % a.ctiles) * 64 + 16 * blk + j, n = 16 * nt + 4 * q;
+    float run[4], a2[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const bool in = c < dg && n + r < a.N;
+        const int64_t at = ((int64_t)g * dg + c) * a.N + n + r;
+        a2[r] = in ? a.A[at] * 1.44269504f : 0.f;
+        run[r] = in && a.from ? a.from[b * a.D * a.N + at] : 0.f;
+    }
+    float4* ends = reinterpret_cast<float4*>(a.ends);
+    for (int k = 0; k < a.nseg; ++k) {
+        const int s = a.rev ? a.nseg - 1 - k : k;
+        const int64_t at = (s * a.tiles * a.ntiles + w) * 256 + e;
+        const float4 own = ends[at];
+        const float sum = a.steps[(s * a.tiles + tile) * 64 + 16 * blk + j];
+        ends[at] = make_float4(run[0], run[1], run[2], run[3]);
+        const float o[4] = {own.x, own.y, own.z, own.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) run[r] = sum == GONE ? o[r] : fmaf(__builtin_amdgcn_exp2f(a2[r] * sum), run[r], o[r]);
+    }
+}
+inline hipError_t sel_carry(const SelCarryArgs& a, const SelCarryArgs& b, int count, hipStream_t st) {
+    hipLaunchKernelGGL(sel_carry_kernel, dim3((unsigned)(a.tiles * a.ntiles), count), dim3(256), 0, st, a, b);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace sdm

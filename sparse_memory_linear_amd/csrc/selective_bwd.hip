@@ -1,0 +1,435 @@
+// selective_bwd.hip -- the gradients of the selective state-space scan (selective.hip) on gfx950. With
+// gy_t = dy_t silu(z_t), u_t = delta_t x_t, a_t = exp(delta_t A) and g_t = C_t gy_t + a_{t+1} g_{t+1} (behind the
+// last token dL/dh):
+//   dC_t = sum_d gy_t h_t             dB_t = sum_d u_t g_t
+//   dx_t = D gy_t + delta_t sum_n g_t B_t
+//   ddelta_t = sum_n A g_t a_t h_{t-1} + x_t sum_n g_t B_t,   ddt_t = ddelta_t sigmoid(dt_t + bias)
+//   dz_t = dy_t (C_t h_t + D x_t) silu'(z_t)
+//   dA = sum_t delta_t g_t a_t h_{t-1},   dD = sum_t gy_t x_t,   dbias = sum_t ddt_t,   dS0 = a_1 g_1
+//
+// Nothing is kept from the forward call. A first pass over the segments forms the states again, from zeros,
+// leaves one every 8 tokens (with the sum of steps since the segment's start, by whose decay the segment's
+// own starting state is added), and sums what a segment passes to the one before it. Carries run through the
+// segments both ways. The last pass walks the chunks backwards, half a chunk (4 tokens) at a time: it forms
+// the 4 states again, keeping each token's decay and decayed state in registers, and then walks them back.
+// Sums over channels leave a row a tile, added by a last pass.
+#include "selective.h"
+
+namespace sdm {
+namespace {
+
+constexpr int HC = SC / 2;
+
+template <bool BF16, bool HASZ>
+__global__ __launch_bounds__(256, 2) void sel_ends_kernel(SelBwdArgs a) {
+    const SelAt w = sel_at(a);
+    const f32x16 a2 = load_dn(a, w, a.A, 1.44269504f);
+    const int64_t wave = w.tile * a.ntiles + w.nt, waves = a.tiles * a.ntiles;
+    const char* px = row<BF16>(a.x, w.b * a.x_b);
+    const char* pd = row<BF16>(a.dt, w.b * a.dt_b);
+    const char* pz = HASZ ? row<BF16>(a.z, w.b * a.z_b) : nullptr;
+    const char* py = row<BF16>(a.dy, w.b * a.dy_b);
+    const char* pB = row<BF16>(a.Bm, w.b * a.B_b + w.g * a.B_g);
+    const char* pC = row<BF16>(a.Cm, w.b * a.C_b + w.g * a.C_g);
+    const float bias = a.bias ? a.bias[w.c] : 0.f;
+    const uint8_t* start = a.start ? a.start + w.b * a.T : nullptr;
+    f32x16 h = zeros16(), g = zeros16(), p;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = 1.f;
+    float steps = 0.f;
+    const bool back = w.seg > 0;
+    int64_t chunk = w.seg * (a.L / SC);
+    for (int64_t t = w.t0; t < w.end; t += SC, ++chunk) {
+        store_tile(a.marks + (chunk * waves + wave) * 1024, w.lane, h);
+        if (w.nt == 0) a.msteps[(chunk * a.tiles + w.tile) * 64 + w.lane] = steps;
+        uint32_t xr[SC], dr[SC], zr[SC], yr[SC];
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            const int64_t u = t + i < w.end ? t + i : w.end - 1;
+            xr[i] = raw<BF16>(row<BF16>(px, u * a.x_t), w.c);
+            dr[i] = raw<BF16>(row<BF16>(pd, u * a.dt_t), w.c);
+            if (back) {
+                yr[i] = raw<BF16>(row<BF16>(py, u * a.dy_t), w.c);
+                if constexpr (HASZ) zr[i] = raw<BF16>(row<BF16>(pz, u * a.z_t), w.c);
+            }
+        }
+        const uint32_t st = starts(start, t, w.end, w.lane);
+        float bq[2][4], cq[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            spread(load_bc<BF16>(pB, a.B_t, t + 4 * k, w, a.N), bq[k]);
+            if (back) spread(load_bc<BF16>(pC, a.C_t, t + 4 * k, w, a.N), cq[k]);
+        }
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            const bool on = w.in && t + i < w.end;
+            const float v = value<BF16>(dr[i]) + bias, x = value<BF16>(xr[i]);
+            float delta = a.softplus ? softplus(v) : v;
+            delta = on ? delta : 0.f;
+            steps = st >> i & 1u ? GONE : steps + delta;
+            if (st >> i & 1u) {
+                h = zeros16();
+                p = zeros16();
+            } else {
+                const f32x16 d = decays(delta, a2);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    h[k] *= d[k];
+                    p[k] *= d[k];
+                }
+            }
+            h = outer_add(bq[i / 4][i % 4], on ? delta * x : 0.f, h);
+            if (back) {
+                float gy = value<BF16>(yr[i]);
+                if constexpr (HASZ) {
+                    const float z = value<BF16>(zr[i]);
+                    gy *= z * sigmoid(z);
+                }
+                const f32x16 cg = outer_add(cq[i / 4][i % 4], on ? gy : 0.f, zeros16());
+#pragma unroll
+                for (int k = 0; k < 16; ++k) g[k] = fmaf(p[k], cg[k], g[k]);
+            }
+        }
+    }
+    const int64_t at = (w.seg * waves + wave) * 1024;
+    store_tile(a.ends + at, w.lane, h);
+    store_tile(a.gends + at, w.lane, g);
+    if (w.nt == 0) a.steps[(w.seg * a.tiles + w.tile) * 64 + w.lane] = steps;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+// Lane j of a row of 16 lanes gets the row's sum of v[j / 4]
+__device__ __forceinline__ float row_sums(const float (&v)[4], int j) {
+    const bool hi = j & 8, odd = j & 4;
+    float s0 = (hi ? v[2] : v[0]) + dpp<0x128>(hi ? v[0] : v[2]);  // row_ror:8
+    float s1 = (hi ? v[3] : v[1]) + dpp<0x128>(hi ? v[1] : v[3]);
+    float s = (odd ? s1 : s0) + dpp<0x141>(odd ? s0 : s1);         // row_half_mirror: lane 7 - j of the half row
+    s += dpp<0x4E>(s);                                             // quad_perm 2,3,0,1
+    return s + dpp<0xB1>(s);                                       // quad_perm 1,0,3,2
+}
+
+template <bool BF16, bool HASZ, bool MULTI>
+__global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdArgs a) {
+    constexpr int NW = MULTI ? 4 : 1;
+    __shared__ float bl[NW][HC][16], cl[NW][HC][16];
+    __shared__ float sl[MULTI ? 2 : 1][NW][MULTI ? HC : 1][3][64];
+    const SelAt w = sel_at(a);
+    const f32x16 a2 = load_dn(a, w, a.A, 1.44269504f);
+    const int64_t wave = w.tile * a.ntiles + w.nt, waves = a.tiles * a.ntiles, per = (int64_t)a.D * a.N;
+    const char* px = row<BF16>(a.x, w.b * a.x_b);
+    const char* pd = row<BF16>(a.dt, w.b * a.dt_b);
+    const char* pz = HASZ ? row<BF16>(a.z, w.b * a.z_b) : nullptr;
+    const char* py = row<BF16>(a.dy, w.b * a.dy_b);
+    const char* pB = row<BF16>(a.Bm, w.b * a.B_b + w.g * a.B_g);
+    const char* pC = row<BF16>(a.Cm, w.b * a.C_b + w.g * a.C_g);
+    const float bias = a.bias ? a.bias[w.c] : 0.f, skip = a.Dskip ? a.Dskip[w.c] : 0.f;
+    const uint8_t* start = a.start ? a.start + w.b * a.T : nullptr;
+    const int64_t at = (w.seg * waves + wave) * 1024;
+    f32x16 g = load_tile(a.gends + at, w.lane), dA = zeros16();
+    float dD = 0.f, dbias = 0.f;
+    int par = 0;
+    // behind the last token: gradients of 0
+    if (w.nt == 0 && w.in)
+        for (int64_t t = w.end > w.t0 ? w.end : w.t0; t < w.t1; ++t) {
+            const int64_t e = (w.b * a.T + t) * a.D;
+            put<BF16>(const_cast<char*>(row<BF16>(a.dx, e)), w.c, 0.f);
+            put<BF16>(const_cast<char*>(row<BF16>(a.ddt, e)), w.c, 0.f);
+            if constexpr (HASZ) put<BF16>(const_cast<char*>(row<BF16>(a.dz, e)), w.c, 0.f);
+        }
+    const int64_t chunks = w.end > w.t0 ? (w.end - w.t0 + SC - 1) / SC : 0, first = w.seg * (a.L / SC);
+    for (int64_t half = 2 * chunks - 1; half >= 0; --half) {
+        const int64_t t8 = w.t0 + half / 2 * SC, t = t8 + (half & 1) * HC, chunk = first + half / 2;
+        if (t >= w.end) continue;
+        // the state in front of the chunk
+        f32x16 h = load_tile(a.marks + (chunk * waves + wave) * 1024, w.lane);
+        {
+            const float* ms = a.msteps + (chunk * a.tiles + w.tile) * 64 + w.j;
+            const f32x16 hs = load_tile(a.ends + at, w.lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float s = ms[16 * k];
+                if (s != GONE)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        h[4 * k + r] = fmaf(__builtin_amdgcn_exp2f(a2[4 * k + r] * s), hs[4 * k + r], h[4 * k + r]);
+            }
+        }
+        const uint32_t sts = starts(start, t8, w.end, w.lane);
+        if (half & 1) {  // and in front of its second half
+            uint32_t xr[HC], dr[HC];
+#pragma unroll
+            for (int i = 0; i < HC; ++i) {
+                xr[i] = raw<BF16>(row<BF16>(px, (t8 + i) * a.x_t), w.c);
+                dr[i] = raw<BF16>(row<BF16>(pd, (t8 + i) * a.dt_t), w.c);
+            }
+            float bq[4];
+            spread(load_bc<BF16>(pB, a.B_t, t8, w, a.N), bq);
+#pragma unroll
+            for (int i = 0; i < HC; ++i) {
+                const float v = value<BF16>(dr[i]) + bias;
+                float delta = a.softplus ? softplus(v) : v;
+                delta = w.in ? delta : 0.f;
+                if (sts >> i & 1u) {
+                    h = zeros16();
+                } else {
+                    const f32x16 d = decays(delta, a2);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) h[k] *= d[k];
+                }
+                h = outer_add(bq[i], w.in ? delta * value<BF16>(xr[i]) : 0.f, h);
+            }
+        }
+        const uint32_t st = half & 1 ? sts >> HC : sts;
+        uint32_t xr[HC], dr[HC], zr[HC], yr[HC];
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+            const int64_t u = t + i < w.end ? t + i : w.end - 1;
+            xr[i] = raw<BF16>(row<BF16>(px, u * a.x_t), w.c);
+            dr[i] = raw<BF16>(row<BF16>(pd, u * a.dt_t), w.c);
+            yr[i] = raw<BF16>(row<BF16>(py, u * a.dy_t), w.c);
+            if constexpr (HASZ) zr[i] = raw<BF16>(row<BF16>(pz, u * a.z_t), w.c);
+        }
+        const float bv = load_bc<BF16>(pB, a.B_t, t, w, a.N), cv = load_bc<BF16>(pC, a.C_t, t, w, a.N);
+        bl[w.nt][w.q][w.j] = bv;
+        cl[w.nt][w.q][w.j] = cv;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        float bq[4], cq[4];
+        spread(bv, bq);
+        spread(cv, cq);
+        float delta[HC], u[HC], gy[HC];
+        f32x16 dec[HC], kept[HC];  // a_t and a_t h_{t-1}
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+            const bool on = w.in && t + i < w.end;
+            const float v = value<BF16>(dr[i]) + bias;
+            const float de = a.softplus ? softplus(v) : v;
+            delta[i] = on ? de : 0.f;
+            u[i] = on ? de * value<BF16>(xr[i]) : 0.f;
+            float y = value<BF16>(yr[i]);
+            if constexpr (HASZ) {
+                const float z = value<BF16>(zr[i]);
+                y *= z * sigmoid(z);
+            }
+            gy[i] = on ? y : 0.f;
+            if (st >> i & 1u) {
+                dec[i] = zeros16();
+                kept[i] = zeros16();
+            } else {
+                dec[i] = decays(delta[i], a2);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) kept[i][k] = dec[i][k] * h[k];
+            }
+            h = outer_add(bq[i], u[i], kept[i]);
+        }
+        // a token's own gradients, from the sums over its states
+        auto finish = [&](int i, float sa, float sbn, float sch) {
+            if (!w.in || t + i >= w.end) return;
+            const float x = value<BF16>(xr[i]), v = value<BF16>(dr[i]) + bias;
+            const int64_t e = (w.b * a.T + t + i) * a.D;
+            put<BF16>(const_cast<char*>(row<BF16>(a.dx, e)), w.c, fmaf(delta[i], sbn, skip * gy[i]));
+            float dd = fmaf(x, sbn, 0.69314718f * sa);
+            if (a.softplus) dd *= sigmoid(v);
+            put<BF16>(const_cast<char*>(row<BF16>(a.ddt, e)), w.c, dd);
+            dbias += dd;
+            dD = fmaf(gy[i], x, dD);
+            if constexpr (HASZ) {
+                const float z = value<BF16>(zr[i]), s = sigmoid(z);
+                const float dz = value<BF16>(yr[i]) * fmaf(skip, x, sch) * s * fmaf(z, 1.f - s, 1.f);
+                put<BF16>(const_cast<char*>(row<BF16>(a.dz, e)), w.c, dz);
+            }
+        };
+#pragma unroll
+        for (int i = HC - 1; i >= 0; --i) {
+            g = outer_add(cq[i], gy[i], g);
+            if (i < HC - 1) h = outer_add(bq[i], u[i], kept[i]);
+            const float4 bn = *reinterpret_cast<const float4*>(&bl[w.nt][i][4 * w.q]);
+            const float4 cn = *reinterpret_cast<const float4*>(&cl[w.nt][i][4 * w.q]);
+            float ds[4], us[4], gs[4], sb[4] = {}, sc[4] = {}, pb[4], pa[4], pc[4];
+            spread(delta[i], ds);
+            spread(u[i], us);
+            spread(gy[i], gs);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                pa[k] = 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int e = 4 * k + r;
+                    sb[r] = fmaf(us[k], g[e], sb[r]);
+                    sc[r] = fmaf(gs[k], h[e], sc[r]);
+                    const float gk = g[e] * kept[i][e];
+                    pa[k] = fmaf(a2[e], gk, pa[k]);
+                    dA[e] = fmaf(ds[k], gk, dA[e]);
+                }
+                pb[k] = fmaf(bn.w, g[4 * k + 3], fmaf(bn.z, g[4 * k + 2], fmaf(bn.y, g[4 * k + 1], bn.x * g[4 * k])));
+                if constexpr (HASZ)
+                    pc[k] = fmaf(cn.w, h[4 * k + 3], fmaf(cn.z, h[4 * k + 2], fmaf(cn.y, h[4 * k + 1], cn.x * h[4 * k])));
+            }
+            if (st >> i & 1u) {
+                g = zeros16();
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) g[k] *= dec[i][k];
+            }
+            float qa = gather_sum(pa), qb = gather_sum(pb), qc = 0.f;
+            if constexpr (HASZ) qc = gather_sum(pc);
+            // the tile's sums over its channels: states 4 q + j / 4, lane 4 j' those of dB, 4 j' + 1 of dC
+            const float rb = row_sums(sb, w.j), rc = row_sums(sc, w.j);
+            if ((w.j & 3) < 2 && t + i < w.end)
+                a.part_bc[((((w.c0 / 64) * a.B + w.b) * a.G + w.g) * a.T + t + i) * a.ntiles * 32 + w.nt * 32 + (w.j & 1) * 16 + 4 * w.q +
+                          (w.j >> 2)] = w.j & 1 ? rc : rb;
+            if constexpr (MULTI) {
+                sl[par][w.nt][i][0][w.lane] = qa;
+                sl[par][w.nt][i][1][w.lane] = qb;
+                sl[par][w.nt][i][2][w.lane] = qc;
+            }
+            if constexpr (!MULTI) {
+                finish(i, qa, qb, qc);
+            }
+        }
+        if constexpr (MULTI) {
+            __syncthreads();  // (the other half of sl: its readers have passed the barrier before)
+#pragma unroll
+            for (int i = 0; i < HC; ++i) {
+                if (i % a.ntiles != w.nt) continue;
+                float s[3] = {};
+                for (int k = 0; k < a.ntiles; ++k)
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) s[m] += sl[par][k][i][m][w.lane];
+                finish(i, s[0], s[1], s[2]);
+            }
+            par ^= 1;
+        }
+    }
+    store_tile(a.part_A + at, w.lane, dA);
+    if (a.dS0 && w.seg == 0) store_dn(a, w, a.dS0 + w.b * per, g);
+    float* pd2 = a.part_D + ((w.seg * a.ntiles + w.nt) * a.tiles + w.tile) * 128 + w.lane;
+    pd2[0] = dD;
+    pd2[64] = dbias;
+}
+
+// dB and dC [B,T,G,N]: the sums of the channel tiles' rows, in their order; 0 behind the last token
+__global__ __launch_bounds__(256) void sel_bc_kernel(SelBwdArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, cols = a.B * a.G * a.T * a.ntiles * 32;  // [b][g][t][nt][2][16]
+    if (i >= cols) return;
+    const int64_t u = i / (a.ntiles * 32);
+    const int m = (int)(i % (a.ntiles * 32)), n = m / 32 * 16 + (m & 15);
+    const int64_t t = u % a.T, bg = u / a.T, b = bg / a.G, g = bg % a.G;
+    if (n >= a.N) return;
+    float s = 0.f;
+    if (!a.lengths || t < a.lengths[b])
+#pragma unroll 8
+        for (int k = 0; k < a.ctiles; ++k) s += a.part_bc[k * cols + i];
+    (m & 16 ? a.dC : a.dB)[((b * a.T + t) * a.G + g) * a.N + n] = s;
+}
+
+// dA [D][N] of the columns [g][ct][nt][blk][lane][r]
+struct SelSumA {
+    float* dA;
+    int G, D, N, ctiles, ntiles;
+    __device__ void operator()(int64_t i, float v) const {
+        const int r = (int)(i & 3), lane = (int)(i >> 2 & 63), blk = (int)(i >> 8 & 3);
+        int64_t w = i >> 10;
+        const int n = (int)(w % ntiles) * 16 + 4 * (lane >> 4) + r;
+        w /= ntiles;
+        const int c = (int)(w % ctiles) * 64 + 16 * blk + (lane & 15), g = (int)(w / ctiles);
+        if (c < D / G && n < N) dA[(int64_t)(g * (D / G) + c) * N + n] = v;
+    }
+};
+// dD and dbias [D] of the columns [g][ct][2][64]
+struct SelSumD {
+    float* dD; float* dbias;
+    int G, D, ctiles;
+    __device__ void operator()(int64_t i, float v) const {
+        const int c = (int)((i >> 7) % ctiles) * 64 + (int)(i & 63), g = (int)((i >> 7) / ctiles);
+        float* o = i & 64 ? dbias : dD;
+        if (o && c < D / G) o[g * (D / G) + c] = v;
+    }
+};
+
+// Segments: enough wavefronts for the SIMDs, of at least 64 tokens
+void sel_bwd_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) {
+    const int64_t waves = sel_tiles(B, G, D) * sel_ntiles(N), want = (4096 + waves - 1) / waves;
+    int64_t len = (T + want - 1) / want;
+    if (len < 64) len = 64;
+    if (len > T) len = T > 0 ? T : 1;
+    len = (len + SC - 1) / SC * SC;
+    *L = len;
+    *nseg = T > len ? (int)((T + len - 1) / len) : 1;
+}
+
+// The workspace's parts, in floats
+struct SelBwdParts {
+    int64_t ends, gends, steps, marks, msteps, part_bc, part_A, part_D, end;
+};
+SelBwdParts sel_bwd_parts(int64_t B, int64_t T, int G, int D, int N, int64_t L, int nseg) {
+    const int64_t tiles = sel_tiles(B, G, D), nt = sel_ntiles(N), tile = tiles * nt * 1024, chunks = nseg * (L / SC);
+    SelBwdParts p;
+    p.ends = 0;
+    p.gends = p.ends + nseg * tile;
+    p.steps = p.gends + nseg * tile;
+    p.marks = p.steps + nseg * tiles * 64;
+    p.msteps = p.marks + chunks * tile;
+    p.part_bc = p.msteps + chunks * tiles * 64;
+    p.part_A = p.part_bc + tiles * T * nt * 32;
+    p.part_D = p.part_A + nseg * tile;
+    p.end = p.part_D + nseg * nt * tiles * 128;
+    return p;
+}
+
+template <bool BF16, bool HASZ>
+void sel_bwd_grads(const SelBwdArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)a.tiles, (unsigned)a.nseg);
+    if (a.ntiles > 1) hipLaunchKernelGGL((sel_grads_kernel<BF16, HASZ, true>), grid, dim3(64 * a.ntiles), 0, st, a);
+    else hipLaunchKernelGGL((sel_grads_kernel<BF16, HASZ, false>), grid, dim3(64), 0, st, a);
+}
+template <bool BF16, bool HASZ>
+void sel_bwd_ends(const SelBwdArgs& a, hipStream_t st) {
+    hipLaunchKernelGGL((sel_ends_kernel<BF16, HASZ>), dim3((unsigned)a.tiles, (unsigned)a.nseg), dim3(64 * a.ntiles), 0, st, a);
+}
+
+}  // namespace
+
+int64_t selective_backward_workspace_bytes(int64_t B, int64_t T, int G, int D, int N) {
+    int64_t L;
+    int nseg;
+    sel_bwd_split(B, T, G, D, N, &L, &nseg);
+    return sel_bwd_parts(B, T, G, D, N, L, nseg).end * 4;
+}
+
+hipError_t launch_selective_backward(SelBwdArgs a, hipStream_t st) {
+    a.ctiles = sel_ctiles(a.G, a.D);
+    a.ntiles = sel_ntiles(a.N);
+    a.tiles = sel_tiles(a.B, a.G, a.D);
+    sel_bwd_split(a.B, a.T, a.G, a.D, a.N, &a.L, &a.nseg);
+    const SelBwdParts p = sel_bwd_parts(a.B, a.T, a.G, a.D, a.N, a.L, a.nseg);
+    float* ws = static_cast<float*>(a.workspace);
+    a.ends = ws + p.ends; a.gends = ws + p.gends; a.steps = ws + p.steps; a.marks = ws + p.marks; a.msteps = ws + p.msteps;
+    a.part_bc = ws + p.part_bc; a.part_A = ws + p.part_A; a.part_D = ws + p.part_D;
+    if (a.z) a.bf16 ? sel_bwd_ends<true, true>(a, st) : sel_bwd_ends<false, true>(a, st);
+    else a.bf16 ? sel_bwd_ends<true, false>(a, st) : sel_bwd_ends<false, false>(a, st);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    SelCarryArgs c{};
+    c.ends = a.ends; c.steps = a.steps; c.A = a.A; c.from = a.S0;
+    c.tiles = a.tiles; c.nseg = a.nseg; c.ntiles = a.ntiles; c.ctiles = a.ctiles; c.G = a.G; c.D = a.D; c.N = a.N;
+    SelCarryArgs r = c;
+    r.ends = a.gends; r.from = a.dS; r.rev = true;
+    if ((e = sel_carry(c, r, 2, st)) != hipSuccess) return e;
+    if (a.z) a.bf16 ? sel_bwd_grads<true, true>(a, st) : sel_bwd_grads<false, true>(a, st);
+    else a.bf16 ? sel_bwd_grads<true, false>(a, st) : sel_bwd_grads<false, false>(a, st);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t cols = a.B * a.G * a.T * a.ntiles * 32, bg = (int64_t)a.G * a.ctiles;
+    if (cols > 0) {
+        hipLaunchKernelGGL(sel_bc_kernel, dim3((unsigned)((cols + 255) / 256)), dim3(256), 0, st, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    e = sum_columns(a.part_A, a.nseg * a.B, bg * a.ntiles * 1024, SelSumA{a.dA, a.G, a.D, a.N, a.ctiles, a.ntiles}, st);
+    if (e != hipSuccess) return e;
+    return sum_columns(a.part_D, a.nseg * a.ntiles * a.B, bg * 128, SelSumD{a.dD, a.dbias, a.G, a.D, a.ctiles}, st);
+}
+
+}  // namespace sdm
