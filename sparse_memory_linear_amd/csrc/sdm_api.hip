@@ -963,6 +963,8 @@ int check_selective_tensors(const char* fn, std::initializer_list<SelTensor> ts,
         if (T > 0 && (rc = check_address(fn, t.name, t.p, es))) return rc;
         rc = t.bc ? check_strides(fn, t.name, {B, T, G}, {t.s[0], t.s[1], t.s[2]}) : check_strides(fn, t.name, {B, T}, {t.s[0], t.s[1]});
         if (rc) return rc;
+        if (t.s[1] >= 1 << 26)  // a chunk's rows lie within 2^31 bytes
+            return fail(SDM_ERR_UNSUPPORTED, "%s: token stride of %s: below 2^26 elements", fn, t.name);
     }
     return 0;
 }

@@ -7,8 +7,12 @@
 // kernels: a state costs a product and an exponential (four issue slots) for the decay and one product to
 // apply it. Sums over n are over r in a lane and over q by two permlane swaps, which put channel c's sum in lane c.
 #pragma once
+#include "sdm_buffer.h"
 #include "sdm_internal.h"
 #include "sdm_rows.h"
+
+// v_mul_legacy_f32: a product that is 0 where either factor is, whatever the other one is
+extern "C" __device__ float sdm_mul_zero(float, float) __asm("llvm.amdgcn.fmul.legacy");
 
 namespace sdm {
 namespace {
@@ -19,24 +23,32 @@ constexpr int SC = 8;               // tokens per chunk
 constexpr float GONE = -INFINITY;   // in place of a sum of steps: a sequence began since, nothing crosses
 
 template <bool BF16>
-__device__ __forceinline__ uint32_t raw(const void* p, uint32_t i) {
-    if constexpr (BF16) return static_cast<const uint16_t*>(p)[i];
-    else return static_cast<const uint32_t*>(p)[i];
-}
-template <bool BF16>
 __device__ __forceinline__ float value(uint32_t u) {
     return BF16 ? bf16_f(u) : __uint_as_float(u);
 }
-template <bool BF16>
-__device__ __forceinline__ void put(void* p, uint32_t i, float f) {
-    if constexpr (BF16) static_cast<uint16_t*>(p)[i] = (uint16_t)f_bf16(f);
-    else static_cast<float*>(p)[i] = f;
-}
-// the row at element e (the same for the wavefront)
+// the address of element e (the same for the wavefront)
 template <bool BF16>
 __device__ __forceinline__ const char* row(const void* p, int64_t e) {
     return static_cast<const char*>(p) + e * (BF16 ? 2 : 4);
 }
+
+// Rows of tokens from token t on: a lane's element at vo bytes (OOB: nothing is read or written) of row i, with the
+// row's offset in a scalar register. Token strides are below 2^26 elements, so that a chunk's rows lie within 2^31 bytes.
+template <bool BF16>
+struct Rows {
+    rsrc_t r;
+    uint32_t step;
+    __device__ __forceinline__ Rows(const char* p, int64_t stride, int64_t t)
+        : r(make_rsrc(row<BF16>(p, t * stride), 0x7FFFFFFF)), step((uint32_t)stride * (BF16 ? 2u : 4u)) {}
+    __device__ __forceinline__ uint32_t get(uint32_t vo, uint32_t i) const {
+        if constexpr (BF16) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)vo, (int)(i * step), 0);
+        else return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)vo, (int)(i * step), 0);
+    }
+    __device__ __forceinline__ void put(uint32_t vo, uint32_t i, float f) const {
+        if constexpr (BF16) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)f_bf16(f), r, (int)vo, (int)(i * step), 0);
+        else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), r, (int)vo, (int)(i * step), 0);
+    }
+};
 
 // log(1 + e^v) = max(v, 0) + log(1 + e^-|v|); the logarithm of 1 + e as 2 artanh(s), s = e / (2 + e) <= 1/3, by a
 // polynomial in s^2 (fitted at Chebyshev points; 4e-9 off): exact to some steps for tiny e too, where 1 + e is not
@@ -78,9 +90,10 @@ struct SelAt {
     int g, c0, dg, seg;          // c0: first channel in its group
     bool in;                     // the lane's channel is there
     uint32_t c;                  // the lane's channel (the group's last one where it is not)
+    uint32_t vo, vput;           // its offset in a row, in bytes; the same for stores, none where it is not there
     int64_t t0, t1, end;         // tokens of the segment, and those of them that are there
 };
-template <typename Args>
+template <bool BF16, typename Args>
 __device__ __forceinline__ SelAt sel_at(const Args& a) {
     SelAt w;
     w.lane = threadIdx.x & 63;
@@ -96,6 +109,8 @@ __device__ __forceinline__ SelAt sel_at(const Args& a) {
     w.dg = a.D / a.G;
     w.in = w.c0 + w.lane < w.dg;
     w.c = (uint32_t)(w.g * w.dg + (w.in ? w.c0 + w.lane : w.dg - 1));
+    w.vo = w.c * (BF16 ? 2u : 4u);
+    w.vput = w.in ? w.vo : OOB;
     w.seg = blockIdx.y;
     w.t0 = (int64_t)w.seg * a.L;
     w.t1 = w.t0 + a.L < a.T ? w.t0 + a.L : a.T;
@@ -162,14 +177,19 @@ __device__ __forceinline__ void store_tile(float* p, int lane, const f32x16& v) 
         reinterpret_cast<float4*>(p)[64 * k + lane] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
 }
 
-// exp(delta A): a2 = A log2(e)
-__device__ __forceinline__ f32x16 decays(float delta, const f32x16& a2) {
+// exp(delta A): a2 = A log2(e). At a sequence's first token `gone` is minus infinity (else 0), and the decay 0.
+__device__ __forceinline__ f32x16 decays(float delta, const f32x16& a2, float gone) {
     float d[4];
     spread(delta, d);
     f32x16 v;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __builtin_amdgcn_exp2f(d[i / 4] * a2[i]);
+    for (int i = 0; i < 16; ++i) v[i] = __builtin_amdgcn_exp2f(fmaf(d[i / 4], a2[i], gone));
     return v;
+}
+// d h, and 0 for a decay of 0 whatever h is: what a sequence left behind, a NaN among it, ends with it
+__device__ __forceinline__ void decay(f32x16& h, const f32x16& d) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) h[i] = sdm_mul_zero(d[i], h[i]);
 }
 __device__ __forceinline__ f32x16 zeros16() {
     f32x16 v;
@@ -185,12 +205,15 @@ __device__ __forceinline__ uint32_t starts(const uint8_t* start, int64_t t, int6
     return (uint32_t)__ballot(on);
 }
 
-// Values of B or C: lane 16 q + j gets state j's of token t + q (0 past the end or the last state)
+// Values of B or C: lane 16 q + j gets state j's of token 4 k + q of a chunk (0 past its `left` tokens or the last state)
 template <bool BF16>
-__device__ __forceinline__ float load_bc(const char* p, int64_t stride, int64_t t, const SelAt& w, int N) {
-    const int n = 16 * w.nt + w.j;
-    return t + w.q < w.end && n < N ? value<BF16>(raw<BF16>(row<BF16>(p, (t + w.q) * stride), n)) : 0.f;
+__device__ __forceinline__ float load_bc(const Rows<BF16>& p, const SelAt& w, int k, int64_t left, int N) {
+    const int n = 16 * w.nt + w.j, q = 4 * k + w.q;
+    const uint32_t vo = q < left && n < N ? (uint32_t)q * p.step + (uint32_t)n * (BF16 ? 2u : 4u) : OOB;
+    return value<BF16>(p.get(vo, 0));
 }
+// Row i of a chunk, or the last one that is there
+__device__ __forceinline__ uint32_t upto(int i, int64_t left) { return i < left ? (uint32_t)i : (uint32_t)left - 1; }
 
 // Tiles' ends carried through the segments: out[s] holds what a segment adds (start state 0) and gets what
 // arrives at it. One float4 a thread.

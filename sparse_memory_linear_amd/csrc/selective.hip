@@ -18,7 +18,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
     constexpr int NW = MULTI ? 4 : 1;
     __shared__ float cl[NW][SC][16];
     __shared__ float yl[MULTI && EMIT ? 2 : 1][NW][MULTI && EMIT ? SC : 1][64];
-    const SelAt w = sel_at(a);
+    const SelAt w = sel_at<BF16>(a);
     const f32x16 a2 = load_dn(a, w, a.A, 1.44269504f);
     const int64_t wave = w.tile * a.ntiles + w.nt, waves = a.tiles * a.ntiles, per = (int64_t)a.D * a.N;
     f32x16 h = zeros16();
@@ -31,46 +31,51 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
     const char* pz = HASZ ? row<BF16>(a.z, w.b * a.z_b) : nullptr;
     const char* pB = row<BF16>(a.Bm, w.b * a.B_b + w.g * a.B_g);
     const char* pC = EMIT ? row<BF16>(a.Cm, w.b * a.C_b + w.g * a.C_g) : nullptr;
+    const char* py = EMIT ? row<BF16>(a.y, w.b * a.T * a.D) : nullptr;
     const float bias = a.bias ? a.bias[w.c] : 0.f, skip = EMIT && a.Dskip ? a.Dskip[w.c] : 0.f;
     const uint8_t* start = a.start ? a.start + w.b * a.T : nullptr;
     float steps = 0.f;
     int par = 0;
     for (int64_t t = w.t0; t < w.end; t += SC) {
+        const int64_t left = w.end - t;
+        const Rows<BF16> X(px, a.x_t, t), T(pd, a.dt_t, t), Z(pz, HASZ ? a.z_t : 0, HASZ ? t : 0), Y(py, EMIT ? a.D : 0, EMIT ? t : 0);
+        const Rows<BF16> B(pB, a.B_t, t), C(pC, EMIT ? a.C_t : 0, EMIT ? t : 0);
         uint32_t xr[SC], dr[SC], zr[SC];
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
-            const int64_t u = t + i < w.end ? t + i : w.end - 1;
-            xr[i] = raw<BF16>(row<BF16>(px, u * a.x_t), w.c);
-            dr[i] = raw<BF16>(row<BF16>(pd, u * a.dt_t), w.c);
-            if constexpr (HASZ && EMIT) zr[i] = raw<BF16>(row<BF16>(pz, u * a.z_t), w.c);
+            xr[i] = X.get(w.vo, upto(i, left));
+            dr[i] = T.get(w.vo, upto(i, left));
+            if constexpr (HASZ && EMIT) zr[i] = Z.get(w.vo, upto(i, left));
         }
-        const float b0 = load_bc<BF16>(pB, a.B_t, t, w, a.N), b1 = load_bc<BF16>(pB, a.B_t, t + 4, w, a.N);
+        float bq[2][4];
+        spread(load_bc(B, w, 0, left, a.N), bq[0]);
+        spread(load_bc(B, w, 1, left, a.N), bq[1]);
         if constexpr (EMIT) {
-            const float c0 = load_bc<BF16>(pC, a.C_t, t, w, a.N), c1 = load_bc<BF16>(pC, a.C_t, t + 4, w, a.N);
-            cl[w.nt][w.q][w.j] = c0;
-            cl[w.nt][4 + w.q][w.j] = c1;
+            cl[w.nt][w.q][w.j] = load_bc(C, w, 0, left, a.N);
+            cl[w.nt][4 + w.q][w.j] = load_bc(C, w, 1, left, a.N);
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
         const uint32_t st = starts(start, t, w.end, w.lane);
-        float bq[2][4];
-        spread(b0, bq[0]);
-        spread(b1, bq[1]);
+        // y's last steps: D x and the gate (a lane without a channel works on the last one's rows, and stores nothing)
+        auto finish = [&](int i, float y) {
+            float o = fmaf(skip, value<BF16>(xr[i]), y);
+            if constexpr (HASZ) {
+                const float z = value<BF16>(zr[i]);
+                o *= z * sigmoid(z);
+            }
+            Y.put(w.vput, i, o);
+        };
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
-            const bool on = w.in && t + i < w.end;
-            const float v = value<BF16>(dr[i]) + bias, x = value<BF16>(xr[i]);
-            float delta = a.softplus ? softplus(v) : v;
+            const bool on = i < left;
+            const float v = value<BF16>(dr[i]) + bias, sp = softplus(v);
+            float delta = a.softplus ? sp : v;
+            const float u = on ? delta * value<BF16>(xr[i]) : 0.f;
             delta = on ? delta : 0.f;
-            const float u = on ? delta * x : 0.f;
-            if constexpr (!EMIT) steps = st >> i & 1u ? GONE : steps + delta;
-            if (st >> i & 1u) {
-                h = zeros16();
-            } else {
-                const f32x16 d = decays(delta, a2);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) h[k] *= d[k];
-            }
+            const float gone = st >> i & 1u ? GONE : 0.f;
+            if constexpr (!EMIT) steps += delta + gone;
+            decay(h, decays(delta, a2, gone));
             h = outer_add(bq[i / 4][i % 4], u, h);
             if constexpr (EMIT) {
                 const float4 c = *reinterpret_cast<const float4*>(&cl[w.nt][i][4 * w.q]);
@@ -79,38 +84,25 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
                 for (int k = 0; k < 4; ++k)
                     p[k] = fmaf(c.w, h[4 * k + 3], fmaf(c.z, h[4 * k + 2], fmaf(c.y, h[4 * k + 1], c.x * h[4 * k])));
                 const float y = gather_sum(p);
-                if constexpr (MULTI) {
-                    yl[par][w.nt][i][w.lane] = y;
-                } else if (on) {
-                    float o = fmaf(skip, x, y);
-                    if constexpr (HASZ) {
-                        const float z = value<BF16>(zr[i]);
-                        o *= z * sigmoid(z);
-                    }
-                    put<BF16>(const_cast<char*>(row<BF16>(a.y, (w.b * a.T + t + i) * a.D)), w.c, o);
-                }
+                if constexpr (MULTI) yl[par][w.nt][i][w.lane] = y;
+                else if (on) finish(i, y);
             }
         }
         if constexpr (MULTI && EMIT) {
-            __syncthreads();  // the other half of yl is read by no one: its readers have passed this barrier's last turn
+            __syncthreads();  // (the other half of yl: its readers have passed the barrier before)
 #pragma unroll
             for (int i = 0; i < SC; ++i) {
-                if (i % a.ntiles != w.nt || t + i >= w.end || !w.in) continue;
-                float o = skip * value<BF16>(xr[i]);
-                for (int k = 0; k < a.ntiles; ++k) o += yl[par][k][i][w.lane];
-                if constexpr (HASZ) {
-                    const float z = value<BF16>(zr[i]);
-                    o *= z * sigmoid(z);
-                }
-                put<BF16>(const_cast<char*>(row<BF16>(a.y, (w.b * a.T + t + i) * a.D)), w.c, o);
+                if (i % a.ntiles != w.nt || i >= left) continue;
+                float y = 0.f;
+                for (int k = 0; k < a.ntiles; ++k) y += yl[par][k][i][w.lane];
+                finish(i, y);
             }
             par ^= 1;
         }
     }
     if constexpr (EMIT) {
-        if (w.nt == 0 && w.in)
-            for (int64_t t = w.end > w.t0 ? w.end : w.t0; t < w.t1; ++t)
-                put<BF16>(const_cast<char*>(row<BF16>(a.y, (w.b * a.T + t) * a.D)), w.c, 0.f);
+        if (w.nt == 0)
+            for (int64_t t = w.end > w.t0 ? w.end : w.t0; t < w.t1; ++t) Rows<BF16>(py, a.D, t).put(w.vput, 0, 0.f);
         if (a.S && w.seg == a.nseg - 1) store_dn(a, w, a.S + w.b * per, h);
     } else {
         store_tile(a.ends + (w.seg * waves + wave) * 1024, w.lane, h);

@@ -22,7 +22,7 @@ constexpr int HC = SC / 2;
 
 template <bool BF16, bool HASZ>
 __global__ __launch_bounds__(256, 2) void sel_ends_kernel(SelBwdArgs a) {
-    const SelAt w = sel_at(a);
+    const SelAt w = sel_at<BF16>(a);
     const f32x16 a2 = load_dn(a, w, a.A, 1.44269504f);
     const int64_t wave = w.tile * a.ntiles + w.nt, waves = a.tiles * a.ntiles;
     const char* px = row<BF16>(a.x, w.b * a.x_b);
@@ -37,58 +37,47 @@ __global__ __launch_bounds__(256, 2) void sel_ends_kernel(SelBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) p[i] = 1.f;
     float steps = 0.f;
-    const bool back = w.seg > 0;
-    int64_t chunk = w.seg * (a.L / SC);
-    for (int64_t t = w.t0; t < w.end; t += SC, ++chunk) {
-        store_tile(a.marks + (chunk * waves + wave) * 1024, w.lane, h);
-        if (w.nt == 0) a.msteps[(chunk * a.tiles + w.tile) * 64 + w.lane] = steps;
-        uint32_t xr[SC], dr[SC], zr[SC], yr[SC];
+    int64_t half = w.seg * (a.L / HC);
+    for (int64_t t = w.t0; t < w.end; t += HC, ++half) {
+        const int64_t left = w.end - t;
+        if (half % 2 == 0) {
+            store_tile(a.marks + (half / 2 * waves + wave) * 1024, w.lane, h);
+            if (w.nt == 0) a.msteps[(half / 2 * a.tiles + w.tile) * 64 + w.lane] = steps;
+        }
+        const Rows<BF16> X(px, a.x_t, t), T(pd, a.dt_t, t), Z(pz, HASZ ? a.z_t : 0, HASZ ? t : 0), Y(py, a.dy_t, t);
+        const Rows<BF16> B(pB, a.B_t, t), C(pC, a.C_t, t);
+        uint32_t xr[HC], dr[HC], zr[HC], yr[HC];
 #pragma unroll
-        for (int i = 0; i < SC; ++i) {
-            const int64_t u = t + i < w.end ? t + i : w.end - 1;
-            xr[i] = raw<BF16>(row<BF16>(px, u * a.x_t), w.c);
-            dr[i] = raw<BF16>(row<BF16>(pd, u * a.dt_t), w.c);
-            if (back) {
-                yr[i] = raw<BF16>(row<BF16>(py, u * a.dy_t), w.c);
-                if constexpr (HASZ) zr[i] = raw<BF16>(row<BF16>(pz, u * a.z_t), w.c);
-            }
+        for (int i = 0; i < HC; ++i) {
+            xr[i] = X.get(w.vo, upto(i, left));
+            dr[i] = T.get(w.vo, upto(i, left));
+            yr[i] = Y.get(w.vo, upto(i, left));
+            if constexpr (HASZ) zr[i] = Z.get(w.vo, upto(i, left));
         }
         const uint32_t st = starts(start, t, w.end, w.lane);
-        float bq[2][4], cq[2][4];
+        float bq[4], cq[4];
+        spread(load_bc(B, w, 0, left, a.N), bq);
+        spread(load_bc(C, w, 0, left, a.N), cq);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            spread(load_bc<BF16>(pB, a.B_t, t + 4 * k, w, a.N), bq[k]);
-            if (back) spread(load_bc<BF16>(pC, a.C_t, t + 4 * k, w, a.N), cq[k]);
-        }
-#pragma unroll
-        for (int i = 0; i < SC; ++i) {
-            const bool on = w.in && t + i < w.end;
-            const float v = value<BF16>(dr[i]) + bias, x = value<BF16>(xr[i]);
-            float delta = a.softplus ? softplus(v) : v;
+        for (int i = 0; i < HC; ++i) {
+            const bool on = i < left;
+            const float v = value<BF16>(dr[i]) + bias, sp = softplus(v);
+            float delta = a.softplus ? sp : v, gy = value<BF16>(yr[i]);
+            const float u = on ? delta * value<BF16>(xr[i]) : 0.f;
             delta = on ? delta : 0.f;
-            steps = st >> i & 1u ? GONE : steps + delta;
-            if (st >> i & 1u) {
-                h = zeros16();
-                p = zeros16();
-            } else {
-                const f32x16 d = decays(delta, a2);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    h[k] *= d[k];
-                    p[k] *= d[k];
-                }
+            if constexpr (HASZ) {
+                const float z = value<BF16>(zr[i]);
+                gy *= z * sigmoid(z);
             }
-            h = outer_add(bq[i / 4][i % 4], on ? delta * x : 0.f, h);
-            if (back) {
-                float gy = value<BF16>(yr[i]);
-                if constexpr (HASZ) {
-                    const float z = value<BF16>(zr[i]);
-                    gy *= z * sigmoid(z);
-                }
-                const f32x16 cg = outer_add(cq[i / 4][i % 4], on ? gy : 0.f, zeros16());
+            gy = on ? gy : 0.f;
+            const float gone = st >> i & 1u ? GONE : 0.f;
+            steps += delta + gone;
+            const f32x16 d = decays(delta, a2, gone), cg = outer_add(cq[i], gy, zeros16());
+            decay(h, d);
+            h = outer_add(bq[i], u, h);
+            decay(p, d);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) g[k] = fmaf(p[k], cg[k], g[k]);
-            }
+            for (int k = 0; k < 16; ++k) g[k] = fmaf(p[k], cg[k], g[k]);
         }
     }
     const int64_t at = (w.seg * waves + wave) * 1024;
@@ -111,12 +100,19 @@ __device__ __forceinline__ float row_sums(const float (&v)[4], int j) {
     return s + dpp<0xB1>(s);                                       // quad_perm 1,0,3,2
 }
 
+// LDS of a wavefront, in floats: half a chunk's decayed states a_t h_{t-1}, its B and C; and with several tiles
+// of states the sums over states that the wavefronts exchange
+constexpr int KEPT = HC * 1024, SHARE = KEPT + 2 * HC * 16, SUMS = HC * 3 * 64;
+
 template <bool BF16, bool HASZ, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdArgs a) {
-    constexpr int NW = MULTI ? 4 : 1;
-    __shared__ float bl[NW][HC][16], cl[NW][HC][16];
-    __shared__ float sl[MULTI ? 2 : 1][NW][MULTI ? HC : 1][3][64];
-    const SelAt w = sel_at(a);
+    extern __shared__ float4 lds4[];
+    const SelAt w = sel_at<BF16>(a);
+    float* mine = reinterpret_cast<float*>(lds4) + w.nt * SHARE;
+    float4* kept = reinterpret_cast<float4*>(mine);
+    float(*bl)[16] = reinterpret_cast<float(*)[16]>(mine + KEPT);
+    float(*cl)[16] = bl + HC;
+    float* sums = reinterpret_cast<float*>(lds4) + (MULTI ? a.ntiles * SHARE : 0);  // [wave][HC][3][64]
     const f32x16 a2 = load_dn(a, w, a.A, 1.44269504f);
     const int64_t wave = w.tile * a.ntiles + w.nt, waves = a.tiles * a.ntiles, per = (int64_t)a.D * a.N;
     const char* px = row<BF16>(a.x, w.b * a.x_b);
@@ -125,183 +121,188 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
     const char* py = row<BF16>(a.dy, w.b * a.dy_b);
     const char* pB = row<BF16>(a.Bm, w.b * a.B_b + w.g * a.B_g);
     const char* pC = row<BF16>(a.Cm, w.b * a.C_b + w.g * a.C_g);
+    const char* pdx = row<BF16>(a.dx, w.b * a.T * a.D);
+    const char* pdd = row<BF16>(a.ddt, w.b * a.T * a.D);
+    const char* pdz = HASZ ? row<BF16>(a.dz, w.b * a.T * a.D) : nullptr;
+    const char* pbc = row<false>(a.part_bc, (((w.c0 / 64) * a.B + w.b) * a.G + w.g) * a.T * a.ntiles * 32 + w.nt * 32);
+    // the lane's element of a token's 16 sums for dB and 16 for dC
+    const uint32_t vbc = (w.j & 3) < 2 ? 4u * ((w.j & 1) * 16 + 4 * w.q + (w.j >> 2)) : OOB;
     const float bias = a.bias ? a.bias[w.c] : 0.f, skip = a.Dskip ? a.Dskip[w.c] : 0.f;
     const uint8_t* start = a.start ? a.start + w.b * a.T : nullptr;
     const int64_t at = (w.seg * waves + wave) * 1024;
     f32x16 g = load_tile(a.gends + at, w.lane), dA = zeros16();
     float dD = 0.f, dbias = 0.f;
-    int par = 0;
     // behind the last token: gradients of 0
-    if (w.nt == 0 && w.in)
+    if (w.nt == 0)
         for (int64_t t = w.end > w.t0 ? w.end : w.t0; t < w.t1; ++t) {
-            const int64_t e = (w.b * a.T + t) * a.D;
-            put<BF16>(const_cast<char*>(row<BF16>(a.dx, e)), w.c, 0.f);
-            put<BF16>(const_cast<char*>(row<BF16>(a.ddt, e)), w.c, 0.f);
-            if constexpr (HASZ) put<BF16>(const_cast<char*>(row<BF16>(a.dz, e)), w.c, 0.f);
+            Rows<BF16>(pdx, a.D, t).put(w.vput, 0, 0.f);
+            Rows<BF16>(pdd, a.D, t).put(w.vput, 0, 0.f);
+            if constexpr (HASZ) Rows<BF16>(pdz, a.D, t).put(w.vput, 0, 0.f);
         }
     const int64_t chunks = w.end > w.t0 ? (w.end - w.t0 + SC - 1) / SC : 0, first = w.seg * (a.L / SC);
-    for (int64_t half = 2 * chunks - 1; half >= 0; --half) {
-        const int64_t t8 = w.t0 + half / 2 * SC, t = t8 + (half & 1) * HC, chunk = first + half / 2;
-        if (t >= w.end) continue;
+    for (int64_t ch = chunks - 1; ch >= 0; --ch) {
+        const int64_t t = w.t0 + ch * SC, left = w.end - t;
+        const Rows<BF16> X(px, a.x_t, t), T(pd, a.dt_t, t), Z(pz, HASZ ? a.z_t : 0, HASZ ? t : 0), Y(py, a.dy_t, t);
+        const Rows<BF16> B(pB, a.B_t, t), C(pC, a.C_t, t);
+        uint32_t xr[SC], dr[SC], zr[SC], yr[SC];
+        float bv[2], cv[2];
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            xr[i] = X.get(w.vo, upto(i, left));
+            dr[i] = T.get(w.vo, upto(i, left));
+            yr[i] = Y.get(w.vo, upto(i, left));
+            if constexpr (HASZ) zr[i] = Z.get(w.vo, upto(i, left));
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            bv[k] = load_bc(B, w, k, left, a.N);
+            cv[k] = load_bc(C, w, k, left, a.N);
+        }
+        const uint32_t st = starts(start, t, w.end, w.lane);
         // the state in front of the chunk
-        f32x16 h = load_tile(a.marks + (chunk * waves + wave) * 1024, w.lane);
+        f32x16 h0 = load_tile(a.marks + ((first + ch) * waves + wave) * 1024, w.lane);
         {
-            const float* ms = a.msteps + (chunk * a.tiles + w.tile) * 64 + w.j;
+            const float* ms = a.msteps + ((first + ch) * a.tiles + w.tile) * 64 + w.j;
             const f32x16 hs = load_tile(a.ends + at, w.lane);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float s = ms[16 * k];
-                if (s != GONE)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        h[4 * k + r] = fmaf(__builtin_amdgcn_exp2f(a2[4 * k + r] * s), hs[4 * k + r], h[4 * k + r]);
-            }
-        }
-        const uint32_t sts = starts(start, t8, w.end, w.lane);
-        if (half & 1) {  // and in front of its second half
-            uint32_t xr[HC], dr[HC];
-#pragma unroll
-            for (int i = 0; i < HC; ++i) {
-                xr[i] = raw<BF16>(row<BF16>(px, (t8 + i) * a.x_t), w.c);
-                dr[i] = raw<BF16>(row<BF16>(pd, (t8 + i) * a.dt_t), w.c);
-            }
-            float bq[4];
-            spread(load_bc<BF16>(pB, a.B_t, t8, w, a.N), bq);
-#pragma unroll
-            for (int i = 0; i < HC; ++i) {
-                const float v = value<BF16>(dr[i]) + bias;
-                float delta = a.softplus ? softplus(v) : v;
-                delta = w.in ? delta : 0.f;
-                if (sts >> i & 1u) {
-                    h = zeros16();
-                } else {
-                    const f32x16 d = decays(delta, a2);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) h[k] *= d[k];
-                }
-                h = outer_add(bq[i], w.in ? delta * value<BF16>(xr[i]) : 0.f, h);
-            }
-        }
-        const uint32_t st = half & 1 ? sts >> HC : sts;
-        uint32_t xr[HC], dr[HC], zr[HC], yr[HC];
-#pragma unroll
-        for (int i = 0; i < HC; ++i) {
-            const int64_t u = t + i < w.end ? t + i : w.end - 1;
-            xr[i] = raw<BF16>(row<BF16>(px, u * a.x_t), w.c);
-            dr[i] = raw<BF16>(row<BF16>(pd, u * a.dt_t), w.c);
-            yr[i] = raw<BF16>(row<BF16>(py, u * a.dy_t), w.c);
-            if constexpr (HASZ) zr[i] = raw<BF16>(row<BF16>(pz, u * a.z_t), w.c);
-        }
-        const float bv = load_bc<BF16>(pB, a.B_t, t, w, a.N), cv = load_bc<BF16>(pC, a.C_t, t, w, a.N);
-        bl[w.nt][w.q][w.j] = bv;
-        cl[w.nt][w.q][w.j] = cv;
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        float bq[4], cq[4];
-        spread(bv, bq);
-        spread(cv, cq);
-        float delta[HC], u[HC], gy[HC];
-        f32x16 dec[HC], kept[HC];  // a_t and a_t h_{t-1}
-#pragma unroll
-        for (int i = 0; i < HC; ++i) {
-            const bool on = w.in && t + i < w.end;
-            const float v = value<BF16>(dr[i]) + bias;
-            const float de = a.softplus ? softplus(v) : v;
-            delta[i] = on ? de : 0.f;
-            u[i] = on ? de * value<BF16>(xr[i]) : 0.f;
-            float y = value<BF16>(yr[i]);
-            if constexpr (HASZ) {
-                const float z = value<BF16>(zr[i]);
-                y *= z * sigmoid(z);
-            }
-            gy[i] = on ? y : 0.f;
-            if (st >> i & 1u) {
-                dec[i] = zeros16();
-                kept[i] = zeros16();
-            } else {
-                dec[i] = decays(delta[i], a2);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) kept[i][k] = dec[i][k] * h[k];
-            }
-            h = outer_add(bq[i], u[i], kept[i]);
-        }
-        // a token's own gradients, from the sums over its states
-        auto finish = [&](int i, float sa, float sbn, float sch) {
-            if (!w.in || t + i >= w.end) return;
-            const float x = value<BF16>(xr[i]), v = value<BF16>(dr[i]) + bias;
-            const int64_t e = (w.b * a.T + t + i) * a.D;
-            put<BF16>(const_cast<char*>(row<BF16>(a.dx, e)), w.c, fmaf(delta[i], sbn, skip * gy[i]));
-            float dd = fmaf(x, sbn, 0.69314718f * sa);
-            if (a.softplus) dd *= sigmoid(v);
-            put<BF16>(const_cast<char*>(row<BF16>(a.ddt, e)), w.c, dd);
-            dbias += dd;
-            dD = fmaf(gy[i], x, dD);
-            if constexpr (HASZ) {
-                const float z = value<BF16>(zr[i]), s = sigmoid(z);
-                const float dz = value<BF16>(yr[i]) * fmaf(skip, x, sch) * s * fmaf(z, 1.f - s, 1.f);
-                put<BF16>(const_cast<char*>(row<BF16>(a.dz, e)), w.c, dz);
-            }
-        };
-#pragma unroll
-        for (int i = HC - 1; i >= 0; --i) {
-            g = outer_add(cq[i], gy[i], g);
-            if (i < HC - 1) h = outer_add(bq[i], u[i], kept[i]);
-            const float4 bn = *reinterpret_cast<const float4*>(&bl[w.nt][i][4 * w.q]);
-            const float4 cn = *reinterpret_cast<const float4*>(&cl[w.nt][i][4 * w.q]);
-            float ds[4], us[4], gs[4], sb[4] = {}, sc[4] = {}, pb[4], pa[4], pc[4];
-            spread(delta[i], ds);
-            spread(u[i], us);
-            spread(gy[i], gs);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                pa[k] = 0.f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int e = 4 * k + r;
-                    sb[r] = fmaf(us[k], g[e], sb[r]);
-                    sc[r] = fmaf(gs[k], h[e], sc[r]);
-                    const float gk = g[e] * kept[i][e];
-                    pa[k] = fmaf(a2[e], gk, pa[k]);
-                    dA[e] = fmaf(ds[k], gk, dA[e]);
+                    const float e = fmaf(__builtin_amdgcn_exp2f(a2[4 * k + r] * s), hs[4 * k + r], h0[4 * k + r]);
+                    h0[4 * k + r] = s == GONE ? h0[4 * k + r] : e;
                 }
-                pb[k] = fmaf(bn.w, g[4 * k + 3], fmaf(bn.z, g[4 * k + 2], fmaf(bn.y, g[4 * k + 1], bn.x * g[4 * k])));
-                if constexpr (HASZ)
-                    pc[k] = fmaf(cn.w, h[4 * k + 3], fmaf(cn.z, h[4 * k + 2], fmaf(cn.y, h[4 * k + 1], cn.x * h[4 * k])));
-            }
-            if (st >> i & 1u) {
-                g = zeros16();
-            } else {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) g[k] *= dec[i][k];
-            }
-            float qa = gather_sum(pa), qb = gather_sum(pb), qc = 0.f;
-            if constexpr (HASZ) qc = gather_sum(pc);
-            // the tile's sums over its channels: states 4 q + j / 4, lane 4 j' those of dB, 4 j' + 1 of dC
-            const float rb = row_sums(sb, w.j), rc = row_sums(sc, w.j);
-            if ((w.j & 3) < 2 && t + i < w.end)
-                a.part_bc[((((w.c0 / 64) * a.B + w.b) * a.G + w.g) * a.T + t + i) * a.ntiles * 32 + w.nt * 32 + (w.j & 1) * 16 + 4 * w.q +
-                          (w.j >> 2)] = w.j & 1 ? rc : rb;
-            if constexpr (MULTI) {
-                sl[par][w.nt][i][0][w.lane] = qa;
-                sl[par][w.nt][i][1][w.lane] = qb;
-                sl[par][w.nt][i][2][w.lane] = qc;
-            }
-            if constexpr (!MULTI) {
-                finish(i, qa, qb, qc);
             }
         }
-        if constexpr (MULTI) {
-            __syncthreads();  // (the other half of sl: its readers have passed the barrier before)
+        auto step_of = [&](int i) {
+            const float v = value<BF16>(dr[i]) + bias, sp = softplus(v);
+            return a.softplus ? sp : v;
+        };
+        f32x16 h = h0;
+        if (left > HC) {  // and in front of its second half
+            float bq[4];
+            spread(bv[0], bq);
 #pragma unroll
             for (int i = 0; i < HC; ++i) {
-                if (i % a.ntiles != w.nt) continue;
-                float s[3] = {};
-                for (int k = 0; k < a.ntiles; ++k)
-#pragma unroll
-                    for (int m = 0; m < 3; ++m) s[m] += sl[par][k][i][m][w.lane];
-                finish(i, s[0], s[1], s[2]);
+                const float delta = step_of(i);
+                decay(h, decays(delta, a2, st >> i & 1u ? GONE : 0.f));
+                h = outer_add(bq[i], delta * value<BF16>(xr[i]), h);
             }
-            par ^= 1;
+        }
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+            if (half * HC >= left) continue;
+            if (half == 0) h = h0;
+            bl[w.q][w.j] = bv[half];
+            cl[w.q][w.j] = cv[half];
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            float bq[4], cq[4], delta[HC], u[HC], gy[HC];
+            spread(bv[half], bq);
+            spread(cv[half], cq);
+            f32x16 dec[HC], last;  // a_t; the last token's a_t h_{t-1}
+#pragma unroll
+            for (int i = 0; i < HC; ++i) {
+                const int m = half * HC + i;
+                const bool on = w.in && m < left;
+                const float de = step_of(m);
+                delta[i] = m < left ? de : 0.f;
+                u[i] = on ? de * value<BF16>(xr[m]) : 0.f;
+                float y = value<BF16>(yr[m]);
+                if constexpr (HASZ) {
+                    const float z = value<BF16>(zr[m]);
+                    y *= z * sigmoid(z);
+                }
+                gy[i] = on ? y : 0.f;
+                dec[i] = decays(delta[i], a2, st >> m & 1u ? GONE : 0.f);
+                decay(h, dec[i]);
+                if (i < HC - 1) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        kept[(i * 4 + k) * 64 + w.lane] = make_float4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+                    h = outer_add(bq[i], u[i], h);
+                } else {
+                    last = h;
+                }
+            }
+            // a token's own gradients, from the sums over its states
+            auto finish = [&](int i, float sa, float sb, float sc) {
+                const int m = half * HC + i;
+                const float x = value<BF16>(xr[m]), v = value<BF16>(dr[m]) + bias;
+                float dd = fmaf(x, sb, 0.69314718f * sa);
+                const float sg = sigmoid(v);
+                dd = m < left ? dd * (a.softplus ? sg : 1.f) : 0.f;
+                dbias += dd;
+                dD = fmaf(gy[i], x, dD);
+                if (m < left) {
+                    Rows<BF16>(pdx, a.D, t).put(w.vput, m, fmaf(delta[i], sb, skip * gy[i]));
+                    Rows<BF16>(pdd, a.D, t).put(w.vput, m, dd);
+                    if constexpr (HASZ) {
+                        const float z = value<BF16>(zr[m]), s = sigmoid(z);
+                        Rows<BF16>(pdz, a.D, t).put(w.vput, m, value<BF16>(yr[m]) * fmaf(skip, x, sc) * s * fmaf(z, 1.f - s, 1.f));
+                    }
+                }
+            };
+#pragma unroll
+            for (int i = HC - 1; i >= 0; --i) {
+                const int m = half * HC + i;
+                g = outer_add(cq[i], gy[i], g);
+                const float4 bn = *reinterpret_cast<const float4*>(&bl[i][4 * w.q]);
+                const float4 cn = *reinterpret_cast<const float4*>(&cl[i][4 * w.q]);
+                const float b4[4] = {bn.x, bn.y, bn.z, bn.w}, c4[4] = {cn.x, cn.y, cn.z, cn.w};
+                float ds[4], us[4], gs[4], sb[4] = {}, sc[4] = {}, pb[4], pa[4], pc[4];
+                spread(delta[i], ds);
+                spread(u[i], us);
+                spread(gy[i], gs);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float k4[4];
+                    if (i < HC - 1) {
+                        const float4 kp = kept[(i * 4 + k) * 64 + w.lane];
+                        k4[0] = kp.x; k4[1] = kp.y; k4[2] = kp.z; k4[3] = kp.w;
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) k4[r] = last[4 * k + r];
+                    }
+                    pa[k] = pb[k] = pc[k] = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int e = 4 * k + r;
+                        const float hv = fmaf(us[k], b4[r], k4[r]), gk = g[e] * k4[r];
+                        sb[r] = fmaf(us[k], g[e], sb[r]);
+                        sc[r] = fmaf(gs[k], hv, sc[r]);
+                        pa[k] = fmaf(a2[e], gk, pa[k]);
+                        pb[k] = fmaf(b4[r], g[e], pb[k]);
+                        if constexpr (HASZ) pc[k] = fmaf(c4[r], hv, pc[k]);
+                        dA[e] = fmaf(ds[k], gk, dA[e]);
+                        g[e] = sdm_mul_zero(dec[i][e], g[e]);
+                    }
+                }
+                const float qa = gather_sum(pa), qb = gather_sum(pb), qc = HASZ ? gather_sum(pc) : 0.f;
+                const float rb = row_sums(sb, w.j), rc = row_sums(sc, w.j);
+                if (m < left) Rows<false>(pbc, a.ntiles * 32, t).put(vbc, m, w.j & 1 ? rc : rb);
+                if constexpr (MULTI) {
+                    float* s = sums + ((w.nt * HC + i) * 3) * 64 + w.lane;
+                    s[0] = qa;
+                    s[64] = qb;
+                    s[128] = qc;
+                } else {
+                    finish(i, qa, qb, qc);
+                }
+            }
+            if constexpr (MULTI) {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < HC; ++i) {
+                    if (i % a.ntiles != w.nt) continue;
+                    float s[3] = {};
+                    for (int k = 0; k < a.ntiles; ++k)
+#pragma unroll
+                        for (int m = 0; m < 3; ++m) s[m] += sums[((k * HC + i) * 3 + m) * 64 + w.lane];
+                    finish(i, s[0], s[1], s[2]);
+                }
+                __syncthreads();  // before the next sums
+            }
         }
     }
     store_tile(a.part_A + at, w.lane, dA);
@@ -381,10 +382,18 @@ SelBwdParts sel_bwd_parts(int64_t B, int64_t T, int G, int D, int N, int64_t L, 
 }
 
 template <bool BF16, bool HASZ>
-void sel_bwd_grads(const SelBwdArgs& a, hipStream_t st) {
+hipError_t sel_bwd_grads(const SelBwdArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)a.tiles, (unsigned)a.nseg);
-    if (a.ntiles > 1) hipLaunchKernelGGL((sel_grads_kernel<BF16, HASZ, true>), grid, dim3(64 * a.ntiles), 0, st, a);
-    else hipLaunchKernelGGL((sel_grads_kernel<BF16, HASZ, false>), grid, dim3(64), 0, st, a);
+    if (a.ntiles == 1) {
+        hipLaunchKernelGGL((sel_grads_kernel<BF16, HASZ, false>), grid, dim3(64), SHARE * 4, st, a);
+    } else {
+        const int bytes = a.ntiles * (SHARE + SUMS) * 4;  // up to 80 KB
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(sel_grads_kernel<BF16, HASZ, true>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((sel_grads_kernel<BF16, HASZ, true>), grid, dim3(64 * a.ntiles), bytes, st, a);
+    }
+    return hipGetLastError();
 }
 template <bool BF16, bool HASZ>
 void sel_bwd_ends(const SelBwdArgs& a, hipStream_t st) {
@@ -419,9 +428,9 @@ hipError_t launch_selective_backward(SelBwdArgs a, hipStream_t st) {
     SelCarryArgs r = c;
     r.ends = a.gends; r.from = a.dS; r.rev = true;
     if ((e = sel_carry(c, r, 2, st)) != hipSuccess) return e;
-    if (a.z) a.bf16 ? sel_bwd_grads<true, true>(a, st) : sel_bwd_grads<false, true>(a, st);
-    else a.bf16 ? sel_bwd_grads<true, false>(a, st) : sel_bwd_grads<false, false>(a, st);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.z) e = a.bf16 ? sel_bwd_grads<true, true>(a, st) : sel_bwd_grads<false, true>(a, st);
+    else e = a.bf16 ? sel_bwd_grads<true, false>(a, st) : sel_bwd_grads<false, false>(a, st);
+    if (e != hipSuccess) return e;
     const int64_t cols = a.B * a.G * a.T * a.ntiles * 32, bg = (int64_t)a.G * a.ctiles;
     if (cols > 0) {
         hipLaunchKernelGGL(sel_bc_kernel, dim3((unsigned)((cols + 255) / 256)), dim3(256), 0, st, a);
