@@ -5,8 +5,9 @@
 //   dx_t = sum_j w_j dz_{t+K-1-j},   dw_j = sum_t dz_t x_{t-K+1+j},   dbias = sum_t dz_t.
 //
 // A thread owns VEC channels (a piece of a row, or one channel where rows are not aligned to pieces) over a
-// tile of tokens: the last K - 1 inputs and the weights stay in its registers, so that each input is
-// read once from HBM (a tile's first K - 1 inputs also by the tile before, out of the L2). HBM-bound.
+// tile of tokens, a wavefront 64 such threads of one tile, so that lengths and begins of sequences are scalar:
+// the last K - 1 inputs and the weights stay in registers, and each input is read once from HBM (a tile's first K - 1
+// inputs also by the tile before, out of the L2). HBM-bound.
 #include "sdm_internal.h"
 #include "sdm_rows.h"
 
@@ -15,21 +16,21 @@ namespace {
 
 constexpr int AHEAD = 4;  // tokens whose loads are in flight together
 
-// The tile that a thread works on: its channels, sequence, head and tokens
+// The tile that a wavefront works on, and the thread's channels in it
 struct ConvAt {
     int c, h;
     int64_t b, t0, t1;
     bool ok;
 };
-template <typename Args>
+template <int VEC, typename Args>
 __device__ __forceinline__ ConvAt conv_at(const Args& a) {
     ConvAt w;
-    uint32_t i = blockIdx.x * 256u + threadIdx.x;  // fewer than 2^31 threads
-    w.ok = i < (uint32_t)a.threads;
-    w.c = (int)(i % (uint32_t)a.nvec) * a.vec;
-    i /= (uint32_t)a.nvec;
-    w.h = (int)(i % (uint32_t)a.H);
-    i /= (uint32_t)a.H;
+    uint32_t i = blockIdx.x;  // [b][tile][64 threads of the pieces of all heads]
+    const uint32_t v = i % (uint32_t)a.groups * 64u + threadIdx.x;
+    i /= (uint32_t)a.groups;
+    w.ok = v < (uint32_t)(a.H * a.nvec);
+    w.c = (int)(v % (uint32_t)a.nvec) * VEC;
+    w.h = (int)(v / (uint32_t)a.nvec);
     w.t0 = (int64_t)(i % (uint32_t)a.ntile) * a.tile;
     w.b = i / (uint32_t)a.ntile;
     w.t1 = w.t0 + a.tile < a.T ? w.t0 + a.tile : a.T;
@@ -53,15 +54,24 @@ __device__ __forceinline__ void taps(const float (&w)[K][VEC], const float (&bia
     }
 }
 
+template <int VEC>
+__device__ __forceinline__ void clear(float (&v)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+}
+
+// The piece's VEC * K weights lie one after another
 template <int K, int VEC, typename Args>
 __device__ __forceinline__ void load_weights(const Args& a, int h, int c, float (&w)[K][VEC], float (&bias)[VEC]) {
     const int64_t row = (int64_t)h * a.d + c;
+    float all[VEC * K];
+    load_piece<VEC * K, false>(a.w, row * K, all);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        bias[i] = a.bias ? a.bias[row + i] : 0.f;
+    for (int i = 0; i < VEC; ++i)
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][i] = a.w[(row + i) * K + j];
-    }
+        for (int j = 0; j < K; ++j) w[j][i] = all[i * K + j];
+    clear<VEC>(bias);
+    if (a.bias) load_piece<VEC, false>(a.bias, row, bias);
 }
 
 // The state's row m (token m - (K - 1)); zeros without a state
@@ -73,12 +83,6 @@ __device__ __forceinline__ void load_state(const void* S0, int64_t bh, int d, in
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = 0.f;
     }
-}
-
-template <int VEC>
-__device__ __forceinline__ void clear(float (&v)[VEC]) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = 0.f;
 }
 
 // The window win[0 .. K - 1]: the newest input last
@@ -111,8 +115,8 @@ __device__ __forceinline__ void window(const Args& a, const ConvAt& w, int64_t n
 }
 
 template <int K, int VEC, bool BF16>
-__global__ __launch_bounds__(256) void conv_kernel(ConvArgs a) {
-    const ConvAt at = conv_at(a);
+__global__ __launch_bounds__(64) void conv_kernel(ConvArgs a) {
+    const ConvAt at = conv_at<VEC>(a);
     if (!at.ok) return;
     const int64_t n = length_of(a.lengths, at.b, a.T), bh = at.b * a.H + at.h;
     const char* x = static_cast<const char*>(a.x) + (at.b * a.x_b + at.h * a.x_h + at.c) * (BF16 ? 2 : 4);
@@ -181,8 +185,8 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a) {
 // A tile walks its tokens and the K - 1 behind them; dx of a token is complete K - 1 tokens later.
 // Its share of dw and dbias goes to a row of `part` [B * ntile][K + 1][H * d].
 template <int K, int VEC, bool BF16>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdArgs a) {
-    const ConvAt at = conv_at(a);
+__global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a) {
+    const ConvAt at = conv_at<VEC>(a);
     if (!at.ok) return;
     const int64_t n = length_of(a.lengths, at.b, a.T), bh = at.b * a.H + at.h;
     const char* x = static_cast<const char*>(a.x) + (at.b * a.x_b + at.h * a.x_h + at.c) * (BF16 ? 2 : 4);
@@ -284,17 +288,16 @@ static_assert(CONV_TILE >= CONV_TILE_MIN && CONV_BWD_TILE >= CONV_TILE_MIN, "");
 
 template <int K, int VEC, bool BF16>
 void conv_go(const ConvArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((conv_kernel<K, VEC, BF16>), dim3((unsigned)((a.threads + 255) / 256)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((conv_kernel<K, VEC, BF16>), dim3((unsigned)(a.B * a.ntile * a.groups)), dim3(64), 0, st, a);
 }
 template <int K, int VEC, bool BF16>
 void conv_go(const ConvBwdArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((conv_bwd_kernel<K, VEC, BF16>), dim3((unsigned)((a.threads + 255) / 256)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((conv_bwd_kernel<K, VEC, BF16>), dim3((unsigned)(a.B * a.ntile * a.groups)), dim3(64), 0, st, a);
 }
 template <int VEC, bool BF16, typename A>
 void conv_taps(A& a, hipStream_t st) {
-    a.vec = VEC;
     a.nvec = a.d / VEC;
-    a.threads = a.B * a.ntile * a.H * a.nvec;
+    a.groups = (int)((a.H * a.nvec + 63) / 64);
     switch (a.K) {
         case 2: conv_go<2, VEC, BF16>(a, st); break;
         case 3: conv_go<3, VEC, BF16>(a, st); break;

@@ -829,8 +829,8 @@ int check_conv(const char* fn, int dtype, int act, int64_t B, int64_t H, int64_t
     if (K < 2 || K > 8) return fail(SDM_ERR_UNSUPPORTED, "%s: K=%lld: from 2 to 8 taps", fn, (long long)K);
     // each factor below 2^31 first, so that the products stay in 64 bits
     const int64_t tiles = T > sdm::CONV_TILE_MIN ? (T + sdm::CONV_TILE_MIN - 1) / sdm::CONV_TILE_MIN : 1;
-    if (B > MOST || H > MOST || T > MOST || d > MOST || B * H > MOST || H * d > MOST || B * H * tiles > MOST ||
-        B * H * tiles * d > MOST || H * d > 1 << 23)
+    if (B > MOST || H > MOST || T > MOST || d > MOST || H * d > 1 << 23 || B * tiles > MOST ||
+        B * tiles * ((H * d + 63) / 64) >= 1 << 26)
         return fail(SDM_ERR_UNSUPPORTED, "%s: too many tokens and channels for one launch", fn);
     return B == 0 || H == 0 ? NO_WORK : 0;
 }

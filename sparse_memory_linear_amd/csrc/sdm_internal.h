@@ -247,8 +247,8 @@ struct ConvArgs {
     int align;               // elements: a power of two that divides d, the strides and the tensors' addresses
     bool bf16, silu;
     // set by the launcher
-    int64_t threads, ntile;
-    int tile, nvec, vec;
+    int64_t ntile;
+    int tile, nvec, groups;  // groups: of 64 threads, over the pieces of all heads
 };
 hipError_t launch_conv(ConvArgs a, hipStream_t st);
 struct ConvBwdArgs {
@@ -261,10 +261,10 @@ struct ConvBwdArgs {
     int d, K;
     int align;
     bool bf16, silu;
-    int64_t threads, ntile;
-    int tile, nvec, vec;
+    int64_t ntile;
+    int tile, nvec, groups;
 };
-constexpr int CONV_TILE_MIN = 32;  // tokens a thread at least, of more than that: bounds the launches' threads
+constexpr int CONV_TILE_MIN = 32;  // tokens a thread at least, of more than that: bounds the launches' wavefronts
 int64_t conv_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t d, int K);
 hipError_t launch_conv_backward(ConvBwdArgs a, hipStream_t st);
 

@@ -235,15 +235,26 @@ __global__ __launch_bounds__(256) void sel_carry_kernel(SelCarryArgs a0, SelCarr
         run[r] = in && a.from ? a.from[b * a.D * a.N + at] : 0.f;
     }
     float4* ends = reinterpret_cast<float4*>(a.ends);
-    for (int k = 0; k < a.nseg; ++k) {
-        const int s = a.rev ? a.nseg - 1 - k : k;
-        const int64_t at = (s * a.tiles * a.ntiles + w) * 256 + e;
-        const float4 own = ends[at];
-        const float sum = a.steps[(s * a.tiles + tile) * 64 + 16 * blk + j];
-        ends[at] = make_float4(run[0], run[1], run[2], run[3]);
-        const float o[4] = {own.x, own.y, own.z, own.w};
+    constexpr int AHEAD = 8;  // segments whose loads are in flight together
+    for (int k = 0; k < a.nseg; k += AHEAD) {
+        float4 own[AHEAD];
+        float sum[AHEAD];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) run[r] = sum == GONE ? o[r] : fmaf(__builtin_amdgcn_exp2f(a2[r] * sum), run[r], o[r]);
+        for (int m = 0; m < AHEAD; ++m) {
+            const int kk = k + m < a.nseg ? k + m : a.nseg - 1, s = a.rev ? a.nseg - 1 - kk : kk;
+            own[m] = ends[(s * a.tiles * a.ntiles + w) * 256 + e];
+            sum[m] = a.steps[(s * a.tiles + tile) * 64 + 16 * blk + j];
+        }
+#pragma unroll
+        for (int m = 0; m < AHEAD; ++m) {
+            if (k + m >= a.nseg) break;
+            const int s = a.rev ? a.nseg - 1 - k - m : k + m;
+            ends[(s * a.tiles * a.ntiles + w) * 256 + e] = make_float4(run[0], run[1], run[2], run[3]);
+            const float o[4] = {own[m].x, own[m].y, own[m].z, own[m].w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                run[r] = sum[m] == GONE ? o[r] : fmaf(__builtin_amdgcn_exp2f(a2[r] * sum[m]), run[r], o[r]);
+        }
     }
 }
 inline hipError_t sel_carry(const SelCarryArgs& a, const SelCarryArgs& b, int count, hipStream_t st) {
