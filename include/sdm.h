@@ -549,7 +549,7 @@ typedef enum sdm_act { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1 } sdm_act;
  *                           (decoding). Rows in front of the last sequence's first token are 0
  *   y       [B, H, T, d]    dtype (out); may not overlap x, S0 or S
  * Products and sums are fp32. T = 0 passes the state on.
- * Supported: K from 2 to 8; H*d <= 2^23, B*ceil(T/32)*ceil(H*d/64) < 2^26.
+ * Supported: K from 2 to 8; H*d <= 2^23, B*ceil(T/8)*ceil(H*d/64) < 2^26.
  */
 int sdm_causal_conv_forward(const void* x, int dtype, const int64_t* x_strides, const float* w, const float* bias,
                             int act, const void* S0, void* S, const uint8_t* start, const int32_t* lengths, void* y,

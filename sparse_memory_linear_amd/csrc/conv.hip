@@ -8,6 +8,8 @@
 // tile of tokens, a wavefront 64 such threads of one tile, so that lengths and begins of sequences are scalar:
 // the last K - 1 inputs and the weights stay in registers, and each input is read once from HBM (a tile's first K - 1
 // inputs also by the tile before, out of the L2). HBM-bound.
+#include <type_traits>
+
 #include "sdm_internal.h"
 #include "sdm_rows.h"
 
@@ -185,7 +187,7 @@ __global__ __launch_bounds__(64) void conv_kernel(ConvArgs a) {
 // A tile walks its tokens and the K - 1 behind them; dx of a token is complete K - 1 tokens later.
 // Its share of dw and dbias goes to a row of `part` [B * ntile][K + 1][H * d].
 template <int K, int VEC, bool BF16>
-__global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a) {
+__global__ __launch_bounds__(64, 2) void conv_bwd_kernel(ConvBwdArgs a) {
     const ConvAt at = conv_at<VEC>(a);
     if (!at.ok) return;
     const int64_t n = length_of(a.lengths, at.b, a.T), bh = at.b * a.H + at.h;
@@ -203,29 +205,41 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a) {
     }
     int64_t first = -K;  // the last sequence's first token among those seen
     // (a start in the tile's last K - 1 tokens before t0 cannot part token t0 from the state: no need to look)
-    for (int64_t t8 = at.t0; t8 < at.t1 + K - 1; t8 += AHEAD) {
-        float xs[AHEAD][VEC], dys[AHEAD][VEC];
+    const int64_t end = at.t1 + K - 1;
+    // AHEAD tokens from t8 on; with ALL, all of them are there (loads without a branch stay in flight together)
+    struct Group {
+        Piece<VEC, BF16> x[AHEAD], dy[AHEAD];
+    };
+    auto fetch = [&](auto whole, int64_t t8) {
+        constexpr bool ALL = decltype(whole)::value;
+        Group f{};
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            clear<VEC>(xs[k]);
-            clear<VEC>(dys[k]);
-            if (t8 + k < n && t8 + k < at.t1 + K - 1) {
-                load_piece<VEC, BF16>(x, (t8 + k) * a.x_t, xs[k]);
-                load_piece<VEC, BF16>(a.dy, (bh * a.T + t8 + k) * a.d + at.c, dys[k]);
+        for (int k = 0; k < AHEAD; ++k)
+            if (ALL || (t8 + k < n && t8 + k < end)) {
+                f.x[k].load(x, (t8 + k) * a.x_t);
+                f.dy[k].load(a.dy, (bh * a.T + t8 + k) * a.d + at.c);
             }
-        }
+        return f;
+    };
+    auto group = [&](auto whole, const Group& f, int64_t t8) {
+        constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int64_t t = t8 + k;
-            if (t >= at.t1 + K - 1) break;
-            float (&dz)[VEC] = dys[k];
-            if (t < n) {
+            if (!ALL && t >= end) break;
+            float dz[VEC], xs[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                dz[i] = f.dy[k][i];
+                xs[i] = f.x[k][i];
+            }
+            if (ALL || t < n) {
                 if (start && start[t]) {
                     first = t;
 #pragma unroll
                     for (int m = 0; m < K - 1; ++m) clear<VEC>(win[m]);
                 }
-                push<K, VEC>(win, xs[k]);
+                push<K, VEC>(win, xs);
                 if (a.silu) {
                     float z[VEC];
                     taps<K, VEC>(w, bias, win, z);
@@ -244,11 +258,18 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a) {
                     }
             }
             // dx[j] is that of token t - (K - 1) + j: it passed through tap j of token t, if in its sequence
+            if (t - (K - 1) >= first) {
 #pragma unroll
-            for (int j = 0; j < K; ++j)
-                if (t - (K - 1) + j >= first)
+                for (int j = 0; j < K; ++j)
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) dx[j][i] = fmaf(w[j][i], dz[i], dx[j][i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (t - (K - 1) + j >= first)
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) dx[j][i] = fmaf(w[j][i], dz[i], dx[j][i]);
+            }
             const int64_t u = t - (K - 1);  // complete
             if (u >= at.t0 || u < 0) {
                 if (a.dS && u < n && u > n - K && u >= first) {  // it is in the last state too
@@ -264,7 +285,21 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a) {
             pop<K, VEC>(dx);
             clear<VEC>(dx[K - 1]);
         }
+    };
+    int64_t t = at.t0;
+    const int64_t e = end < n ? end : n;
+    if (BF16 && t + AHEAD <= e) {  // a group ahead
+        Group f = fetch(std::true_type{}, t);
+        for (; t + 2 * AHEAD <= e; t += AHEAD) {
+            const Group next = fetch(std::true_type{}, t + AHEAD);
+            group(std::true_type{}, f, t);
+            f = next;
+        }
+        group(std::true_type{}, f, t);
+        t += AHEAD;
     }
+    for (; t + AHEAD <= e; t += AHEAD) group(std::true_type{}, fetch(std::true_type{}, t), t);
+    for (; t < end; t += AHEAD) group(std::false_type{}, fetch(std::false_type{}, t), t);
     const int64_t hd = (int64_t)a.H * a.d, row = (at.b * a.ntile + at.t0 / a.tile) * (K + 1) * hd + (int64_t)at.h * a.d + at.c;
 #pragma unroll
     for (int j = 0; j < K; ++j) store_piece<VEC, false>(a.part, row + j * hd, dw[j]);
@@ -283,8 +318,17 @@ struct ConvSums {
     }
 };
 
-constexpr int CONV_TILE = 32, CONV_BWD_TILE = 64;  // at least K - 1 tokens: only the first tile reads the state
-static_assert(CONV_TILE >= CONV_TILE_MIN && CONV_BWD_TILE >= CONV_TILE_MIN, "");
+// Tokens a tile: so many that the wavefronts (of 64 pieces of `vec` channels) fill the SIMDs once, within bounds.
+// Forwards 4 wavefronts fit a SIMD and short tiles cost little; backwards 3, a tile reads K - 1 tokens more and leaves a row
+// of sums, and a second round of few wavefronts would cost as much as a full one (4 x 8192 x 2048: 125 us by
+// tiles of 64). At least 8 tokens, so that only the first tile reads the state.
+int64_t tile_of(int64_t B, int64_t H, int64_t T, int64_t d, int vec, int slots, int most) {
+    const int64_t waves = B * ((H * d + 64 * vec - 1) / (64 * vec)), want = waves < slots ? slots / waves : 1;
+    int64_t t = (T + want - 1) / want;
+    t = (t + AHEAD - 1) / AHEAD * AHEAD;
+    return t < CONV_TILE_MIN ? CONV_TILE_MIN : t > most ? most : t;
+}
+static_assert(CONV_TILE_MIN >= 7, "");
 
 template <int K, int VEC, bool BF16>
 void conv_go(const ConvArgs& a, hipStream_t st) {
@@ -309,16 +353,18 @@ void conv_taps(A& a, hipStream_t st) {
     }
 }
 
-int64_t tiles(int64_t T, int tile) { return T > tile ? (T + tile - 1) / tile : 1; }
+int64_t tiles(int64_t T, int64_t tile) { return T > tile ? (T + tile - 1) / tile : 1; }
+
+int64_t bwd_tile(int64_t B, int64_t H, int64_t T, int64_t d) { return tile_of(B, H, T, d, 4, 2048, 1024); }
 
 }  // namespace
 
 int64_t conv_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t d, int K) {
-    return B * tiles(T, CONV_BWD_TILE) * (K + 1) * H * d * 4;
+    return B * tiles(T, bwd_tile(B, H, T, d)) * (K + 1) * H * d * 4;
 }
 
 hipError_t launch_conv(ConvArgs a, hipStream_t st) {
-    a.tile = CONV_TILE;
+    a.tile = (int)tile_of(a.B, a.H, a.T, a.d, 8, 4096, 32);
     a.ntile = tiles(a.T, a.tile);
     if (a.bf16) a.align >= 8 ? conv_taps<8, true>(a, st) : conv_taps<1, true>(a, st);
     else a.align >= 4 ? conv_taps<4, false>(a, st) : conv_taps<1, false>(a, st);
@@ -326,7 +372,7 @@ hipError_t launch_conv(ConvArgs a, hipStream_t st) {
 }
 
 hipError_t launch_conv_backward(ConvBwdArgs a, hipStream_t st) {
-    a.tile = CONV_BWD_TILE;
+    a.tile = (int)bwd_tile(a.B, a.H, a.T, a.d);
     a.ntile = tiles(a.T, a.tile);
     if (a.bf16) a.align >= 4 ? conv_taps<4, true>(a, st) : conv_taps<1, true>(a, st);
     else a.align >= 4 ? conv_taps<4, false>(a, st) : conv_taps<1, false>(a, st);

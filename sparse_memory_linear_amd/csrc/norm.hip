@@ -168,10 +168,8 @@ __device__ __forceinline__ void row_reduce(float& sum, float& mx, float (*buf)[2
 // Sums of x and y over them; buf is free on entry, and may be used again behind the next barrier
 template <int TPR>
 __device__ __forceinline__ void row_sums(float& x, float& y, float (*buf)[2]) {
-    for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) {
-        x += __shfl_xor(x, m);
-        y += __shfl_xor(y, m);
-    }
+    x = lane_sum<TPR < 64 ? TPR : 64>(x);
+    y = lane_sum<TPR < 64 ? TPR : 64>(y);
     if constexpr (TPR > 64) {
         const int w = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) { buf[w][0] = x; buf[w][1] = y; }
@@ -297,22 +295,19 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
 // A block's rows' share of dgamma stays in registers, its wavefronts' shares are
 // added in order in LDS, and the blocks' rows of `part` by norm_dgamma_kernel:
 // the order of all sums follows from the sizes alone.
-template <int TPR, int NV, bool TAIL, bool MEAN>
+template <int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwdArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     extern __shared__ float dg[];  // [d] (TPR < 256)
     __shared__ float buf[TPR < 64 ? 1 : TPR / 64][2];
     const int lane = threadIdx.x % TPR;
-    float ga[NV][VEC], acc[NV][VEC], accb[MEAN ? NV : 1][VEC];  // accb: dbias
+    float ga[NV][VEC], acc[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + lane) * VEC;
         if (c < a.d) load_vec(a.gamma, false, c, left<TAIL>(a.d, c), ga[j]);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            acc[j][i] = 0.f;
-            if constexpr (MEAN) accb[j][i] = 0.f;
-        }
+        for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
     }
     for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
         float h[NV][VEC], dy[NV][VEC];
@@ -324,31 +319,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
             if (c >= a.d) break;
             load_vec(a.h, a.h_bf16, at + c, left<TAIL>(a.d, c), h[j]);
             load_vec(a.dy, a.g_bf16, at + c, left<TAIL>(a.d, c), dy[j]);
-        }
-        float mg = 0.f;  // mean of gamma dy
-        if constexpr (MEAN) {
-            __shared__ float buf2[TPR < 64 ? 1 : TPR / 64][2];
-            float m = 0.f;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * TPR + lane) * VEC;
-                if (c >= a.d) break;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    m += h[j][i];
-                    mg = fmaf(dy[j][i], ga[j][i], mg);
-                }
-            }
-            row_sums<TPR>(m, mg, buf2);  // (buf's two barriers lie between this row's use of buf2 and the next one's)
-            m /= (float)a.d;
-            mg /= (float)a.d;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * TPR + lane) * VEC;
-                if (c >= a.d) break;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) h[j][i] = i < left<TAIL>(a.d, c) ? h[j][i] - m : 0.f;
-            }
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -383,8 +353,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 acc[j][i] = fmaf(dy[j][i], h[j][i] * r, acc[j][i]);
-                if constexpr (MEAN) accb[j][i] += dy[j][i];
-                o[i] = r * ((MEAN ? dy[j][i] * ga[j][i] - mg : dy[j][i] * ga[j][i]) - h[j][i] * k);
+                o[i] = r * (dy[j][i] * ga[j][i] - h[j][i] * k);
             }
             if (a.dh) {
                 float t[VEC];
@@ -395,36 +364,28 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
             store_vec(a.dx, a.g_bf16, at + c, left<TAIL>(a.d, c), o);
         }
     }
-    // the wavefronts' shares of one of the sums, in order, into the block's row of part
-    auto leave = [&](float (&acc)[NV][VEC], float* part) {
-        if constexpr (TPR < 256) {
-            for (int w = 0; w < RPB; ++w) {
-                if (threadIdx.x / TPR == w)
+    float* part = a.part + (int64_t)blockIdx.x * a.d;
+    if constexpr (TPR < 256) {
+        for (int w = 0; w < RPB; ++w) {
+            if (threadIdx.x / TPR == w)
 #pragma unroll
-                    for (int j = 0; j < NV; ++j) {
-                        const int c = (j * TPR + lane) * VEC;
-                        if (c >= a.d) break;
+                for (int j = 0; j < NV; ++j) {
+                    const int c = (j * TPR + lane) * VEC;
+                    if (c >= a.d) break;
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i)
-                            if (c + i < a.d) dg[c + i] = w ? dg[c + i] + acc[j][i] : acc[j][i];
-                    }
-                __syncthreads();
-            }
-            for (int c = threadIdx.x; c < a.d; c += 256) part[c] = dg[c];
-        } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * TPR + lane) * VEC;
-                if (c >= a.d) break;
-                store_vec(part, false, c, left<TAIL>(a.d, c), acc[j]);
-            }
+                    for (int i = 0; i < VEC; ++i)
+                        if (c + i < a.d) dg[c + i] = w ? dg[c + i] + acc[j][i] : acc[j][i];
+                }
+            __syncthreads();
         }
-    };
-    float* part = a.part + (int64_t)blockIdx.x * a.d * (MEAN ? 2 : 1);
-    leave(acc, part);
-    if constexpr (MEAN) {
-        __syncthreads();
-        leave(accb, part + a.d);
+        for (int c = threadIdx.x; c < a.d; c += 256) part[c] = dg[c];
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            if (c >= a.d) break;
+            store_vec(part, false, c, left<TAIL>(a.d, c), acc[j]);
+        }
     }
 }
 
@@ -443,6 +404,162 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* part, fl
         if (w < n) s[w][l] = x += s[w + n][l];
     }
     if (w == 0 && c < d) dgamma[c] = x;
+}
+
+// dh in flight during the sums, gamma and the sums over rows in registers: above rows of 8192 they would take too many
+// of them, and the sums are in LDS, 16 bytes a thread and piece of 4 columns.
+constexpr bool layer_early(int tpr, int nv) { return tpr * nv < 2048; }
+
+// The layer norm's rows: a row's loads without a branch between them, so that they are in flight together
+// (the types of dy and h are template arguments). acc and accb: the thread's share of dgamma and dbias.
+template <int TPR, int NV, bool TAIL, bool GB, bool HB>
+__device__ __forceinline__ void layer_rows(const NormBwdArgs& a, float (&acc)[NV][VEC], float (&accb)[NV][VEC], float4* sums, float (*buf)[2],
+                                           float (*buf2)[2]) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    constexpr bool EARLY = layer_early(TPR, NV);
+    const int lane = threadIdx.x % TPR;
+    float ga[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + lane) * VEC;
+        clear_vec(ga[j]);
+        if (EARLY && c < a.d) load_vec(a.gamma, false, c, left<TAIL>(a.d, c), ga[j]);
+    }
+    auto again = [&] {  // gamma where it is not kept
+        if constexpr (!EARLY) {
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * TPR + lane) * VEC;
+                if (c < a.d) load_vec(a.gamma, false, c, left<TAIL>(a.d, c), ga[j]);
+            }
+        }
+    };
+    const float per = 1.f / (float)a.d;
+    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+        float h[NV][VEC], dy[NV][VEC], dh[NV][VEC];
+        const int64_t at = row * a.d;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC, n = left<TAIL>(a.d, c);
+            clear_vec(h[j]);
+            clear_vec(dy[j]);
+            clear_vec(dh[j]);
+            if (c < a.d) {
+                load_vec(a.h, HB, at + c, n, h[j]);
+                load_vec(a.dy, GB, at + c, n, dy[j]);
+                if (EARLY && a.dh) load_vec(a.dh, GB, at + c, n, dh[j]);
+            }
+        }
+        float m = 0.f, mg = 0.f;
+        again();
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                m += h[j][i];
+                mg = fmaf(dy[j][i], ga[j][i], mg);
+            }
+        row_sums<TPR>(m, mg, buf);
+        m *= per;
+        mg *= per;
+        float ss = 0.f, dot = 0.f;
+        again();
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                h[j][i] = c + i < a.d ? h[j][i] - m : 0.f;
+                ss = fmaf(h[j][i], h[j][i], ss);
+                dot = fmaf(dy[j][i] * ga[j][i], h[j][i], dot);
+            }
+        }
+        row_sums<TPR>(ss, dot, buf2);  // (its barrier, and that of the first sums, lie between two rows' uses of each buffer)
+        const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+        const float k = dot * r * r * per;  // n mean(g dy n) = (h - m) (dot r^2 / d)
+        again();
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + lane) * VEC;
+            float o[VEC];
+            if (!EARLY && a.dh && c < a.d) load_vec(a.dh, GB, at + c, left<TAIL>(a.d, c), dh[j]);
+            if constexpr (EARLY) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    acc[j][i] = fmaf(dy[j][i], h[j][i] * r, acc[j][i]);
+                    accb[j][i] += dy[j][i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; i += 4) {
+                    float4 &sg = sums[(4 * j + i / 4) * TPR + lane], &sb = sums[(4 * j + 2 + i / 4) * TPR + lane];
+                    sg = make_float4(fmaf(dy[j][i], h[j][i] * r, sg.x), fmaf(dy[j][i + 1], h[j][i + 1] * r, sg.y),
+                                     fmaf(dy[j][i + 2], h[j][i + 2] * r, sg.z), fmaf(dy[j][i + 3], h[j][i + 3] * r, sg.w));
+                    sb = make_float4(sb.x + dy[j][i], sb.y + dy[j][i + 1], sb.z + dy[j][i + 2], sb.w + dy[j][i + 3]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = r * (dy[j][i] * ga[j][i] - mg - h[j][i] * k) + dh[j][i];
+            if (c < a.d) store_vec(a.dx, GB, at + c, left<TAIL>(a.d, c), o);
+        }
+    }
+}
+
+template <int TPR, int NV, bool TAIL, bool GB, bool HB>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_bwd_kernel(NormBwdArgs a) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    extern __shared__ float4 sums[];  // TPR < 256: [d] floats; above rows of 8192: [NV][dgamma, dbias][2][TPR]
+    float* dg = reinterpret_cast<float*>(sums);
+    constexpr bool EARLY = layer_early(TPR, NV);
+    __shared__ float buf[TPR < 64 ? 1 : TPR / 64][2], buf2[TPR < 64 ? 1 : TPR / 64][2];
+    const int lane = threadIdx.x % TPR;
+    float acc[NV][VEC], accb[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        clear_vec(acc[j]);
+        clear_vec(accb[j]);
+    }
+    if constexpr (!EARLY)
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) sums[i * TPR + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    layer_rows<TPR, NV, TAIL, GB, HB>(a, acc, accb, sums, buf, buf2);
+    if constexpr (!EARLY)
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) {
+            float(&to)[VEC] = i & 2 ? accb[i / 4] : acc[i / 4];
+            const float4 x = sums[i * TPR + lane];
+            to[4 * (i & 1)] = x.x; to[4 * (i & 1) + 1] = x.y; to[4 * (i & 1) + 2] = x.z; to[4 * (i & 1) + 3] = x.w;
+        }
+    // the thread groups' shares of a sum, in order, into the block's row of part
+    auto leave = [&](float (&sum)[NV][VEC], float* part) {
+        if constexpr (TPR < 256) {
+            for (int w = 0; w < RPB; ++w) {
+                if (threadIdx.x / TPR == w)
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        const int c = (j * TPR + lane) * VEC;
+                        if (c >= a.d) break;
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i)
+                            if (c + i < a.d) dg[c + i] = w ? dg[c + i] + sum[j][i] : sum[j][i];
+                    }
+                __syncthreads();
+            }
+            for (int c = threadIdx.x; c < a.d; c += 256) part[c] = dg[c];
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * TPR + lane) * VEC;
+                if (c >= a.d) break;
+                store_vec(part, false, c, left<TAIL>(a.d, c), sum[j]);
+            }
+        }
+    };
+    float* part = a.part + (int64_t)blockIdx.x * a.d * 2;
+    leave(acc, part);
+    leave(accb, part + a.d);
 }
 
 // dgamma and dbias of the columns [2][d]
@@ -467,8 +584,11 @@ template <int TPR, int NV, bool TAIL>
 void norm_launch(const NormBwdArgs& a, hipStream_t st) {
     constexpr int THR = TPR < 256 ? 256 : TPR;
     const dim3 grid((unsigned)a.blocks);
-    if (a.mean) hipLaunchKernelGGL((norm_bwd_kernel<TPR, NV, TAIL, true>), grid, dim3(THR), TPR < 256 ? a.d * 4 : 0, st, a);
-    else hipLaunchKernelGGL((norm_bwd_kernel<TPR, NV, TAIL, false>), grid, dim3(THR), TPR < 256 ? a.d * 4 : 0, st, a);
+    if (a.mean) {
+        auto kernel = a.g_bf16 ? (a.h_bf16 ? layer_norm_bwd_kernel<TPR, NV, TAIL, true, true> : layer_norm_bwd_kernel<TPR, NV, TAIL, true, false>)
+                               : (a.h_bf16 ? layer_norm_bwd_kernel<TPR, NV, TAIL, false, true> : layer_norm_bwd_kernel<TPR, NV, TAIL, false, false>);
+        hipLaunchKernelGGL(kernel, grid, dim3(THR), TPR < 256 ? a.d * 4 : layer_early(TPR, NV) ? 0 : 4 * NV * TPR * 16, st, a);
+    } else hipLaunchKernelGGL((norm_bwd_kernel<TPR, NV, TAIL>), grid, dim3(THR), TPR < 256 ? a.d * 4 : 0, st, a);
 }
 
 // Threads a row: as many as it has pieces up to a wavefront (16 and 32 for the
@@ -496,16 +616,17 @@ hipError_t norm_any(const A& a, hipStream_t st) {
 
 }  // namespace
 
-int64_t norm_bwd_blocks(int64_t rows, int d) {
-    const int tpr = row_threads((d + VEC - 1) / VEC), rpb = tpr < 256 ? 256 / tpr : 1;
-    const int64_t need = (rows + rpb - 1) / rpb, most = 256 * (tpr == 1024 ? 1 : 4);  // what the CUs hold at once
+int64_t norm_bwd_blocks(int64_t rows, int d, bool mean) {
+    const int n = (d + VEC - 1) / VEC, tpr = row_threads(n), rpb = tpr < 256 ? 256 / tpr : 1;
+    // what the CUs hold at once: 4 of 256 threads, with the layer norm's two sums of two pieces 3
+    const int64_t need = (rows + rpb - 1) / rpb, most = 256 * (tpr == 1024 ? 1 : mean && n > tpr ? 3 : 4);
     return need < most ? need : most;
 }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t st) { return norm_any(a, st); }
 
 hipError_t launch_norm_backward(NormBwdArgs a, hipStream_t st) {
-    a.blocks = (int)norm_bwd_blocks(a.rows, a.d);
+    a.blocks = (int)norm_bwd_blocks(a.rows, a.d, a.mean);
     hipError_t e = norm_any(a, st);
     if (e != hipSuccess) return e;
     if (a.mean) return sum_columns(a.part, a.blocks, 2 * a.d, NormSums{a.dgamma, a.dbias, a.d}, st);

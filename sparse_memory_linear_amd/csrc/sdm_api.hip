@@ -666,7 +666,7 @@ int norm_impl(const char* fn, bool mean, const void* x, int x_dtype, const void*
 
 int64_t norm_backward_bytes(bool mean, int64_t rows, int64_t d) {
     if (rows < 0 || d < 1 || d > 16384 || rows > 0x7FFFFFFFll) return -1;
-    return rows == 0 ? 0 : sdm::norm_bwd_blocks(rows, (int)d) * d * (mean ? 8 : 4);
+    return rows == 0 ? 0 : sdm::norm_bwd_blocks(rows, (int)d, mean) * d * (mean ? 8 : 4);
 }
 
 int norm_backward_impl(const char* fn, bool mean, const void* dy, const void* dh, int g_dtype, const void* h,

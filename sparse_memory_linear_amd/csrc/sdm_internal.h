@@ -233,7 +233,7 @@ struct NormBwdArgs {
     float* dbias = nullptr;
     bool mean = false;
 };
-int64_t norm_bwd_blocks(int64_t rows, int d);
+int64_t norm_bwd_blocks(int64_t rows, int d, bool mean);
 hipError_t launch_norm_backward(NormBwdArgs a, hipStream_t st);
 
 // The causal convolution: x [B,H,T,d] by strides, everything else contiguous.
@@ -264,7 +264,7 @@ struct ConvBwdArgs {
     int64_t ntile;
     int tile, nvec, groups;
 };
-constexpr int CONV_TILE_MIN = 32;  // tokens a thread at least, of more than that: bounds the launches' wavefronts
+constexpr int CONV_TILE_MIN = 8;  // tokens a thread at least, of more than that: bounds the launches' wavefronts
 int64_t conv_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t d, int K);
 hipError_t launch_conv_backward(ConvBwdArgs a, hipStream_t st);
 

@@ -16,37 +16,41 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x));
 }
 
-// VEC elements from element e on: pieces of 4 or 8 elements aligned to their bytes (at most 16), or single ones
+// VEC elements of a row as they are stored: pieces of 4 or more elements aligned to their bytes (16 at most), or single ones
 template <int VEC, bool BF16>
-__device__ __forceinline__ void load_piece(const void* p, int64_t e, float (&v)[VEC]) {
-    if constexpr (BF16) {
-        const uint16_t* b = static_cast<const uint16_t*>(p) + e;
-        if constexpr (VEC == 8) {
-            const uint4 x = *reinterpret_cast<const uint4*>(b);
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+struct Piece {
+    static constexpr int W = BF16 ? (VEC + 1) / 2 : VEC;
+    uint32_t u[W];
+    __device__ __forceinline__ void load(const void* p, int64_t e) {
+        const char* at = static_cast<const char*>(p) + e * (BF16 ? 2 : 4);
+        if constexpr (W % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
-        } else if constexpr (VEC == 4) {
-            const uint2 x = *reinterpret_cast<const uint2*>(b);
-            v[0] = bf16_f(x.x); v[1] = __uint_as_float(x.x & 0xFFFF0000u);
-            v[2] = bf16_f(x.y); v[3] = __uint_as_float(x.y & 0xFFFF0000u);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = bf16_f(b[i]);
-        }
-    } else {
-        const float* f = static_cast<const float*>(p) + e;
-        if constexpr (VEC % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < VEC; i += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(f + i);
-                v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+            for (int i = 0; i < W; i += 4) {
+                const uint4 x = reinterpret_cast<const uint4*>(at)[i / 4];
+                u[i] = x.x; u[i + 1] = x.y; u[i + 2] = x.z; u[i + 3] = x.w;
             }
+        } else if constexpr (BF16 && VEC == 4) {
+            const uint2 x = *reinterpret_cast<const uint2*>(at);
+            u[0] = x.x; u[1] = x.y;
         } else {
+            static_assert(!BF16 || VEC == 1, "");
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = f[i];
+            for (int i = 0; i < W; ++i)
+                if constexpr (BF16) u[i] = reinterpret_cast<const uint16_t*>(at)[i];
+                else u[i] = reinterpret_cast<const uint32_t*>(at)[i];
         }
     }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (BF16) return __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+        else return __uint_as_float(u[i]);
+    }
+};
+template <int VEC, bool BF16>
+__device__ __forceinline__ void load_piece(const void* p, int64_t e, float (&v)[VEC]) {
+    Piece<VEC, BF16> x;
+    x.load(p, e);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = x[i];
 }
 
 template <int VEC, bool BF16>
@@ -73,6 +77,30 @@ __device__ __forceinline__ void store_piece(void* p, int64_t e, const float (&v)
             for (int i = 0; i < VEC; ++i) f[i] = v[i];
         }
     }
+}
+
+// the value of another lane of the 16: quad permutes 0xB1 (lane ^ 1) and 0x4E (lane ^ 2), 0x141 (lane 7 - j of the half
+// row), 0x140 (lane 15 - j), 0x128 (lane ^ 8)
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+// The sum over groups of N lanes (16, 32, 64), the same in all of them
+template <int N>
+__device__ __forceinline__ float lane_sum(float x) {
+    x += dpp<0xB1>(x);
+    x += dpp<0x4E>(x);
+    x += dpp<0x141>(x);
+    x += dpp<0x140>(x);
+    if constexpr (N >= 32) {
+        const auto h = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+    }
+    if constexpr (N >= 64) {
+        const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+    }
+    return x;
 }
 
 // out(i, the sum of column i of part [rows][cols], in 64 bits): 32 columns a workgroup, 32 groups of lanes

@@ -62,6 +62,14 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(s, p, fmaxf(v, 0.f));
 }
 
+// The step: softplus(v), or v as it is. (A branch on it, which the compiler makes of a plain choice, would cut the token's
+// instructions in pieces that are scheduled by themselves.)
+__device__ __forceinline__ float step_of(float v, bool plus) {
+    float s = softplus(v);
+    asm volatile("" : "+v"(s));
+    return plus ? s : v;
+}
+
 // v's four rows of 16 lanes, each in all rows
 __device__ __forceinline__ void spread(float v, float (&o)[4]) {
     const uint32_t u = __float_as_uint(v);

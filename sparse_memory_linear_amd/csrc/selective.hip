@@ -89,7 +89,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
             if (!ALL && i >= left) break;
-            const float v = value<BF16>(f.d[i]) + bias, delta = a.softplus ? softplus(v) : v;
+            const float delta = step_of(value<BF16>(f.d[i]) + bias, a.softplus);
             const float gone = f.st >> i & 1u ? GONE : 0.f;
             if constexpr (!EMIT) steps += delta + gone;
             decay(h, decays(delta, a2, gone));

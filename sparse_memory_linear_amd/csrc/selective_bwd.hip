@@ -13,6 +13,8 @@
 // segments both ways. The last pass walks the chunks backwards, half a chunk (4 tokens) at a time: it forms
 // the 4 states again, keeping each token's decay and decayed state in registers, and then walks them back.
 // Sums over channels leave a row a tile, added by a last pass.
+#include <type_traits>
+
 #include "selective.h"
 
 namespace sdm {
@@ -21,7 +23,7 @@ namespace {
 constexpr int HC = SC / 2;
 
 template <bool BF16, bool HASZ>
-__global__ __launch_bounds__(256, 2) void sel_ends_kernel(SelBwdArgs a) {
+__global__ __launch_bounds__(256, 4) void sel_ends_kernel(SelBwdArgs a) {
     const SelAt w = sel_at<BF16>(a);
     const f32x16 a2 = load_dn(a, w, a.A, 1.44269504f);
     const int64_t wave = w.tile * a.ntiles + w.nt, waves = a.tiles * a.ntiles;
@@ -61,8 +63,7 @@ __global__ __launch_bounds__(256, 2) void sel_ends_kernel(SelBwdArgs a) {
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
             const bool on = i < left;
-            const float v = value<BF16>(dr[i]) + bias, sp = softplus(v);
-            float delta = a.softplus ? sp : v, gy = value<BF16>(yr[i]);
+            float delta = step_of(value<BF16>(dr[i]) + bias, a.softplus), gy = value<BF16>(yr[i]);
             const float u = on ? delta * value<BF16>(xr[i]) : 0.f;
             delta = on ? delta : 0.f;
             if constexpr (HASZ) {
@@ -86,10 +87,6 @@ __global__ __launch_bounds__(256, 2) void sel_ends_kernel(SelBwdArgs a) {
     if (w.nt == 0) a.steps[(w.seg * a.tiles + w.tile) * 64 + w.lane] = steps;
 }
 
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
-}
 // Lane j of a row of 16 lanes gets the row's sum of v[j / 4]
 __device__ __forceinline__ float row_sums(const float (&v)[4], int j) {
     const bool hi = j & 8, odd = j & 4;
@@ -100,9 +97,10 @@ __device__ __forceinline__ float row_sums(const float (&v)[4], int j) {
     return s + dpp<0xB1>(s);                                       // quad_perm 1,0,3,2
 }
 
-// LDS of a wavefront, in floats: half a chunk's decayed states a_t h_{t-1}, its B and C; and with several tiles
-// of states the sums over states that the wavefronts exchange
-constexpr int KEPT = HC * 1024, SHARE = KEPT + 2 * HC * 16, SUMS = HC * 3 * 64;
+// LDS of a wavefront, in floats: half a chunk's decayed states a_t h_{t-1}, its B and C, and its steps, inputs and
+// gradients (with several tiles of states, in their place, the sums over states that the wavefronts exchange)
+constexpr int KEPT = HC * 1024, FAN = KEPT + 2 * HC * 16, SHARE = FAN + 3 * HC * 64;
+static_assert(8 * SHARE * 4 <= 160 * 1024, "8 wavefronts a CU");
 
 template <bool BF16, bool HASZ, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdArgs a) {
@@ -112,7 +110,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
     float4* kept = reinterpret_cast<float4*>(mine);
     float(*bl)[16] = reinterpret_cast<float(*)[16]>(mine + KEPT);
     float(*cl)[16] = bl + HC;
-    float* sums = reinterpret_cast<float*>(lds4) + (MULTI ? a.ntiles * SHARE : 0);  // [wave][HC][3][64]
+    float* fan = mine + FAN;  // [HC][3][64]: a channel's values at 4 j + blk, so that a lane reads its 4 channels' at once
     const f32x16 a2 = load_dn(a, w, a.A, 1.44269504f);
     const int64_t wave = w.tile * a.ntiles + w.nt, waves = a.tiles * a.ntiles, per = (int64_t)a.D * a.N;
     const char* px = row<BF16>(a.x, w.b * a.x_b);
@@ -140,18 +138,21 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
             if constexpr (HASZ) Rows<BF16>(pdz, a.D, t).put(w.vput, 0, 0.f);
         }
     const int64_t chunks = w.end > w.t0 ? (w.end - w.t0 + SC - 1) / SC : 0, first = w.seg * (a.L / SC);
-    for (int64_t ch = chunks - 1; ch >= 0; --ch) {
-        const int64_t t = w.t0 + ch * SC, left = w.end - t;
+    // A chunk's 8 tokens, or the first `left` of them
+    auto chunk = [&](auto whole, int64_t ch, int64_t left) {
+        constexpr bool ALL = decltype(whole)::value;
+        const int64_t t = w.t0 + ch * SC;
         const Rows<BF16> X(px, a.x_t, t), T(pd, a.dt_t, t), Z(pz, HASZ ? a.z_t : 0, HASZ ? t : 0), Y(py, a.dy_t, t);
         const Rows<BF16> B(pB, a.B_t, t), C(pC, a.C_t, t);
         uint32_t xr[SC], dr[SC], zr[SC], yr[SC];
         float bv[2], cv[2];
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
-            xr[i] = X.get(w.vo, upto(i, left));
-            dr[i] = T.get(w.vo, upto(i, left));
-            yr[i] = Y.get(w.vo, upto(i, left));
-            if constexpr (HASZ) zr[i] = Z.get(w.vo, upto(i, left));
+            const uint32_t m = ALL ? i : upto(i, left);
+            xr[i] = X.get(w.vo, m);
+            dr[i] = T.get(w.vo, m);
+            yr[i] = Y.get(w.vo, m);
+            if constexpr (HASZ) zr[i] = Z.get(w.vo, m);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -164,9 +165,11 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
         {
             const float* ms = a.msteps + ((first + ch) * a.tiles + w.tile) * 64 + w.j;
             const f32x16 hs = load_tile(a.ends + at, w.lane);
+            const float s4[4] = {ms[0], ms[16], ms[32], ms[48]};
+            __builtin_amdgcn_sched_barrier(0);  // all of the chunk's loads in flight before the first one is waited for
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float s = ms[16 * k];
+                const float s = s4[k];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float e = fmaf(__builtin_amdgcn_exp2f(a2[4 * k + r] * s), hs[4 * k + r], h0[4 * k + r]);
@@ -174,39 +177,33 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
                 }
             }
         }
-        auto step_of = [&](int i) {
-            const float v = value<BF16>(dr[i]) + bias, sp = softplus(v);
-            return a.softplus ? sp : v;
-        };
         f32x16 h = h0;
-        if (left > HC) {  // and in front of its second half
+        if (ALL || left > HC) {  // and in front of its second half
             float bq[4];
             spread(bv[0], bq);
 #pragma unroll
             for (int i = 0; i < HC; ++i) {
-                const float delta = step_of(i);
+                const float delta = step_of(value<BF16>(dr[i]) + bias, a.softplus);
                 decay(h, decays(delta, a2, st >> i & 1u ? GONE : 0.f));
                 h = outer_add(bq[i], delta * value<BF16>(xr[i]), h);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
 #pragma unroll
         for (int half = 1; half >= 0; --half) {
-            if (half * HC >= left) continue;
+            if (!ALL && half * HC >= left) continue;
             if (half == 0) h = h0;
             bl[w.q][w.j] = bv[half];
             cl[w.q][w.j] = cv[half];
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            float bq[4], cq[4], delta[HC], u[HC], gy[HC];
+            float bq[4], cq[4], delta[HC], gy[HC], u[HC];
             spread(bv[half], bq);
             spread(cv[half], cq);
-            f32x16 dec[HC], last;  // a_t; the last token's a_t h_{t-1}
 #pragma unroll
             for (int i = 0; i < HC; ++i) {
                 const int m = half * HC + i;
-                const bool on = w.in && m < left;
-                const float de = step_of(m);
-                delta[i] = m < left ? de : 0.f;
+                const bool there = ALL || m < left, on = w.in && there;
+                const float de = step_of(value<BF16>(dr[m]) + bias, a.softplus);
+                delta[i] = there ? de : 0.f;
                 u[i] = on ? de * value<BF16>(xr[m]) : 0.f;
                 float y = value<BF16>(yr[m]);
                 if constexpr (HASZ) {
@@ -214,33 +211,48 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
                     y *= z * sigmoid(z);
                 }
                 gy[i] = on ? y : 0.f;
-                dec[i] = decays(delta[i], a2, st >> m & 1u ? GONE : 0.f);
-                decay(h, dec[i]);
-                if (i < HC - 1) {
+                float* f = fan + i * 192 + 4 * w.j + w.q;
+                f[0] = delta[i];
+                f[64] = u[i];
+                f[128] = gy[i];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            auto fanned = [&](int i, int what, float (&o)[4]) {
+                const float4 v = *reinterpret_cast<const float4*>(fan + i * 192 + what * 64 + 4 * w.j);
+                o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+            };
+            f32x16 dec[HC];  // a_t
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        kept[(i * 4 + k) * 64 + w.lane] = make_float4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-                    h = outer_add(bq[i], u[i], h);
-                } else {
-                    last = h;
-                }
+            for (int i = 0; i < HC; ++i) {
+                float ds[4];
+                fanned(i, 0, ds);
+                const float gone = st >> (half * HC + i) & 1u ? GONE : 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) dec[i][k] = __builtin_amdgcn_exp2f(fmaf(ds[k / 4], a2[k], gone));
+                decay(h, dec[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    kept[(i * 4 + k) * 64 + w.lane] = make_float4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+                if (i < HC - 1) h = outer_add(bq[i], u[i], h);
+                __builtin_amdgcn_sched_barrier(0);
             }
             // a token's own gradients, from the sums over its states
             auto finish = [&](int i, float sa, float sb, float sc) {
                 const int m = half * HC + i;
-                const float x = value<BF16>(xr[m]), v = value<BF16>(dr[m]) + bias;
+                const float x = value<BF16>(xr[m]);
                 float dd = fmaf(x, sb, 0.69314718f * sa);
-                const float sg = sigmoid(v);
-                dd = m < left ? dd * (a.softplus ? sg : 1.f) : 0.f;
+                const float sg = sigmoid(value<BF16>(dr[m]) + bias);
+                dd *= a.softplus ? sg : 1.f;
+                if (!ALL) dd = m < left ? dd : 0.f;
                 dbias += dd;
                 dD = fmaf(gy[i], x, dD);
-                if (m < left) {
-                    Rows<BF16>(pdx, a.D, t).put(w.vput, m, fmaf(delta[i], sb, skip * gy[i]));
-                    Rows<BF16>(pdd, a.D, t).put(w.vput, m, dd);
-                    if constexpr (HASZ) {
-                        const float z = value<BF16>(zr[m]), s = sigmoid(z);
-                        Rows<BF16>(pdz, a.D, t).put(w.vput, m, value<BF16>(yr[m]) * fmaf(skip, x, sc) * s * fmaf(z, 1.f - s, 1.f));
-                    }
+                const uint32_t vo = ALL || m < left ? w.vput : OOB;
+                Rows<BF16>(pdx, a.D, t).put(vo, m, fmaf(delta[i], sb, skip * gy[i]));
+                Rows<BF16>(pdd, a.D, t).put(vo, m, dd);
+                if constexpr (HASZ) {
+                    const float z = value<BF16>(zr[m]), s = sigmoid(z);
+                    Rows<BF16>(pdz, a.D, t).put(vo, m, value<BF16>(yr[m]) * fmaf(skip, x, sc) * s * fmaf(z, 1.f - s, 1.f));
                 }
             };
 #pragma unroll
@@ -251,19 +263,13 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
                 const float4 cn = *reinterpret_cast<const float4*>(&cl[i][4 * w.q]);
                 const float b4[4] = {bn.x, bn.y, bn.z, bn.w}, c4[4] = {cn.x, cn.y, cn.z, cn.w};
                 float ds[4], us[4], gs[4], sb[4] = {}, sc[4] = {}, pb[4], pa[4], pc[4];
-                spread(delta[i], ds);
-                spread(u[i], us);
-                spread(gy[i], gs);
+                fanned(i, 0, ds);
+                fanned(i, 1, us);
+                fanned(i, 2, gs);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float k4[4];
-                    if (i < HC - 1) {
-                        const float4 kp = kept[(i * 4 + k) * 64 + w.lane];
-                        k4[0] = kp.x; k4[1] = kp.y; k4[2] = kp.z; k4[3] = kp.w;
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) k4[r] = last[4 * k + r];
-                    }
+                    const float4 kp = kept[(i * 4 + k) * 64 + w.lane];
+                    const float k4[4] = {kp.x, kp.y, kp.z, kp.w};
                     pa[k] = pb[k] = pc[k] = 0.f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -280,17 +286,19 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
                 }
                 const float qa = gather_sum(pa), qb = gather_sum(pb), qc = HASZ ? gather_sum(pc) : 0.f;
                 const float rb = row_sums(sb, w.j), rc = row_sums(sc, w.j);
-                if (m < left) Rows<false>(pbc, a.ntiles * 32, t).put(vbc, m, w.j & 1 ? rc : rb);
+                Rows<false>(pbc, a.ntiles * 32, t).put(ALL || m < left ? vbc : OOB, m, w.j & 1 ? rc : rb);
                 if constexpr (MULTI) {
-                    float* s = sums + ((w.nt * HC + i) * 3) * 64 + w.lane;
+                    float* s = fan + i * 192 + w.lane;  // token i's values there have been read
                     s[0] = qa;
                     s[64] = qb;
                     s[128] = qc;
                 } else {
                     finish(i, qa, qb, qc);
                 }
+                __builtin_amdgcn_sched_barrier(0x100);
             }
             if constexpr (MULTI) {
+                const float* all = reinterpret_cast<const float*>(lds4);
                 __syncthreads();
 #pragma unroll
                 for (int i = 0; i < HC; ++i) {
@@ -298,13 +306,19 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
                     float s[3] = {};
                     for (int k = 0; k < a.ntiles; ++k)
 #pragma unroll
-                        for (int m = 0; m < 3; ++m) s[m] += sums[((k * HC + i) * 3 + m) * 64 + w.lane];
+                        for (int m = 0; m < 3; ++m) s[m] += all[k * SHARE + FAN + i * 192 + m * 64 + w.lane];
                     finish(i, s[0], s[1], s[2]);
                 }
                 __syncthreads();  // before the next sums
             }
         }
+    };
+    int64_t ch = chunks - 1;
+    if (ch >= 0 && w.end - w.t0 < chunks * SC) {
+        chunk(std::false_type{}, ch, w.end - w.t0 - ch * SC);
+        --ch;
     }
+    for (; ch >= 0; --ch) chunk(std::true_type{}, ch, SC);
     store_tile(a.part_A + at, w.lane, dA);
     if (a.dS0 && w.seg == 0) store_dn(a, w, a.dS0 + w.b * per, g);
     float* pd2 = a.part_D + ((w.seg * a.ntiles + w.nt) * a.tiles + w.tile) * 128 + w.lane;
@@ -387,10 +401,7 @@ hipError_t sel_bwd_grads(const SelBwdArgs& a, hipStream_t st) {
     if (a.ntiles == 1) {
         hipLaunchKernelGGL((sel_grads_kernel<BF16, HASZ, false>), grid, dim3(64), SHARE * 4, st, a);
     } else {
-        const int bytes = a.ntiles * (SHARE + SUMS) * 4;  // up to 80 KB
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(sel_grads_kernel<BF16, HASZ, true>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != hipSuccess) return e;
+        const int bytes = a.ntiles * SHARE * 4;  // up to 80 KB
         hipLaunchKernelGGL((sel_grads_kernel<BF16, HASZ, true>), grid, dim3(64 * a.ntiles), bytes, st, a);
     }
     return hipGetLastError();

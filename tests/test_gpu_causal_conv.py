@@ -4,7 +4,7 @@ Tolerances count roundings of half a step (2^-24 in fp32, 2^-8 for outputs in bf
 sums, so (K + 1) of the terms' magnitudes. The sigmoid: its argument, rounded, is off by 1.25 half
 steps of |z|, the exponential and the reciprocal by two each; the products by one each, so silu and its derivative
 are off by (3 |z| + 14) half steps of their terms, and by 1.1 and 0.6 times what z is off by. The weights' gradient is
-a chain of at most 64 sums a tile, and 64-bit sums over the tiles.
+a chain of at most 64 sums a tile at these sizes, and 64-bit sums over the tiles.
 """
 import pytest
 import torch
