@@ -599,7 +599,8 @@ int64_t sdm_selective_scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int6
  *   workspace >= sdm_selective_scan_workspace_bytes bytes, 16-byte aligned (may be NULL where that is 0)
  * Products, sums and states are fp32. Meant for delta A <= 0; inputs and states must be finite (a NaN or
  * infinity in one channel's x, dt, z or state stays in that channel). T = 0 passes the state on.
- * Supported: N <= 64, D <= 2^20 with G dividing it, B*G*ceil(D/G/64) < 2^21, token strides below 2^26.
+ * Supported: N <= 64, D <= 2^20 with G dividing it, B*G*ceil(D/G/64)*ceil(N/16) < 2^22, token
+ * strides below 2^26.
  */
 int sdm_selective_scan_forward(const void* x, const void* dt, const void* z, const void* Bm, const void* Cm,
                                int in_dtype, const int64_t* strides, const float* A, const float* Dskip,

@@ -745,6 +745,7 @@ def sdm_balance_backward(idx: torch.Tensor, counts: torch.Tensor, tokens: torch.
 # Rows by strides: consecutive channels, the other dimensions at any stride.
 
 ACTS = {None: 0, "silu": 1}
+_I3, _I12, _I14 = (ctypes.c_int64 * n for n in (3, 12, 14))
 
 
 def _rows(name: str, t: torch.Tensor, like: torch.Tensor, shape):
@@ -794,7 +795,7 @@ def _conv_inputs(fn, x, w, bias, act, S0, S, start, lengths):
     if x.get_device() != w.get_device():
         raise ValueError("all tensors must be on the same GPU")
     _sequences(start, lengths, B, T, w)
-    return dev, (B, H, T, d, K), state, (ctypes.c_int64 * 3)(*s)
+    return dev, (B, H, T, d, K), state, _I3(*s)
 
 
 def sdm_causal_conv_forward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -857,7 +858,7 @@ def sdm_causal_conv_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
     ws = _workspace(workspace, sdm_causal_conv_backward_workspace_bytes(*sizes), d_)
     _call("sdm_causal_conv_backward", d_,
         _at(dy), _at(x), _dtype_code(x), xs, _at(w), _at(bias), ACTS[act], _at(S0), _at(dS), _at(start), _at(lengths),
-        _at(dx), (ctypes.c_int64 * 3)(*gs), _at(dw), _at(dbias), _at(dS0), *sizes, _at(ws), ws.numel())
+        _at(dx), _I3(*gs), _at(dw), _at(dbias), _at(dS0), *sizes, _at(ws), ws.numel())
     return {"dx": dx, "dw": dw, "dbias": dbias, "dS0": dS0}
 
 
@@ -897,7 +898,7 @@ def _selective_inputs(fn, x, dt, A, Bm, Cm, D, z, dt_bias, states, start, length
         if t is not None:
             _out(t, A, (B, n, N), torch.float32, name)
     _sequences(start, lengths, B, T, A)
-    return dev, (B, T, n, G, N), (ctypes.c_int64 * len(s))(*s)
+    return dev, (B, T, n, G, N), (_I12 if dy is None else _I14)(*s)
 
 
 def sdm_selective_scan_forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,

@@ -938,8 +938,8 @@ int check_selective(const char* fn, int in_dtype, int64_t B, int64_t T, int64_t 
         return fail(SDM_ERR_SHAPE, "%s: invalid sizes (G has to divide D)", fn);
     if (N > 64) return fail(SDM_ERR_UNSUPPORTED, "%s: N=%lld: at most 64 states a channel", fn, (long long)N);
     if (D > (1 << 20)) return fail(SDM_ERR_UNSUPPORTED, "%s: D=%lld: at most 2^20 channels", fn, (long long)D);
-    // fewer than 2^21 tiles, in at most 2^11 segments; each factor is bounded first
-    if (B > MOST || T > MOST || B * G >= 1 << 21 || sdm::sel_tiles(B, (int)G, (int)D) >= 1 << 21)
+    // fewer than 2^32 threads a launch, 1024 a tile of 64 channels and 16 states; each factor is bounded first
+    if (B > MOST || T > MOST || B * G >= 1 << 22 || sdm::sel_tiles(B, (int)G, (int)D) * ((N + 15) / 16) >= 1 << 22)
         return fail(SDM_ERR_UNSUPPORTED, "%s: too many sequences and channels for one launch", fn);
     return B == 0 ? NO_WORK : 0;
 }

@@ -223,50 +223,59 @@ __device__ __forceinline__ float load_bc(const Rows<BF16>& p, const SelAt& w, in
 // Row i of a chunk, or the last one that is there
 __device__ __forceinline__ uint32_t upto(int i, int64_t left) { return i < left ? (uint32_t)i : (uint32_t)left - 1; }
 
-// Tiles' ends carried through the segments: out[s] holds what a segment adds (start state 0) and gets what
-// arrives at it. One float4 a thread.
+// Tiles' ends carried through the segments: ends[s] holds what a segment adds (start state 0) and gets what
+// arrives at it. A state a thread, the loads of 32 segments in flight together: their latency is what it takes
+// (64 segments of 128 tiles: 19 us by 8 segments and 16 bytes a thread).
 __global__ __launch_bounds__(256) void sel_carry_kernel(SelCarryArgs a0, SelCarryArgs a1) {
-    const SelCarryArgs& a = blockIdx.y ? a1 : a0;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // [tile][nt][blk][lane]
-    const int e = (int)(i & 255), lane = e & 63, blk = e >> 6, j = lane & 15, q = lane >> 4;
-    const int64_t w = i >> 8, tile = w / a.ntiles;
+    const SelCarryArgs a = blockIdx.y ? a1 : a0;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // [tile][nt][blk][lane][r]
+    const int e = (int)(i & 1023), r = e & 3, lane = e >> 2 & 63, blk = e >> 8, j = lane & 15, q = lane >> 4;
+    const int64_t w = i >> 10, tile = w / a.ntiles;
     if (tile >= a.tiles) return;
     const int nt = (int)(w % a.ntiles);
     const int64_t bg = tile / a.ctiles, b = bg / a.G;
-    const int g = (int)(bg % a.G), dg = a.D / a.G, c = (int)(tile % a.ctiles) * 64 + 16 * blk + j, n = 16 * nt + 4 * q;
-    float run[4], a2[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const bool in = c < dg && n + r < a.N;
-        const int64_t at = ((int64_t)g * dg + c) * a.N + n + r;
-        a2[r] = in ? a.A[at] * 1.44269504f : 0.f;
-        run[r] = in && a.from ? a.from[b * a.D * a.N + at] : 0.f;
-    }
-    float4* ends = reinterpret_cast<float4*>(a.ends);
-    constexpr int AHEAD = 8;  // segments whose loads are in flight together
+    const int g = (int)(bg % a.G), dg = a.D / a.G, c = (int)(tile % a.ctiles) * 64 + 16 * blk + j, n = 16 * nt + 4 * q + r;
+    const bool in = c < dg && n < a.N;
+    const int64_t at = ((int64_t)g * dg + c) * a.N + n;
+    const float a2 = in ? a.A[at] * 1.44269504f : 0.f;
+    float run = in && a.from ? a.from[b * a.D * a.N + at] : 0.f;
+    const int64_t step = a.rev ? -1 : 1, first = a.rev ? a.nseg - 1 : 0;
+    float* ends = a.ends + (first * a.tiles * a.ntiles + w) * 1024 + e;
+    const float* sums = a.steps + (first * a.tiles + tile) * 64 + 16 * blk + j;
+    const int64_t de = step * a.tiles * a.ntiles * 1024, ds = step * a.tiles * 64;
+    constexpr int AHEAD = 32;
     for (int k = 0; k < a.nseg; k += AHEAD) {
-        float4 own[AHEAD];
-        float sum[AHEAD];
+        float own[AHEAD], sum[AHEAD];
 #pragma unroll
         for (int m = 0; m < AHEAD; ++m) {
-            const int kk = k + m < a.nseg ? k + m : a.nseg - 1, s = a.rev ? a.nseg - 1 - kk : kk;
-            own[m] = ends[(s * a.tiles * a.ntiles + w) * 256 + e];
-            sum[m] = a.steps[(s * a.tiles + tile) * 64 + 16 * blk + j];
+            own[m] = sum[m] = 0.f;
+            if (k + m < a.nseg) {
+                own[m] = ends[m * de];
+                sum[m] = sums[m * ds];
+            }
         }
 #pragma unroll
         for (int m = 0; m < AHEAD; ++m) {
             if (k + m >= a.nseg) break;
-            const int s = a.rev ? a.nseg - 1 - k - m : k + m;
-            ends[(s * a.tiles * a.ntiles + w) * 256 + e] = make_float4(run[0], run[1], run[2], run[3]);
-            const float o[4] = {own[m].x, own[m].y, own[m].z, own[m].w};
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                run[r] = sum[m] == GONE ? o[r] : fmaf(__builtin_amdgcn_exp2f(a2[r] * sum[m]), run[r], o[r]);
+            ends[m * de] = run;
+            run = sum[m] == GONE ? own[m] : fmaf(__builtin_amdgcn_exp2f(a2 * sum[m]), run, own[m]);
         }
+        ends += AHEAD * de;
+        sums += AHEAD * ds;
     }
 }
+// Segments so that `waves` wavefronts work, of whole chunks and at least 16 tokens; one for `few` tokens and less
+inline void sel_segments(int64_t B, int64_t T, int G, int D, int N, int64_t waves, int few, int64_t* L, int* nseg) {
+    const int64_t per = sel_tiles(B, G, D) * sel_ntiles(N), want = (waves + per - 1) / per;
+    int64_t len = T <= few ? T : (T + want - 1) / want;
+    if (len < 16) len = 16;
+    len = (len + SC - 1) / SC * SC;
+    *L = len;
+    *nseg = T > len ? (int)((T + len - 1) / len) : 1;
+}
+
 inline hipError_t sel_carry(const SelCarryArgs& a, const SelCarryArgs& b, int count, hipStream_t st) {
-    hipLaunchKernelGGL(sel_carry_kernel, dim3((unsigned)(a.tiles * a.ntiles), count), dim3(256), 0, st, a, b);
+    hipLaunchKernelGGL(sel_carry_kernel, dim3((unsigned)(a.tiles * a.ntiles * 4), count), dim3(256), 0, st, a, b);
     return hipGetLastError();
 }
 

@@ -148,16 +148,10 @@ void sel_go(const SelArgs& a, int nseg, hipStream_t st) {
     else hipLaunchKernelGGL((sel_kernel<BF16, HASZ, false, EMIT>), grid, dim3(64), 0, st, a);
 }
 
-// Segments: enough wavefronts for the SIMDs, of at least 64 tokens
-void sel_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) {
-    const int64_t waves = sel_tiles(B, G, D) * sel_ntiles(N), want = (4096 + waves - 1) / waves;
-    int64_t len = (T + want - 1) / want;
-    if (len < 64) len = 64;
-    if (len > T) len = T > 0 ? T : 1;
-    len = (len + SC - 1) / SC * SC;
-    *L = len;
-    *nseg = T > len ? (int)((T + len - 1) / len) : 1;
-}
+// 8192 wavefronts, twice what fits: shorter ones even out what padding leaves uneven (2 x 40001 x 520 with one sequence
+// padded: 714 us with 4096, 654 so). A token in turn costs some 0.3 us, two more launches some 10: 64 tokens of one sequence
+// took 25 us in one launch, 72 take 22 in three.
+void sel_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) { sel_segments(B, T, G, D, N, 8192, 48, L, nseg); }
 
 }  // namespace
 

@@ -365,16 +365,8 @@ struct SelSumD {
     }
 };
 
-// Segments: enough wavefronts for the SIMDs, of at least 64 tokens
-void sel_bwd_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) {
-    const int64_t waves = sel_tiles(B, G, D) * sel_ntiles(N), want = (4096 + waves - 1) / waves;
-    int64_t len = (T + want - 1) / want;
-    if (len < 64) len = 64;
-    if (len > T) len = T > 0 ? T : 1;
-    len = (len + SC - 1) / SC * SC;
-    *L = len;
-    *nseg = T > len ? (int)((T + len - 1) / len) : 1;
-}
+// The launches are the same for one segment: any is cut (64 tokens of one sequence: 107 -> 45 us)
+void sel_bwd_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) { sel_segments(B, T, G, D, N, 4096, 16, L, nseg); }
 
 // The workspace's parts, in floats
 struct SelBwdParts {

@@ -78,7 +78,7 @@ def test_selective_scan_checks(lib):
     assert call(ln=P(4098)) == 4
     assert call(ty=2) == 3 and call(ty=-1) == 3
     assert call(T=-1) == 2 and call(N=0) == 2 and call(G=0) == 2 and call(G=3) == 2
-    assert call(N=65) == 5 and call(Dn=1 << 21) == 5 and call(B=1 << 21) == 5 and call(B=1 << 62) == 5 and call(T=1 << 40) == 5
+    assert call(N=65) == 5 and call(Dn=1 << 21) == 5 and call(B=1 << 21) == 5 and call(s=strides(*[1 << 26] * 12)) == 5 and call(B=1 << 62) == 5 and call(T=1 << 40) == 5
     for k in range(12):
         bad = [300 * 128, 128] * 3 + [300 * 32, 32, 16] * 2
         bad[k] = -bad[k]
