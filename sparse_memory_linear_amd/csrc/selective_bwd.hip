@@ -62,10 +62,10 @@ __global__ __launch_bounds__(256, 4) void sel_ends_kernel(SelBwdArgs a) {
         spread(load_bc(C, w, 0, left, a.N), cq);
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
-            const bool on = i < left;
+            const bool on = w.in && i < left;  // (a lane without a channel adds nothing: its states go into the sums below times 0)
             float delta = step_of(value<BF16>(dr[i]) + bias, a.softplus), gy = value<BF16>(yr[i]);
             const float u = on ? delta * value<BF16>(xr[i]) : 0.f;
-            delta = on ? delta : 0.f;
+            delta = i < left ? delta : 0.f;
             if constexpr (HASZ) {
                 const float z = value<BF16>(zr[i]);
                 gy *= z * sigmoid(z);
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
             for (int i = 0; i < HC; ++i) {
                 const float delta = step_of(value<BF16>(dr[i]) + bias, a.softplus);
                 decay(h, decays(delta, a2, st >> i & 1u ? GONE : 0.f));
-                h = outer_add(bq[i], delta * value<BF16>(xr[i]), h);
+                h = outer_add(bq[i], w.in ? delta * value<BF16>(xr[i]) : 0.f, h);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -198,19 +198,23 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
             float bq[4], cq[4], delta[HC], gy[HC], u[HC];
             spread(bv[half], bq);
             spread(cv[half], cq);
-#pragma unroll
-            for (int i = 0; i < HC; ++i) {
+            // a token's step and output gradient (0 where it is not there; no gradient of a channel that is not there)
+            auto token = [&](int i) {
                 const int m = half * HC + i;
-                const bool there = ALL || m < left, on = w.in && there;
+                const bool there = ALL || m < left;
                 const float de = step_of(value<BF16>(dr[m]) + bias, a.softplus);
                 delta[i] = there ? de : 0.f;
-                u[i] = on ? de * value<BF16>(xr[m]) : 0.f;
                 float y = value<BF16>(yr[m]);
                 if constexpr (HASZ) {
                     const float z = value<BF16>(zr[m]);
                     y *= z * sigmoid(z);
                 }
-                gy[i] = on ? y : 0.f;
+                gy[i] = w.in && there ? y : 0.f;
+            };
+#pragma unroll
+            for (int i = 0; i < HC; ++i) {
+                token(i);
+                u[i] = w.in && (ALL || half * HC + i < left) ? delta[i] * value<BF16>(xr[half * HC + i]) : 0.f;
                 float* f = fan + i * 192 + 4 * w.j + w.q;
                 f[0] = delta[i];
                 f[64] = u[i];
@@ -304,9 +308,16 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
                 for (int i = 0; i < HC; ++i) {
                     if (i % a.ntiles != w.nt) continue;
                     float s[3] = {};
+                    const int at8 = half * HC + i;
+                    const uint32_t m8 = ALL ? at8 : upto(at8, left);  // (again, out of the cache: kept, they would not fit the registers)
+                    xr[at8] = X.get(w.vo, m8);
+                    dr[at8] = T.get(w.vo, m8);
+                    yr[at8] = Y.get(w.vo, m8);
+                    if constexpr (HASZ) zr[at8] = Z.get(w.vo, m8);
                     for (int k = 0; k < a.ntiles; ++k)
 #pragma unroll
                         for (int m = 0; m < 3; ++m) s[m] += all[k * SHARE + FAN + i * 192 + m * 64 + w.lane];
+                    token(i);
                     finish(i, s[0], s[1], s[2]);
                 }
                 __syncthreads();  // before the next sums

@@ -136,6 +136,21 @@ def test_packed_and_padded(T, K, d, dtype):
     check(run(p, "silu", start, lengths), want, tol)
 
 
+def test_a_sequence_ends_with_its_infinities():
+    p = make(1, 2, 60, 8, 4, F32, 3)
+    start = torch.zeros((1, 60), dtype=torch.uint8)
+    start[0, [20, 40]] = 1
+    want, tol = reference(p, "silu", start)
+    p["x"][0, :, 39] = float("inf")
+    p["dy"][0, :, 20] = float("nan")
+    got = run(p, "silu", start)
+    for k in ("y", "dx"):
+        e = (got[k].cpu().double() - want[k]).abs() <= tol[k] + 1e-37
+        assert e[:, :, :20].all() and e[:, :, 40:].all(), k
+    for k in ("S", "dS0"):
+        assert ((got[k].cpu().double() - want[k]).abs() <= tol[k] + 1e-37).all(), k
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("d", [16, 13])
 def test_strides(d, dtype):

@@ -270,6 +270,26 @@ def test_a_channel_keeps_its_infinities():
     assert ((got["dB"].cpu()[1].double() - want["dB"][1]).abs() <= tol["dB"][1] + 1e-37).all()
 
 
+@pytest.mark.parametrize("N", [16, 40])
+def test_a_sequence_ends_with_its_infinities(N):
+    """What is not finite in one packed sequence reaches neither the next one nor, backwards, the one before."""
+    T = 150
+    p = make(1, T, 70, 1, N, F32, 13)
+    start = torch.zeros((1, T), dtype=torch.uint8)
+    start[0, [40, 90]] = 1
+    p["S0"], p["dS"] = None, None
+    want, tol = reference(p, True, start)
+    for bad in ("nan", "inf"):
+        q = dict(p, x=p["x"].clone(), dy=p["dy"].clone())
+        q["x"][0, 50, 69] = float(bad)
+        q["dy"][0, 60, 3] = float(bad)
+        got = run(q, True, start)
+        for k in ("y", "dx", "ddt", "dz", "dB", "dC"):
+            e = (got[k].cpu().double().reshape(want[k].shape) - want[k]).abs() <= tol[k] + 1e-37
+            assert e[:, :40].all() and e[:, 90:].all(), (k, bad)
+        assert ((got["S"].cpu().double() - want["S"]).abs() <= tol["S"]).all()
+
+
 def test_extreme_steps():
     """Steps so large that nothing is left of a state, and so small that nothing happens."""
     p = make(1, 20, 64, 1, 16, F32, 9)
