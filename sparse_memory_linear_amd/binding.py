@@ -478,9 +478,17 @@ def _call(fn: str, d: torch.device, *args):
     if torch.cuda.current_device() != i:
         with torch.cuda.device(i):
             return _call(fn, d, *args)
-    rc = getattr(lib(), fn)(*args, torch.cuda.current_stream(i).cuda_stream)
+    rc = getattr(_lib or lib(), fn)(*args, _stream_of(i))
     if rc:
         _check(fn, rc)
+
+
+def _stream_of(i: int) -> int:
+    return torch.cuda.current_stream(i).cuda_stream
+
+
+# the handle itself, without a Stream object around it (2 of 11 us of a short call)
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 
 
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -770,32 +778,35 @@ def _sequences(start, lengths, B, T, like):
 
 
 def _conv_inputs(fn, x, w, bias, act, S0, S, start, lengths):
-    if act not in ACTS:
-        raise ValueError(f"unknown activation {act!r}")
-    if x.dim() == 4:
-        (B, H, T, d), lead = x.shape, x.shape[:2]
-        s = (x.stride(0), x.stride(1), x.stride(2))
-    elif x.dim() == 3:
-        (B, T, d), H, lead = x.shape, 1, x.shape[:1]
-        s = (x.stride(0), 0, x.stride(1))
+    shape, st = x.shape, x.stride()
+    if len(shape) == 3:
+        (B, T, d), H, s = shape, 1, _I3(st[0], 0, st[1])
+        per = (d,)
+    elif len(shape) == 4:
+        (B, H, T, d), s = shape, _I3(st[0], st[1], st[2])
+        per = (H, d)
     else:
         raise ValueError("x must be [B, T, d] or [B, H, T, d]")
-    _rows("x", x, x, x.shape)
-    if w.dim() != x.dim() - 1 or w.shape[:-1] != (*lead[1:], d) or w.dtype != torch.float32 \
-            or (bias is not None and (bias.shape != w.shape[:-1] or bias.dtype != torch.float32)):
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    if st[-1] != 1 and d > 1:
+        raise ValueError("the channels of x must be consecutive")
+    if w.dim() != len(shape) - 1 or w.shape[:-1] != per or w.dtype != torch.float32 \
+            or (bias is not None and (bias.shape != per or bias.dtype != torch.float32)):
         raise ValueError(f"shape or dtype mismatch in {fn}")
     K = w.shape[-1]
     if K < 2:
         raise ValueError("w must hold at least 2 taps")
-    dev = _gpu(w, bias)
-    state = (*lead, K - 1, d)
-    for name, t in (("S0", S0), ("S", S)):
-        if t is not None:
-            _out(t, w, state, x.dtype, name)
-    if x.get_device() != w.get_device():
+    dev = _gpu(w, bias, S0, S)
+    if x.get_device() != dev.index:
         raise ValueError("all tensors must be on the same GPU")
-    _sequences(start, lengths, B, T, w)
-    return dev, (B, H, T, d, K), state, _I3(*s)
+    state = (*shape[:-2], K - 1, d)
+    for name, t in (("S0", S0), ("S", S)):
+        if t is not None and (t.shape != state or t.dtype != x.dtype):
+            raise ValueError(f"{name} has the wrong shape or dtype")
+    if start is not None or lengths is not None:
+        _sequences(start, lengths, B, T, w)
+    return dev, (B, H, T, d, K), state, s
 
 
 def sdm_causal_conv_forward(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -872,32 +883,36 @@ def sdm_selective_scan_workspace_bytes(B: int, T: int, D: int, G: int, N: int) -
 def _selective_inputs(fn, x, dt, A, Bm, Cm, D, z, dt_bias, states, start, lengths, dy=None):
     if x.dim() != 3 or Bm.dim() not in (3, 4) or A.dim() != 2:
         raise ValueError("x must be [B, T, D], A [D, N], Bm and Cm [B, T, N] or [B, T, G, N]")
-    B, T, n = x.shape
-    G, N = (Bm.shape[2] if Bm.dim() == 4 else 1), A.shape[1]
-    groups = (B, T, G, N) if Bm.dim() == 4 else (B, T, N)
+    shape, dtype = x.shape, x.dtype
+    B, T, n = shape
+    N, four = A.shape[1], Bm.dim() == 4
+    G = Bm.shape[2] if four else 1
+    groups = (B, T, G, N) if four else (B, T, N)
+    dev = _gpu(A, D, dt_bias, *(t for _, t in states))
     s = []
-    for name, t in (("x", x), ("dt", dt), ("z", z)):
+    for name, t, shp in (("x", x, shape), ("dt", dt, shape), ("z", z, shape), ("Bm", Bm, groups), ("Cm", Cm, groups), ("dy", dy, shape)):
         if t is None:
-            s += (0, 0)
+            if name == "z":
+                s += (0, 0)
             continue
-        _rows(name, t, x, x.shape)
-        s += t.stride()[:2]
-    for name, t in (("Bm", Bm), ("Cm", Cm)):
-        _rows(name, t, x, groups)
-        s += t.stride()[:3] if Bm.dim() == 4 else (*t.stride()[:2], 0)
-    if dy is not None:
-        _rows("dy", dy, x, x.shape)
-        s += dy.stride()[:2]
+        st = t.stride()
+        if t.shape != shp or t.dtype != dtype:
+            raise ValueError(f"{name} has the wrong shape or dtype")
+        if st[-1] != 1 and shp[-1] > 1:
+            raise ValueError(f"the channels of {name} must be consecutive")
+        if t.get_device() != dev.index:
+            raise ValueError("all tensors must be on the same GPU")
+        s += st[:-1]
+        if shp is groups and not four:
+            s.append(0)
     if G < 1 or n % G or A.shape[0] != n or A.dtype != torch.float32 \
             or any(p is not None and (p.shape != (n,) or p.dtype != torch.float32) for p in (D, dt_bias)):
         raise ValueError(f"shape or dtype mismatch in {fn}")
-    dev = _gpu(A, D, dt_bias)
-    if x.get_device() != A.get_device():
-        raise ValueError("all tensors must be on the same GPU")
     for name, t in states:
-        if t is not None:
-            _out(t, A, (B, n, N), torch.float32, name)
-    _sequences(start, lengths, B, T, A)
+        if t is not None and (t.shape != (B, n, N) or t.dtype != torch.float32):
+            raise ValueError(f"{name} has the wrong shape or dtype")
+    if start is not None or lengths is not None:
+        _sequences(start, lengths, B, T, A)
     return dev, (B, T, n, G, N), (_I12 if dy is None else _I14)(*s)
 
 
