@@ -37,6 +37,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
     const float bias = a.bias ? a.bias[w.c] : 0.f, skip = EMIT && a.Dskip ? a.Dskip[w.c] : 0.f;
     const uint8_t* start = a.start ? a.start + w.b * a.T : nullptr;
     float steps = 0.f;
+    bool cut = false;  // a sequence began in the segment: nothing crosses it
     int par = 0;
     // A chunk's inputs: the first `left` of its tokens
     struct Chunk {
@@ -68,6 +69,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
     auto chunk = [&](auto whole, const Chunk& f, int64_t t, int64_t left) {
         constexpr bool ALL = decltype(whole)::value;
         const Rows<BF16> Y(py, EMIT ? a.D : 0, EMIT ? t : 0);
+        if constexpr (!EMIT) cut |= f.st != 0;
         float bq[2][4];
         spread(f.b[0], bq[0]);
         spread(f.b[1], bq[1]);
@@ -91,7 +93,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
             if (!ALL && i >= left) break;
             const float delta = step_of(value<BF16>(f.d[i]) + bias, a.softplus);
             const float gone = f.st >> i & 1u ? GONE : 0.f;
-            if constexpr (!EMIT) steps += delta + gone;
+            if constexpr (!EMIT) steps += delta;
             decay(h, decays(delta, a2, gone));
             h = outer_add(bq[i / 4][i % 4], delta * value<BF16>(f.x[i]), h);
             if constexpr (EMIT) {
@@ -137,7 +139,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
         if (a.S && w.seg == a.nseg - 1) store_dn(a, w, a.S + w.b * per, h);
     } else {
         store_tile(a.ends + (w.seg * waves + wave) * 1024, w.lane, h);
-        if (w.nt == 0) a.steps[(w.seg * a.tiles + w.tile) * 64 + w.lane] = steps;
+        if (w.nt == 0) a.steps[(w.seg * a.tiles + w.tile) * 64 + w.lane] = cut ? GONE : steps;
     }
 }
 

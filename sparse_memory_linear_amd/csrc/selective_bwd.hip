@@ -39,12 +39,13 @@ __global__ __launch_bounds__(256, 4) void sel_ends_kernel(SelBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) p[i] = 1.f;
     float steps = 0.f;
+    bool cut = false;  // a sequence began in the segment: nothing crosses it
     int64_t half = w.seg * (a.L / HC);
     for (int64_t t = w.t0; t < w.end; t += HC, ++half) {
         const int64_t left = w.end - t;
         if (half % 2 == 0) {
             store_tile(a.marks + (half / 2 * waves + wave) * 1024, w.lane, h);
-            if (w.nt == 0) a.msteps[(half / 2 * a.tiles + w.tile) * 64 + w.lane] = steps;
+            if (w.nt == 0) a.msteps[(half / 2 * a.tiles + w.tile) * 64 + w.lane] = cut ? GONE : steps;
         }
         const Rows<BF16> X(px, a.x_t, t), T(pd, a.dt_t, t), Z(pz, HASZ ? a.z_t : 0, HASZ ? t : 0), Y(py, a.dy_t, t);
         const Rows<BF16> B(pB, a.B_t, t), C(pC, a.C_t, t);
@@ -70,10 +71,11 @@ __global__ __launch_bounds__(256, 4) void sel_ends_kernel(SelBwdArgs a) {
                 const float z = value<BF16>(zr[i]);
                 gy *= z * sigmoid(z);
             }
-            gy = on ? gy : 0.f;
             const float gone = st >> i & 1u ? GONE : 0.f;
-            steps += delta + gone;
-            const f32x16 d = decays(delta, a2, gone), cg = outer_add(cq[i], gy, zeros16());
+            cut |= gone == GONE;
+            gy = on && !cut ? gy : 0.f;
+            steps += delta;
+            const f32x16 d = decays(delta, a2, gone), cg = outer_add(cut ? 0.f : cq[i], gy, zeros16());
             decay(h, d);
             h = outer_add(bq[i], u, h);
             decay(p, d);
@@ -84,7 +86,7 @@ __global__ __launch_bounds__(256, 4) void sel_ends_kernel(SelBwdArgs a) {
     const int64_t at = (w.seg * waves + wave) * 1024;
     store_tile(a.ends + at, w.lane, h);
     store_tile(a.gends + at, w.lane, g);
-    if (w.nt == 0) a.steps[(w.seg * a.tiles + w.tile) * 64 + w.lane] = steps;
+    if (w.nt == 0) a.steps[(w.seg * a.tiles + w.tile) * 64 + w.lane] = cut ? GONE : steps;
 }
 
 // Lane j of a row of 16 lanes gets the row's sum of v[j / 4]
@@ -216,7 +218,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
                 token(i);
                 u[i] = w.in && (ALL || half * HC + i < left) ? delta[i] * value<BF16>(xr[half * HC + i]) : 0.f;
                 float* f = fan + i * 192 + 4 * w.j + w.q;
-                f[0] = delta[i];
+                f[0] = st >> (half * HC + i) & 1u ? 0.f : delta[i];  // (behind a begin there is no state for dA either)
                 f[64] = u[i];
                 f[128] = gy[i];
             }

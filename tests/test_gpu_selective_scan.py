@@ -290,6 +290,28 @@ def test_a_sequence_ends_with_its_infinities(N):
         assert ((got["S"].cpu().double() - want["S"]).abs() <= tol["S"]).all()
 
 
+@pytest.mark.parametrize("name", ["x", "dt", "B", "C", "z", "dy"])
+@pytest.mark.parametrize("N", [16, 40])
+def test_a_sequence_ends_with_its_infinities_at_its_ends(N, name):
+    """The same for its first and last token and those next to them, whichever tensor holds them."""
+    T = 150
+    p = make(1, T, 70, 1, N, F32, 14)
+    start = torch.zeros((1, T), dtype=torch.uint8)
+    start[0, [40, 90]] = 1
+    want, tol = reference(p, True, start)
+    for bad in ("nan", "inf", "-inf"):
+        for t in (40, 41, 47, 81, 88, 89):
+            q = dict(p)
+            q[name] = p[name].clone()
+            q[name][0, t, ..., 1] = float(bad)
+            got = run(q, True, start)
+            for k in ("y", "dx", "ddt", "dz", "dB", "dC"):
+                e = (got[k].cpu().double().reshape(want[k].shape) - want[k]).abs() <= tol[k] + 1e-37
+                assert e[:, :40].all() and e[:, 90:].all(), (k, bad, t)
+            for k in ("S", "dS0"):
+                assert ((got[k].cpu().double() - want[k]).abs() <= tol[k]).all(), (k, bad, t)
+
+
 def test_extreme_steps():
     """Steps so large that nothing is left of a state, and so small that nothing happens."""
     p = make(1, 20, 64, 1, 16, F32, 9)
