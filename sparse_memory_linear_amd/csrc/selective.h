@@ -185,11 +185,10 @@ __device__ __forceinline__ void store_tile(float* p, int lane, const f32x16& v) 
         reinterpret_cast<float4*>(p)[64 * k + lane] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
 }
 
-// exp(delta A): a2 = A log2(e). At a sequence's first token `gone` is minus infinity (else 0), and the decay 0,
-// whatever the step is.
-__device__ __forceinline__ f32x16 decays(float delta, const f32x16& a2, float gone) {
-    float d[4];
-    spread(gone == GONE ? 0.f : delta, d);
+// exp(delta A) of the lane's 4 channels: a2 = A log2(e). At a sequence's first token delta is 0 and `gone` minus
+// infinity (else 0): the decay is 0.
+__device__ __forceinline__ f32x16 decays(const float4& delta, const f32x16& a2, float gone) {
+    const float d[4] = {delta.x, delta.y, delta.z, delta.w};
     f32x16 v;
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __builtin_amdgcn_exp2f(fmaf(d[i / 4], a2[i], gone));

@@ -13,14 +13,17 @@
 namespace sdm {
 namespace {
 
+constexpr int SEL_SHARE = SC * 16 + SC * 16 / 4;  // LDS of a wavefront in 16 bytes: a chunk's steps and its C
+
 // EMIT: the pass that writes y and the last state; else the first pass. MULTI: several tiles of states, one
 // a wavefront, whose shares of y are added in their order.
 template <bool BF16, bool HASZ, bool MULTI, bool EMIT>
 __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
-    constexpr int NW = MULTI ? 4 : 1;
-    __shared__ float cl[NW][SC][16];
-    __shared__ float yl[MULTI && EMIT ? 2 : 1][NW][MULTI && EMIT ? SC : 1][64];
+    extern __shared__ float4 lds4[];  // a wavefront's share, then the shares of y: [2][ntiles][SC][64]
     const SelAt w = sel_at<BF16>(a);
+    float4(*dl)[16] = reinterpret_cast<float4(*)[16]>(lds4 + w.nt * SEL_SHARE);  // a chunk's steps: a lane's 4 channels side by side
+    float(*cl)[16] = reinterpret_cast<float(*)[16]>(dl + SC);
+    float(*yl)[SC][64] = reinterpret_cast<float(*)[SC][64]>(lds4 + a.ntiles * SEL_SHARE);
     const f32x16 a2 = load_dn(a, w, a.A, 1.44269504f);
     const int64_t wave = w.tile * a.ntiles + w.nt, waves = a.tiles * a.ntiles, per = (int64_t)a.D * a.N;
     f32x16 h = zeros16();
@@ -74,11 +77,20 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
         spread(f.b[0], bq[0]);
         spread(f.b[1], bq[1]);
         if constexpr (EMIT) {
-            cl[w.nt][w.q][w.j] = f.c[0];
-            cl[w.nt][4 + w.q][w.j] = f.c[1];
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            cl[w.q][w.j] = f.c[0];
+            cl[4 + w.q][w.j] = f.c[1];
         }
+        float u[SC];
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            if (!ALL && i >= left) break;
+            const float delta = step_of(value<BF16>(f.d[i]) + bias, a.softplus);
+            u[i] = delta * value<BF16>(f.x[i]);
+            if constexpr (!EMIT) steps += delta;
+            reinterpret_cast<float*>(dl[i])[4 * w.j + w.q] = f.st >> i & 1u ? 0.f : delta;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
         // y's last steps: D x and the gate (a lane without a channel works on the last one's rows, and stores nothing)
         auto finish = [&](int i, float y) {
             float o = fmaf(skip, value<BF16>(f.x[i]), y);
@@ -91,19 +103,16 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
             if (!ALL && i >= left) break;
-            const float delta = step_of(value<BF16>(f.d[i]) + bias, a.softplus);
-            const float gone = f.st >> i & 1u ? GONE : 0.f;
-            if constexpr (!EMIT) steps += delta;
-            decay(h, decays(delta, a2, gone));
-            h = outer_add(bq[i / 4][i % 4], delta * value<BF16>(f.x[i]), h);
+            decay(h, decays(dl[i][w.j], a2, f.st >> i & 1u ? GONE : 0.f));
+            h = outer_add(bq[i / 4][i % 4], u[i], h);
             if constexpr (EMIT) {
-                const float4 c = *reinterpret_cast<const float4*>(&cl[w.nt][i][4 * w.q]);
+                const float4 c = *reinterpret_cast<const float4*>(&cl[i][4 * w.q]);
                 float p[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     p[k] = fmaf(c.w, h[4 * k + 3], fmaf(c.z, h[4 * k + 2], fmaf(c.y, h[4 * k + 1], c.x * h[4 * k])));
                 const float y = gather_sum(p);
-                if constexpr (MULTI) yl[par][w.nt][i][w.lane] = y;
+                if constexpr (MULTI) yl[par * a.ntiles + w.nt][i][w.lane] = y;
                 else finish(i, y);
             }
         }
@@ -113,7 +122,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
             for (int i = 0; i < SC; ++i) {
                 if (i % a.ntiles != w.nt || (!ALL && i >= left)) continue;
                 float y = 0.f;
-                for (int k = 0; k < a.ntiles; ++k) y += yl[par][k][i][w.lane];
+                for (int k = 0; k < a.ntiles; ++k) y += yl[par * a.ntiles + k][i][w.lane];
                 finish(i, y);
             }
             par ^= 1;
@@ -146,8 +155,9 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
 template <bool BF16, bool HASZ, bool EMIT>
 void sel_go(const SelArgs& a, int nseg, hipStream_t st) {
     const dim3 grid((unsigned)a.tiles, (unsigned)nseg);
-    if (a.ntiles > 1) hipLaunchKernelGGL((sel_kernel<BF16, HASZ, true, EMIT>), grid, dim3(64 * a.ntiles), 0, st, a);
-    else hipLaunchKernelGGL((sel_kernel<BF16, HASZ, false, EMIT>), grid, dim3(64), 0, st, a);
+    const int lds = SEL_SHARE * 16 * a.ntiles;
+    if (a.ntiles > 1) hipLaunchKernelGGL((sel_kernel<BF16, HASZ, true, EMIT>), grid, dim3(64 * a.ntiles), lds + (EMIT ? 2 * a.ntiles * SC * 256 : 0), st, a);
+    else hipLaunchKernelGGL((sel_kernel<BF16, HASZ, false, EMIT>), grid, dim3(64), lds, st, a);
 }
 
 // 8192 wavefronts, twice what fits: shorter ones even out what padding leaves uneven (2 x 40001 x 520 with one sequence

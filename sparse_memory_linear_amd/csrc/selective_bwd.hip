@@ -24,9 +24,11 @@ constexpr int HC = SC / 2;
 
 template <bool BF16, bool HASZ>
 __global__ __launch_bounds__(256, 4) void sel_ends_kernel(SelBwdArgs a) {
+    __shared__ float4 fan[4][HC][16];  // half a chunk's steps: a lane's 4 channels side by side
     const SelAt w = sel_at<BF16>(a);
     const f32x16 a2 = load_dn(a, w, a.A, 1.44269504f);
     const int64_t wave = w.tile * a.ntiles + w.nt, waves = a.tiles * a.ntiles;
+    float4(*dl)[16] = fan[w.nt];
     const char* px = row<BF16>(a.x, w.b * a.x_b);
     const char* pd = row<BF16>(a.dt, w.b * a.dt_b);
     const char* pz = HASZ ? row<BF16>(a.z, w.b * a.z_b) : nullptr;
@@ -61,26 +63,35 @@ __global__ __launch_bounds__(256, 4) void sel_ends_kernel(SelBwdArgs a) {
         float bq[4], cq[4];
         spread(load_bc(B, w, 0, left, a.N), bq);
         spread(load_bc(C, w, 0, left, a.N), cq);
+        float u[HC], gy[HC];
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
             const bool on = w.in && i < left;  // (a lane without a channel adds nothing: its states go into the sums below times 0)
-            float delta = step_of(value<BF16>(dr[i]) + bias, a.softplus), gy = value<BF16>(yr[i]);
-            const float u = on ? delta * value<BF16>(xr[i]) : 0.f;
+            float delta = step_of(value<BF16>(dr[i]) + bias, a.softplus);
+            u[i] = on ? delta * value<BF16>(xr[i]) : 0.f;
             delta = i < left ? delta : 0.f;
+            steps += delta;
+            gy[i] = value<BF16>(yr[i]);
             if constexpr (HASZ) {
                 const float z = value<BF16>(zr[i]);
-                gy *= z * sigmoid(z);
+                gy[i] *= z * sigmoid(z);
             }
-            const float gone = st >> i & 1u ? GONE : 0.f;
-            cut |= gone == GONE;
-            gy = on && !cut ? gy : 0.f;
-            steps += delta;
-            const f32x16 d = decays(delta, a2, gone), cg = outer_add(cut ? 0.f : cq[i], gy, zeros16());
+            cut |= (st >> i & 1u) != 0;
+            gy[i] = on && !cut ? gy[i] : 0.f;
+            cq[i] = cut ? 0.f : cq[i];
+            reinterpret_cast<float*>(dl[i])[4 * w.j + w.q] = st >> i & 1u ? 0.f : delta;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+            const f32x16 d = decays(dl[i][w.j], a2, st >> i & 1u ? GONE : 0.f), cg = outer_add(cq[i], gy[i], zeros16());
             decay(h, d);
-            h = outer_add(bq[i], u, h);
+            h = outer_add(bq[i], u[i], h);
             decay(p, d);
 #pragma unroll
             for (int k = 0; k < 16; ++k) g[k] = fmaf(p[k], cg[k], g[k]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     const int64_t at = (w.seg * waves + wave) * 1024;
@@ -108,6 +119,7 @@ template <bool BF16, bool HASZ, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdArgs a) {
     extern __shared__ float4 lds4[];
     const SelAt w = sel_at<BF16>(a);
+    const int NT = MULTI ? a.ntiles : 1;
     float* mine = reinterpret_cast<float*>(lds4) + w.nt * SHARE;
     float4* kept = reinterpret_cast<float4*>(mine);
     float(*bl)[16] = reinterpret_cast<float(*)[16]>(mine + KEPT);
@@ -124,7 +136,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
     const char* pdx = row<BF16>(a.dx, w.b * a.T * a.D);
     const char* pdd = row<BF16>(a.ddt, w.b * a.T * a.D);
     const char* pdz = HASZ ? row<BF16>(a.dz, w.b * a.T * a.D) : nullptr;
-    const char* pbc = row<false>(a.part_bc, (((w.c0 / 64) * a.B + w.b) * a.G + w.g) * a.T * a.ntiles * 32 + w.nt * 32);
+    const char* pbc = row<false>(a.part_bc, (((w.c0 / 64) * a.B + w.b) * a.G + w.g) * a.T * NT * 32 + w.nt * 32);
     // the lane's element of a token's 16 sums for dB and 16 for dC
     const uint32_t vbc = (w.j & 3) < 2 ? 4u * ((w.j & 1) * 16 + 4 * w.q + (w.j >> 2)) : OOB;
     const float bias = a.bias ? a.bias[w.c] : 0.f, skip = a.Dskip ? a.Dskip[w.c] : 0.f;
@@ -186,7 +198,10 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
 #pragma unroll
             for (int i = 0; i < HC; ++i) {
                 const float delta = step_of(value<BF16>(dr[i]) + bias, a.softplus);
-                decay(h, decays(delta, a2, st >> i & 1u ? GONE : 0.f));
+                const bool begins = st >> i & 1u;
+                float d4[4];
+                spread(begins ? 0.f : delta, d4);
+                decay(h, decays(make_float4(d4[0], d4[1], d4[2], d4[3]), a2, begins ? GONE : 0.f));
                 h = outer_add(bq[i], w.in ? delta * value<BF16>(xr[i]) : 0.f, h);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -231,11 +246,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
             f32x16 dec[HC];  // a_t
 #pragma unroll
             for (int i = 0; i < HC; ++i) {
-                float ds[4];
-                fanned(i, 0, ds);
-                const float gone = st >> (half * HC + i) & 1u ? GONE : 0.f;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) dec[i][k] = __builtin_amdgcn_exp2f(fmaf(ds[k / 4], a2[k], gone));
+                dec[i] = decays(*reinterpret_cast<const float4*>(fan + i * 192 + 4 * w.j), a2, st >> (half * HC + i) & 1u ? GONE : 0.f);
                 decay(h, dec[i]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -292,7 +303,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
                 }
                 const float qa = gather_sum(pa), qb = gather_sum(pb), qc = HASZ ? gather_sum(pc) : 0.f;
                 const float rb = row_sums(sb, w.j), rc = row_sums(sc, w.j);
-                Rows<false>(pbc, a.ntiles * 32, t).put(ALL || m < left ? vbc : OOB, m, w.j & 1 ? rc : rb);
+                Rows<false>(pbc, NT * 32, t).put(ALL || m < left ? vbc : OOB, m, w.j & 1 ? rc : rb);
                 if constexpr (MULTI) {
                     float* s = fan + i * 192 + w.lane;  // token i's values there have been read
                     s[0] = qa;
