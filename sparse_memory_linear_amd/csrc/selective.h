@@ -264,10 +264,10 @@ __global__ __launch_bounds__(256) void sel_carry_kernel(SelCarryArgs a0, SelCarr
         sums += AHEAD * ds;
     }
 }
-// Segments so that `waves` wavefronts work, of whole chunks and at least 16 tokens; one for `few` tokens and less
-inline void sel_segments(int64_t B, int64_t T, int G, int D, int N, int64_t waves, int few, int64_t* L, int* nseg) {
+// Segments so that `waves` wavefronts work, of whole chunks and at least 16 tokens
+inline void sel_segments(int64_t B, int64_t T, int G, int D, int N, int64_t waves, int64_t* L, int* nseg) {
     const int64_t per = sel_tiles(B, G, D) * sel_ntiles(N), want = (waves + per - 1) / per;
-    int64_t len = T <= few ? T : (T + want - 1) / want;
+    int64_t len = (T + want - 1) / want;
     if (len < 16) len = 16;
     len = (len + SC - 1) / SC * SC;
     *L = len;

@@ -6,6 +6,7 @@
 // With few streams of channels the tokens are cut into segments: a first pass leaves what each adds to a state
 // of zeros and its sum of steps (a segment's decay is exp(A times that)), a carry runs through them, and the
 // last pass starts every segment where it belongs. See selective.h for a wavefront's tile.
+#include <cmath>
 #include <type_traits>
 
 #include "selective.h"
@@ -160,10 +161,20 @@ void sel_go(const SelArgs& a, int nseg, hipStream_t st) {
     else hipLaunchKernelGGL((sel_kernel<BF16, HASZ, false, EMIT>), grid, dim3(64), lds, st, a);
 }
 
-// 8192 wavefronts, twice what fits: shorter ones even out what padding leaves uneven (2 x 40001 x 520 with one sequence
-// padded: 714 us with 4096, 654 so). A token in turn costs some 0.3 us, two more launches some 10: 64 tokens of one sequence
-// took 25 us in one launch, 72 take 22 in three.
-void sel_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) { sel_segments(B, T, G, D, N, 8192, 48, L, nseg); }
+// One segment where that takes no longer, by estimates in microseconds. A token after the other: 0.32 of one wavefront a
+// SIMD, 0.45 where every SIMD has one, 0.19 more for each further one, and 0.15 or 0.06 where wavefronts meet in a workgroup. Cut:
+// two more launches, and both passes' vector instructions, 4.1e-4 a token and wavefront. (One segment / cut, 16 states, 2048
+// channels; 1 sequence of 32 tokens: 15.7 / 19.2, of 64: 26 / 19.6; 8 of 64: 26.6 / 27.1; 32 of 160: 73 / 93, of 1024:
+// 458 / 407; 48 of 1024: 561 / 597; 100 of 1024: 948 / 1171. Near the crossing the choice costs up to 6%.)
+// Cut into 8192 wavefronts, twice what fits: shorter ones even out what padding leaves uneven (2 x 40001 x 520 with one
+// sequence padded: 714 with 4096, 654 so).
+void sel_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) {
+    const double per = (double)(sel_tiles(B, G, D) * sel_ntiles(N)), full = per / 1024.0;
+    const bool multi = sel_ntiles(N) > 1;
+    const double token = full <= 1.0 ? 0.32 + 0.13 * full + (multi ? 0.15 : 0.0) : 0.18 + 0.19 * ceil(full) + (multi ? 0.06 : 0.0);
+    const bool cut = 4.0 + token * (double)T > 18.0 + 6.0 * full + 4.1e-4 * per * (double)T;
+    sel_segments(B, T, G, D, N, cut ? 8192 : 1, L, nseg);
+}
 
 }  // namespace
 

@@ -389,8 +389,8 @@ struct SelSumD {
     }
 };
 
-// The launches are the same for one segment: any is cut (64 tokens of one sequence: 107 -> 45 us)
-void sel_bwd_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) { sel_segments(B, T, G, D, N, 4096, 16, L, nseg); }
+// The launches are the same for one segment: any is cut (64 tokens of one sequence: 107 -> 45 us), into twice what fits
+void sel_bwd_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) { sel_segments(B, T, G, D, N, 4096, L, nseg); }
 
 // The workspace's parts, in floats
 struct SelBwdParts {
