@@ -4,8 +4,10 @@
 // n. The tile lies in the registers as v_mfma_f32_16x16x1 (4 blocks) gives it: h[4 blk + r] of lane 16 q + j is
 // state 4 q + r of channel 16 blk + j. That instruction adds a token's u (x) B to the decayed tile, from B_n
 // in lane j = n and u in the channels' own lanes, in fp32 and beside the vector units, which bound these
-// kernels: a state costs a product and an exponential (four issue slots) for the decay and one product to
-// apply it. Sums over n are over r in a lane and over q by two permlane swaps, which put channel c's sum in lane c.
+// kernels: a state costs a product and an exponential (together three issue slots) for the decay, one product to
+// apply it and one for y; what a channel has once a token costs a sixteenth of that. The steps reach the lanes of their
+// channels' states through LDS (by permutes: 7% more time). Sums over n are over r in a lane and over q by two permlane
+// swaps, which put channel c's sum in lane c.
 #pragma once
 #include "sdm_buffer.h"
 #include "sdm_internal.h"

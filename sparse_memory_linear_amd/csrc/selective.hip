@@ -6,6 +6,10 @@
 // With few streams of channels the tokens are cut into segments: a first pass leaves what each adds to a state
 // of zeros and its sum of steps (a segment's decay is exp(A times that)), a carry runs through them, and the
 // last pass starts every segment where it belongs. See selective.h for a wavefront's tile.
+//
+// Bound by vector instructions (103 a token and tile in the last pass, 74 in the first; issued in 96% of the cycles):
+// 4 x 8192 x 2048 with 16 states in bf16, 185 us first pass + 18 carry + 250 last pass, for 105 us of HBM at a copy's rate
+// and 137 of one pass's exponentials and products alone; one token of 256 sequences 17.1 us (71 MB, 4.2 TB/s): HBM.
 #include <cmath>
 #include <type_traits>
 

@@ -11,8 +11,13 @@
 // leaves one every 8 tokens (with the sum of steps since the segment's start, by whose decay the segment's
 // own starting state is added), and sums what a segment passes to the one before it. Carries run through the
 // segments both ways. The last pass walks the chunks backwards, half a chunk (4 tokens) at a time: it forms
-// the 4 states again, keeping each token's decay and decayed state in registers, and then walks them back.
+// the 4 states again, keeping each token's decay in registers and its decayed state in LDS, and then walks them back.
 // Sums over channels leave a row a tile, added by a last pass.
+//
+// Bound by vector instructions (335 a token and tile in the last pass, 123 in the first; issued in 84 and 80% of the cycles,
+// at 2 and 4 wavefronts a SIMD): 4 x 4096 x 2048 with 16 states in bf16, first pass 168 us, carries 15, last pass 410, sums
+// 28, for 92 us of HBM at a copy's rate. (A state every 4 tokens instead would spare forming 4 states of 8 twice, a tenth
+// of the last pass, but the first one has no room for 268 MB more: it moves 606 MB in its 168 us.)
 #include <type_traits>
 
 #include "selective.h"
