@@ -9,7 +9,7 @@
 //
 // Bound by vector instructions (103 a token and tile in the last pass, 74 in the first; issued in 96% of the cycles):
 // 4 x 8192 x 2048 with 16 states in bf16, 185 us first pass + 18 carry + 250 last pass, for 105 us of HBM at a copy's rate
-// and 137 of one pass's exponentials and products alone; one token of 256 sequences 17.1 us (71 MB, 4.2 TB/s): HBM.
+// and 137 of one pass's exponentials and products alone; one token of 256 sequences 15.4 us (71 MB, 4.6 TB/s): HBM.
 #include <cmath>
 #include <type_traits>
 
@@ -21,9 +21,11 @@ namespace {
 constexpr int SEL_SHARE = SC * 16 + SC * 16 / 4;  // LDS of a wavefront in 16 bytes: a chunk's steps and its C
 
 // EMIT: the pass that writes y and the last state; else the first pass. MULTI: several tiles of states, one
-// a wavefront, whose shares of y are added in their order.
-template <bool BF16, bool HASZ, bool MULTI, bool EMIT>
-__global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
+// a wavefront, whose shares of y are added in their order. ONE: single tokens, in 60 registers in place of 116, so
+// that twice the wavefronts have their states' loads in flight (256 sequences of 2048 x 16 17.3 -> 15.4 us, 512: 29.5 -> 25.4).
+template <bool BF16, bool HASZ, bool MULTI, bool EMIT, bool ONE>
+__global__ __launch_bounds__(MULTI ? 256 : 64, ONE ? 6 : 3) void sel_kernel(SelArgs a) {
+    constexpr int TOK = ONE ? 1 : SC, QS = (TOK + 3) / 4;  // tokens at once, and their quarters of a wavefront
     extern __shared__ float4 lds4[];  // a wavefront's share, then the shares of y: [2][ntiles][SC][64]
     const SelAt w = sel_at<BF16>(a);
     float4(*dl)[16] = reinterpret_cast<float4(*)[16]>(lds4 + w.nt * SEL_SHARE);  // a chunk's steps: a lane's 4 channels side by side
@@ -49,8 +51,8 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
     int par = 0;
     // A chunk's inputs: the first `left` of its tokens
     struct Chunk {
-        uint32_t x[SC], d[SC], z[SC];
-        float b[2], c[2];
+        uint32_t x[TOK], d[TOK], z[TOK];
+        float b[QS], c[QS];
         uint32_t st;
     };
     auto fetch = [&](auto whole, int64_t t, int64_t left) {
@@ -59,14 +61,14 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
         const Rows<BF16> B(pB, a.B_t, t), C(pC, EMIT ? a.C_t : 0, EMIT ? t : 0);
         Chunk f;
 #pragma unroll
-        for (int i = 0; i < SC; ++i)
+        for (int i = 0; i < TOK; ++i)
             if (ALL || i < left) {
                 f.x[i] = X.get(w.vo, i);
                 f.d[i] = T.get(w.vo, i);
                 if constexpr (HASZ && EMIT) f.z[i] = Z.get(w.vo, i);
             }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < QS; ++k) {
             f.b[k] = load_bc(B, w, k, left, a.N);
             if constexpr (EMIT) f.c[k] = load_bc(C, w, k, left, a.N);
         }
@@ -78,16 +80,15 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
         constexpr bool ALL = decltype(whole)::value;
         const Rows<BF16> Y(py, EMIT ? a.D : 0, EMIT ? t : 0);
         if constexpr (!EMIT) cut |= f.st != 0;
-        float bq[2][4];
-        spread(f.b[0], bq[0]);
-        spread(f.b[1], bq[1]);
-        if constexpr (EMIT) {
-            cl[w.q][w.j] = f.c[0];
-            cl[4 + w.q][w.j] = f.c[1];
-        }
-        float u[SC];
+        float bq[QS][4];
 #pragma unroll
-        for (int i = 0; i < SC; ++i) {
+        for (int k = 0; k < QS; ++k) {
+            spread(f.b[k], bq[k]);
+            if constexpr (EMIT) cl[4 * k + w.q][w.j] = f.c[k];
+        }
+        float u[TOK];
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) {
             if (!ALL && i >= left) break;
             const float delta = step_of(value<BF16>(f.d[i]) + bias, a.softplus);
             u[i] = delta * value<BF16>(f.x[i]);
@@ -106,7 +107,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
             Y.put(w.vput, i, o);
         };
 #pragma unroll
-        for (int i = 0; i < SC; ++i) {
+        for (int i = 0; i < TOK; ++i) {
             if (!ALL && i >= left) break;
             decay(h, decays(dl[i][w.j], a2, f.st >> i & 1u ? GONE : 0.f));
             h = outer_add(bq[i / 4][i % 4], u[i], h);
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
         if constexpr (MULTI && EMIT) {
             __syncthreads();  // (the other half of yl: its readers have passed the barrier before)
 #pragma unroll
-            for (int i = 0; i < SC; ++i) {
+            for (int i = 0; i < TOK; ++i) {
                 if (i % a.ntiles != w.nt || (!ALL && i >= left)) continue;
                 float y = 0.f;
                 for (int k = 0; k < a.ntiles; ++k) y += yl[par * a.ntiles + k][i][w.lane];
@@ -134,9 +135,9 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
         }
     };
     int64_t t = w.t0;
-    if constexpr (EMIT) {
+    if constexpr (EMIT && !ONE) {
         for (; t + SC <= w.end; t += SC) chunk(std::true_type{}, fetch(std::true_type{}, t, SC), t, SC);
-    } else if (t + SC <= w.end) {  // a chunk ahead (203 -> 195 us; with z it would take a wavefront's room a SIMD: 272 -> 276)
+    } else if (!EMIT && t + SC <= w.end) {  // a chunk ahead (203 -> 195 us; with z it would take a wavefront's room a SIMD: 272 -> 276)
         Chunk f = fetch(std::true_type{}, t, SC);
         for (; t + 2 * SC <= w.end; t += SC) {
             const Chunk next = fetch(std::true_type{}, t + SC, SC);
@@ -157,12 +158,17 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 3) void sel_kernel(SelArgs a) {
     }
 }
 
-template <bool BF16, bool HASZ, bool EMIT>
+template <bool BF16, bool HASZ, bool EMIT, bool ONE>
 void sel_go(const SelArgs& a, int nseg, hipStream_t st) {
     const dim3 grid((unsigned)a.tiles, (unsigned)nseg);
     const int lds = SEL_SHARE * 16 * a.ntiles;
-    if (a.ntiles > 1) hipLaunchKernelGGL((sel_kernel<BF16, HASZ, true, EMIT>), grid, dim3(64 * a.ntiles), lds + (EMIT ? 2 * a.ntiles * SC * 256 : 0), st, a);
-    else hipLaunchKernelGGL((sel_kernel<BF16, HASZ, false, EMIT>), grid, dim3(64), lds, st, a);
+    if (a.ntiles > 1) hipLaunchKernelGGL((sel_kernel<BF16, HASZ, true, EMIT, ONE>), grid, dim3(64 * a.ntiles), lds + (EMIT ? 2 * a.ntiles * SC * 256 : 0), st, a);
+    else hipLaunchKernelGGL((sel_kernel<BF16, HASZ, false, EMIT, ONE>), grid, dim3(64), lds, st, a);
+}
+template <bool ONE>
+void sel_emit(const SelArgs& a, hipStream_t st) {
+    if (a.z) a.bf16 ? sel_go<true, true, true, ONE>(a, a.nseg, st) : sel_go<false, true, true, ONE>(a, a.nseg, st);
+    else a.bf16 ? sel_go<true, false, true, ONE>(a, a.nseg, st) : sel_go<false, false, true, ONE>(a, a.nseg, st);
 }
 
 // One segment where that takes no longer, by estimates in microseconds. A token after the other: 0.32 of one wavefront a
@@ -197,7 +203,7 @@ hipError_t launch_selective(SelArgs a, hipStream_t st) {
     a.ends = static_cast<float*>(a.workspace);
     a.steps = a.ends + a.nseg * a.tiles * a.ntiles * 1024;
     if (a.nseg > 1) {
-        a.bf16 ? sel_go<true, false, false>(a, a.nseg - 1, st) : sel_go<false, false, false>(a, a.nseg - 1, st);
+        a.bf16 ? sel_go<true, false, false, false>(a, a.nseg - 1, st) : sel_go<false, false, false, false>(a, a.nseg - 1, st);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         SelCarryArgs c{};
@@ -205,8 +211,7 @@ hipError_t launch_selective(SelArgs a, hipStream_t st) {
         c.tiles = a.tiles; c.nseg = a.nseg; c.ntiles = a.ntiles; c.ctiles = a.ctiles; c.G = a.G; c.D = a.D; c.N = a.N;
         if ((e = sel_carry(c, c, 1, st)) != hipSuccess) return e;
     }
-    if (a.z) a.bf16 ? sel_go<true, true, true>(a, a.nseg, st) : sel_go<false, true, true>(a, a.nseg, st);
-    else a.bf16 ? sel_go<true, false, true>(a, a.nseg, st) : sel_go<false, false, true>(a, a.nseg, st);
+    a.T == 1 ? sel_emit<true>(a, st) : sel_emit<false>(a, st);
     return hipGetLastError();
 }
 

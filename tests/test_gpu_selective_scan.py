@@ -141,7 +141,7 @@ def test_steps_as_given():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("T,D,N", [(1, 64, 16), (6, 10, 3), (43, 70, 16), (43, 64, 40), (150, 70, 16), (203, 64, 30)])
+@pytest.mark.parametrize("T,D,N", [(1, 64, 16), (1, 70, 40), (6, 10, 3), (43, 70, 16), (43, 64, 40), (150, 70, 16), (203, 64, 30)])
 def test_packed_and_padded(T, D, N, dtype):
     B = 5
     g = torch.Generator().manual_seed(T)
