@@ -9,6 +9,8 @@
 // channels' states through LDS (by permutes: 7% more time). Sums over n are over r in a lane and over q by two permlane
 // swaps, which put channel c's sum in lane c.
 #pragma once
+#include <cmath>
+
 #include "sdm_buffer.h"
 #include "sdm_internal.h"
 #include "sdm_rows.h"
@@ -266,10 +268,14 @@ __global__ __launch_bounds__(256) void sel_carry_kernel(SelCarryArgs a0, SelCarr
         sums += AHEAD * ds;
     }
 }
-// Segments so that `waves` wavefronts work, of whole chunks and at least 16 tokens
+// Segments so that `waves` wavefronts work, of whole chunks and at least 16 tokens; with few channels as long as evens out the
+// chains of a pass (some 0.3 us a token) and of the carry (0.06 a segment): the root of T / 10 tokens (one sequence of
+// 131072 x 64: 810 us by segments of 16, 215 of 120; 8192 x 64: 66 and 51 of 32; of T / 4: no faster, backwards up to 18% slower)
 inline void sel_segments(int64_t B, int64_t T, int G, int D, int N, int64_t waves, int64_t* L, int* nseg) {
     const int64_t per = sel_tiles(B, G, D) * sel_ntiles(N), want = (waves + per - 1) / per;
     int64_t len = (T + want - 1) / want;
+    const int64_t least = (int64_t)sqrt(0.1 * (double)T);
+    if (len < least) len = least;
     if (len < 16) len = 16;
     len = (len + SC - 1) / SC * SC;
     *L = len;
