@@ -9,7 +9,8 @@
 // the last K - 1 inputs and the weights stay in registers, and each input is read once from HBM (a tile's first K - 1
 // inputs also by the tile before, out of the L2). HBM-bound: 4 x 8192 x 2048 in bf16 with 4 taps, forward 54 us in the
 // kernel and 61 a call over inputs in turn (269 MB, 4.4 TB/s; a copy of that card 5.15), backward 98 (403 MB); pieces of 8
-// elements forwards (16 bytes), 4 backwards, where each channel holds 3 K + 2 floats.
+// elements forwards (16 bytes), 4 backwards, where each channel holds 3 K + 2 floats; narrower where sizes, strides or
+// addresses need it (4 x 8192, forward: 2044 channels in pieces of 4 63 us, 77 one by one; 2047 one by one 81).
 // One token of 256 sequences: 6.4 us, and 8.7 a call (the host's side).
 #include <type_traits>
 
@@ -370,7 +371,7 @@ int64_t conv_backward_workspace_bytes(int64_t B, int64_t H, int64_t T, int64_t d
 hipError_t launch_conv(ConvArgs a, hipStream_t st) {
     a.tile = (int)tile_of(a.B, a.H, a.T, a.d, 8, 4096, 32);
     a.ntile = tiles(a.T, a.tile);
-    if (a.bf16) a.align >= 8 ? conv_taps<8, true>(a, st) : conv_taps<1, true>(a, st);
+    if (a.bf16) a.align >= 8 ? conv_taps<8, true>(a, st) : a.align >= 4 ? conv_taps<4, true>(a, st) : conv_taps<1, true>(a, st);
     else a.align >= 4 ? conv_taps<4, false>(a, st) : conv_taps<1, false>(a, st);
     return hipGetLastError();
 }
