@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import sparse_memory_linear_amd as sdm
+from sparse_memory_linear_amd import binding
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -220,3 +221,62 @@ def test_captured_and_replayed():
         for (c, o), e in zip(sets, eager):
             for k, t in flat(o).items():
                 assert torch.equal(t, flat(e)[k]), (turn, k)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_the_library_without_strides_and_wanted_outputs(dtype):
+    """The C entry points with no strides (contiguous tensors) and no optional outputs: the binding's bits, twice."""
+    L, code = binding.lib(), 1 if dtype == torch.bfloat16 else 0
+    B, T, D, G, N, K = 2, 77, 72, 2, 20, 4
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(s, generator=g).to(DEV)  # noqa: E731
+    x, dt, dy = r(B, T, D).to(dtype), r(B, T, D).to(dtype), r(B, T, D).to(dtype)
+    w, A, Bm, Cm = r(D, K), -r(D, N).abs(), r(B, T, G, N).to(dtype), r(B, T, G, N).to(dtype)
+    st = torch.cuda.current_stream().cuda_stream
+    p = lambda t: t.data_ptr()  # noqa: E731
+    ws = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)  # noqa: E731
+
+    want, _ = sdm.sdm_causal_conv_forward(x, w, None, None)
+    grads = sdm.sdm_causal_conv_backward(dy, x, w, None, None)
+    bytes_ = L.sdm_causal_conv_backward_workspace_bytes(B, 1, T, D, K)
+    for _ in range(2):
+        y, dx, dw, tmp = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w), ws(bytes_)
+        assert L.sdm_causal_conv_forward(p(x), code, None, p(w), None, 0, None, None, None, None, p(y), B, 1, T, D, K, st) == 0
+        assert L.sdm_causal_conv_backward(p(dy), p(x), code, None, p(w), None, 0, None, None, None, None, p(dx), None, p(dw),
+                                          None, None, B, 1, T, D, K, p(tmp), tmp.numel(), st) == 0
+        assert torch.equal(y, want) and torch.equal(dx, grads["dx"]) and torch.equal(dw, grads["dw"])
+
+    want, _ = sdm.sdm_selective_scan_forward(x, dt, A, Bm, Cm)
+    grads = sdm.sdm_selective_scan_backward(dy, x, dt, A, Bm, Cm)
+    bytes_ = L.sdm_selective_scan_workspace_bytes(B, T, D, G, N), L.sdm_selective_scan_backward_workspace_bytes(B, T, D, G, N)
+    for _ in range(2):
+        y, dx, ddt, dA = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty_like(A)
+        dB, dC = torch.empty(Bm.shape, device=DEV), torch.empty(Bm.shape, device=DEV)
+        tmp, tmp2 = ws(bytes_[0]), ws(bytes_[1])
+        assert L.sdm_selective_scan_forward(p(x), p(dt), None, p(Bm), p(Cm), code, None, p(A), None, None, 1, None, None, None,
+                                            None, p(y), B, T, D, G, N, p(tmp), tmp.numel(), st) == 0
+        assert L.sdm_selective_scan_backward(p(dy), p(x), p(dt), None, p(Bm), p(Cm), code, None, p(A), None, None, 1, None, None,
+                                             None, None, p(dx), p(ddt), None, p(dA), p(dB), p(dC), None, None, None, B, T, D, G, N,
+                                             p(tmp2), tmp2.numel(), st) == 0
+        for got, name in ((y, None), (dx, "dx"), (ddt, "ddt"), (dA, "dA"), (dB, "dB"), (dC, "dC")):
+            assert torch.equal(got, want if name is None else grads[name]), name
+
+
+def test_inputs_that_share_their_rows():
+    """Inputs of stride 0 over the sequences or heads are what their copies are."""
+    g = torch.Generator().manual_seed(4)
+    r = lambda *s: torch.randn(s, generator=g).to(DEV)  # noqa: E731
+    x, dt, w, A, Bc = r(1, 50, 40), r(1, 50, 40), r(40, 3), -r(40, 8).abs(), r(1, 50, 1, 8)
+    xe, dte, Be = x.expand(3, 50, 40), dt.expand(3, 50, 40), Bc.expand(3, 50, 2, 8)
+    c = lambda t: t.contiguous()  # noqa: E731
+    dy = r(3, 50, 40)
+    for a, b in zip(sdm.sdm_causal_conv_forward(xe, w), sdm.sdm_causal_conv_forward(c(xe), w)):
+        assert torch.equal(a, b)
+    a, b = sdm.sdm_causal_conv_backward(dy, xe, w, out={"dx": torch.empty_like(dy)}), sdm.sdm_causal_conv_backward(dy, c(xe), w)
+    assert all(torch.equal(a[k], b[k]) for k in b)
+    for a, b in zip(sdm.sdm_selective_scan_forward(xe, dte, A, Be, Be), sdm.sdm_selective_scan_forward(c(xe), c(dte), A, c(Be), c(Be))):
+        assert torch.equal(a, b)
+    a, b = sdm.sdm_selective_scan_backward(dy, xe, dte, A, Be, Be), sdm.sdm_selective_scan_backward(dy, c(xe), c(dte), A, c(Be), c(Be))
+    assert all(torch.equal(a[k], b[k]) for k in b)
+    a, b = (sdm.sdm_causal_conv_backward(dy, t, w)["dx"] for t in (xe, c(xe)))  # (its gradient does not share them)
+    assert torch.equal(a, b)
