@@ -902,8 +902,8 @@ int sdm_causal_conv_backward(const void* dy, const void* x, int dtype, const int
     const int64_t *xs = x_strides ? x_strides : flat, *gs = dx_strides ? dx_strides : flat;
     if ((rc = check_strides(fn, "x", {B, H, T}, {xs[0], xs[1], xs[2]}))) return rc;
     if ((rc = check_strides(fn, "dx", {B, H, T}, {gs[0], gs[1], gs[2]}))) return rc;
-    if ((rc = check_apart(fn, "dx", d, {B, H, T}, {gs[0], gs[1], gs[2]}))) return rc;
-    if (T > 0) {
+    if (T > 0) {  // (of no tokens dx has no element, whatever its strides)
+        if ((rc = check_apart(fn, "dx", d, {B, H, T}, {gs[0], gs[1], gs[2]}))) return rc;
         if ((rc = check_address(fn, "x", x, es)) || (rc = check_address(fn, "dx", dx, es)) || (rc = check_buffers(fn, {dy})))
             return rc;
         if (dx == x || dx == dy || (dS0 && (dS0 == dS || dS0 == S0 || dS0 == dx)))

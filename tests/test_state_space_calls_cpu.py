@@ -1,0 +1,42 @@
+"""Host-side checks (no GPU) of calls at the edges of what the state-space layer's entry points take: no tokens, the
+largest sizes, tensors over each other. Every call here is refused before any launch."""
+import ctypes
+import os
+
+import pytest
+
+from sparse_memory_linear_amd import binding
+
+P = ctypes.c_void_p
+NULL, SHAPE, UNSUPPORTED, WORKSPACE = 1, 2, 5, 7
+
+
+def at(k):
+    """Aligned addresses far from each other; never dereferenced."""
+    return P((k + 1) << 40)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(binding.LIB_PATH):
+        import __graft_entry__
+        __graft_entry__.build()
+    return binding.lib()
+
+
+CONV_BWD = dict(dy=at(0), x=at(1), dtype=1, xs=None, w=at(2), bias=at(3), act=1, S0=at(4), dS=at(5), start=None, lengths=None,
+                dx=at(6), gs=None, dw=at(7), dbias=at(8), dS0=at(9), B=2, H=2, T=5, d=8, K=4, ws=None, bytes=0, stream=None)
+
+
+def conv_bwd(lib, **kw):
+    return lib.sdm_causal_conv_backward(*dict(CONV_BWD, **kw).values())
+
+
+def test_convolution_backward_of_no_tokens(lib):
+    """Contiguous tensors (no strides given) of no tokens hold no element twice: what is missing is the workspace."""
+    for B, H in ((1, 1), (2, 1), (1, 2), (2, 2), (300, 7)):
+        assert conv_bwd(lib, B=B, H=H, T=0, dy=None, x=None, dx=None) == WORKSPACE, (B, H)
+        assert conv_bwd(lib, B=B, H=H, T=0, dy=None, x=None, dx=None, dS0=CONV_BWD["dS"]) == WORKSPACE, (B, H)
+    zero = (ctypes.c_int64 * 3)(0, 0, 8)
+    assert conv_bwd(lib, T=0, gs=zero) == WORKSPACE
+    assert conv_bwd(lib, T=1, gs=zero) == SHAPE and conv_bwd(lib, T=1) == WORKSPACE
