@@ -623,7 +623,7 @@ int64_t sdm_selective_scan_backward_workspace_bytes(int64_t B, int64_t T, int64_
  *   NULL; dS0 may be dS)
  *   workspace >= sdm_selective_scan_backward_workspace_bytes bytes, 16-byte aligned
  * The order of all sums follows from the sizes alone. Same support as the forward, and
- * B*T*G*ceil(N/16) < 2^27, G*ceil(D/G/64)*ceil(N/16) < 2^17.
+ * B*T*G*ceil(N/16) <= 2^27 - 8, G*ceil(D/G/64)*ceil(N/16) < 2^17.
  * B = 0 is empty work (dA, dD and ddt_bias are not written).
  */
 int sdm_selective_scan_backward(const void* dy, const void* x, const void* dt, const void* z, const void* Bm,

@@ -945,8 +945,8 @@ int check_selective(const char* fn, int in_dtype, int64_t B, int64_t T, int64_t 
 }
 int check_selective_backward(const char* fn, int in_dtype, int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     const int rc = check_selective(fn, in_dtype, B, T, D, G, N);
-    // fewer than 2^32 threads for the sums: 32 a token, group and tile of states; 32768 a tile's gradient of A
-    if (rc == 0 && (B * G * T * ((N + 15) / 16) >= 1 << 27 || sdm::sel_tiles(1, (int)G, (int)D) * ((N + 15) / 16) >= 1 << 17))
+    // fewer than 2^32 threads for the sums: 32 a token, group and tile of states, in workgroups of 256; 32768 a tile's gradient of A
+    if (rc == 0 && (B * G * T * ((N + 15) / 16) > (1 << 27) - 8 || sdm::sel_tiles(1, (int)G, (int)D) * ((N + 15) / 16) >= 1 << 17))
         return fail(SDM_ERR_UNSUPPORTED, "%s: too many tokens or groups for one launch", fn);
     return rc;
 }

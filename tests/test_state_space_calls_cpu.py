@@ -40,3 +40,14 @@ def test_convolution_backward_of_no_tokens(lib):
     zero = (ctypes.c_int64 * 3)(0, 0, 8)
     assert conv_bwd(lib, T=0, gs=zero) == WORKSPACE
     assert conv_bwd(lib, T=1, gs=zero) == SHAPE and conv_bwd(lib, T=1) == WORKSPACE
+
+
+def test_selective_scan_backward_at_its_largest(lib):
+    """dB and dC are added by 32 threads a token, group and tile of 16 states, in workgroups of 256: with those rounded up, the
+    launch has to stay below 2^32 threads, or it would fail behind the passes in front of it."""
+    n = lib.sdm_selective_scan_backward_workspace_bytes
+    for B, T, D, G, N in ((1, 1 << 27, 64, 1, 16), (2, 1 << 26, 64, 1, 16), (1, 1 << 26, 64, 2, 16), (1, 1 << 25, 64, 1, 64)):
+        per = B * G * -(-N // 16)
+        fits = [T - k for k in range(0, 12) if -(-per * (T - k) * 32 // 256) * 256 < 1 << 32]
+        assert fits and all(n(B, t, D, G, N) > 0 for t in fits), (B, T)
+        assert all(n(B, T - k, D, G, N) == -1 for k in range(0, 12) if T - k not in fits), (B, T)
