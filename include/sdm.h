@@ -620,7 +620,7 @@ int64_t sdm_selective_scan_backward_workspace_bytes(int64_t B, int64_t T, int64_
  *   dS [B, D, N] fp32: dL/dS, or NULL (zeros); the other inputs as given to the forward call
  *   dx, ddt, dz [B, T, D] in_dtype (out; dz NULL where z is)
  *   dA [D, N], dB, dC [B, T, G, N], dD, ddt_bias [D], dS0 [B, D, N] fp32 (out; dD, ddt_bias and dS0 may be
- *   NULL; dS0 may be dS)
+ *   NULL; dS0 may be dS). Outputs may not overlap each other, nor, that apart, an input
  *   workspace >= sdm_selective_scan_backward_workspace_bytes bytes, 16-byte aligned
  * The order of all sums follows from the sizes alone. Same support as the forward, and
  * B*T*G*ceil(N/16) <= 2^27 - 8, G*ceil(D/G/64)*ceil(N/16) < 2^17.

@@ -951,6 +951,17 @@ int check_selective_backward(const char* fn, int in_dtype, int64_t B, int64_t T,
     return rc;
 }
 
+// Outputs (NULL: not given) at addresses of their own, and at none of the inputs that are read beside their stores
+int check_own(const char* fn, std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+    for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+        for (const void* const* p = outs.begin(); *o && p != o; ++p)
+            if (*p == *o) return fail(SDM_ERR_SHAPE, "%s: two outputs at one address", fn);
+        for (const void* i : ins)
+            if (*o && i == *o) return fail(SDM_ERR_SHAPE, "%s: an output may not alias an input", fn);
+    }
+    return 0;
+}
+
 struct SelTensor {
     const char* name;
     const void* p;
@@ -1061,6 +1072,12 @@ int sdm_selective_scan_backward(const void* dy, const void* x, const void* dt, c
     }
     if ((rc = check_workspace(workspace, workspace_bytes,
                               sdm::selective_backward_workspace_bytes(B, T, (int)G, (int)D, (int)N))))
+        return rc;
+    // dA, dD and ddt_bias are written behind the last pass, which reads all inputs but S0 and dS
+    const bool any = T > 0;
+    const void *tx = any ? dx : nullptr, *tdt = any ? ddt : nullptr, *tz = any && z ? dz : nullptr, *tB = any ? dB : nullptr, *tC = any ? dC : nullptr;
+    if ((rc = check_own(fn, {tx, tdt, tz, tB, tC, dS0, dA, dD, ddt_bias}, {})) ||
+        (any && (rc = check_own(fn, {tx, tdt, tz, tB, tC, dS0}, {dy, x, dt, z, Bm, Cm, A, Dskip, dt_bias}))))
         return rc;
     sdm::SelBwdArgs a{};
     selective_args(a, x, dt, z, Bm, Cm, in_dtype, s, A, Dskip, dt_bias, softplus, S0, start, lengths, B, T, D, G, N, workspace);

@@ -51,3 +51,24 @@ def test_selective_scan_backward_at_its_largest(lib):
         fits = [T - k for k in range(0, 12) if -(-per * (T - k) * 32 // 256) * 256 < 1 << 32]
         assert fits and all(n(B, t, D, G, N) > 0 for t in fits), (B, T)
         assert all(n(B, T - k, D, G, N) == -1 for k in range(0, 12) if T - k not in fits), (B, T)
+
+
+SCAN_IN = ("x", "dt", "z", "Bm", "Cm", "A", "D", "bias")
+SCAN_BWD = dict(dy=at(0), x=at(1), dt=at(2), z=at(3), Bm=at(4), Cm=at(5), dtype=1, strides=None, A=at(6), D=at(7), bias=at(8), softplus=1,
+                S0=at(9), dS=at(10), start=None, lengths=None, dx=at(11), ddt=at(12), dz=at(13), dA=at(14), dB=at(15), dC=at(16), dD=at(17),
+                dbias=at(18), dS0=at(19), B=2, T=300, Dn=128, G=2, N=16, ws=at(20), bytes=1 << 40, stream=None)
+
+
+def test_selective_scan_gradients_over_each_other(lib):
+    """Two gradients at one address, or one at that of an input which is read beside it."""
+    call = lambda **kw: lib.sdm_selective_scan_backward(*dict(SCAN_BWD, **kw).values())  # noqa: E731
+    outs = ("dx", "ddt", "dz", "dA", "dB", "dC", "dD", "dbias", "dS0")
+    for i, a in enumerate(outs):
+        for b in outs[:i]:
+            assert call(**{a: SCAN_BWD[b]}) == SHAPE, (a, b)
+    for a in ("dx", "ddt", "dz", "dB", "dC", "dS0"):
+        for b in ("dy", *SCAN_IN):
+            assert call(**{a: SCAN_BWD[b]}) == SHAPE, (a, b)
+    for a, b in (("dD", "dA"), ("dbias", "dD"), ("dS0", "dA")):  # without tokens too
+        assert call(T=0, **{a: SCAN_BWD[b]}) == SHAPE, (a, b)
+    assert call(dS0=SCAN_BWD["dS"], ws=None) == WORKSPACE and call(dz=SCAN_BWD["x"], z=None, ws=None) == WORKSPACE
