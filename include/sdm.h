@@ -546,7 +546,8 @@ typedef enum sdm_act { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1 } sdm_act;
  *   w       [H, d, K], bias [H, d] fp32 (bias may be NULL)
  *   S0      [B, H, K-1, d]  dtype: the K-1 inputs in front of token 0, oldest first, or NULL (zeros)
  *   S       [B, H, K-1, d]  dtype (out): those behind the last token, or NULL (not wanted); may be S0
- *                           (decoding). Rows in front of the last sequence's first token are 0
+ *                           (decoding), and may not overlap another input. Rows in front of the last
+ *                           sequence's first token are 0
  *   y       [B, H, T, d]    dtype (out); may not overlap x, S0 or S
  * Products and sums are fp32. T = 0 passes the state on.
  * Supported: K from 2 to 8; H*d <= 2^23, B*ceil(T/8)*ceil(H*d/64) < 2^26.
@@ -594,7 +595,8 @@ int64_t sdm_selective_scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int6
  *   strides   [12]: x's batch and token, dt's, z's, then Bm's batch, token and group, and Cm's
  *   A [D, N], Dskip [D] (or NULL), dt_bias [D] (or NULL) fp32
  *   S0        [B, D, N]     fp32: the state before token 0, or NULL (zeros)
- *   S         [B, D, N]     fp32 (out): the state behind the last token, or NULL; may be S0 (decoding)
+ *   S         [B, D, N]     fp32 (out): the state behind the last token, or NULL; may be S0 (decoding), and may
+ *                           not overlap another input
  *   y         [B, T, D]     in_dtype (out); may not overlap an input
  *   workspace >= sdm_selective_scan_workspace_bytes bytes, 16-byte aligned (may be NULL where that is 0)
  * Products, sums and states are fp32. Meant for delta A <= 0; inputs and states must be finite (a NaN or

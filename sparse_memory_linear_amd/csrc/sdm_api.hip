@@ -835,6 +835,17 @@ int check_conv(const char* fn, int dtype, int act, int64_t B, int64_t H, int64_t
     return B == 0 || H == 0 ? NO_WORK : 0;
 }
 
+// Outputs (NULL: not given) at addresses of their own, and at none of the inputs that are read beside their stores
+int check_own(const char* fn, std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+    for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+        for (const void* const* p = outs.begin(); *o && p != o; ++p)
+            if (*p == *o) return fail(SDM_ERR_SHAPE, "%s: two outputs at one address", fn);
+        for (const void* i : ins)
+            if (*o && i == *o) return fail(SDM_ERR_SHAPE, "%s: an output may not alias an input", fn);
+    }
+    return 0;
+}
+
 // Rows by strides that a call writes: no element twice
 int check_apart(const char* fn, const char* name, int64_t row, std::initializer_list<int64_t> sizes,
                 std::initializer_list<int64_t> strides) {
@@ -873,6 +884,7 @@ int sdm_causal_conv_forward(const void* x, int dtype, const int64_t* x_strides, 
         if (p && !aligned16(p)) return fail(SDM_ERR_ALIGN, "%s: pointer %p not 16-byte aligned", fn, p);
     if (lengths && (rc = check_address(fn, "lengths", lengths, 4))) return rc;
     if (T > 0 && (y == x || y == S0 || y == S)) return fail(SDM_ERR_SHAPE, "%s: y may not alias x, S0 or S", fn);
+    if (T > 0 && (rc = check_own(fn, {S}, {x, w, bias}))) return rc;
     sdm::ConvArgs a{};
     a.x = x; a.w = w; a.bias = bias; a.S0 = S0; a.S = S; a.start = start; a.lengths = lengths; a.y = y;
     a.x_b = xs[0]; a.x_h = xs[1]; a.x_t = xs[2];
@@ -951,17 +963,6 @@ int check_selective_backward(const char* fn, int in_dtype, int64_t B, int64_t T,
     return rc;
 }
 
-// Outputs (NULL: not given) at addresses of their own, and at none of the inputs that are read beside their stores
-int check_own(const char* fn, std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
-    for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
-        for (const void* const* p = outs.begin(); *o && p != o; ++p)
-            if (*p == *o) return fail(SDM_ERR_SHAPE, "%s: two outputs at one address", fn);
-        for (const void* i : ins)
-            if (*o && i == *o) return fail(SDM_ERR_SHAPE, "%s: an output may not alias an input", fn);
-    }
-    return 0;
-}
-
 struct SelTensor {
     const char* name;
     const void* p;
@@ -1028,6 +1029,7 @@ int sdm_selective_scan_forward(const void* x, const void* dt, const void* z, con
         return fail(SDM_ERR_SHAPE, "%s: y may not alias an input or S", fn);
     const int64_t need = sdm::selective_workspace_bytes(B, T, (int)G, (int)D, (int)N);
     if (need > 0 && (rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+    if (T > 0 && (rc = check_own(fn, {S}, {x, dt, z, Bm, Cm, A, Dskip, dt_bias}))) return rc;
     sdm::SelArgs a{};
     selective_args(a, x, dt, z, Bm, Cm, in_dtype, s, A, Dskip, dt_bias, softplus, S0, start, lengths, B, T, D, G, N, workspace);
     a.S = S; a.y = y;

@@ -72,3 +72,17 @@ def test_selective_scan_gradients_over_each_other(lib):
     for a, b in (("dD", "dA"), ("dbias", "dD"), ("dS0", "dA")):  # without tokens too
         assert call(T=0, **{a: SCAN_BWD[b]}) == SHAPE, (a, b)
     assert call(dS0=SCAN_BWD["dS"], ws=None) == WORKSPACE and call(dz=SCAN_BWD["x"], z=None, ws=None) == WORKSPACE
+
+
+def test_states_over_inputs(lib):
+    """The state behind the last token may be written over S0, and over nothing that the call reads."""
+    conv = dict(x=at(0), dtype=1, xs=None, w=at(1), bias=at(2), act=1, S0=at(3), S=at(4), start=None, lengths=None, y=at(5), B=2, H=2, T=5, d=8,
+                K=4, stream=None)
+    for b in ("x", "w", "bias"):
+        assert lib.sdm_causal_conv_forward(*dict(conv, S=conv[b]).values()) == SHAPE, b
+    scan = {k: v for k, v in SCAN_BWD.items() if k in (*SCAN_IN, "dtype", "strides", "softplus", "S0", "start", "lengths")}
+    names = ("x", "dt", "z", "Bm", "Cm", "dtype", "strides", "A", "D", "bias", "softplus", "S0", "S", "start", "lengths", "y")
+    scan.update(S=at(10), y=at(11))
+    tail = (2, 300, 128, 2, 16, at(20), 1 << 40, None)
+    for b in SCAN_IN:
+        assert lib.sdm_selective_scan_forward(*(dict(scan, S=scan[b])[n] for n in names), *tail) == SHAPE, b
