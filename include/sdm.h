@@ -569,7 +569,8 @@ int64_t sdm_causal_conv_backward_workspace_bytes(int64_t B, int64_t H, int64_t T
  *   dx [B, H, T, d] dtype (out), by strides [3] (so that it may be a part of a projection's gradient); its
  *   elements may not share an address, nor overlap an input
  *   dw [H, d, K], dbias [H, d] fp32 (out; dbias may be NULL), summed over all tokens in an order that
- *   follows from the sizes alone;  dS0 [B, H, K-1, d] dtype (out), or NULL; may be dS only where T = 0
+ *   follows from the sizes alone;  dS0 [B, H, K-1, d] dtype (out), or NULL; may be dS only where T = 0.
+ *   Outputs may not overlap each other, nor, that apart, an input
  *   workspace >= sdm_causal_conv_backward_workspace_bytes bytes, 16-byte aligned
  * Same support as the forward. B = 0 is empty work (dw and dbias are not written).
  */

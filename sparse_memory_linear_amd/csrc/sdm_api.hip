@@ -927,6 +927,9 @@ int sdm_causal_conv_backward(const void* dy, const void* x, int dtype, const int
         if (p && !aligned16(p)) return fail(SDM_ERR_ALIGN, "%s: pointer %p not 16-byte aligned", fn, p);
     if (lengths && (rc = check_address(fn, "lengths", lengths, 4))) return rc;
     if ((rc = check_workspace(workspace, workspace_bytes, sdm::conv_backward_workspace_bytes(B, H, T, d, (int)K)))) return rc;
+    // dw and dbias are written behind the pass that reads the inputs; of no tokens only the states are looked at
+    const void* tx = T > 0 ? dx : nullptr;
+    if ((rc = check_own(fn, {tx, dS0, dw, dbias}, {})) || (T > 0 && (rc = check_own(fn, {tx, dS0}, {dy, x, w, bias, S0, dS})))) return rc;
     sdm::ConvBwdArgs a{};
     a.dy = dy; a.x = x; a.w = w; a.bias = bias; a.S0 = S0; a.dS = dS; a.start = start; a.lengths = lengths;
     a.dx = dx; a.dw = dw; a.dbias = dbias; a.dS0 = dS0;

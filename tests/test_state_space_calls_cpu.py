@@ -86,3 +86,15 @@ def test_states_over_inputs(lib):
     tail = (2, 300, 128, 2, 16, at(20), 1 << 40, None)
     for b in SCAN_IN:
         assert lib.sdm_selective_scan_forward(*(dict(scan, S=scan[b])[n] for n in names), *tail) == SHAPE, b
+
+
+def test_convolution_gradients_over_each_other(lib):
+    big = dict(ws=at(10), bytes=1 << 40)
+    outs = ("dx", "dw", "dbias", "dS0")
+    for i, a in enumerate(outs):
+        for b in outs[:i]:
+            assert conv_bwd(lib, **{a: CONV_BWD[b]}, **big) == SHAPE, (a, b)
+    for a in ("dx", "dS0"):
+        for b in ("dy", "x", "w", "bias", "S0", "dS"):
+            assert conv_bwd(lib, **{a: CONV_BWD[b]}, **big) == SHAPE, (a, b)
+    assert conv_bwd(lib, T=0, dw=CONV_BWD["dbias"], **big) == SHAPE and conv_bwd(lib, T=0, dw=CONV_BWD["dS0"], **big) == SHAPE
