@@ -641,6 +641,7 @@ int sdm_selective_scan_backward(const void* dy, const void* x, const void* dt, c
  * sdm_residual_layer_norm -- sdm_residual_norm with the mean taken off and a bias, per row:
  *   h = x + res,   m = mean_j h_j,   y = (h - m) / sqrt(mean_j (h_j - m)^2 + eps) * gamma + bias
  *   bias [d] fp32, or NULL (zeros); everything else, e4m3 outputs with their scales among it, as there
+ *   (y, h and scale may not overlap gamma, bias or each other)
  * The mean and the squares about it are summed in fp32, over the fp32 sums h.
  */
 int sdm_residual_layer_norm(const void* x, int x_dtype, const void* res, void* h, int h_dtype, const float* gamma,
@@ -658,7 +659,8 @@ int64_t sdm_residual_layer_norm_backward_workspace_bytes(int64_t rows, int64_t d
  * r = 1 / sqrt(mean (h - m)^2 + eps) and n = (h - m) r:
  *   dx = dh + r (gamma dy - mean_j(gamma dy) - n mean_j(gamma dy n))
  *   dgamma = sum over rows of dy n,   dbias = sum over rows of dy (may be NULL)
- * Arguments, aliases and support as sdm_residual_norm_backward.
+ * Arguments, aliases and support as sdm_residual_norm_backward; dx, dgamma and dbias may not overlap each other
+ * or gamma.
  */
 int sdm_residual_layer_norm_backward(const void* dy, const void* dh, int g_dtype, const void* h, int h_dtype,
                                      const float* gamma, float eps, int64_t rows, int64_t d, void* dx, float* dgamma,

@@ -631,6 +631,17 @@ int check_norm_sizes(const char* fn, int64_t rows, int64_t d, float eps) {
 
 namespace {
 
+// Outputs (NULL: not given) at addresses of their own, and at none of the inputs that are read beside their stores
+int check_own(const char* fn, std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+    for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+        for (const void* const* p = outs.begin(); *o && p != o; ++p)
+            if (*p == *o) return fail(SDM_ERR_SHAPE, "%s: two outputs at one address", fn);
+        for (const void* i : ins)
+            if (*o && i == *o) return fail(SDM_ERR_SHAPE, "%s: an output may not alias an input", fn);
+    }
+    return 0;
+}
+
 int norm_impl(const char* fn, bool mean, const void* x, int x_dtype, const void* res, void* h, int h_dtype,
               const float* gamma, const float* bias, float eps, int64_t rows, int64_t d, void* y, int y_dtype,
               float* scale, int64_t group, void* stream) {
@@ -654,6 +665,10 @@ int norm_impl(const char* fn, bool mean, const void* x, int x_dtype, const void*
     if (y_dtype == SDM_E4M3 && (rc = check_buffers(fn, {scale}))) return rc;
     if (y == x || y == h || (res && y == res)) return fail(SDM_ERR_SHAPE, "%s: y may not alias x, res or h", fn);
     if (h && h == x && x_dtype != h_dtype) return fail(SDM_ERR_SHAPE, "%s: h may alias x only in the same dtype", fn);
+    if (mean) {  // (a row's inputs and outputs go by rows, scales and parameters do not)
+        const void* sc = y_dtype == SDM_E4M3 ? scale : nullptr;
+        if ((rc = check_own(fn, {y, h, sc}, {gamma, bias})) || (rc = check_own(fn, {sc}, {x, res}))) return rc;
+    }
     sdm::NormArgs a{};
     a.x = x; a.res = res; a.h = h; a.gamma = gamma; a.y = y; a.scale = scale;
     a.rows = rows; a.d = (int)d; a.group = (int)group; a.eps = eps;
@@ -682,6 +697,7 @@ int norm_backward_impl(const char* fn, bool mean, const void* dy, const void* dh
     if (dbias && !aligned16(dbias)) return fail(SDM_ERR_ALIGN, "%s: dbias not 16-byte aligned", fn);
     if (dx == h && g_dtype != h_dtype) return fail(SDM_ERR_SHAPE, "%s: dx may alias h only in the same dtype", fn);
     if ((rc = check_workspace(workspace, workspace_bytes, norm_backward_bytes(mean, rows, d)))) return rc;
+    if (mean && ((rc = check_own(fn, {dx, dgamma, dbias}, {})) || (rc = check_own(fn, {dx}, {gamma})))) return rc;
     sdm::NormBwdArgs a{};
     a.dy = dy; a.dh = dh; a.h = h; a.gamma = gamma; a.dx = dx; a.dgamma = dgamma;
     a.part = static_cast<float*>(workspace);
@@ -833,17 +849,6 @@ int check_conv(const char* fn, int dtype, int act, int64_t B, int64_t H, int64_t
         B * tiles * ((H * d + 63) / 64) >= 1 << 26)
         return fail(SDM_ERR_UNSUPPORTED, "%s: too many tokens and channels for one launch", fn);
     return B == 0 || H == 0 ? NO_WORK : 0;
-}
-
-// Outputs (NULL: not given) at addresses of their own, and at none of the inputs that are read beside their stores
-int check_own(const char* fn, std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
-    for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
-        for (const void* const* p = outs.begin(); *o && p != o; ++p)
-            if (*p == *o) return fail(SDM_ERR_SHAPE, "%s: two outputs at one address", fn);
-        for (const void* i : ins)
-            if (*o && i == *o) return fail(SDM_ERR_SHAPE, "%s: an output may not alias an input", fn);
-    }
-    return 0;
 }
 
 // Rows by strides that a call writes: no element twice

@@ -98,3 +98,18 @@ def test_convolution_gradients_over_each_other(lib):
         for b in ("dy", "x", "w", "bias", "S0", "dS"):
             assert conv_bwd(lib, **{a: CONV_BWD[b]}, **big) == SHAPE, (a, b)
     assert conv_bwd(lib, T=0, dw=CONV_BWD["dbias"], **big) == SHAPE and conv_bwd(lib, T=0, dw=CONV_BWD["dS0"], **big) == SHAPE
+
+
+def test_layer_norm_outputs_over_each_other(lib):
+    f = ctypes.c_float
+    norm = dict(x=at(0), xd=1, res=at(1), h=at(2), hd=1, gamma=at(3), bias=at(4), eps=f(1e-5), rows=4, d=256, y=at(5), yd=2, scale=at(6),
+                group=128, stream=None)
+    for a, b in (("y", "gamma"), ("y", "bias"), ("h", "gamma"), ("h", "bias"), ("scale", "gamma"), ("scale", "bias"), ("scale", "x"),
+                 ("scale", "res"), ("scale", "y"), ("scale", "h")):
+        assert lib.sdm_residual_layer_norm(*dict(norm, **{a: norm[b]}).values()) == SHAPE, (a, b)
+    back = dict(dy=at(0), dh=at(1), gd=0, h=at(2), hd=0, gamma=at(3), eps=f(1e-5), rows=4, d=256, dx=at(4), dgamma=at(5), dbias=at(6), ws=at(7),
+                bytes=1 << 40, stream=None)
+    for a, b in (("dgamma", "dbias"), ("dx", "dgamma"), ("dx", "dbias"), ("dx", "gamma")):
+        assert lib.sdm_residual_layer_norm_backward(*dict(back, **{a: back[b]}).values()) == SHAPE, (a, b)
+    for b in ("dy", "dh", "h"):  # (over a row's own inputs it may be)
+        assert lib.sdm_residual_layer_norm_backward(*dict(back, dx=back[b], ws=None).values()) == WORKSPACE, b
