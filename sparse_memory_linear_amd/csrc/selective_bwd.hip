@@ -18,6 +18,7 @@
 // at 2 and 4 wavefronts a SIMD): 4 x 4096 x 2048 with 16 states in bf16, first pass 168 us, carries 15, last pass 410, sums
 // 28, for 92 us of HBM at a copy's rate. (A state every 4 tokens instead would spare forming 4 states of 8 twice, a tenth
 // of the last pass, but the first one has no room for 268 MB more: it moves 606 MB in its 168 us.)
+#include <cmath>
 #include <type_traits>
 
 #include "selective.h"
@@ -394,8 +395,19 @@ struct SelSumD {
     }
 };
 
-// The launches are the same for one segment: any is cut (64 tokens of one sequence: 107 -> 45 us), into twice what fits
-void sel_bwd_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) { sel_segments(B, T, G, D, N, 4096, L, nseg); }
+// The launches are the same for one segment: any is cut (64 tokens of one sequence: 107 -> 45 us), into twice what fits.
+// A segment's sums for dA, dD and dt_bias are one chain of fp32 additions, up to n / 2 half steps off in n like terms, so
+// it has 1024 tokens at most, or the root of T / 10 (more in 10^7 tokens and up, and fewer than 2^16 segments of 2^27).
+// 64 x 4096 x 2048 with 16 states, bf16: 9.5 ms by one segment of 2048 tokens a wavefront, 9.3 so.
+void sel_bwd_split(int64_t B, int64_t T, int G, int D, int N, int64_t* L, int* nseg) {
+    sel_segments(B, T, G, D, N, 4096, L, nseg);
+    int64_t most = ((int64_t)sqrt(0.1 * (double)T) + SC - 1) / SC * SC;
+    if (most < 1024) most = 1024;
+    if (*L > most) {
+        *L = most;
+        *nseg = (int)((T + most - 1) / most);
+    }
+}
 
 // The workspace's parts, in floats
 struct SelBwdParts {

@@ -1,7 +1,10 @@
 """Calls at the edges of what the state-space layer's entry points take, on the GPU."""
+import math
+
 import pytest
 import torch
 
+import sparse_memory_linear_amd as sdm
 from sparse_memory_linear_amd import binding
 
 pytestmark = pytest.mark.gpu
@@ -28,3 +31,31 @@ def test_convolution_backward_of_no_tokens(B, H, d, K, dtype):
                                         p(dS0), B, H, 0, d, K, p(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
         assert rc == 0, L.sdm_last_error()
         assert torch.equal(dS0, want) and (dw == 0).all() and (db == 0).all()
+
+
+def test_sums_of_many_like_terms():
+    """So many sequences that none has to be cut, of 8192 tokens all alike: a sum of n like terms in one chain of fp32 is off
+    by up to n / 2 half steps (each addition by half a step of the sum so far), and no more than 1024 may be in one. The terms
+    themselves are off by 64 half steps at most (decays of 0.6 off by 4, 2.5 times over in a state and its gradient each)."""
+    B, T, c = 4096, 8192, 0.9
+    full = lambda v: torch.full((1, 1, 1), v, device=DEV)  # noqa: E731
+    x, dt, dy, Bm, Cm = (full(v).expand(B, T, 1) for v in (1.0, 0.5, c, 0.7, 0.3))
+    A, D = torch.full((1, 1), -1.0, device=DEV), torch.zeros(1, device=DEV)
+    got = sdm.sdm_selective_scan_backward(dy, x, dt, A, Bm, Cm, D, softplus=False)
+    f = lambda t: float(t.flatten()[0])  # noqa: E731  (as fp32 holds them)
+    c, b, k = f(dy), f(Bm), f(Cm)
+    a, h, hs = math.exp(-0.5), 0.0, [0.0]
+    for _ in range(T):
+        h = a * h + 0.5 * b
+        hs.append(h)
+    q, dA, dbias = 0.0, 0.0, 0.0
+    for t in reversed(range(T)):
+        q += c * k
+        w = q * a * hs[t]
+        dA += 0.5 * w
+        dbias += q * b - w
+        q *= a
+    # the sums, and the magnitudes of what their terms are made of (a step's: w and q b, w in all 2 dA)
+    for name, want, size in (("dD", c * T, c * T), ("dA", dA, dA), ("ddt_bias", dbias, dbias + 4 * dA)):
+        e = abs(float(got[name].flatten()[0].double()) / B - want)
+        assert e <= (1024 / 2 * want + 64 * size) * 2.0 ** -24, (name, e / want)
