@@ -356,7 +356,7 @@ __global__ __launch_bounds__(MULTI ? 256 : 64, 2) void sel_grads_kernel(SelBwdAr
     pd2[64] = dbias;
 }
 
-// dB and dC [B,T,G,N]: the sums of the channel tiles' rows, in their order; 0 behind the last token
+// dB and dC [B,T,G,N]: the sums of the channel tiles' rows, in 64 bits and in their order; 0 behind the last token
 __global__ __launch_bounds__(256) void sel_bc_kernel(SelBwdArgs a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, cols = a.B * a.G * a.T * a.ntiles * 32;  // [b][g][t][nt][2][16]
     if (i >= cols) return;
@@ -364,11 +364,11 @@ __global__ __launch_bounds__(256) void sel_bc_kernel(SelBwdArgs a) {
     const int m = (int)(i % (a.ntiles * 32)), n = m / 32 * 16 + (m & 15);
     const int64_t t = u % a.T, bg = u / a.T, b = bg / a.G, g = bg % a.G;
     if (n >= a.N) return;
-    float s = 0.f;
+    double s = 0.0;
     if (!a.lengths || t < a.lengths[b])
 #pragma unroll 8
         for (int k = 0; k < a.ctiles; ++k) s += a.part_bc[k * cols + i];
-    (m & 16 ? a.dC : a.dB)[((b * a.T + t) * a.G + g) * a.N + n] = s;
+    (m & 16 ? a.dC : a.dB)[((b * a.T + t) * a.G + g) * a.N + n] = (float)s;
 }
 
 // dA [D][N] of the columns [g][ct][nt][blk][lane][r]

@@ -59,3 +59,19 @@ def test_sums_of_many_like_terms():
     for name, want, size in (("dD", c * T, c * T), ("dA", dA, dA), ("ddt_bias", dbias, dbias + 4 * dA)):
         e = abs(float(got[name].flatten()[0].double()) / B - want)
         assert e <= (1024 / 2 * want + 64 * size) * 2.0 ** -24, (name, e / want)
+
+
+def test_sums_over_many_channels():
+    """The gradients of B and C of 2^17 like channels: 64 are added in a tree (6 half steps of the sum), the 2048 tiles' sums in
+    64 bits, rounded once; a term is off by 16 half steps at most (a decay by 4, and its products)."""
+    D, x, dt, c, b, k = 1 << 17, 1.0, 0.5, 0.9, 0.7, 0.3
+    full = lambda v, n: torch.full((1, 2, n), v, device=DEV)  # noqa: E731
+    tx, td, tc, tb, tk = full(x, D), full(dt, D), full(c, D), full(b, 1), full(k, 1)
+    got = sdm.sdm_selective_scan_backward(tc, tx, td, torch.full((D, 1), -1.0, device=DEV), tb, tk, softplus=False)
+    c, b, k = (float(t.flatten()[0]) for t in (tc, tb, tk))
+    a, h1 = math.exp(-dt), dt * b
+    h2, g2 = a * h1 + dt * b, c * k
+    for name, want in (("dC", (c * h1, c * h2)), ("dB", (dt * (g2 + a * g2), dt * g2))):
+        for t in range(2):
+            e = abs(float(got[name][0, t, 0].double()) / (D * want[t]) - 1)
+            assert e <= (6 + 16 + 1) * 2.0 ** -24, (name, t, e)
