@@ -581,8 +581,10 @@ int sdm_causal_conv_backward(const void* dy, const void* x, int dtype, const int
                              int64_t workspace_bytes, void* stream);
 
 /*
- * sdm_selective_scan_workspace_bytes -- device workspace sdm_selective_scan_forward needs (0: none; -1: sizes
- * that the call refuses).
+ * sdm_selective_scan_workspace_bytes -- device workspace sdm_selective_scan_forward needs (0: none, as when there
+ * is no work, for short calls or many streams of channels; -1: sizes that the call refuses). Fewer sequences or
+ * tokens can need more than many (2048 channels, 16 states, 4096 tokens: 36 MB for 32 sequences, none for 48):
+ * one workspace for calls of several sizes is as large as the largest of their answers.
  */
 int64_t sdm_selective_scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);
 
@@ -613,7 +615,8 @@ int sdm_selective_scan_forward(const void* x, const void* dt, const void* z, con
 
 /*
  * sdm_selective_scan_backward_workspace_bytes -- device workspace sdm_selective_scan_backward needs: a state
- * every 8 tokens and rows of partial sums (0: no work; -1: sizes that the call refuses).
+ * every 8 tokens and rows of partial sums (0: no work; -1: sizes that the call refuses; calls of several sizes as
+ * there).
  */
 int64_t sdm_selective_scan_backward_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);
 

@@ -874,6 +874,8 @@ def sdm_causal_conv_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
 
 
 def sdm_selective_scan_workspace_bytes(B: int, T: int, D: int, G: int, N: int) -> int:
+    """Workspace of one forward call; fewer sequences or tokens can need more than many, so one workspace for calls of
+    several sizes takes the largest of their answers."""
     n = lib().sdm_selective_scan_workspace_bytes(B, T, D, G, N)
     if n < 0:
         raise ValueError("invalid sizes for the selective scan workspace")
