@@ -7,11 +7,12 @@
 // A thread owns VEC channels (a piece of a row, or one channel where rows are not aligned to pieces) over a
 // tile of tokens, a wavefront 64 such threads of one tile, so that lengths and begins of sequences are scalar:
 // the last K - 1 inputs and the weights stay in registers, and each input is read once from HBM (a tile's first K - 1
-// inputs also by the tile before, out of the L2). HBM-bound: 4 x 8192 x 2048 in bf16 with 4 taps, forward 54 us in the
+// inputs also by the tile before, out of the L2). HBM-bound: 4 x 8192 x 2048 in bf16 with 4 taps, forward 54 to 58 us in the
 // kernel and 61 a call over inputs in turn (269 MB, 4.4 TB/s; a copy of that card 5.15), backward 98 (403 MB); pieces of 8
 // elements forwards (16 bytes), 4 backwards, where each channel holds 3 K + 2 floats; narrower where sizes, strides or
-// addresses need it (4 x 8192, forward: 2044 channels in pieces of 4 63 us, 77 one by one; 2047 one by one 81).
-// One token of 256 sequences: 6.4 us, and 8.7 a call (the host's side).
+// addresses need it (4 x 8192, forward: 2044 channels in pieces of 4 61 us, 77 one by one; 2047 one by one
+// 81, 90 in rows of odd strides; in fp32 2048 channels 108, backward 169).
+// One token of 256 sequences: 6.3 us, and 8.9 a call (the host's side).
 #include <type_traits>
 
 #include "sdm_internal.h"

@@ -8,8 +8,9 @@
 // last pass starts every segment where it belongs. See selective.h for a wavefront's tile.
 //
 // Bound by vector instructions (103 a token and tile in the last pass, 74 in the first; issued in 96% of the cycles):
-// 4 x 8192 x 2048 with 16 states in bf16, 185 us first pass + 18 carry + 250 last pass, for 105 us of HBM at a copy's rate
-// and 137 of one pass's exponentials and products alone; one token of 256 sequences 15.3 us (71 MB, 4.7 TB/s): HBM.
+// 4 x 8192 x 2048 with 16 states in bf16, 171 to 185 us first pass, 18 carry and 232 to 251 last pass (422 a call), for 105 us
+// of HBM at a copy's rate and 137 of one pass's exponentials and products alone; one token of 256 sequences 15.3 us (71 MB,
+// 4.7 TB/s): HBM.
 #include <cmath>
 #include <type_traits>
 

@@ -15,9 +15,9 @@
 // Sums over channels leave a row a tile, added by a last pass.
 //
 // Bound by vector instructions (335 a token and tile in the last pass, 123 in the first; issued in 84 and 80% of the cycles,
-// at 2 and 4 wavefronts a SIMD): 4 x 4096 x 2048 with 16 states in bf16, first pass 168 us, carries 15, last pass 410, sums
-// 28, for 92 us of HBM at a copy's rate. (A state every 4 tokens instead would spare forming 4 states of 8 twice, a tenth
-// of the last pass, but the first one has no room for 268 MB more: it moves 606 MB in its 168 us.)
+// at 2 and 4 wavefronts a SIMD): 4 x 4096 x 2048 with 16 states in bf16, first pass 163 to 174 us, carries 15, last pass 403 to 431,
+// sums 28 (610 a call), for 92 us of HBM at a copy's rate. (A state every 4 tokens instead would spare forming 4 states of 8 twice, a tenth
+// of the last pass, but the first one has no room for 268 MB more: it moves 606 MB as it is.)
 #include <cmath>
 #include <type_traits>
 
